@@ -51,7 +51,8 @@ EXPORTS = ("cba_workspace_bytes", "cba_workspace_bytes_ex", "cba_workspace_bytes
            "cba_get_status", "cba_bn_act_backward_noalloc",
            "cba_selftest_bounded_wait", "cba_yolo_backward", "cba_route_backward",
            "cba_pooled_size", "cba_maxpool_backward", "cba_error_string", "cba_last_cuda_error",
-           "cba_version", "cba_plan_info")
+           "cba_version", "cba_plan_info",
+           "cba_layernorm_forward", "cba_layernorm_workspace_bytes", "cba_layernorm_backward")
 CBA_ROUTE_MAX_INPUTS = 8
 CBA_WS_RECOMPUTE_Z = 1
 CBA_PHASE_EVENTS = 5
@@ -59,6 +60,9 @@ CBA_PATH_FFMA = 0
 CBA_PATH_TC_ROWS = 1
 CBA_PATH_TC_BATCH_INNER = 2
 CBA_PATH_TC_GEMM_1X1 = 3
+CBA_F32 = 0
+CBA_F16 = 1
+CBA_BF16 = 2
 
 
 class cba_desc_t(ctypes.Structure):
@@ -77,6 +81,14 @@ class cba_plan_info_t(ctypes.Structure):
 class cba_pool_desc_t(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("N", "C", "H", "W", "kernel_h", "kernel_w",
                                               "stride_h", "stride_w", "pad_h", "pad_w")]
+
+
+class cba_layernorm_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("cols", ctypes.c_int), ("type", ctypes.c_int),
+                ("param_type", ctypes.c_int), ("accumulate", ctypes.c_int),
+                ("eps", ctypes.c_float), ("ld_x", ctypes.c_longlong),
+                ("ld_y", ctypes.c_longlong), ("ld_dy", ctypes.c_longlong),
+                ("ld_dx", ctypes.c_longlong), ("ld_residual", ctypes.c_longlong)]
 
 
 class CbaError(RuntimeError):
@@ -140,6 +152,13 @@ def load(path=LIB_PATH):
     L.cba_plan_info.restype = ctypes.c_int
     L.cba_plan_info.argtypes = [ctypes.POINTER(cba_desc_t), ctypes.c_int, ctypes.c_int,
                                 ctypes.POINTER(cba_plan_info_t)]
+    ln = ctypes.POINTER(cba_layernorm_desc_t)
+    L.cba_layernorm_forward.restype = ctypes.c_int
+    L.cba_layernorm_forward.argtypes = [ln] + [vp] * 7
+    L.cba_layernorm_workspace_bytes.restype = sz
+    L.cba_layernorm_workspace_bytes.argtypes = [ln]
+    L.cba_layernorm_backward.restype = ctypes.c_int
+    L.cba_layernorm_backward.argtypes = [ln] + [vp] * 10 + [sz, vp]
     _lib = L
     return L
 
@@ -349,3 +368,43 @@ def cba_maxpool_backward(desc, top_diff, mask, bottom_diff, stream=None, check=T
     rc = load().cba_maxpool_backward(ctypes.byref(desc), _ptr(top_diff), _ptr(mask),
                                      _ptr(bottom_diff), _stream(stream))
     return _checked(rc, "cba_maxpool_backward", check)
+
+
+# ------------------------------------------------ transformer-layer operators
+
+def dtype_code(dtype):
+    """The cba_dtype_t of a torch dtype."""
+    import torch
+    codes = {torch.float32: CBA_F32, torch.float16: CBA_F16, torch.bfloat16: CBA_BF16}
+    if dtype not in codes:
+        raise TypeError(f"no cba_dtype_t for {dtype}")
+    return codes[dtype]
+
+
+def make_layernorm_desc(rows, cols, type=CBA_F32, param_type=CBA_F32, accumulate=0, eps=1e-5,
+                        ld_x=0, ld_y=0, ld_dy=0, ld_dx=0, ld_residual=0):
+    return cba_layernorm_desc_t(rows, cols, type, param_type, int(accumulate), eps, ld_x, ld_y,
+                                ld_dy, ld_dx, ld_residual)
+
+
+def cba_layernorm_forward(desc, x, gamma, beta, y, mean=None, rstd=None, stream=None, check=True):
+    """y = (x - mean) * rstd * gamma + beta over the rows of x; mean and rstd
+    (fp32 [rows]) are written when given."""
+    rc = load().cba_layernorm_forward(ctypes.byref(desc), _ptr(x), _ptr(gamma), _ptr(beta),
+                                      _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream))
+    return _checked(rc, "cba_layernorm_forward", check)
+
+
+def cba_layernorm_workspace_bytes(desc):
+    return load().cba_layernorm_workspace_bytes(ctypes.byref(desc))
+
+
+def cba_layernorm_backward(desc, x, dy, gamma, mean, rstd, residual, dx, dgamma, dbeta,
+                           workspace, workspace_bytes=None, stream=None, check=True):
+    """dx (+ residual), and dgamma and dbeta written or accumulated."""
+    wsb = _bytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    rc = load().cba_layernorm_backward(
+        ctypes.byref(desc), _ptr(x), _ptr(dy), _ptr(gamma), _ptr(mean), _ptr(rstd),
+        _ptr(residual), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), wsb,
+        _stream(stream))
+    return _checked(rc, "cba_layernorm_backward", check)

@@ -9,6 +9,7 @@
 
 #include "cba_internal.cuh"
 #include "cba_repack.cuh"
+#include "cba_types.cuh"
 
 namespace cba {
 
@@ -182,6 +183,7 @@ cudaError_t select_device(cudaStream_t stream, const void *ptr) {
 
 namespace cba {
 int report_cuda_error(cudaError_t e) { return fail_cuda(e); }
+cudaError_t select_device_of(const void *ptr) { return select_device(nullptr, ptr); }
 }  // namespace cba
 
 extern "C" {

@@ -1,0 +1,47 @@
+// cba_types.cuh -- element types of the normalisation, attention and
+// orthogonalisation operators (cba_dtype_t): conversion to and from fp32,
+// vector loads and stores, and the host-side checks they share.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/cba.h"
+
+namespace cba {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// VEC consecutive elements as they lie in memory; aligned to their size up to
+// 16 bytes, so a load or store of one is at most a few 16-byte accesses.
+template <typename T, int VEC>
+struct __align__(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
+    T v[VEC];
+};
+
+inline size_t dtype_bytes(int t) { return t == CBA_F32 ? 4 : 2; }
+inline bool dtype_ok(int t) { return t == CBA_F32 || t == CBA_F16 || t == CBA_BF16; }
+inline bool aligned_to(const void *p, size_t a) {
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// The device that holds `ptr` becomes current for this library's runtime
+// (cba_api.cu).
+cudaError_t select_device_of(const void *ptr);
+
+}  // namespace cba

@@ -335,6 +335,54 @@ int cba_pooled_size(int in, int kernel, int stride, int pad);
 int cba_maxpool_backward(const cba_pool_desc_t *d, const float *top_diff, const int *mask,
                          float *bottom_diff, void *stream);
 
+/* ---- Operators of transformer layers: layer norm, attention, orthogonalised
+ * updates ----
+ * Conventions as above: device pointers owned by the caller, stream-ordered,
+ * asynchronous, no allocation, capturable; scratch from the caller's 256-byte
+ * aligned workspace (two calls that share one must not overlap in time); on an
+ * error nothing is launched.  Sums, statistics and products accumulate in
+ * fp32 whatever the element type, in a fixed order: the same inputs give the
+ * same bits. */
+
+/* Element type of a tensor. */
+typedef enum { CBA_F32 = 0, CBA_F16 = 1, CBA_BF16 = 2 } cba_dtype_t;
+
+/* Layer norm over the last axis of [rows][cols].  With mu = mean_c x and
+ * r = 1 / sqrt(mean_c (x - mu)^2 + eps):
+ *   forward   y = (x - mu) r gamma + beta; mean = mu, rstd = r
+ *   backward  g = dy gamma, h = (x - mu) r,
+ *             dx = r (g - mean_c g - h mean_c(g h)) + residual
+ *             dgamma (= or +=) sum_rows dy h,  dbeta (= or +=) sum_rows dy
+ * x, y, dy, residual and dx have elements of `type`; gamma and beta [cols] of
+ * `param_type` (fp32, or the same as type: CBA_ERR_UNSUPPORTED otherwise);
+ * mean, rstd [rows], dgamma and dbeta [cols] are fp32.  ld_*: elements from one
+ * row of a tensor to the next (0: cols).  Rows of 16-byte multiples on 16-byte
+ * aligned bases and strides move as vectors; any other element-aligned layout
+ * is correct and slower. */
+typedef struct {
+    long long rows;   /* may be 0 */
+    int cols;
+    int type, param_type; /* cba_dtype_t */
+    int accumulate;   /* dgamma, dbeta: 0 writes, 1 adds onto their contents */
+    float eps;
+    long long ld_x, ld_y, ld_dy, ld_dx, ld_residual;
+} cba_layernorm_desc_t;
+
+/* gamma, beta: NULL for 1 and 0.  mean, rstd: NULL when not wanted.  y may be x. */
+int cba_layernorm_forward(const cba_layernorm_desc_t *d, const void *x, const void *gamma,
+                          const void *beta, void *y, float *mean, float *rstd, void *stream);
+
+/* Bytes of scratch of one backward call (0 on an invalid descriptor). */
+size_t cba_layernorm_workspace_bytes(const cba_layernorm_desc_t *d);
+
+/* residual (nullable): the shortcut's delta, added to dx.  gamma NULL: 1.
+ * dgamma, dbeta: NULL when not wanted.  dx may be x, dy or residual.  With
+ * rows = 0, dgamma and dbeta become 0 (accumulate = 0) or stay. */
+int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const void *dy,
+                           const void *gamma, const float *mean, const float *rstd,
+                           const void *residual, void *dx, float *dgamma, float *dbeta,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable text of a CBA_* code (static storage). */
 const char *cba_error_string(int code);
 
