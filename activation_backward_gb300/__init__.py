@@ -24,4 +24,6 @@ from ._binding import (ACT_NAMES, CBA_ACT_ELU, CBA_ACT_HARDTAN, CBA_ACT_LEAKY,  
                        cba_plan_info, CBA_PHASE_EVENTS, CBA_PATH_FFMA, CBA_PATH_TC_ROWS,
                        CBA_PATH_TC_BATCH_INNER, CBA_PATH_TC_GEMM_1X1, CBA_F32, CBA_F16, CBA_BF16, dtype_code,
                        make_layernorm_desc, cba_layernorm_forward,
-                       cba_layernorm_workspace_bytes, cba_layernorm_backward)
+                       cba_layernorm_workspace_bytes, cba_layernorm_backward, cba_attn_strides_t,
+                       cba_attention_desc_t, make_attention_desc, cba_attention_workspace_bytes,
+                       cba_attention_backward)

@@ -52,7 +52,8 @@ EXPORTS = ("cba_workspace_bytes", "cba_workspace_bytes_ex", "cba_workspace_bytes
            "cba_selftest_bounded_wait", "cba_yolo_backward", "cba_route_backward",
            "cba_pooled_size", "cba_maxpool_backward", "cba_error_string", "cba_last_cuda_error",
            "cba_version", "cba_plan_info",
-           "cba_layernorm_forward", "cba_layernorm_workspace_bytes", "cba_layernorm_backward")
+           "cba_layernorm_forward", "cba_layernorm_workspace_bytes", "cba_layernorm_backward",
+           "cba_attention_workspace_bytes", "cba_attention_backward")
 CBA_ROUTE_MAX_INPUTS = 8
 CBA_WS_RECOMPUTE_Z = 1
 CBA_PHASE_EVENTS = 5
@@ -89,6 +90,18 @@ class cba_layernorm_desc_t(ctypes.Structure):
                 ("eps", ctypes.c_float), ("ld_x", ctypes.c_longlong),
                 ("ld_y", ctypes.c_longlong), ("ld_dy", ctypes.c_longlong),
                 ("ld_dx", ctypes.c_longlong), ("ld_residual", ctypes.c_longlong)]
+
+
+class cba_attn_strides_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_longlong) for n in ("batch", "token", "head")]
+
+
+class cba_attention_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("batch", "heads_q", "heads_kv", "dim", "len_q",
+                                              "len_k", "packed", "type")] +
+                [("total_q", ctypes.c_longlong), ("total_k", ctypes.c_longlong),
+                 ("causal", ctypes.c_int), ("scale", ctypes.c_float)] +
+                [(n, cba_attn_strides_t) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")])
 
 
 class CbaError(RuntimeError):
@@ -159,6 +172,11 @@ def load(path=LIB_PATH):
     L.cba_layernorm_workspace_bytes.argtypes = [ln]
     L.cba_layernorm_backward.restype = ctypes.c_int
     L.cba_layernorm_backward.argtypes = [ln] + [vp] * 10 + [sz, vp]
+    at = ctypes.POINTER(cba_attention_desc_t)
+    L.cba_attention_workspace_bytes.restype = sz
+    L.cba_attention_workspace_bytes.argtypes = [at]
+    L.cba_attention_backward.restype = ctypes.c_int
+    L.cba_attention_backward.argtypes = [at] + [vp] * 12 + [sz, vp]
     _lib = L
     return L
 
@@ -408,3 +426,60 @@ def cba_layernorm_backward(desc, x, dy, gamma, mean, rstd, residual, dx, dgamma,
         _ptr(residual), _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), wsb,
         _stream(stream))
     return _checked(rc, "cba_layernorm_backward", check)
+
+
+def make_attention_desc(q, k, v, o, dout, dq, dk, dv, causal=False, scale=None, sequences=None,
+                        max_q=None, max_k=None):
+    """The descriptor of a call on these tensors (their shapes, strides and type).
+
+    Dense: [batch, len, heads, dim].  Packed: [tokens, heads, dim], with the
+    number of ``sequences`` and upper bounds of their lengths (default: all
+    tokens).  Any strides whose innermost one is 1.  ``scale`` defaults to
+    dim ** -0.5."""
+    tensors = dict(q=q, k=k, v=v, o=o, dout=dout, dq=dq, dk=dk, dv=dv)
+    packed = q.dim() == 3
+    if packed and sequences is None:
+        raise ValueError("packed tensors need the number of sequences")
+    if not packed and (q.dim() != 4 or sequences is not None):
+        raise ValueError("q is [batch, len, heads, dim], or packed [tokens, heads, dim]")
+    if k.shape[:-3] != q.shape[:-3] or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k differ in batch or dim")
+    for name, t in tensors.items():
+        want = k if name in ("k", "v", "dk", "dv") else q
+        if t.shape != want.shape or t.dtype != q.dtype or t.device != q.device:
+            raise ValueError(f"{name}: shape, type or device differs from {'k' if want is k else 'q'}'s")
+        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the innermost axis is not contiguous")
+    d = cba_attention_desc_t()
+    d.heads_q, d.heads_kv, d.dim = q.shape[-2], k.shape[-2], q.shape[-1]
+    d.type, d.causal, d.packed = dtype_code(q.dtype), int(causal), int(packed)
+    d.scale = d.dim ** -0.5 if scale is None else scale
+    if packed:
+        d.batch, d.total_q, d.total_k = sequences, q.shape[0], k.shape[0]
+        d.len_q = q.shape[0] if max_q is None else max_q
+        d.len_k = k.shape[0] if max_k is None else max_k
+    else:
+        d.batch, d.len_q, d.len_k = q.shape[0], q.shape[1], k.shape[1]
+    for name, t in tensors.items():
+        # an axis of one index has no stride that matters
+        st = [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+        if t.numel() and any(st):
+            setattr(d, name, cba_attn_strides_t(0 if packed else st[0], st[-2], st[-1]))
+    return d
+
+
+def cba_attention_workspace_bytes(desc):
+    return load().cba_attention_workspace_bytes(ctypes.byref(desc))
+
+
+def cba_attention_backward(desc, q, k, v, o, lse, dout, cu_q, cu_k, dq, dk, dv, workspace,
+                           workspace_bytes=None, stream=None, check=True):
+    """dq, dk and dv of softmax(scale q k^T) v from the forward's o and lse
+    (fp32 [batch, heads, len], packed [heads, tokens]); cu_q and cu_k: int32
+    device tensors of the packed sequences' starts, None when dense."""
+    wsb = _bytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    rc = load().cba_attention_backward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout),
+        _ptr(cu_q), _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), wsb,
+        _stream(stream))
+    return _checked(rc, "cba_attention_backward", check)

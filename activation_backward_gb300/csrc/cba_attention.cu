@@ -1,0 +1,1017 @@
+// cba_attention.cu -- attention's backward pass, which recomputes the
+// probabilities from q, k and the rows' log-sum-exp.
+//
+//   S = scale q k^T,  P = exp(S - lse) on the allowed pairs, 0 elsewhere
+//   D = rowsum(do o),  dP = do v^T,  dS = P (dP - D)
+//   dv = P^T do,  dk = scale dS^T q,  dq = scale dS k
+//   (dk and dv summed over the query heads that share a key/value head)
+//
+// Three launches:
+//   attn_prep_kernel   D and lse in base 2 per query row, in rows padded to
+//                      whole tiles (padding rows: lse = +inf, so P = 0)
+//   attn_kv_kernel     one 128-row tile of keys per block, all its queries and
+//                      query heads in turn: S^T and dP^T (keys on TMEM lanes),
+//                      dv += P^T do, dk += dS^T q
+//   attn_q_kernel      one 128-row tile of queries per block, all its keys in
+//                      turn: S and dP (queries on TMEM lanes), dq += dS k
+// S and dP are computed in both, 7 products of 128 x 128 x dim per tile pair
+// where 5 would do: in exchange every gradient is a sum in a fixed order held
+// in TMEM, with no fp32 dq buffer in memory and no atomics on it.
+//
+// P and dS are rounded to the inputs' 16-bit type for their products (the
+// tensor cores take two operands of one type); they go from registers into
+// TMEM, which the MMAs read as their A operand, and never to shared memory.
+// In f16 both are scaled by powers of two first (P by 2^12, dS by a power that
+// puts the bound 2 max|do| max|v| of |dP - D| at 2^15), so that their small
+// values stay clear of f16's subnormals and none can overflow.
+//
+// Roles of a block: warp 0 issues the TMA loads (and zeroes the rows of a
+// packed sequence's last tile that belong to its neighbour), warp 1 owns TMEM
+// and issues the MMAs, warps 4-11 compute P and dS (two warpgroups, 64 columns
+// of a tile each) and the epilogue.  Every wait is bounded (2 s); on a timeout
+// the block sets the workspace status bit, stops, waits (bounded) for its
+// copies in flight, frees its TMEM and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "cba_internal.cuh"
+#include "cba_ptx.cuh"
+#include "cba_types.cuh"
+
+namespace cba {
+
+namespace {
+
+constexpr uint64_t kAtLimitNs = 2000000000ull;
+constexpr int kAtThreads = 384;
+constexpr int kT = 128;                       // tile rows, of queries and of keys
+constexpr uint32_t kBoxBytes = kT * 128u;     // 128 rows x 64 16-bit elements
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kPShift = 12.f;               // f16: P is held as 2^12 P
+
+// A query- or key-side tensor on the host: bytes between batches, tokens, heads.
+struct AtArgs {
+    const int *cu_q, *cu_k;      // packed: sequence starts; dense: NULL
+    int batch, hq, hkv, group, dim, len_q, len_k;  // packed: the lengths are upper bounds
+    long long total_q, total_k;  // packed: tokens
+    int causal, tiles, tile_slow;
+    float scale;
+    const float *lse;
+    float *lse2, *dsum;          // [head][padded rows] (dense: [batch][head][padded rows])
+    long long head_rows;         // padded rows of a head (dense: of a batch's head)
+    unsigned *status, *maxima;   // maxima: bits of max |do|^2, max |v|^2 over rows (f16)
+    const void *o, *dout, *v;
+    void *dq, *dk, *dv;
+    long long so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
+};
+
+// The sequence b: its first query and key token, its lengths, and the first
+// padded row of its lse2 / dsum.  Values of cu are clamped into the tensors, so
+// that wrong ones give wrong results but no access out of bounds.
+struct AtSeq {
+    long long q0, k0, row0;
+    int lq, lk;
+};
+
+__device__ __forceinline__ AtSeq at_seq(const AtArgs &a, int b) {
+    AtSeq s;
+    if (a.cu_q == nullptr) {
+        s.q0 = s.k0 = 0;
+        s.lq = a.len_q;
+        s.lk = a.len_k;
+        s.row0 = (long long)b * a.hq * a.head_rows;
+        return s;
+    }
+    const long long qa = min(max((long long)a.cu_q[b], 0LL), a.total_q);
+    const long long qb = min(max((long long)a.cu_q[b + 1], qa), a.total_q);
+    const long long ka = min(max((long long)a.cu_k[b], 0LL), a.total_k);
+    const long long kb = min(max((long long)a.cu_k[b + 1], ka), a.total_k);
+    s.q0 = qa;
+    s.k0 = ka;
+    s.lq = (int)min(qb - qa, (long long)a.len_q);
+    s.lk = (int)min(kb - ka, (long long)a.len_k);
+    s.row0 = (qa + kT - 1) / kT * kT + (long long)b * kT;
+    return s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (BF16) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    } else {
+        __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<uint32_t *>(&h);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+    if constexpr (BF16) return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&u));
+    else return __half22float2(*reinterpret_cast<__half2 *>(&u));
+}
+
+// f16: the power of two by which dS is held, from the rows' largest norms.
+__device__ __forceinline__ float ds_scale(const unsigned *maxima) {
+    const float b = 2.f * sqrtf(__uint_as_float(__ldcg(maxima))) * sqrtf(__uint_as_float(__ldcg(maxima + 1)));
+    if (!(b > 0.f) || !isfinite(b)) return 1.f;
+    int e;
+    frexpf(b, &e);  // b <= 2^e
+    return exp2f((float)min(max(15 - e, -60), 60));
+}
+
+// ---- D, lse in base 2, and (f16) the largest row norms of do and v.  One block
+// per 128-row tile of one head; 16 (DP = 128) or 8 lanes per row.
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_tiles, int v_blocks) {
+    constexpr int LPR = DP / 8;
+    const int t = threadIdx.x, lane = t % LPR;
+    ptx::griddep_launch_dependents();
+    float most = 0.f;
+    int which = 0;
+    if ((int)blockIdx.x >= v_blocks) {
+        const int u = (int)blockIdx.x - v_blocks;
+        const int tile = u % q_tiles, h = u / q_tiles % a.hq, b = u / q_tiles / a.hq;
+        const AtSeq s = at_seq(a, b);
+        if (u == 0 && t == 0 && BF16) *a.status = 0;  // f16: cleared with the maxima before
+        if (tile * kT < s.lq) {
+            const long long row0 = s.row0 + (long long)h * a.head_rows + tile * kT;
+            for (int r = t / LPR; r < kT; r += 256 / LPR) {
+                const int i = tile * kT + r;
+                float d = 0.f, n = 0.f;
+                if (i < s.lq && lane * 8 < a.dim) {
+                    const long long ob = b * a.so[0] + (s.q0 + i) * a.so[1] + h * a.so[2] + lane * 8;
+                    const long long db = b * a.sdo[0] + (s.q0 + i) * a.sdo[1] + h * a.sdo[2] + lane * 8;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + ob);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + db);
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 p = unpack2<BF16>(xs[j]), q = unpack2<BF16>(ys[j]);
+                        d = fmaf(p.x, q.x, fmaf(p.y, q.y, d));
+                        if (!BF16) n = fmaf(q.x, q.x, fmaf(q.y, q.y, n));
+                    }
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) {
+                    d += __shfl_xor_sync(0xffffffffu, d, o);
+                    if (!BF16) n += __shfl_xor_sync(0xffffffffu, n, o);
+                }
+                most = fmaxf(most, n);
+                if (lane == 0) {
+                    float l = INFINITY;  // a padding row, or one whose keys are all masked: P = 0
+                    if (i < s.lq) {
+                        const long long li = a.cu_q ? (long long)h * a.total_q + s.q0 + i
+                                                    : ((long long)b * a.hq + h) * a.len_q + i;
+                        l = a.lse[li];
+                        l = l == -INFINITY ? INFINITY : l * kLog2e - (BF16 ? 0.f : kPShift);
+                    }
+                    a.lse2[row0 + r] = l;
+                    a.dsum[row0 + r] = d;
+                }
+            }
+        }
+    } else if constexpr (!BF16) {
+        // v's rows: [batch][token][head] flattened, strided over the blocks
+        which = 1;
+        const long long tokens = a.cu_k ? a.total_k : a.len_k;
+        const long long rows = (a.cu_k ? 1 : (long long)a.batch) * tokens * a.hkv;
+        const long long per = (rows + v_blocks - 1) / v_blocks;
+        const long long r1 = min(rows, (blockIdx.x + 1LL) * per);
+        for (long long r0 = blockIdx.x * per; r0 < r1; r0 += 256 / LPR) {
+            const long long r = r0 + t / LPR;
+            float n = 0.f;
+            if (r < r1 && lane * 8 < a.dim) {
+                const int h = (int)(r % a.hkv);
+                const long long tok = r / a.hkv % tokens, b = r / a.hkv / tokens;
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    static_cast<const uint16_t *>(a.v) + b * a.sv[0] + tok * a.sv[1] + h * a.sv[2] + lane * 8);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 p = unpack2<false>(xs[j]);
+                    n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
+                }
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            most = fmaxf(most, n);
+        }
+    }
+    if constexpr (!BF16) {  // a maximum does not depend on the order
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if ((t & 31) == 0) atomicMax(a.maxima + which, __float_as_uint(most));
+    }
+}
+
+// ---- shared pieces of the two main kernels
+
+template <int NA, int NB>
+struct AtBars {
+    uint64_t stat;                     // the block's own two tiles
+    uint64_t a_full[NA], a_empty[NA];  // the ring used by the accumulating product
+    uint64_t b_full[NB], b_empty[NB];
+    uint64_t r_full[2], r_empty[2];    // row statistics (kv kernel)
+    uint64_t s_full, p_ready;
+    uint64_t dp_full[2], ds_ready;
+    uint64_t fix, acc, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// Loads a 128-row tile (DP / 64 boxes) into `dst`, completing `bar`'s phase.
+// Where only `valid` of its rows are the sequence's own (packed sequences; the
+// tensor map itself fills rows past a dense one with zeros), the tile arrives on
+// the barrier `fix` first and the rows past them are zeroed: they are contracted
+// over with P = dS = 0, which an infinity or NaN next door must not meet.
+// Called by a whole warp.
+template <int DP>
+__device__ __forceinline__ bool load_tile(uint32_t dst, const CUtensorMap *tm, long long token,
+                                          int head, int b, int valid, bool packed, uint32_t bar,
+                                          uint32_t fix, uint32_t &fix_phase, uint32_t extra,
+                                          volatile int *abort, unsigned *status) {
+    const int lane = threadIdx.x & 31;
+    const bool tail = packed && valid < kT;
+    if (lane == 0) {
+        const uint32_t on = tail ? fix : bar;
+        ptx::mbar_arrive_expect_tx(on, DP / 64 * kBoxBytes + (tail ? 0u : extra));
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j)
+            ptx::tma_load_4d(dst + j * kBoxBytes, tm, j * 64, (int)token, head, b, on);
+    }
+    if (tail) {
+        bool ok = ptx::mbar_wait_bounded(fix, fix_phase, abort, status, kAtLimitNs);
+        fix_phase ^= 1;
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        for (int r = valid * 8 + lane; r < kT * 8; r += 32)
+#pragma unroll
+            for (int j = 0; j < DP / 64; ++j)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + j * kBoxBytes + r * 16),
+                             "r"(0)
+                             : "memory");
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, extra);
+    }
+    __syncwarp();
+    return true;
+}
+
+// D[128 x 128] = A[128 x dim] B[128 x dim]^T, both tiles row-major in 64-column boxes.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb, int dim,
+                                         uint32_t idesc) {
+    const int steps = (dim + 15) / 16;
+    for (int ks = 0; ks < steps; ++ks) {
+        const uint32_t off = (ks >> 2) * kBoxBytes + (ks & 3) * 32;
+        ptx::mma_f16(d, ptx::smem_desc(sa + off, 16, 1024, 2), ptx::smem_desc(sb + off, 16, 1024, 2),
+                     idesc, ks > 0);
+    }
+}
+
+// D[128 x DP] (+)= A[128 x 128] B[128 x DP]: A in TMEM (16-bit, the first 64
+// columns' 32 words at ta, the others' at ta + 64), B's rows contracted over.
+__device__ __forceinline__ void mma_acc(uint32_t d, uint32_t ta, uint32_t sb, uint32_t idesc,
+                                        bool accumulate) {
+#pragma unroll
+    for (int ks = 0; ks < kT / 16; ++ks)
+        ptx::mma_f16_ts(d, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                        ptx::smem_desc(sb + ks * 2048, kBoxBytes, 1024, 2), idesc,
+                        accumulate || ks > 0);
+}
+
+// One thread's row of a gradient tile: COLS fp32 columns of TMEM at `ta`,
+// scaled, rounded and stored 16 bytes at a time.  Called by whole warps.
+template <int COLS, bool BF16>
+__device__ __forceinline__ void store_row(uint32_t ta, float scale, bool zero, bool live,
+                                          uint16_t *out, int cols) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+        float v[32];
+        if (!zero) {
+            ptx::tmem_ld32(ta + c, v);
+            ptx::tmem_ld_wait();
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+            if (live && c + j < cols) {
+                uint4 w;
+                uint32_t *u = &w.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] = zero ? 0u : pack2<BF16>(v[j + 2 * e] * scale, v[j + 2 * e + 1] * scale);
+                *reinterpret_cast<uint4 *>(out + c + j) = w;
+            }
+    }
+}
+
+__device__ __forceinline__ void at_init_bars(uint64_t *first, int n, uint32_t count) {
+    for (int i = 0; i < n; ++i) ptx::mbar_init(ptx::smem_u32(first + i), count);
+}
+
+// ---- dk, dv: one tile of keys, its queries in turn
+
+constexpr int kQStages = 3, kDoStages = 2;
+using KvBars = AtBars<kQStages, kDoStages>;
+
+template <int DP>
+constexpr uint32_t kv_smem_bytes() {
+    return (2 + kQStages + kDoStages) * (DP / 64) * kBoxBytes + 2 * 1024 + sizeof(KvBars);
+}
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    attn_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                   const AtArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr uint32_t TILE = DP / 64 * kBoxBytes;
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t sK = sbase, sV = sK + TILE, sQ = sV + TILE, sDo = sQ + kQStages * TILE;
+    float *rows = reinterpret_cast<float *>(smem + (2 + kQStages + kDoStages) * TILE);
+    KvBars &sb = *reinterpret_cast<KvBars *>(smem + (2 + kQStages + kDoStages) * TILE + 2048);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (sbase & 1023) {  // the swizzled tiles need it
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    if (tid == 0) {
+        at_init_bars(&sb.stat, 1, 1);
+        at_init_bars(sb.a_full, kQStages, 1);
+        at_init_bars(sb.a_empty, kQStages, 1);
+        at_init_bars(sb.b_full, kDoStages, 1);
+        at_init_bars(sb.b_empty, kDoStages, 1);
+        at_init_bars(sb.r_full, 2, 1);
+        at_init_bars(sb.r_empty, 2, 8);  // the 8 compute warps
+        at_init_bars(&sb.s_full, 1, 1);
+        at_init_bars(&sb.p_ready, 1, 8);
+        at_init_bars(sb.dp_full, 2, 1);
+        at_init_bars(&sb.ds_ready, 1, 8);
+        at_init_bars(&sb.fix, 3, 1);  // fix, acc, drain
+        sb.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sb.tmem_base;
+    ptx::griddep_wait();  // lse2, dsum and the maxima come from the kernel before
+    ptx::griddep_launch_dependents();
+
+    // this block's tile
+    int u = (int)blockIdx.x, tile, h, b;
+    if (a.tile_slow) {
+        b = u % a.batch, u /= a.batch;
+        h = u % a.hkv, tile = u / a.hkv;
+    } else {
+        tile = u % a.tiles, u /= a.tiles;
+        h = u % a.hkv, b = u / a.hkv;
+    }
+    const AtSeq s = at_seq(a, b);
+    const int k0 = tile * kT;
+    const int off = s.lk - s.lq;  // causal: key j is seen by the queries i >= j - off
+    const int qt_end = (s.lq + kT - 1) / kT;
+    const int qt_begin = a.causal ? min(max(k0 - off, 0) / kT, qt_end) : 0;
+    const int nq = qt_end - qt_begin;
+    const bool live_tile = k0 < s.lk;
+    const int n = live_tile ? nq * a.group : 0;
+    const uint32_t tS = tmem, tDp = tmem + 128, tDv = tmem + 256, tDk = tmem + 256 + DP;
+    volatile int *ab = &sb.abort_flag;
+    const int tb = a.cu_q ? 0 : b;  // the tensor maps' batch index
+
+    if (warp == 0) {
+        if (n > 0) {
+            uint32_t fphase = 0;
+            const uint32_t bfix = ptx::smem_u32(&sb.fix);
+            if (lane == 0) {
+                const uint32_t bar = ptx::smem_u32(&sb.stat);
+                ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
+#pragma unroll
+                for (int j = 0; j < DP / 64; ++j) {
+                    ptx::tma_load_4d(sK + j * kBoxBytes, &tk, j * 64, (int)s.k0 + k0, h, tb, bar);
+                    ptx::tma_load_4d(sV + j * kBoxBytes, &tv, j * 64, (int)s.k0 + k0, h, tb, bar);
+                }
+            }
+            bool ok = true;
+            int it = 0;
+            for (; ok && it < n; ++it) {
+                const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, hq = h * a.group + g;
+                const int st = it % kQStages, sd = it % kDoStages, sr = it & 1;
+                if (it >= kQStages)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_empty[st]),
+                                                (uint32_t)(it / kQStages - 1) & 1u, ab, a.status, kAtLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int valid = min(kT, s.lq - q0);
+                ok = load_tile<DP>(sQ + st * TILE, &tq, s.q0 + q0, hq, tb, valid, a.cu_q != nullptr,
+                                   ptx::smem_u32(&sb.a_full[st]), bfix, fphase, 0, ab, a.status);
+                if (ok && it >= 2)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_empty[sr]), (uint32_t)(it / 2 - 1) & 1u,
+                                                ab, a.status, kAtLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t bar = ptx::smem_u32(&sb.r_full[sr]);
+                    const long long r0 = s.row0 + (long long)hq * a.head_rows + q0;
+                    ptx::mbar_arrive_expect_tx(bar, 2 * kT * 4);
+                    ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT), a.lse2 + r0, kT * 4, bar);
+                    ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT + kT), a.dsum + r0, kT * 4, bar);
+                }
+                if (it >= kDoStages)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_empty[sd]),
+                                                (uint32_t)(it / kDoStages - 1) & 1u, ab, a.status, kAtLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ok = load_tile<DP>(sDo + sd * TILE, &tdo, s.q0 + q0, hq, tb, valid, a.cu_q != nullptr,
+                                   ptx::smem_u32(&sb.b_full[sd]), bfix, fphase, 0, ab, a.status);
+            }
+            if (!ok) {
+                // no copy may be in flight when the block exits: the barriers of
+                // the last stages' phases that were begun
+                int no = 0;
+                ptx::mbar_wait_bounded(ptx::smem_u32(&sb.stat), 0, &no, a.status, kAtLimitNs);
+                for (int v = max(0, it - kQStages); v <= it && v < n; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_full[v % kQStages]),
+                                           (uint32_t)(v / kQStages) & 1u, &no, a.status, kAtLimitNs / 8);
+                for (int v = max(0, it - kDoStages); v <= it && v < n; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_full[v % kDoStages]),
+                                           (uint32_t)(v / kDoStages) & 1u, &no, a.status, kAtLimitNs / 8);
+                for (int v = max(0, it - 2); v <= it && v < n; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_full[v & 1]), (uint32_t)(v / 2) & 1u, &no,
+                                           a.status, kAtLimitNs / 8);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
+            constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+                ptx::tc_fence_after();
+                return r;
+            };
+            bool ok = wait(&sb.stat, 0) && wait(&sb.a_full[0], 0);
+            if (ok) {
+                mma_rows(tS, sK, sQ, a.dim, id_s);
+                ptx::mma_commit(ptx::smem_u32(&sb.s_full));
+                ok = wait(&sb.b_full[0], 0);
+            }
+            if (ok) {
+                mma_rows(tDp, sV, sDo, a.dim, id_s);
+                ptx::mma_commit(ptx::smem_u32(&sb.dp_full[0]));
+            }
+            for (int it = 0; ok && it < n; ++it) {
+                const int st = it % kQStages, sd = it % kDoStages;
+                const int nx = it + 1;
+                if (!(ok = wait(&sb.p_ready, (uint32_t)it))) break;
+                mma_acc(tDv, tS, sDo + sd * TILE, id_a, it > 0);
+                ptx::mma_commit(ptx::smem_u32(&sb.b_empty[sd]));
+                if (nx < n) {
+                    // S overwrites P: this thread's MMAs run in the order of issue
+                    if (!(ok = wait(&sb.a_full[nx % kQStages], (uint32_t)(nx / kQStages)))) break;
+                    mma_rows(tS, sK, sQ + (nx % kQStages) * TILE, a.dim, id_s);
+                    ptx::mma_commit(ptx::smem_u32(&sb.s_full));
+                }
+                if (!(ok = wait(&sb.ds_ready, (uint32_t)it))) break;
+                mma_acc(tDk, tDp, sQ + st * TILE, id_a, it > 0);
+                ptx::mma_commit(ptx::smem_u32(&sb.a_empty[st]));
+                if (nx < n) {
+                    if (!(ok = wait(&sb.b_full[nx % kDoStages], (uint32_t)(nx / kDoStages)))) break;
+                    mma_rows(tDp, sV, sDo + (nx % kDoStages) * TILE, a.dim, id_s);
+                    ptx::mma_commit(ptx::smem_u32(&sb.dp_full[0]));
+                }
+            }
+            if (ok) ptx::mma_commit(ptx::smem_u32(&sb.acc));
+            else *ab = 1;
+            // every MMA issued has finished before TMEM is released
+            ptx::mma_commit(ptx::smem_u32(&sb.drain));
+            int no = 0;
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kAtLimitNs);
+        }
+    } else if (warp >= 4 && live_tile) {
+        const int wg = (warp - 4) >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const int j = k0 + quarter * 32 + lane;  // this thread's key
+        const float cs = a.scale * kLog2e;
+        const float sds = BF16 ? 1.f : ds_scale(a.maxima);       // dS is held times sds
+        const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);    // from the held P
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+            return __all_sync(0xffffffffu, r);
+        };
+        for (int it = 0; it < n; ++it) {
+            const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, sr = it & 1;
+            const float *lse = rows + sr * 2 * kT + wg * 64, *ds = lse + kT;
+            float p[64];
+            if (!(ok = wait(&sb.r_full[sr], (uint32_t)(it / 2)) && wait(&sb.s_full, (uint32_t)it))) break;
+            ptx::tc_fence_after();
+            {
+                float x[32], y[32];
+                ptx::tmem_ld32(tS + lanes + wg * 64, x);
+                ptx::tmem_ld32(tS + lanes + wg * 64 + 32, y);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) p[c] = x[c], p[32 + c] = y[c];
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                const float4 l = *reinterpret_cast<const float4 *>(lse + c);
+                p[c] = ptx::ex2(fmaf(p[c], cs, -l.x));
+                p[c + 1] = ptx::ex2(fmaf(p[c + 1], cs, -l.y));
+                p[c + 2] = ptx::ex2(fmaf(p[c + 2], cs, -l.z));
+                p[c + 3] = ptx::ex2(fmaf(p[c + 3], cs, -l.w));
+            }
+            if (a.causal && k0 + kT - 1 > q0 + off) {
+                const int first = j - off - q0 - wg * 64;  // columns before it do not see key j
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c < first) p[c] = 0.f;
+            }
+            {
+                float w[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(pack2<BF16>(p[2 * c], p[2 * c + 1]));
+                ptx::tmem_st32(tS + lanes + wg * 64, w);
+                ptx::tmem_st_wait();
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
+            if (!(ok = wait(&sb.dp_full[0], (uint32_t)it))) break;
+            ptx::tc_fence_after();
+            float w[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float x[32];
+                ptx::tmem_ld32(tDp + lanes + wg * 64 + half * 32, x);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    const float4 d = *reinterpret_cast<const float4 *>(ds + half * 32 + c);
+                    const float *pp = p + half * 32 + c;
+                    x[c] = pp[0] * (x[c] - d.x);
+                    x[c + 1] = pp[1] * (x[c + 1] - d.y);
+                    x[c + 2] = pp[2] * (x[c + 2] - d.z);
+                    x[c + 3] = pp[3] * (x[c + 3] - d.w);
+                    if constexpr (!BF16)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[c + e] *= pds;
+                    w[half * 16 + c / 2] = __uint_as_float(pack2<BF16>(x[c], x[c + 1]));
+                    w[half * 16 + c / 2 + 1] = __uint_as_float(pack2<BF16>(x[c + 2], x[c + 3]));
+                }
+            }
+            ptx::tmem_st32(tDp + lanes + wg * 64, w);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready));
+                ptx::mbar_arrive(ptx::smem_u32(&sb.r_empty[sr]));
+            }
+        }
+        if (n > 0 && ok) ok = wait(&sb.acc, 0);
+        if (ok) {
+            ptx::tc_fence_after();
+            // warpgroup 0 stores dv, warpgroup 1 dk
+            const long long *sg = wg ? a.sdk : a.sdv;
+            uint16_t *out = static_cast<uint16_t *>(wg ? a.dk : a.dv) + tb * sg[0] + (s.k0 + j) * sg[1] + h * sg[2];
+            const float f = wg ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
+            store_row<DP, BF16>((wg ? tDk : tDv) + lanes, f, n == 0, j < s.lk, out, a.dim);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- dq: one tile of queries, its keys in turn
+
+constexpr int kKStages = 3, kVStages = 2;
+using QBars = AtBars<kKStages, kVStages>;
+
+template <int DP>
+constexpr uint32_t q_smem_bytes() {
+    return (2 + kKStages + kVStages) * (DP / 64) * kBoxBytes + sizeof(QBars);
+}
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    attn_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+                  const AtArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr uint32_t TILE = DP / 64 * kBoxBytes;
+    const uint32_t sbase = ptx::smem_u32(smem);
+    const uint32_t sQ = sbase, sDo = sQ + TILE, sK = sDo + TILE, sV = sK + kKStages * TILE;
+    QBars &sb = *reinterpret_cast<QBars *>(smem + (2 + kKStages + kVStages) * TILE);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (sbase & 1023) {
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    if (tid == 0) {
+        at_init_bars(&sb.stat, 1, 1);
+        at_init_bars(sb.a_full, kKStages, 1);
+        at_init_bars(sb.a_empty, kKStages, 1);
+        at_init_bars(sb.b_full, kVStages, 1);
+        at_init_bars(sb.b_empty, kVStages, 1);
+        at_init_bars(&sb.s_full, 1, 1);
+        at_init_bars(&sb.p_ready, 1, 8);
+        at_init_bars(sb.dp_full, 2, 1);
+        at_init_bars(&sb.ds_ready, 1, 8);
+        at_init_bars(&sb.fix, 3, 1);
+        sb.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sb.tmem_base;
+
+    int u = (int)blockIdx.x, tile, h, b;
+    if (a.tile_slow) {  // causal: the tiles with the most keys first
+        b = u % a.batch, u /= a.batch;
+        h = u % a.hq, tile = a.tiles - 1 - u / a.hq;
+    } else {
+        tile = u % a.tiles, u /= a.tiles;
+        h = u % a.hq, b = u / a.hq;
+    }
+    const AtSeq s = at_seq(a, b);
+    const int q0 = tile * kT, hk = h / a.group;
+    const int off = s.lk - s.lq;
+    const bool live_tile = q0 < s.lq;
+    int n = live_tile ? (s.lk + kT - 1) / kT : 0;
+    if (a.causal && live_tile) {
+        const int last = min(q0 + kT, s.lq) - 1 + off;  // the last key any of its queries sees
+        n = last < 0 ? 0 : min(n, last / kT + 1);
+    }
+    const uint32_t tS = tmem, tDp = tmem + 128, tDq = tmem + 384;
+    volatile int *ab = &sb.abort_flag;
+    const int tb = a.cu_q ? 0 : b;
+
+    if (warp == 0) {
+        if (n > 0) {
+            uint32_t fphase = 0;
+            const uint32_t bfix = ptx::smem_u32(&sb.fix);
+            if (lane == 0) {
+                const uint32_t bar = ptx::smem_u32(&sb.stat);
+                ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
+#pragma unroll
+                for (int j = 0; j < DP / 64; ++j) {
+                    ptx::tma_load_4d(sQ + j * kBoxBytes, &tq, j * 64, (int)s.q0 + q0, h, tb, bar);
+                    ptx::tma_load_4d(sDo + j * kBoxBytes, &tdo, j * 64, (int)s.q0 + q0, h, tb, bar);
+                }
+            }
+            bool ok = true;
+            int it = 0;
+            for (; ok && it < n; ++it) {
+                const int st = it % kKStages, sv = it % kVStages;
+                const int valid = min(kT, s.lk - it * kT);
+                if (it >= kKStages)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_empty[st]),
+                                                (uint32_t)(it / kKStages - 1) & 1u, ab, a.status, kAtLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ok = load_tile<DP>(sK + st * TILE, &tk, s.k0 + it * kT, hk, tb, valid, a.cu_q != nullptr,
+                                   ptx::smem_u32(&sb.a_full[st]), bfix, fphase, 0, ab, a.status);
+                if (ok && it >= kVStages)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_empty[sv]),
+                                                (uint32_t)(it / kVStages - 1) & 1u, ab, a.status, kAtLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ok = load_tile<DP>(sV + sv * TILE, &tv, s.k0 + it * kT, hk, tb, valid, a.cu_q != nullptr,
+                                   ptx::smem_u32(&sb.b_full[sv]), bfix, fphase, 0, ab, a.status);
+            }
+            if (!ok) {
+                int no = 0;
+                ptx::mbar_wait_bounded(ptx::smem_u32(&sb.stat), 0, &no, a.status, kAtLimitNs);
+                for (int v = max(0, it - kKStages); v <= it && v < n; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_full[v % kKStages]),
+                                           (uint32_t)(v / kKStages) & 1u, &no, a.status, kAtLimitNs / 8);
+                for (int v = max(0, it - kVStages); v <= it && v < n; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_full[v % kVStages]),
+                                           (uint32_t)(v / kVStages) & 1u, &no, a.status, kAtLimitNs / 8);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
+            constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+                ptx::tc_fence_after();
+                return r;
+            };
+            bool ok = wait(&sb.stat, 0);
+            // S and dP of tile it; dP alternates between two buffers, so that it
+            // runs while the other's dS waits for its product
+            auto scores = [&](int it) {
+                if (!wait(&sb.a_full[it % kKStages], (uint32_t)(it / kKStages))) return false;
+                mma_rows(tS, sQ, sK + (it % kKStages) * TILE, a.dim, id_s);
+                ptx::mma_commit(ptx::smem_u32(&sb.s_full));
+                if (!wait(&sb.b_full[it % kVStages], (uint32_t)(it / kVStages))) return false;
+                mma_rows(tDp + (it & 1) * 128, sDo, sV + (it % kVStages) * TILE, a.dim, id_s);
+                ptx::mma_commit(ptx::smem_u32(&sb.dp_full[it & 1]));
+                ptx::mma_commit(ptx::smem_u32(&sb.b_empty[it % kVStages]));
+                return true;
+            };
+            if (ok) ok = scores(0);
+            for (int it = 0; ok && it < n; ++it) {
+                if (it + 1 < n) {
+                    if (!(ok = wait(&sb.p_ready, (uint32_t)it))) break;  // S(it) is in registers
+                    if (!(ok = scores(it + 1))) break;
+                }
+                if (!(ok = wait(&sb.ds_ready, (uint32_t)it))) break;
+                mma_acc(tDq, tDp + (it & 1) * 128, sK + (it % kKStages) * TILE, id_a, it > 0);
+                ptx::mma_commit(ptx::smem_u32(&sb.a_empty[it % kKStages]));
+            }
+            if (ok) ptx::mma_commit(ptx::smem_u32(&sb.acc));
+            else *ab = 1;
+            ptx::mma_commit(ptx::smem_u32(&sb.drain));
+            int no = 0;
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kAtLimitNs);
+        }
+    } else if (warp >= 4 && live_tile) {
+        const int wg = (warp - 4) >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const int r = quarter * 32 + lane, i = q0 + r;  // this thread's query
+        const long long row = s.row0 + (long long)h * a.head_rows + i;
+        const float lse = __ldcg(a.lse2 + row), dsum = __ldcg(a.dsum + row);
+        const float cs = a.scale * kLog2e;
+        const float sds = BF16 ? 1.f : ds_scale(a.maxima);
+        const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            const bool w = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+            return __all_sync(0xffffffffu, w);
+        };
+        for (int it = 0; it < n; ++it) {
+            float p[64];
+            if (!(ok = wait(&sb.s_full, (uint32_t)it))) break;
+            ptx::tc_fence_after();
+            {
+                float x[32], y[32];
+                ptx::tmem_ld32(tS + lanes + wg * 64, x);
+                ptx::tmem_ld32(tS + lanes + wg * 64 + 32, y);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) p[c] = x[c], p[32 + c] = y[c];
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
+#pragma unroll
+            for (int c = 0; c < 64; ++c) p[c] = ptx::ex2(fmaf(p[c], cs, -lse));
+            const int kb = it * kT;
+            if (kb + kT > s.lk || (a.causal && kb + kT - 1 > q0 + off)) {
+                int lim = s.lk - kb;  // columns from it on are masked
+                if (a.causal) lim = min(lim, i + off - kb + 1);
+                lim -= wg * 64;
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c >= lim) p[c] = 0.f;
+            }
+            if (!(ok = wait(&sb.dp_full[it & 1], (uint32_t)(it / 2)))) break;
+            ptx::tc_fence_after();
+            const uint32_t td = tDp + (it & 1) * 128 + lanes + wg * 64;
+            float w[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float x[32];
+                ptx::tmem_ld32(td + half * 32, x);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    x[c] = p[half * 32 + c] * (x[c] - dsum);
+                    if constexpr (!BF16) x[c] *= pds;
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    w[half * 16 + c] = __uint_as_float(pack2<BF16>(x[2 * c], x[2 * c + 1]));
+            }
+            ptx::tmem_st32(td, w);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready));
+        }
+        if (n > 0 && ok) ok = wait(&sb.acc, 0);
+        if (ok) {
+            ptx::tc_fence_after();
+            // each warpgroup stores half of the columns
+            const int c0 = wg * (DP / 2);
+            uint16_t *out = static_cast<uint16_t *>(a.dq) + tb * a.sdq[0] + (s.q0 + i) * a.sdq[1] + h * a.sdq[2] + c0;
+            store_row<DP / 2, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < s.lq, out, a.dim - c0);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+    // the launch before this one has written dk and dv: this grid completes
+    // after it (its own reads depend only on what that one waited for)
+    ptx::griddep_wait();
+}
+
+// ---- host side
+
+struct AtPlan {
+    int dp, q_tiles, k_tiles;
+    long long head_rows;   // padded rows of one head
+    size_t off_lse2, off_dsum, total;
+};
+
+void fill_strides(const cba_attn_strides_t &s, int heads, int dim, long long len, long long *out) {
+    if (s.batch == 0 && s.token == 0 && s.head == 0) {
+        out[0] = len * heads * dim;
+        out[1] = (long long)heads * dim;
+        out[2] = dim;
+    } else {
+        out[0] = s.batch;
+        out[1] = s.token;
+        out[2] = s.head;
+    }
+}
+
+int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
+    if (!d || d->batch < 1 || d->heads_q < 1 || d->heads_kv < 1 || d->dim < 1 || d->len_q < 0 ||
+        d->len_k < 0 || d->heads_q % d->heads_kv != 0)
+        return CBA_ERR_ARG;
+    if (!dtype_ok(d->type) || (d->causal != 0 && d->causal != 1) || (d->packed != 0 && d->packed != 1) ||
+        !std::isfinite(d->scale))
+        return CBA_ERR_ARG;
+    if (d->packed && (d->total_q < 0 || d->total_k < 0)) return CBA_ERR_ARG;
+    if (d->type == CBA_F32 || d->dim > 128 || d->dim % 8 != 0) return CBA_ERR_UNSUPPORTED;
+    const long long lim = 1LL << 30;
+    if (d->len_q > lim || d->len_k > lim || (d->packed && (d->total_q > lim || d->total_k > lim)))
+        return CBA_ERR_UNSUPPORTED;
+    const cba_attn_strides_t *ss[] = {&d->q, &d->k, &d->v, &d->o, &d->dout, &d->dq, &d->dk, &d->dv};
+    for (int i = 0; i < 8; ++i) {
+        const auto *s = ss[i];
+        if (s->batch == 0 && s->token == 0 && s->head == 0) continue;  // contiguous
+        const bool kside = s == &d->k || s == &d->v || s == &d->dk || s == &d->dv;
+        const long long v[] = {s->batch, s->token, s->head};
+        const long long n[] = {d->packed ? 1 : d->batch,
+                               d->packed ? (kside ? d->total_k : d->total_q) : (kside ? d->len_k : d->len_q),
+                               kside ? d->heads_kv : d->heads_q};
+        for (int j = 0; j < 3; ++j) {
+            const long long x = v[j];
+            if (x < 0 || (n[j] > 1 && x < d->dim)) return CBA_ERR_ARG;
+            if (x % 8 != 0) return CBA_ERR_ALIGN;
+            if (x >= (1LL << 38)) return CBA_ERR_UNSUPPORTED;
+        }
+    }
+    p->dp = d->dim <= 64 ? 64 : 128;
+    p->q_tiles = (d->len_q + kT - 1) / kT;
+    p->k_tiles = (d->len_k + kT - 1) / kT;
+    long long rows;
+    if (d->packed) {
+        p->head_rows = (d->total_q + kT - 1) / kT * kT + (long long)kT * (d->batch + 1);
+        rows = p->head_rows * d->heads_q;
+    } else {
+        p->head_rows = (long long)p->q_tiles * kT;
+        rows = p->head_rows * d->heads_q * d->batch;
+    }
+    const long long grid = std::max((long long)p->k_tiles * d->heads_kv, (long long)p->q_tiles * d->heads_q);
+    if (grid * d->batch >= (1LL << 30) || rows >= (1LL << 40)) return CBA_ERR_UNSUPPORTED;
+    p->off_lse2 = 256;
+    p->off_dsum = p->off_lse2 + ((size_t)rows * 4 + 255) / 256 * 256;
+    p->total = p->off_dsum + ((size_t)rows * 4 + 255) / 256 * 256;
+    return CBA_OK;
+}
+
+// The map of one tensor: (dim, token, head, batch), boxes of 128 tokens x 64.
+bool attn_map(CUtensorMap *m, const void *base, const cba_attention_desc_t &d, int heads, long long tokens,
+              const long long *st) {
+    const uint64_t dims[4] = {(uint64_t)d.dim, (uint64_t)tokens, (uint64_t)heads, (uint64_t)(d.packed ? 1 : d.batch)};
+    uint64_t strides[3] = {(uint64_t)st[1] * 2, (uint64_t)st[2] * 2, (uint64_t)st[0] * 2};
+    for (int i = 0; i < 3; ++i)  // an axis of one index has no stride of its own
+        if (dims[i + 1] == 1) strides[i] = 16;
+    const uint32_t box[4] = {64, kT, 1, 1};
+    return tma_encode_16(m, base, d.type == CBA_BF16, 4, dims, strides, box);
+}
+
+template <int DP, bool BF16>
+cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a, const CUtensorMap *tm,
+                        cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (!BF16) e = cudaMemsetAsync(a.status, 0, 256, st);  // the status word and the maxima
+    if (e != cudaSuccess) return e;
+    // f16: the blocks that look for v's largest row
+    const int vb = BF16 ? 0 : kNumSMs;
+    const unsigned qgrid = (unsigned)((long long)p.q_tiles * d.heads_q * d.batch);
+    attn_prep_kernel<DP, BF16><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), vb);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(attn_kv_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kv_smem_bytes<DP>());
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attn_q_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)q_smem_bytes<DP>());
+    if (e != cudaSuccess) return e;
+    if (p.k_tiles > 0) {
+        a.tiles = p.k_tiles;
+        e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)((long long)p.k_tiles * d.heads_kv * d.batch)),
+                       dim3(kAtThreads), kv_smem_bytes<DP>(), st, tm[0], tm[1], tm[2], tm[3], a);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.q_tiles > 0) {
+        a.tiles = p.q_tiles;
+        // without keys there is no launch between this one and the preparation
+        if (p.k_tiles > 0)
+            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(qgrid), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[0],
+                           tm[1], tm[2], tm[3], a);
+        else
+            attn_q_kernel<DP, BF16><<<qgrid, kAtThreads, q_smem_bytes<DP>(), st>>>(tm[0], tm[1], tm[2], tm[3], a);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace cba
+
+using namespace cba;
+
+extern "C" {
+
+size_t cba_attention_workspace_bytes(const cba_attention_desc_t *d) {
+    AtPlan p;
+    return check_attn(d, &p) == CBA_OK ? p.total : 0;
+}
+
+int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const void *k, const void *v,
+                           const void *o, const float *lse, const void *dout, const int *cu_q,
+                           const int *cu_k, void *dq, void *dk, void *dv, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    AtPlan p;
+    const int rc = check_attn(d, &p);
+    if (rc != CBA_OK) return rc;
+    const long long tq = d->packed ? d->total_q : d->len_q, tk = d->packed ? d->total_k : d->len_k;
+    if (tq > 0 && (!q || !o || !lse || !dout || !dq)) return CBA_ERR_ARG;
+    if (tk > 0 && (!k || !v || !dk || !dv)) return CBA_ERR_ARG;
+    if (d->packed ? (!cu_q || !cu_k) : (cu_q || cu_k)) return CBA_ERR_ARG;
+    const void *ptrs[] = {q, k, v, o, dout, dq, dk, dv};
+    for (const void *x : ptrs)
+        if (!aligned_to(x, 16)) return CBA_ERR_ALIGN;
+    if (!aligned_to(lse, 4) || !aligned_to(cu_q, 4) || !aligned_to(cu_k, 4)) return CBA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < p.total) return CBA_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 256)) return CBA_ERR_ALIGN;
+
+    AtArgs a{};
+    a.cu_q = cu_q; a.cu_k = cu_k;
+    a.batch = d->batch; a.hq = d->heads_q; a.hkv = d->heads_kv; a.group = d->heads_q / d->heads_kv;
+    a.dim = d->dim; a.len_q = d->len_q; a.len_k = d->len_k;
+    a.total_q = d->total_q; a.total_k = d->total_k;
+    a.causal = d->causal; a.tile_slow = d->causal; a.scale = d->scale;
+    a.lse = lse;
+    a.status = static_cast<unsigned *>(workspace);
+    a.maxima = a.status + 4;
+    a.lse2 = ws_at<float>(workspace, p.off_lse2);
+    a.dsum = ws_at<float>(workspace, p.off_dsum);
+    a.head_rows = p.head_rows;
+    a.o = o; a.dout = dout; a.v = v; a.dq = dq; a.dk = dk; a.dv = dv;
+    long long sq[3], sk[3];
+    fill_strides(d->q, d->heads_q, d->dim, tq, sq);
+    fill_strides(d->k, d->heads_kv, d->dim, tk, sk);
+    fill_strides(d->v, d->heads_kv, d->dim, tk, a.sv);
+    fill_strides(d->o, d->heads_q, d->dim, tq, a.so);
+    fill_strides(d->dout, d->heads_q, d->dim, tq, a.sdo);
+    fill_strides(d->dq, d->heads_q, d->dim, tq, a.sdq);
+    fill_strides(d->dk, d->heads_kv, d->dim, tk, a.sdk);
+    fill_strides(d->dv, d->heads_kv, d->dim, tk, a.sdv);
+    // without queries (or keys) the main kernels load nothing of them
+    CUtensorMap tm[4] = {};
+    if (tq > 0 && tk > 0 &&
+        (!attn_map(&tm[0], q, *d, d->heads_q, tq, sq) || !attn_map(&tm[1], k, *d, d->heads_kv, tk, sk) ||
+         !attn_map(&tm[2], v, *d, d->heads_kv, tk, a.sv) || !attn_map(&tm[3], dout, *d, d->heads_q, tq, a.sdo)))
+        return CBA_ERR_UNSUPPORTED;
+    cudaGetLastError();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = select_device_of(workspace);
+    if (e == cudaSuccess) {
+        const bool bf = d->type == CBA_BF16;
+        if (p.dp == 64) e = bf ? attn_launch<64, true>(*d, p, a, tm, st) : attn_launch<64, false>(*d, p, a, tm, st);
+        else e = bf ? attn_launch<128, true>(*d, p, a, tm, st) : attn_launch<128, false>(*d, p, a, tm, st);
+    }
+    return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
+}
+
+}  // extern "C"

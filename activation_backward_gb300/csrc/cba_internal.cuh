@@ -164,6 +164,11 @@ bool tma_encode_f32(void *tmap, const void *base, int rank, const uint64_t *dims
 // The same with the swizzle span in bytes: 0 (none), 64 or 128.
 bool tma_encode_f32_swz(void *tmap, const void *base, int rank, const uint64_t *dims,
                         const uint32_t *box, int swizzle_bytes);
+// Strided map of 16-bit elements (f16 or bf16), 128-byte swizzle: dims[0]
+// innermost and contiguous, strides_bytes[i] from one index of dims[i + 1] to
+// the next (multiples of 16).
+bool tma_encode_16(void *tmap, const void *base, bool bf16, int rank, const uint64_t *dims,
+                   const uint64_t *strides_bytes, const uint32_t *box);
 // Weight gradient on batch-innermost layouts (cba_wgrad_nb.cu): xn
 // [nc][H][W][C][nb] and dzn [nc][P][Q][K][nb] (nb = 16 or 32 images, zeros past
 // N), written by launch_layouts; tile accumulators of wgrad_nb_acc_bytes,

@@ -1052,6 +1052,25 @@ bool tma_encode_f32_swz(void *tmap, const void *base, int rank, const uint64_t *
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_encode_16(void *tmap, const void *base, bool bf16, int rank, const uint64_t *dims,
+                   const uint64_t *strides_bytes, const uint32_t *box) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i > 0) st[i - 1] = strides_bytes[i - 1];
+    }
+    return fn(static_cast<CUtensorMap *>(tmap),
+              bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              (cuuint32_t)rank, const_cast<void *>(base), d, st, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tma_encode_f32(void *tmap, const void *base, int rank, const uint64_t *dims,
                     const uint32_t *box, bool swizzle128) {
     return tma_encode_f32_swz(tmap, base, rank, dims, box, swizzle128 ? 128 : 0);

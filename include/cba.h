@@ -383,6 +383,50 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
                            const void *residual, void *dx, float *dgamma, float *dbeta,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* Attention's backward pass.  For each query head h, with the key/value head
+ * h / (heads_q / heads_kv):
+ *   S = scale q k^T,  P = exp(S - lse) on the allowed pairs (0 elsewhere),
+ *   D = rowsum(dout o),  dS = P (dout v^T - D),
+ *   dq = scale dS k,  dk = scale sum_h dS^T q,  dv = sum_h P^T dout
+ * q, o, dout, dq: heads_q heads; k, v, dk, dv: heads_kv heads; elements f16 or
+ * bf16 (CBA_F32: CBA_ERR_UNSUPPORTED); dim a multiple of 8 up to 128.  o and lse
+ * are the forward's: lse fp32 = log sum_j exp S_ij, contiguous [batch][heads_q]
+ * [len_q] (packed: [heads_q][total_q]).  Row i of a sequence sees the keys
+ * j <= i + len_k - len_q when causal, all of them otherwise.  A row that sees
+ * none (or whose lse is -infinity) has P = 0: it gets dq = 0 and adds nothing.
+ *
+ * Dense: `batch` sequences of len_q queries and len_k keys, element (b, t, h, c)
+ * of a tensor at b * batch + t * token + h * head + c.  Packed: `batch`
+ * sequences one after another, cu_q and cu_k DEVICE int32 [batch + 1] with their
+ * first tokens (non-decreasing, from 0 to total_q / total_k); len_q and len_k are
+ * upper bounds of the sequences' lengths (tokens past them are not computed) and
+ * the batch strides are not used.  A sequence may be empty.  Strides all 0 mean
+ * contiguous [batch][token][head][dim].  Strides must be multiples of 8 elements
+ * and bases 16-byte aligned (CBA_ERR_ALIGN).  Outputs must not overlap inputs.
+ *
+ * P and dS are rounded to the elements' type for their products, the sums are
+ * fp32.  In a sequence's own rows, infinities and NaN spread as in the formulas
+ * (a masked pair still multiplies its row by 0); another sequence's never do. */
+typedef struct { long long batch, token, head; } cba_attn_strides_t;
+typedef struct {
+    int batch, heads_q, heads_kv, dim;
+    int len_q, len_k;
+    int packed;                 /* 0 dense, 1 packed (cu_q, cu_k) */
+    int type;                   /* cba_dtype_t */
+    long long total_q, total_k; /* packed: tokens */
+    int causal;
+    float scale;
+    cba_attn_strides_t q, k, v, o, dout, dq, dk, dv;
+} cba_attention_desc_t;
+
+/* Bytes of scratch of one call (0 on an invalid descriptor).  cba_get_status
+ * reads the same workspace after the call. */
+size_t cba_attention_workspace_bytes(const cba_attention_desc_t *d);
+int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const void *k,
+                           const void *v, const void *o, const float *lse, const void *dout,
+                           const int *cu_q, const int *cu_k, void *dq, void *dk, void *dv,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable text of a CBA_* code (static storage). */
 const char *cba_error_string(int code);
 
