@@ -26,4 +26,6 @@ from ._binding import (ACT_NAMES, CBA_ACT_ELU, CBA_ACT_HARDTAN, CBA_ACT_LEAKY,  
                        make_layernorm_desc, cba_layernorm_forward,
                        cba_layernorm_workspace_bytes, cba_layernorm_backward, cba_attn_strides_t,
                        cba_attention_desc_t, make_attention_desc, cba_attention_workspace_bytes,
-                       cba_attention_backward)
+                       cba_attention_backward, NEWTON_SCHULZ,
+                       make_orthogonalize_desc, cba_orthogonalize_workspace_bytes,
+                       cba_orthogonalize)

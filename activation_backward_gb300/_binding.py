@@ -53,7 +53,8 @@ EXPORTS = ("cba_workspace_bytes", "cba_workspace_bytes_ex", "cba_workspace_bytes
            "cba_pooled_size", "cba_maxpool_backward", "cba_error_string", "cba_last_cuda_error",
            "cba_version", "cba_plan_info",
            "cba_layernorm_forward", "cba_layernorm_workspace_bytes", "cba_layernorm_backward",
-           "cba_attention_workspace_bytes", "cba_attention_backward")
+           "cba_attention_workspace_bytes", "cba_attention_backward",
+           "cba_orthogonalize_workspace_bytes", "cba_orthogonalize")
 CBA_ROUTE_MAX_INPUTS = 8
 CBA_WS_RECOMPUTE_Z = 1
 CBA_PHASE_EVENTS = 5
@@ -102,6 +103,13 @@ class cba_attention_desc_t(ctypes.Structure):
                 [("total_q", ctypes.c_longlong), ("total_k", ctypes.c_longlong),
                  ("causal", ctypes.c_int), ("scale", ctypes.c_float)] +
                 [(n, cba_attn_strides_t) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")])
+
+
+class cba_orthogonalize_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("batch", "rows", "cols", "in_type", "out_type",
+                                              "steps")] +
+                [(n, ctypes.c_float) for n in ("a", "b", "c", "eps", "scale")] +
+                [(n, ctypes.c_longlong) for n in ("ld_in", "ld_out", "batch_in", "batch_out")])
 
 
 class CbaError(RuntimeError):
@@ -177,6 +185,11 @@ def load(path=LIB_PATH):
     L.cba_attention_workspace_bytes.argtypes = [at]
     L.cba_attention_backward.restype = ctypes.c_int
     L.cba_attention_backward.argtypes = [at] + [vp] * 12 + [sz, vp]
+    ns = ctypes.POINTER(cba_orthogonalize_desc_t)
+    L.cba_orthogonalize_workspace_bytes.restype = sz
+    L.cba_orthogonalize_workspace_bytes.argtypes = [ns]
+    L.cba_orthogonalize.restype = ctypes.c_int
+    L.cba_orthogonalize.argtypes = [ns, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -483,3 +496,26 @@ def cba_attention_backward(desc, q, k, v, o, lse, dout, cu_q, cu_k, dq, dk, dv, 
         _ptr(cu_q), _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), wsb,
         _stream(stream))
     return _checked(rc, "cba_attention_backward", check)
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def make_orthogonalize_desc(batch, rows, cols, in_type=CBA_F32, out_type=CBA_BF16, steps=5,
+                            coefficients=NEWTON_SCHULZ, eps=1e-7, scale=1.0, ld_in=0, ld_out=0,
+                            batch_in=0, batch_out=0):
+    a, b, c = coefficients
+    return cba_orthogonalize_desc_t(batch, rows, cols, in_type, out_type, steps, a, b, c, eps,
+                                    scale, ld_in, ld_out, batch_in, batch_out)
+
+
+def cba_orthogonalize_workspace_bytes(desc):
+    return load().cba_orthogonalize_workspace_bytes(ctypes.byref(desc))
+
+
+def cba_orthogonalize(desc, G, O, workspace, workspace_bytes=None, stream=None, check=True):
+    """O = the Newton-Schulz iterate of each matrix of G."""
+    wsb = _bytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    rc = load().cba_orthogonalize(ctypes.byref(desc), _ptr(G), _ptr(O), _ptr(workspace), wsb,
+                                  _stream(stream))
+    return _checked(rc, "cba_orthogonalize", check)

@@ -290,6 +290,7 @@ __device__ __forceinline__ void store_row(uint32_t ta, float scale, bool zero, b
 #pragma unroll
     for (int c = 0; c < COLS; c += 32) {
         float v[32];
+        __syncwarp();  // rows that are not stored skip the code below
         if (!zero) {
             ptx::tmem_ld32(ta + c, v);
             ptx::tmem_ld_wait();

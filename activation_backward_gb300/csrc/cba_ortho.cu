@@ -1,0 +1,595 @@
+// cba_ortho.cu -- orthogonalising a matrix by Newton-Schulz products.
+//
+//   X_0 = G / (|G|_F + eps);  S = X X^T,  B = b S + c S^2,  X <- a X + B X
+// (rows <= cols; otherwise S = X^T X and X <- a X + X B, the same polynomial of
+// the singular values from the short side).  m = min(rows, cols), n = max.
+//
+// Per step three products, each one launch of ns_gemm_kernel:
+//   S = X X^T      m x m, contraction n   (both operands are X)
+//   B = b S + c S S   m x m, contraction m   (S is symmetric: S S = S S^T)
+//   X' = a X + B X    m x n, contraction m
+// X is kept in the caller's orientation.  An operand whose contraction runs
+// along its rows' elements is loaded K-major, one whose contraction runs across
+// its rows M/N-major; the tensor cores take both, so nothing is transposed.
+//
+// Operands are f16, products accumulate in fp32: 11 significant bits where
+// bf16, the usual choice for this iteration, has 8.  f16's short range is met
+// with powers of two: X is held times 2^round(log2(n)/2) (its elements are of
+// order 1/sqrt(n) or 1/sqrt(m n)), S and B times 2^12 (their largest elements
+// are below 3 for singular values up to 1.2, which the iteration keeps).
+//
+// The product kernel: TMA-fed tcgen05 tiles of 128 rows per block; with CG = 2
+// a pair of blocks computes 256 x 256 tiles (each holds half of A's and of B's
+// rows, which halves the traffic of both per product), with CG = 1 a block
+// computes 128 x BN.  Persistent: two accumulators in TMEM, so the epilogue of
+// one tile runs under the products of the next.  Warp 0 issues the TMA loads,
+// warp 1 the MMAs, warps 2-5 the epilogue.  Every wait is bounded (2 s); on a
+// timeout the block sets the workspace status bit, stops, waits (bounded) for
+// copies and MMAs in flight, frees its TMEM and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "cba_internal.cuh"
+#include "cba_ptx.cuh"
+#include "cba_types.cuh"
+
+namespace cba {
+
+namespace {
+
+constexpr uint64_t kNsLimitNs = 2000000000ull;
+constexpr int kNsThreads = 192;
+constexpr int kNsStages = 6;
+constexpr int kNsBK = 64;                      // contraction elements per stage (128 bytes)
+constexpr float kNsSym = 4096.f;               // S and B are held times 2^12
+constexpr int kNormBlocks = 128;               // partial sums of |G|^2 per matrix (at most)
+
+struct NsArgs {
+    int M, N, K;            // output rows, columns, contraction
+    int mt, nt, units;      // tiles; units = batch * mt * nt
+    int a_major, b_major;   // 0: K-major, 1: M- / N-major
+    float alpha, beta;      // out = alpha * product + beta * aux
+    const __half *aux;      // same shape as out, or NULL
+    long long aux_ld, aux_batch;
+    void *out;
+    int out_type;
+    long long out_ld, out_batch;
+    int vec;                // 16-byte accesses to out (and aux)
+    unsigned *status;
+};
+
+struct NsBars {
+    uint64_t full[kNsStages], empty[kNsStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int CG, int BN>
+struct NsTile {
+    static constexpr int ROWS_B = BN / CG;  // B rows a block loads
+    static constexpr uint32_t A_BYTES = 128u * 128u, B_BYTES = ROWS_B * 128u;
+    static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
+    static constexpr uint32_t SMEM = kNsStages * STAGE + 1024 + sizeof(NsBars);
+    static constexpr int TM = 128 * CG;     // tile rows
+    static constexpr uint32_t TMEM_COLS = 2 * BN;
+};
+
+// `rows` rows (a multiple of 64) of one operand's stage: K-major, one box of 64
+// contraction elements x rows; M/N-major, boxes of 64 rows x 64 contraction
+// elements.
+template <int CG>
+__device__ __forceinline__ void ns_load(uint32_t dst, const CUtensorMap *tm, int major, int rows,
+                                        int row0, int k0, int b, uint32_t bar) {
+    auto box = [&](uint32_t to, int x, int y) {
+        if constexpr (CG == 2) ptx::tma_load_3d_pair(to, tm, x, y, b, bar);
+        else ptx::tma_load_3d(to, tm, x, y, b, bar);
+    };
+    if (major == 0) {
+        box(dst, k0, row0);
+    } else {
+        for (int i = 0; i < rows / 64; ++i) box(dst + i * 8192, row0 + i * 64, k0);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void ns_store(void *out, long long at, const float (&v)[32], int n,
+                                         int vec) {
+    T *o = static_cast<T *>(out) + at;
+    if (vec && n >= 32) {
+        constexpr int V = 16 / sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 32; i += V) {
+            Pack<T, V> p;
+#pragma unroll
+            for (int j = 0; j < V; ++j) p.v[j] = from_f32<T>(v[i + j]);
+            *reinterpret_cast<Pack<T, V> *>(o + i) = p;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) o[i] = from_f32<T>(v[i]);
+    }
+}
+
+template <int CG, int BN>
+__global__ void __launch_bounds__(kNsThreads, 1)
+    ns_gemm_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                   const NsArgs a) {
+    using L = NsTile<CG, BN>;
+    extern __shared__ uint8_t smem_dyn[];
+    // both blocks of a pair round up alike: the same kernel, the same layout
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    NsBars &sb = *reinterpret_cast<NsBars *>(smem + kNsStages * L::STAGE);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0;
+    if (tid == 0) {
+        for (int i = 0; i < kNsStages; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&sb.full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sb.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&sb.acc_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sb.acc_empty[i]), 4 * CG);  // the epilogue warps
+        }
+        ptx::mbar_init(ptx::smem_u32(&sb.drain), 1);
+        sb.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            ptx::tmem_alloc_pair(ptx::smem_u32(&sb.tmem_base), L::TMEM_COLS);
+        } else {
+            ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), L::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::tc_fence_before();
+    if constexpr (CG == 2) ptx::cluster_sync();
+    else __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sb.tmem_base;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    const int g0 = (int)blockIdx.x / CG, gstep = (int)gridDim.x / CG;
+    const int nk = (a.K + kNsBK - 1) / kNsBK;
+    const int mine = a.units > g0 ? (a.units - 1 - g0) / gstep + 1 : 0;
+    volatile int *ab = &sb.abort_flag;
+    // unit -> batch, tile row, tile column; tile rows fastest, so that blocks
+    // running together share B's rows in L2
+    auto where = [&](int i, int &b, int &m0, int &n0) {
+        int u = g0 + i * gstep;
+        m0 = u % a.mt * L::TM;
+        u /= a.mt;
+        n0 = u % a.nt * BN;
+        b = u / a.nt;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int gs = 0;
+            for (int i = 0; ok && i < mine; ++i) {
+                int b, m0, n0;
+                where(i, b, m0, n0);
+                const int ar = m0 + (int)rank * 128, br = n0 + (int)rank * L::ROWS_B;
+                for (int kb = 0; kb < nk; ++kb, ++gs) {
+                    const int s = gs % kNsStages;
+                    if (gs >= kNsStages)
+                        ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.empty[s]),
+                                                    (uint32_t)(gs / kNsStages - 1) & 1u, ab, a.status, kNsLimitNs);
+                    if (!ok) break;
+                    uint32_t bar = ptx::smem_u32(&sb.full[s]);
+                    // the pair's copies all complete on the even block's barrier
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(bar, CG * L::STAGE);
+                    if constexpr (CG == 2) bar = ptx::mapa(bar, 0);
+                    const uint32_t to = ptx::smem_u32(smem + s * L::STAGE);
+                    ns_load<CG>(to, &ta, a.a_major, 128, ar, kb * kNsBK, b, bar);
+                    ns_load<CG>(to + L::A_BYTES, &tb, a.b_major, L::ROWS_B, br, kb * kNsBK, b, bar);
+                }
+            }
+            if (!ok && rank == 0) {  // no copy may be in flight when the block exits
+                int no = 0;
+                for (int v = max(0, gs - kNsStages); v < gs; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.full[v % kNsStages]),
+                                           (uint32_t)(v / kNsStages) & 1u, &no, a.status, kNsLimitNs / 8);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = ptx::idesc_f16(L::TM, BN, false, a.b_major != 0, a.a_major != 0);
+            // bytes of one K = 16 step, and between the 64-row boxes
+            const uint32_t sa = a.a_major ? 2048 : 32, sbk = a.b_major ? 2048 : 32;
+            auto commit = [&](uint64_t *bar) {
+                if constexpr (CG == 2) ptx::mma_commit_pair(ptx::smem_u32(bar));
+                else ptx::mma_commit(ptx::smem_u32(bar));
+            };
+            bool ok = true;
+            int gs = 0;
+            for (int i = 0; ok && i < mine; ++i) {
+                const int ac = i & 1;
+                if (i >= 2)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.acc_empty[ac]), (uint32_t)(i / 2 - 1) & 1u,
+                                                ab, a.status, kNsLimitNs);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                for (int kb = 0; kb < nk; ++kb, ++gs) {
+                    const int s = gs % kNsStages;
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.full[s]), (uint32_t)(gs / kNsStages) & 1u, ab,
+                                                a.status, kNsLimitNs);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t at = ptx::smem_u32(smem + s * L::STAGE);
+#pragma unroll
+                    for (int ks = 0; ks < kNsBK / 16; ++ks) {
+                        const uint64_t da = ptx::smem_desc(at + ks * sa, a.a_major ? 8192 : 16, 1024, 2);
+                        const uint64_t db = ptx::smem_desc(at + L::A_BYTES + ks * sbk, a.b_major ? 8192 : 16, 1024, 2);
+                        const uint32_t acc = (kb > 0 || ks > 0) ? 1u : 0u;
+                        if constexpr (CG == 2) ptx::mma_f16_pair(tmem + ac * BN, da, db, idesc, acc);
+                        else ptx::mma_f16(tmem + ac * BN, da, db, idesc, acc);
+                    }
+                    commit(&sb.empty[s]);
+                }
+                if (ok) commit(&sb.acc_full[ac]);
+            }
+            if (!ok) *ab = 1;
+            // every MMA issued has finished before TMEM is released
+            if constexpr (CG == 2) ptx::mma_commit_pair(ptx::smem_u32(&sb.drain));
+            else ptx::mma_commit(ptx::smem_u32(&sb.drain));
+            int no = 0;
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kNsLimitNs);
+        }
+    } else {
+        const int quarter = warp & 3;
+        bool ok = true;
+        for (int i = 0; ok && i < mine; ++i) {
+            const int ac = i & 1;
+            ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.acc_full[ac]), (uint32_t)(i / 2) & 1u, ab, a.status,
+                                        kNsLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            int b, m0, n0;
+            where(i, b, m0, n0);
+            const int row = m0 + (int)rank * 128 + quarter * 32 + lane;
+            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + ac * BN;
+            const __half *aux = a.aux ? a.aux + b * a.aux_batch + row * a.aux_ld : nullptr;
+            const long long at = b * a.out_batch + row * a.out_ld;
+            for (int c = 0; c < BN; c += 32) {
+                float v[32];
+                __syncwarp();  // rows past M skip the stores below
+                ptx::tmem_ld32(t0 + c, v);
+                ptx::tmem_ld_wait();
+                if (c + 32 == BN) {  // the accumulator is read: the MMAs may reuse it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (CG == 2)
+                            ptx::mbar_arrive_cluster(ptx::mapa(ptx::smem_u32(&sb.acc_empty[ac]), 0));
+                        else
+                            ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty[ac]));
+                    }
+                }
+                const int col = n0 + c, n = a.N - col;
+                if (row >= a.M || n <= 0) continue;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= a.alpha;
+                if (aux) {
+                    if (n >= 32) {  // aux rows are 16-byte multiples
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            const Pack<__half, 8> p = *reinterpret_cast<const Pack<__half, 8> *>(aux + col + j);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[j + e] = fmaf(a.beta, __half2float(p.v[e]), v[j + e]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < n) v[j] = fmaf(a.beta, __half2float(aux[col + j]), v[j]);
+                    }
+                }
+                if (a.out_type == CBA_F16) ns_store<__half>(a.out, at + col, v, n, a.vec);
+                else if (a.out_type == CBA_BF16) ns_store<__nv_bfloat16>(a.out, at + col, v, n, a.vec);
+                else ns_store<float>(a.out, at + col, v, n, a.vec);
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    if constexpr (CG == 2) ptx::cluster_sync();  // the peer's arrivals on this block's barriers are done
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        if constexpr (CG == 2) ptx::tmem_dealloc_pair(tmem, L::TMEM_COLS);
+        else ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+// ---- |G|^2 and the scaled f16 copy
+
+// Partial sums of squares: block (p, b) takes every gridDim.x-th slab of 256
+// rows x columns' elements of matrix b; summed in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    ns_norm_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, double *part) {
+    __shared__ double sm[8];
+    ptx::griddep_launch_dependents();
+    const T *gb = g + (long long)blockIdx.y * batch_stride;
+    const long long n = (long long)rows * cols;
+    const long long per = (n + gridDim.x - 1) / gridDim.x;
+    const long long e1 = min(n, (blockIdx.x + 1) * per);
+    double total = 0.0;
+    for (long long e = blockIdx.x * per + threadIdx.x; e < e1;) {
+        float s = 0.f;  // 16 squares in fp32, their sums in fp64
+#pragma unroll
+        for (int j = 0; j < 16; ++j, e += 256)
+            if (e < e1) {
+                const long long r = ld == cols ? 0 : e / cols;
+                const float x = to_f32(gb[ld == cols ? e : r * ld + (e - r * cols)]);
+                s = fmaf(x, x, s);
+            }
+        total += s;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) total += sm[i];
+        part[(long long)blockIdx.y * kNormBlocks + blockIdx.x] = total;
+    }
+}
+
+// X = G * (held / (|G| + eps)) in f16, rows `pitch` apart (the padding is never
+// read: the maps end at cols).  One warp per row, strided.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    ns_cast_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, const double *part,
+                   int nparts, float eps, float held, __half *x, long long pitch, long long x_batch,
+                   unsigned *status) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    __shared__ float f;
+    const int b = blockIdx.y;
+    if (threadIdx.x < 32) {
+        double s = 0.0;
+        for (int i = threadIdx.x; i < nparts; i += 32) s += part[(long long)b * kNormBlocks + i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) f = (float)((double)held / (sqrt(s) + (double)eps));
+    }
+    if (blockIdx.x == 0 && b == 0 && threadIdx.x == 0) *status = 0;
+    __syncthreads();
+    const float k = f;
+    const int lane = threadIdx.x & 31;
+    for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
+        const T *src = g + b * batch_stride + r * ld;
+        __half *dst = x + b * x_batch + r * pitch;
+        for (int c = lane; c < cols; c += 32) dst[c] = __float2half_rn(to_f32(src[c]) * k);
+    }
+}
+
+// ---- host side
+
+struct NsPlan {
+    int m, n;
+    bool wide;                 // rows <= cols
+    long long x_pitch, s_pitch;
+    long long x_batch, s_batch;  // elements of one matrix
+    size_t off_part, off_x0, off_x1, off_s, off_b, total;
+};
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+int check_ns(const cba_orthogonalize_desc_t *d, NsPlan *p) {
+    if (!d || d->batch < 1 || d->rows < 1 || d->cols < 1 || d->steps < 1) return CBA_ERR_ARG;
+    if (!dtype_ok(d->in_type) || !dtype_ok(d->out_type)) return CBA_ERR_ARG;
+    if (!std::isfinite(d->a) || !std::isfinite(d->b) || !std::isfinite(d->c) || !std::isfinite(d->scale) ||
+        !(std::isfinite(d->eps) && d->eps >= 0.f))
+        return CBA_ERR_ARG;
+    const long long need = (long long)d->rows * d->cols;
+    if ((d->ld_in != 0 && d->ld_in < d->cols) || (d->ld_out != 0 && d->ld_out < d->cols)) return CBA_ERR_ARG;
+    const long long ldi = d->ld_in ? d->ld_in : d->cols, ldo = d->ld_out ? d->ld_out : d->cols;
+    if (d->steps > 100 || d->rows > (1 << 20) || d->cols > (1 << 20) || d->batch > 65535 || need >= (1LL << 36) ||
+        ldi >= (1LL << 31) || ldo >= (1LL << 31))
+        return CBA_ERR_UNSUPPORTED;
+    // a matrix's own rows fit its batch stride
+    if (d->batch > 1) {
+        if (d->batch_in != 0 && d->batch_in < (d->rows - 1) * ldi + d->cols) return CBA_ERR_ARG;
+        if (d->batch_out != 0 && d->batch_out < (d->rows - 1) * ldo + d->cols) return CBA_ERR_ARG;
+    }
+    p->wide = d->rows <= d->cols;
+    p->m = std::min(d->rows, d->cols);
+    p->n = std::max(d->rows, d->cols);
+    p->x_pitch = (d->cols + 7LL) / 8 * 8;
+    p->s_pitch = (p->m + 7LL) / 8 * 8;
+    p->x_batch = p->x_pitch * d->rows;
+    p->s_batch = p->s_pitch * p->m;
+    const size_t xb = up256((size_t)p->x_batch * d->batch * 2), sb = up256((size_t)p->s_batch * d->batch * 2);
+    p->off_part = 256;
+    p->off_x0 = p->off_part + up256((size_t)d->batch * kNormBlocks * sizeof(double));
+    p->off_x1 = p->off_x0 + xb;
+    p->off_s = p->off_x1 + xb;
+    p->off_b = p->off_s + sb;
+    p->total = p->off_b + sb;
+    return CBA_OK;
+}
+
+// One operand: [batch][rows][cols] of f16, rows `pitch` apart, `tile` rows of the
+// operand per load (K-major) or boxes of 64 x 64 (M/N-major).
+bool ns_map(CUtensorMap *m, const __half *base, int batch, int rows, int cols, long long pitch, int major, int tile) {
+    const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)batch};
+    const uint64_t strides[2] = {(uint64_t)pitch * 2, (uint64_t)pitch * 2 * (uint64_t)rows};
+    const uint32_t box[3] = {64, major ? 64u : (uint32_t)tile, 1};
+    return tma_encode_16(m, base, false, 3, dims, strides, box);
+}
+
+struct NsOperand {
+    const __half *base;
+    int rows, cols;
+    long long pitch;
+    int major;
+};
+
+template <int CG, int BN>
+cudaError_t ns_launch(const NsOperand &oa, const NsOperand &ob, NsArgs a, int batch, cudaStream_t st) {
+    using L = NsTile<CG, BN>;
+    a.mt = (a.M + L::TM - 1) / L::TM;
+    a.nt = (a.N + BN - 1) / BN;
+    a.units = a.mt * a.nt * batch;
+    a.a_major = oa.major;
+    a.b_major = ob.major;
+    CUtensorMap ta, tb;
+    if (!ns_map(&ta, oa.base, batch, oa.rows, oa.cols, oa.pitch, oa.major, 128) ||
+        !ns_map(&tb, ob.base, batch, ob.rows, ob.cols, ob.pitch, ob.major, L::ROWS_B))
+        return cudaErrorInvalidValue;
+    auto kern = ns_gemm_kernel<CG, BN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CG * std::min(a.units, kNumSMs / CG)));
+    cfg.blockDim = dim3(kNsThreads);
+    cfg.dynamicSmemBytes = L::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, ta, tb, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The tile: 256 x 256 by pairs of blocks once they fill half of the SMs; below
+// that smaller ones, which spread the product over more SMs.
+cudaError_t ns_gemm(const NsOperand &oa, const NsOperand &ob, const NsArgs &a, int batch, cudaStream_t st) {
+    const long long t256 = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256) * batch;
+    const long long t128 = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128) * batch;
+    if (t256 >= kNumSMs / 4) return ns_launch<2, 256>(oa, ob, a, batch, st);
+    if (t128 >= kNumSMs / 2) return ns_launch<1, 128>(oa, ob, a, batch, st);
+    return ns_launch<1, 64>(oa, ob, a, batch, st);
+}
+
+template <typename T>
+cudaError_t ns_start(const cba_orthogonalize_desc_t &d, const NsPlan &p, const void *G, void *ws, float held,
+                     cudaStream_t st) {
+    const long long ld = d.ld_in ? d.ld_in : d.cols, bs = d.batch_in ? d.batch_in : ld * d.rows;
+    const long long n = (long long)d.rows * d.cols;
+    const int parts = (int)std::max(1LL, std::min<long long>(kNormBlocks, n / 4096));
+    double *part = ws_at<double>(ws, p.off_part);
+    ns_norm_kernel<T><<<dim3(parts, d.batch), 256, 0, st>>>(static_cast<const T *>(G), d.rows, d.cols, ld, bs, part);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int blocks = std::max(1, std::min((d.rows + 7) / 8, 8 * kNumSMs / std::min(d.batch, 8 * kNumSMs)));
+    return launch_pdl(ns_cast_kernel<T>, dim3(blocks, d.batch), dim3(256), 0, st, static_cast<const T *>(G), d.rows,
+                      d.cols, ld, bs, static_cast<const double *>(part), parts, d.eps, held,
+                      ws_at<__half>(ws, p.off_x0), p.x_pitch, p.x_batch, static_cast<unsigned *>(ws));
+}
+
+cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const void *G, void *O, void *ws,
+                   cudaStream_t st) {
+    const float held = exp2f(roundf(0.5f * log2f((float)p.n)));
+    cudaError_t e = d.in_type == CBA_F32   ? ns_start<float>(d, p, G, ws, held, st)
+                    : d.in_type == CBA_F16 ? ns_start<__half>(d, p, G, ws, held, st)
+                                           : ns_start<__nv_bfloat16>(d, p, G, ws, held, st);
+    __half *x = ws_at<__half>(ws, p.off_x0), *xn = ws_at<__half>(ws, p.off_x1);
+    __half *S = ws_at<__half>(ws, p.off_s), *B = ws_at<__half>(ws, p.off_b);
+    NsArgs sq{};  // the products of m x m
+    sq.M = sq.N = p.m;
+    sq.out_ld = p.s_pitch;
+    sq.out_batch = p.s_batch;
+    sq.out_type = CBA_F16;
+    sq.vec = 1;
+    sq.status = static_cast<unsigned *>(ws);
+    const NsOperand so{S, p.m, p.m, p.s_pitch, 0}, bo{B, p.m, p.m, p.s_pitch, 0};
+    for (int i = 0; e == cudaSuccess && i < d.steps; ++i) {
+        // S: the contraction runs along X's rows (wide) or across them (tall)
+        const NsOperand xs{x, d.rows, d.cols, p.x_pitch, p.wide ? 0 : 1};
+        NsArgs g = sq;
+        g.K = p.n;
+        g.alpha = kNsSym / (held * held);
+        g.out = S;
+        e = ns_gemm(xs, xs, g, d.batch, st);
+        if (e != cudaSuccess) return e;
+        g = sq;
+        g.K = p.m;
+        g.alpha = d.c / kNsSym;
+        g.beta = d.b;
+        g.aux = S;
+        g.aux_ld = p.s_pitch;
+        g.aux_batch = p.s_batch;
+        g.out = B;
+        e = ns_gemm(so, so, g, d.batch, st);
+        if (e != cudaSuccess) return e;
+        g = NsArgs{};
+        g.M = d.rows;
+        g.N = d.cols;
+        g.K = p.m;
+        g.alpha = 1.f / kNsSym;
+        g.beta = d.a;
+        g.aux = x;
+        g.aux_ld = p.x_pitch;
+        g.aux_batch = p.x_batch;
+        g.out = xn;
+        g.out_ld = p.x_pitch;
+        g.out_batch = p.x_batch;
+        g.out_type = CBA_F16;
+        g.vec = 1;
+        g.status = sq.status;
+        if (i + 1 == d.steps) {  // the last product writes the caller's matrix
+            g.alpha *= d.scale / held;
+            g.beta *= d.scale / held;
+            g.out = O;
+            g.out_type = d.out_type;
+            g.out_ld = d.ld_out ? d.ld_out : d.cols;
+            g.out_batch = d.batch_out ? d.batch_out : g.out_ld * d.rows;
+            const long long v = 16 / (long long)dtype_bytes(d.out_type);
+            g.vec = aligned_to(O, 16) && g.out_ld % v == 0 && g.out_batch % v == 0;
+        }
+        // wide: X' = B X, X's rows contracted over; tall: X' = X B
+        const NsOperand xk{x, d.rows, d.cols, p.x_pitch, 0}, xn_major{x, d.rows, d.cols, p.x_pitch, 1};
+        e = p.wide ? ns_gemm(bo, xn_major, g, d.batch, st) : ns_gemm(xk, bo, g, d.batch, st);
+        std::swap(x, xn);
+    }
+    return e;
+}
+
+}  // namespace
+
+}  // namespace cba
+
+using namespace cba;
+
+extern "C" {
+
+size_t cba_orthogonalize_workspace_bytes(const cba_orthogonalize_desc_t *d) {
+    NsPlan p;
+    return check_ns(d, &p) == CBA_OK ? p.total : 0;
+}
+
+int cba_orthogonalize(const cba_orthogonalize_desc_t *d, const void *G, void *O, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    NsPlan p;
+    const int rc = check_ns(d, &p);
+    if (rc != CBA_OK) return rc;
+    if (!G || !O) return CBA_ERR_ARG;
+    if (!aligned_to(G, dtype_bytes(d->in_type)) || !aligned_to(O, dtype_bytes(d->out_type))) return CBA_ERR_ALIGN;
+    if (!workspace || workspace_bytes < p.total) return CBA_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 256)) return CBA_ERR_ALIGN;
+    cudaGetLastError();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = select_device_of(workspace);
+    if (e == cudaSuccess) e = ns_run(*d, p, G, O, workspace, st);
+    return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
+}
+
+}  // extern "C"

@@ -427,6 +427,39 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
                            const int *cu_q, const int *cu_k, void *dq, void *dk, void *dv,
                            void *workspace, size_t workspace_bytes, void *stream);
 
+/* Orthogonalising a matrix by Newton-Schulz products (the update of a Muon
+ * optimiser, e.g. of a momentum of dW [K][C*R*S]).  For each of `batch` matrices
+ * G [rows][cols]:
+ *   X = G / (|G|_F + eps); `steps` times: X <- a X + (b S + c S^2) X, S = X X^T
+ *   O = scale X
+ * (with rows > cols the same from the right, S = X^T X).  Every singular value s
+ * of G / (|G|_F + eps) becomes p(p(...p(s))), p(s) = a s + b s^3 + c s^5; with
+ * (3.4445, -4.7750, 2.0315) and 5 steps they end near 1.
+ *
+ * The products' operands are f16 scaled by powers of two, their sums fp32: O is
+ * good to about 1e-3 of its size whatever out_type is, so that type is usually
+ * bf16.  The range of the scaling is that of singular values up to 2, which
+ * coefficients that converge keep.  Squares of G's elements are taken in fp32:
+ * elements below 1e-19 count as 0.
+ *
+ * Element types f32, f16 or bf16.  ld_*: elements from one row to the next (0:
+ * cols); batch_*: from one matrix to the next (0: rows * ld).  O may be G when
+ * type and strides agree. */
+typedef struct {
+    int batch, rows, cols;
+    int in_type, out_type;  /* cba_dtype_t */
+    int steps;              /* 1 to 100 */
+    float a, b, c;
+    float eps, scale;
+    long long ld_in, ld_out, batch_in, batch_out;
+} cba_orthogonalize_desc_t;
+
+/* Bytes of scratch of one call (0 on an invalid descriptor).  cba_get_status
+ * reads the same workspace after the call. */
+size_t cba_orthogonalize_workspace_bytes(const cba_orthogonalize_desc_t *d);
+int cba_orthogonalize(const cba_orthogonalize_desc_t *d, const void *G, void *O, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
 /* Human-readable text of a CBA_* code (static storage). */
 const char *cba_error_string(int code);
 

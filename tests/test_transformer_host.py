@@ -152,3 +152,34 @@ def test_attention_descriptor_of_tensors():
         a.update(bad)
         with pytest.raises(ValueError):
             cba.make_attention_desc(**a)
+
+
+# ---- Newton-Schulz orthogonalisation
+
+def ns(**kw):
+    return cba.make_orthogonalize_desc(**{**dict(batch=2, rows=40, cols=70), **kw})
+
+
+def ns_call(lib, d, G=FAKE, O=FAKE, ws=WS, wsb=1 << 40):
+    return lib.cba_orthogonalize(ctypes.byref(d), G, O, ws, wsb, None)
+
+
+@pytest.mark.parametrize("bad", [dict(batch=0), dict(rows=0), dict(cols=-1), dict(steps=0), dict(in_type=4), dict(out_type=-1),
+                                 dict(coefficients=(NAN, 1, 1)), dict(eps=-1.0), dict(scale=float("inf")), dict(ld_in=69),
+                                 dict(ld_out=-1), dict(batch_in=2799), dict(batch_out=5)], ids=str)
+def test_orthogonalize_rejects_a_bad_descriptor(lib, bad):
+    d = ns(**bad)
+    assert lib.cba_orthogonalize_workspace_bytes(ctypes.byref(d)) == 0
+    assert ns_call(lib, d) == cba.CBA_ERR_ARG
+
+
+def test_orthogonalize_limits_pointers_workspace(lib):
+    for kw in (dict(steps=101), dict(rows=1 << 21, cols=3), dict(batch=1 << 17)):
+        assert ns_call(lib, ns(**kw)) == cba.CBA_ERR_UNSUPPORTED
+    d = ns()
+    assert ns_call(lib, d, G=None) == cba.CBA_ERR_ARG and ns_call(lib, d, O=None) == cba.CBA_ERR_ARG
+    assert ns_call(lib, d, G=FAKE + 2) == cba.CBA_ERR_ALIGN and ns_call(lib, d, O=FAKE + 1) == cba.CBA_ERR_ALIGN
+    need = lib.cba_orthogonalize_workspace_bytes(ctypes.byref(d))
+    assert need > 2 * (2 * 40 * 72 + 2 * 40 * 40) * 2
+    assert ns_call(lib, d, wsb=need - 1) == cba.CBA_ERR_WORKSPACE and ns_call(lib, d, ws=None) == cba.CBA_ERR_WORKSPACE
+    assert ns_call(lib, d, ws=WS + 64) == cba.CBA_ERR_ALIGN
