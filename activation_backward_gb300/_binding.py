@@ -195,11 +195,7 @@ def load(path=LIB_PATH):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _bytes(t):
@@ -208,10 +204,18 @@ def _bytes(t):
     return t.numel() * t.element_size()
 
 
+def _current_stream():
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    # the handle alone: making a Stream object costs as much as a kernel launch
+    return raw(torch.cuda.current_device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -169,6 +169,37 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnArgs a) {
     }
 }
 
+// One partial row of dgamma and dbeta per block: the groups' sums added in group
+// order through `gsum` ((GROUPS - 1) TPR EPT floats).
+template <int VEC, int TPR, int EPT, int GROUPS>
+__device__ __forceinline__ void write_partials(const LnArgs &a, float (&dg)[EPT], float (&db)[EPT],
+                                               int group, int t, float *gsum) {
+    float *part = a.part + (size_t)blockIdx.x * 2 * a.cols;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float(&acc)[EPT] = w ? db : dg;
+        if constexpr (GROUPS > 1) {
+            __syncthreads();
+            if (group > 0)
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) gsum[((group - 1) * EPT + e) * TPR + t] = acc[e];
+            __syncthreads();
+            if (group == 0)
+                for (int g = 0; g < GROUPS - 1; ++g)
+#pragma unroll
+                    for (int e = 0; e < EPT; ++e) acc[e] += gsum[(g * EPT + e) * TPR + t];
+        }
+        if (group == 0)
+#pragma unroll
+            for (int i = 0; i < EPT / VEC; ++i) {
+                const int c = (i * TPR + t) * VEC;
+                if (c < a.cols)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) part[(size_t)w * a.cols + c + j] = acc[i * VEC + j];
+            }
+    }
+}
+
 // ---- backward: a group of TPR threads walks rows; threads own columns
 
 template <typename T, typename P, int VEC, int TPR, int EPT, bool RES>
@@ -262,31 +293,202 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
             }
         }
     }
-    // one partial row per block: the groups' sums added in group order
-    float *part = a.part + (size_t)blockIdx.x * 2 * a.cols;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        float(&acc)[EPT] = w ? db : dg;
-        if constexpr (GROUPS > 1) {
-            __syncthreads();
-            if (group > 0)
-#pragma unroll
-                for (int e = 0; e < EPT; ++e) gsum[((group - 1) * EPT + e) * TPR + t] = acc[e];
-            __syncthreads();
-            if (group == 0)
-                for (int g = 0; g < GROUPS - 1; ++g)
-#pragma unroll
-                    for (int e = 0; e < EPT; ++e) acc[e] += gsum[(g * EPT + e) * TPR + t];
-        }
-        if (group == 0)
+    write_partials<VEC, TPR, EPT, GROUPS>(a, dg, db, group, t, gsum);
+}
+
+// ---- many rows: the same two kernels fed by asynchronous copies
+
+// Each thread copies the 16-byte vectors it will use itself, S - 1 rows ahead,
+// into its own slots of shared memory: the bytes in flight cost no registers,
+// and as no thread reads another's slots the ring needs no barrier.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+constexpr int kRing = 4;  // rows of a group in flight or in use (backward)
+__host__ __device__ constexpr int ring_block(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+template <typename T, typename P, int TPR, int EPT, int RING>
+__global__ void __launch_bounds__(ring_block(TPR)) ln_fwd_ring_kernel(const LnArgs a) {
+    constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC, BLOCK = ring_block(TPR);
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float buf[BLOCK / 32 * 2];
+    const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    const long long step = (long long)gridDim.x * (BLOCK / TPR);
+    long long row = (long long)blockIdx.x * (BLOCK / TPR) + group;
+    int half = 0;
+    const T *xb = static_cast<const T *>(a.x);
+    const P *ga = static_cast<const P *>(a.gamma), *be = static_cast<const P *>(a.beta);
+    const uint32_t mine = ptx::smem_u32(ring) + threadIdx.x * 16;
+    auto fetch = [&](long long r, int st) {
+        if (r < a.rows) {
+            const T *x = xb + r * a.ld_x;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (i * TPR + t) * VEC;
-                if (c < a.cols)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) part[(size_t)w * a.cols + c + j] = acc[i * VEC + j];
+                if (c < a.cols) copy16(mine + (st * NV + i) * (BLOCK * 16), x + c);
             }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) fetch(row + i * step, i);
+    for (int st = 0; row < a.rows; row += step, st = (st + 1) % RING) {
+        copies_wait<RING - 2>();
+        float v[EPT];
+        float s[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * TPR + t) * VEC < a.cols) {
+                const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(
+                    ring + ((st * NV + i) * BLOCK + threadIdx.x) * 16);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s[0] += v[i * VEC + j] = to_f32(p.v[j]);
+            }
+        fetch(row + (RING - 1) * step, (st + RING - 1) % RING);
+        row_sum<TPR, 1>(s, buf, half, group, t);
+        const float mean = s[0] * a.inv_cols;
+        s[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((i * TPR + t) * VEC < a.cols)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float d = v[i * VEC + j] - mean;
+                    s[0] = fmaf(d, d, s[0]);
+                }
+        row_sum<TPR, 1>(s, buf, half, group, t);
+        const float rstd = 1.f / sqrtf(s[0] * a.inv_cols + a.eps);
+        if (t == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+        T *y = static_cast<T *>(a.y) + row * a.ld_y;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < a.cols) {
+                Pack<P, VEC> g, b;  // from L1 after the first row
+                if (ga) g = load_pack<P, VEC>(ga + c);
+                if (be) b = load_pack<P, VEC>(be + c);
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    float h = (v[i * VEC + j] - mean) * rstd;
+                    if (ga) h *= to_f32(g.v[j]);
+                    if (be) h += to_f32(b.v[j]);
+                    o.v[j] = from_f32<T>(h);
+                }
+                *reinterpret_cast<Pack<T, VEC> *>(y + c) = o;
+            }
+        }
     }
+}
+
+// Blocks per SM that the ring backward is compiled and launched for.
+__host__ __device__ constexpr int ring_bwd_per_sm(int tpr) { return tpr <= 256 ? 2 : 1; }
+
+template <typename T, typename P, int TPR, int EPT, bool RES>
+__global__ void __launch_bounds__(ring_block(TPR), ring_bwd_per_sm(TPR))
+    ln_bwd_ring_kernel(const LnArgs a) {
+    constexpr int VEC = 16 / sizeof(T), NV = EPT / VEC, BLOCK = ring_block(TPR);
+    constexpr int GROUPS = BLOCK / TPR, NT = RES ? 3 : 2;
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float buf[BLOCK / 32 * 2 * 2];
+    const int group = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    int half = 0;
+    float dg[EPT], db[EPT];
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) dg[i] = db[i] = 0.f;
+    ptx::griddep_launch_dependents();
+    const P *gp = static_cast<const P *>(a.gamma);
+    const T *xb = static_cast<const T *>(a.x), *dyb = static_cast<const T *>(a.dy);
+    const T *rb = static_cast<const T *>(a.residual);
+    T *dxb = static_cast<T *>(a.dx);
+    const long long step = (long long)gridDim.x * GROUPS;
+    long long row = (long long)blockIdx.x * GROUPS + group;
+    const uint32_t mine = ptx::smem_u32(ring) + threadIdx.x * 16;
+    float nmean = 0.f, nrstd = 0.f;
+    auto fetch = [&](long long r, int st) {
+        if (r < a.rows) {
+            const T *x = xb + r * a.ld_x, *dy = dyb + r * a.ld_dy;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * TPR + t) * VEC;
+                const uint32_t to = mine + (st * NT * NV + i) * (BLOCK * 16);
+                if (c < a.cols) {
+                    copy16(to, x + c);
+                    copy16(to + NV * BLOCK * 16, dy + c);
+                    if constexpr (RES) copy16(to + 2 * NV * BLOCK * 16, rb + r * a.ld_res + c);
+                }
+            }
+        }
+        copies_commit();
+    };
+    auto stats = [&](long long r) {
+        if (r < a.rows) nmean = a.mean_in[r], nrstd = a.rstd_in[r];
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(row + i * step, i);
+    stats(row);
+    for (int st = 0; row < a.rows; row += step, st = (st + 1) % kRing) {
+        const float mean = nmean, r = nrstd;
+        stats(row + step);
+        copies_wait<kRing - 2>();
+        auto slot = [&](int which, int i) {
+            return *reinterpret_cast<const Pack<T, VEC> *>(
+                ring + (((st * NT + which) * NV + i) * BLOCK + threadIdx.x) * 16);
+        };
+        float h[EPT], g[EPT];
+        Pack<T, VEC> pr[RES ? NV : 1];
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < a.cols) {
+                const Pack<T, VEC> px = slot(0, i), pd = slot(1, i);
+                if constexpr (RES) pr[i] = slot(2, i);
+                Pack<P, VEC> pg;  // from L1 after the first row
+                if (gp) pg = load_pack<P, VEC>(gp + c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = i * VEC + j;
+                    h[e] = (to_f32(px.v[j]) - mean) * r;
+                    const float dv = to_f32(pd.v[j]);
+                    dg[e] = fmaf(dv, h[e], dg[e]);
+                    db[e] += dv;
+                    g[e] = gp ? dv * to_f32(pg.v[j]) : dv;
+                    s[0] += g[e];
+                    s[1] = fmaf(g[e], h[e], s[1]);
+                }
+            }
+        }
+        fetch(row + (kRing - 1) * step, (st + kRing - 1) % kRing);
+        row_sum<TPR, 2>(s, buf, half, group, t);
+        const float m1 = s[0] * a.inv_cols, m2 = s[1] * a.inv_cols;
+        T *dx = dxb + row * a.ld_dx;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < a.cols) {
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int e = i * VEC + j;
+                    float v = r * (g[e] - fmaf(h[e], m2, m1));
+                    if constexpr (RES) v += to_f32(pr[i].v[j]);
+                    o.v[j] = from_f32<T>(v);
+                }
+                *reinterpret_cast<Pack<T, VEC> *>(dx + c) = o;
+            }
+        }
+    }
+    write_partials<VEC, TPR, EPT, GROUPS>(a, dg, db, group, t, reinterpret_cast<float *>(ring));
 }
 
 // Rows too long for registers: mean g and mean(g h) of each row first, then dx
@@ -353,12 +555,12 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_kernel(const LnArgs a) {
     }
 }
 
-// dgamma and dbeta from the blocks' partial rows, added in a fixed order: 8
-// warps take every 8th partial of 32 columns, then one adds the 8 sums.
-__global__ void __launch_bounds__(256)
+// dgamma and dbeta from the blocks' partial rows, added in a fixed order: 32
+// warps take every 32nd partial of 32 columns, then one adds the 32 sums.
+__global__ void __launch_bounds__(1024)
     ln_colsum_kernel(const float *part, int nblk, int cols, int accumulate, float *dgamma,
                      float *dbeta) {
-    __shared__ float sm[8][33];
+    __shared__ float sm[32][33];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
     float *out = which ? dbeta : dgamma;
@@ -367,19 +569,17 @@ __global__ void __launch_bounds__(256)
     float s = 0.f;
     if (c < cols) {
         const float *p = part + (size_t)which * cols + c;
+        const size_t row = (size_t)2 * cols;
         int b = w;
-        for (; b + 24 < nblk; b += 32) {  // four loads in flight
-            const float v0 = p[(size_t)b * 2 * cols], v1 = p[(size_t)(b + 8) * 2 * cols];
-            const float v2 = p[(size_t)(b + 16) * 2 * cols], v3 = p[(size_t)(b + 24) * 2 * cols];
-            s += (v0 + v1) + (v2 + v3);
-        }
-        for (; b < nblk; b += 8) s += p[(size_t)b * 2 * cols];
+        for (; b + 96 < nblk; b += 128)  // four loads in flight
+            s += (p[b * row] + p[(b + 32) * row]) + (p[(b + 64) * row] + p[(b + 96) * row]);
+        for (; b < nblk; b += 32) s += p[b * row];
     }
     sm[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < cols) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sm[i][lane];
+        for (int i = 1; i < 32; ++i) s += sm[i][lane];
         out[c] = accumulate ? out[c] + s : s;
     }
 }
@@ -387,10 +587,10 @@ __global__ void __launch_bounds__(256)
 // ---- launch plans
 
 struct LnPlan {
-    int vec;    // 16-byte accesses (1: one element at a time)
-    int tpr;    // backward: threads per row, 0 = the wide path
-    int nblk;   // backward: partial rows
-    size_t off_rowc, total;
+    int tpr;       // backward: threads per row, 0 = the wide path
+    int ring_tpr;  // backward: the ring kernel's threads per row, 0 = not that kernel
+    int nblk;      // backward: partial rows
+    size_t off_rowc, part_bytes, total;
 };
 
 int bwd_tpr(int cols) {
@@ -399,29 +599,75 @@ int bwd_tpr(int cols) {
     return 0;
 }
 
-// Blocks of the backward: a row per group while that needs no more than a block
-// per SM; past that at least 4 rows per group, so that the partial rows stay
-// small beside the data they come from.
-LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d) {
+// Whether a call's rows move as 16-byte vectors and are enough for the ring:
+// with fewer than 4 rows per group it has nothing to run ahead of.
+bool ring_rows(long long rows, int tpr) {
+    const int groups = tpr < 256 ? 256 / tpr : 1;
+    return rows >= 4LL * groups * kNumSMs;
+}
+
+// The plan of a backward call whose rows move as 16-byte vectors or not.  Blocks:
+// a row per group while that needs no more than a block per SM; past that at
+// least 4 rows per group, so that the partial rows stay small beside the data
+// they come from.
+LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d, bool vec) {
     LnPlan p{};
     p.tpr = bwd_tpr(d.cols);
-    const int groups = p.tpr && p.tpr < 128 ? 128 / p.tpr : 1;
-    const int per_sm = p.tpr == 0 ? 1 : p.tpr >= 512 ? 1 : p.tpr == 256 ? 2 : 4;
-    long long most = (long long)kNumSMs * per_sm;
-    if (p.tpr == 0) most = std::max(1LL, most * 6 / ((d.cols + kWideCols - 1) / kWideCols));
-    const long long one = std::min<long long>(kNumSMs, (d.rows + groups - 1) / groups);
-    const long long four = (d.rows + 4LL * groups - 1) / (4LL * groups);
-    p.nblk = (int)std::max(1LL, std::min(most, std::max(one, four)));
-    if (d.rows == 0) p.nblk = 0;
-    size_t off = ((size_t)p.nblk * 2 * d.cols * sizeof(float) + 255) / 256 * 256;
-    p.off_rowc = off;
-    if (p.tpr == 0) off += ((size_t)d.rows * sizeof(float2) + 255) / 256 * 256;
-    p.total = std::max<size_t>(off, 256);
+    if (vec) {
+        const int e = d.type == CBA_F32 ? 8 : 16;
+        for (int t = 32; t <= kLnMaxTpr && !p.ring_tpr; t *= 2)
+            if (d.cols <= t * e) p.ring_tpr = t;
+        if (p.ring_tpr && !ring_rows(d.rows, p.ring_tpr)) p.ring_tpr = 0;
+    }
+    if (p.ring_tpr) {
+        p.nblk = kNumSMs * ring_bwd_per_sm(p.ring_tpr);
+    } else {
+        const int groups = p.tpr && p.tpr < 128 ? 128 / p.tpr : 1;
+        const int per_sm = p.tpr == 0 ? 1 : p.tpr >= 512 ? 1 : p.tpr == 256 ? 2 : 4;
+        long long most = (long long)kNumSMs * per_sm;
+        if (p.tpr == 0) most = std::max(1LL, most * 6 / ((d.cols + kWideCols - 1) / kWideCols));
+        const long long one = std::min<long long>(kNumSMs, (d.rows + groups - 1) / groups);
+        const long long four = (d.rows + 4LL * groups - 1) / (4LL * groups);
+        p.nblk = (int)std::max(1LL, std::min(most, std::max(one, four)));
+        if (d.rows == 0) p.nblk = 0;
+    }
+    p.part_bytes = ((size_t)p.nblk * 2 * d.cols * sizeof(float) + 255) / 256 * 256;
+    p.off_rowc = p.part_bytes;
+    p.total = p.part_bytes;
+    if (p.tpr == 0) p.total += ((size_t)d.rows * sizeof(float2) + 255) / 256 * 256;
+    p.total = std::max<size_t>(p.total, 256);
     return p;
+}
+
+template <typename T, typename P, int TPR, int EPT>
+cudaError_t fwd_ring(const LnArgs &a, cudaStream_t st) {
+    // rows of 128 bytes per thread: two ahead fill the memory pipe
+    constexpr int ring = EPT * (int)sizeof(T) >= 128 ? 3 : 4;
+    constexpr int block = ring_block(TPR), rpb = block / TPR, smem = ring * block * EPT * (int)sizeof(T);
+    auto kern = ln_fwd_ring_kernel<T, P, TPR, EPT, ring>;
+    static const int per_sm = [&] {
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, block, smem) == cudaSuccess ? n : 0;
+    }();
+    if (per_sm == 0) return cudaErrorInvalidConfiguration;
+    const long long blocks = std::min<long long>((a.rows + rpb - 1) / rpb, (long long)kNumSMs * per_sm);
+    kern<<<(unsigned)blocks, block, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <typename T, typename P, int VEC>
 cudaError_t fwd_vec(const LnArgs &a, cudaStream_t st) {
+    if constexpr (VEC > 1) {
+        // a row per warp as long as it fits: its two sums then need no barrier
+        constexpr int E = 128 / sizeof(T);
+        if (a.cols <= 8 * E && ring_rows(a.rows, 32)) return fwd_ring<T, P, 32, E / 4>(a, st);
+        if (a.cols <= 16 * E && ring_rows(a.rows, 32)) return fwd_ring<T, P, 32, E / 2>(a, st);
+        if (a.cols <= 32 * E && ring_rows(a.rows, 32)) return fwd_ring<T, P, 32, E>(a, st);
+        if (a.cols <= 64 * E && ring_rows(a.rows, 64)) return fwd_ring<T, P, 64, E>(a, st);
+        if (a.cols <= 128 * E && ring_rows(a.rows, 128)) return fwd_ring<T, P, 128, E>(a, st);
+        if (a.cols <= 256 * E && ring_rows(a.rows, 256)) return fwd_ring<T, P, 256, E>(a, st);
+    }
 #define CBA_LN_FWD(TPR, EPT)                                                                    \
     do {                                                                                        \
         constexpr int block = TPR < 128 ? 128 : TPR, rpb = block / TPR;                         \
@@ -441,8 +687,29 @@ cudaError_t fwd_vec(const LnArgs &a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename T, typename P, int TPR, int EPT, bool RES>
+cudaError_t bwd_ring(const LnArgs &a, const LnPlan &p, cudaStream_t st) {
+    constexpr int block = ring_block(TPR), smem = kRing * (RES ? 3 : 2) * block * EPT * (int)sizeof(T);
+    static_assert((block / TPR - 1) * TPR * EPT * 4 <= smem, "the groups' sums fit the ring");
+    auto kern = ln_bwd_ring_kernel<T, P, TPR, EPT, RES>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.nblk, block, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
 template <typename T, typename P, int VEC, bool RES>
 cudaError_t bwd_vec(const LnArgs &a, const LnPlan &p, cudaStream_t st) {
+    if constexpr (VEC > 1) {
+        constexpr int E = sizeof(T) == 4 ? 8 : 16;
+        if (p.ring_tpr) switch (p.ring_tpr) {
+            case 32: return bwd_ring<T, P, 32, E, RES>(a, p, st);
+            case 64: return bwd_ring<T, P, 64, E, RES>(a, p, st);
+            case 128: return bwd_ring<T, P, 128, E, RES>(a, p, st);
+            case 256: return bwd_ring<T, P, 256, E, RES>(a, p, st);
+            default: return bwd_ring<T, P, 512, E, RES>(a, p, st);
+            }
+    }
     switch (p.tpr) {
     case 32:
         if (a.cols <= 256) ln_bwd_kernel<T, P, VEC, 32, 8, RES><<<p.nblk, 128, 0, st>>>(a);
@@ -544,7 +811,8 @@ int cba_layernorm_forward(const cba_layernorm_desc_t *d, const void *x, const vo
 
 size_t cba_layernorm_workspace_bytes(const cba_layernorm_desc_t *d) {
     if (check_desc(d) != CBA_OK) return 0;
-    return ln_bwd_plan(*d).total;
+    // whether rows move as vectors depends on the call's pointers: room for both
+    return std::max(ln_bwd_plan(*d, false).total, ln_bwd_plan(*d, true).total);
 }
 
 int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const void *dy,
@@ -558,14 +826,12 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
         !elements_aligned(dtype_bytes(d->param_type), {gamma}) ||
         !elements_aligned(4, {mean, rstd, dgamma, dbeta}))
         return CBA_ERR_ALIGN;
-    const LnPlan p = ln_bwd_plan(*d);
-    if (!workspace || workspace_bytes < p.total) return CBA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < cba_layernorm_workspace_bytes(d)) return CBA_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return CBA_ERR_ALIGN;
     LnArgs a{};
     a.x = x; a.dy = dy; a.gamma = gamma; a.residual = residual; a.dx = dx;
     a.mean_in = mean; a.rstd_in = rstd;
     a.part = static_cast<float *>(workspace);
-    a.rowc = ws_at<float2>(workspace, p.off_rowc);
     a.rows = d->rows; a.cols = d->cols; a.inv_cols = 1.f / (float)d->cols;
     a.ld_x = d->ld_x ? d->ld_x : d->cols;
     a.ld_dy = d->ld_dy ? d->ld_dy : d->cols;
@@ -574,9 +840,10 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
     cudaGetLastError();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = select_device_of(workspace);
+    const bool v = vector_ok(*d, {x, dy, gamma, residual, dx}, {a.ld_x, a.ld_dy, a.ld_dx, residual ? a.ld_res : 0});
+    const LnPlan p = ln_bwd_plan(*d, v);
+    a.rowc = ws_at<float2>(workspace, p.off_rowc);
     if (e == cudaSuccess && d->rows > 0) {
-        const bool v = vector_ok(*d, {x, dy, gamma, residual, dx},
-                                 {a.ld_x, a.ld_dy, a.ld_dx, residual ? a.ld_res : 0});
         e = with_types(*d, [&](auto t, auto pt) {
             using T = decltype(t);
             using P = decltype(pt);
@@ -586,7 +853,7 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
         });
     }
     if (e == cudaSuccess && (dgamma || dbeta))
-        e = launch_pdl(ln_colsum_kernel, dim3((unsigned)((d->cols + 31) / 32), 2), dim3(256), 0, st,
+        e = launch_pdl(ln_colsum_kernel, dim3((unsigned)((d->cols + 31) / 32), 2), dim3(1024), 0, st,
                        a.part, p.nblk, d->cols, d->accumulate, dgamma, dbeta);
     return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
 }

@@ -25,7 +25,9 @@ TYPES = [(torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16), (torc
          (torch.float16, torch.float16), (torch.float16, torch.float32)]
 # one row and one column, odd rows, each row width class of the kernels, one past each, and rows too long for registers
 SIZES = [(1, 1), (3, 1), (5, 7), (169, 255), (33, 256), (130, 260), (700, 512), (65, 520), (41, 1024), (9, 1032), (17, 2048),
-         (5, 2056), (11, 4096), (3, 4104), (400, 333), (7, 8192), (3, 8200), (2, 12345), (5, 16392)]
+         (5, 2056), (11, 4096), (3, 4104), (400, 333), (7, 8192), (3, 8200), (2, 12345), (5, 16392),
+         # enough rows for the kernels that run ahead of them
+         (9800, 8), (5003, 264), (4900, 520), (2467, 1024), (1301, 2056), (620, 4096), (613, 8192)]
 
 
 def f8(t):
