@@ -1,13 +1,15 @@
 // cba_ortho.cu -- orthogonalising a matrix by Newton-Schulz products.
 //
-//   X_0 = G / (|G|_F + eps);  S = X X^T,  B = b S + c S^2,  X <- a X + B X
-// (rows <= cols; otherwise S = X^T X and X <- a X + X B, the same polynomial of
-// the singular values from the short side).  m = min(rows, cols), n = max.
+//   X_0 = G / (|G|_F + eps);  S = X X^T,  X <- (a I + b S + c S^2) X
+// (rows <= cols; otherwise S = X^T X and X <- X (a I + b S + c S^2), the same
+// polynomial of the singular values from the short side).  m = min(rows, cols), n = max.
 //
 // Per step three products, each one launch of ns_gemm_kernel:
-//   S = X X^T      m x m, contraction n   (both operands are X)
-//   B = b S + c S S   m x m, contraction m   (S is symmetric: S S = S S^T)
-//   X' = a X + B X    m x n, contraction m
+//   S = X X^T                m x m, contraction n   (both operands are X)
+//   C = a I + b S + c S S    m x m, contraction m   (S is symmetric: S S = S S^T)
+//   X' = C X                 m x n, contraction m
+// (a I inside C: one matrix less to read, and C's diagonal, a - |b| + c near the
+// end, is smaller than B's, so its rounding costs no more than B's would).
 // X is kept in the caller's orientation.  An operand whose contraction runs
 // along its rows' elements is loaded K-major, one whose contraction runs across
 // its rows M/N-major; the tensor cores take both, so nothing is transposed.
@@ -43,14 +45,17 @@ constexpr uint64_t kNsLimitNs = 2000000000ull;
 constexpr int kNsThreads = 192;
 constexpr int kNsStages = 6;
 constexpr int kNsBK = 64;                      // contraction elements per stage (128 bytes)
-constexpr float kNsSym = 4096.f;               // S and B are held times 2^12
-constexpr int kNormBlocks = 128;               // partial sums of |G|^2 per matrix (at most)
+constexpr float kNsSym = 4096.f;               // S and C are held times 2^12
+constexpr int kNormBlocks = 512;               // partial sums of |G|^2 per matrix (at most)
 
 struct NsArgs {
     int M, N, K;            // output rows, columns, contraction
     int mt, nt, units;      // tiles; units = batch * mt * nt
     int a_major, b_major;   // 0: K-major, 1: M- / N-major
-    float alpha, beta;      // out = alpha * product + beta * aux
+    int sym;                // the output is symmetric: only tiles on and above the
+                            // diagonal are computed, the others stored transposed
+    float alpha, beta;      // out = alpha * product + beta * aux + diag * I
+    float diag;
     const __half *aux;      // same shape as out, or NULL
     long long aux_ld, aux_batch;
     void *out;
@@ -164,6 +169,17 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     // running together share B's rows in L2
     auto where = [&](int i, int &b, int &m0, int &n0) {
         int u = g0 + i * gstep;
+        if (a.sym) {  // column j of the triangle holds tiles 0 .. j
+            const int tri = a.mt * (a.mt + 1) / 2;
+            b = u / tri;
+            u -= b * tri;
+            int j = (int)((sqrtf(8.f * u + 1.f) - 1.f) * 0.5f);
+            while (j * (j + 1) / 2 > u) --j;
+            while ((j + 1) * (j + 2) / 2 <= u) ++j;
+            m0 = (u - j * (j + 1) / 2) * L::TM;
+            n0 = j * BN;
+            return;
+        }
         m0 = u % a.mt * L::TM;
         u /= a.mt;
         n0 = u % a.nt * BN;
@@ -293,6 +309,17 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                             if (j < n) v[j] = fmaf(a.beta, __half2float(aux[col + j]), v[j]);
                     }
                 }
+                if (a.diag != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (col + j == row) v[j] += a.diag;
+                }
+                if (a.sym && m0 < n0) {  // 32 rows of a column side by side
+                    __half *o = static_cast<__half *>(a.out) + b * a.out_batch + row;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j < n) o[(col + j) * a.out_ld] = __float2half_rn(v[j]);
+                }
                 if (a.out_type == CBA_F16) ns_store<__half>(a.out, at + col, v, n, a.vec);
                 else if (a.out_type == CBA_BF16) ns_store<__nv_bfloat16>(a.out, at + col, v, n, a.vec);
                 else ns_store<float>(a.out, at + col, v, n, a.vec);
@@ -312,43 +339,57 @@ __global__ void __launch_bounds__(kNsThreads, 1)
 
 // ---- |G|^2 and the scaled f16 copy
 
-// Partial sums of squares: block (p, b) takes every gridDim.x-th slab of 256
-// rows x columns' elements of matrix b; summed in a fixed order.
-template <typename T>
+// The sum of `v` over a block of 256 threads, in thread 0 (fixed order).
+__device__ __forceinline__ double block_sum(double v, double *sm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+#pragma unroll
+        for (int i = 1; i < 8; ++i) v += sm[i];
+    return v;
+}
+
+// Partial sums of squares: block (p, b) takes the p-th part of matrix b's 16-byte
+// vectors (VEC elements; 1 where rows are not whole vectors), summed in a fixed
+// order: 4 vectors in fp32, their sums in fp64.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
     ns_norm_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, double *part) {
     __shared__ double sm[8];
     ptx::griddep_launch_dependents();
     const T *gb = g + (long long)blockIdx.y * batch_stride;
-    const long long n = (long long)rows * cols;
+    const bool flat = ld == cols;
+    const long long per_row = cols / VEC, n = per_row * rows;
     const long long per = (n + gridDim.x - 1) / gridDim.x;
     const long long e1 = min(n, (blockIdx.x + 1) * per);
     double total = 0.0;
-    for (long long e = blockIdx.x * per + threadIdx.x; e < e1;) {
-        float s = 0.f;  // 16 squares in fp32, their sums in fp64
+    for (long long e = blockIdx.x * per + threadIdx.x; e < e1; e += 4 * 256) {
+        Pack<T, VEC> p[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j, e += 256)
-            if (e < e1) {
-                const long long r = ld == cols ? 0 : e / cols;
-                const float x = to_f32(gb[ld == cols ? e : r * ld + (e - r * cols)]);
-                s = fmaf(x, x, s);
+        for (int j = 0; j < 4; ++j) {
+            const long long i = e + j * 256;
+            if (i < e1) {
+                const long long r = flat ? 0 : i / per_row;
+                p[j] = *reinterpret_cast<const Pack<T, VEC> *>(gb + (flat ? i * VEC : r * ld + (i - r * per_row) * VEC));
             }
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e + j * 256 < e1)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) s = fmaf(to_f32(p[j].v[k]), to_f32(p[j].v[k]), s);
         total += s;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) total += sm[i];
-        part[(long long)blockIdx.y * kNormBlocks + blockIdx.x] = total;
-    }
+    total = block_sum(total, sm);
+    if (threadIdx.x == 0) part[(long long)blockIdx.y * kNormBlocks + blockIdx.x] = total;
 }
 
 // X = G * (held / (|G| + eps)) in f16, rows `pitch` apart (the padding is never
 // read: the maps end at cols).  One warp per row, strided.
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
     ns_cast_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, const double *part,
                    int nparts, float eps, float held, __half *x, long long pitch, long long x_batch,
@@ -371,7 +412,294 @@ __global__ void __launch_bounds__(256)
     for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
         const T *src = g + b * batch_stride + r * ld;
         __half *dst = x + b * x_batch + r * pitch;
-        for (int c = lane; c < cols; c += 32) dst[c] = __float2half_rn(to_f32(src[c]) * k);
+#pragma unroll 4
+        for (int c = lane * VEC; c < cols; c += 32 * VEC) {
+            const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(src + c);
+            Pack<__half, VEC> o;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) o.v[j] = __float2half_rn(to_f32(p.v[j]) * k);
+            *reinterpret_cast<Pack<__half, VEC> *>(dst + c) = o;
+        }
+    }
+}
+
+// ---- one block per matrix: all steps in shared memory
+
+// For m <= 128, X [R][n] (R = 64 or 128 rows, zero padded) stays in shared
+// memory in boxes of R rows x 64 columns with the 128-byte swizzle: as rows it
+// is the K-major operand of S = X X^T, as columns the N-major operand of C X.
+// Each 256-column chunk of X' depends on that chunk of X alone, so X is replaced
+// chunk by chunk.  The MMAs have M = 128 rows; with R = 64 the upper 64 lanes
+// compute with whatever lies behind the operand and are not read.  A tall
+// matrix is transposed on its way in and out.
+constexpr int kSmThreads = 512;
+constexpr size_t kSmMax = 227 * 1024;
+
+struct SmBars {
+    uint64_t sq, x, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    float factor;
+    double part[kSmThreads / 32];
+};
+
+struct SmArgs {
+    const void *G;
+    void *O;
+    int rows, cols, m, n, steps;
+    int wide, R, nb;              // nb: 64-column boxes of X
+    int in_type, out_type;
+    long long ld_in, batch_in, ld_out, batch_out;
+    float a, b, c, eps, scale, held;
+    unsigned *status;
+};
+
+size_t small_smem(int R, int nb) {
+    return (size_t)nb * R * 128 + 2 * (size_t)(R / 64) * R * 128 + (R == 64 ? 8192 : 0) + sizeof(SmBars) + 1024;
+}
+
+// Byte offset of elements 8 c8 .. 8 c8 + 7 of row r in boxes of R rows.
+__device__ __forceinline__ uint32_t box_at(int R, int r, int c8) {
+    return (uint32_t)((c8 >> 3) * R * 128 + r * 128 + (((c8 & 7) ^ (r & 7)) << 4));
+}
+
+// |G|^2 and the scaled, zero-padded f16 copy.  G is read twice (the second time
+// from L2); 16 loads of a thread are in flight at a time.
+template <typename T>
+__device__ __forceinline__ void small_load(const SmArgs &a, const T *g, uint8_t *sx, SmBars &sb) {
+    const int tid = threadIdx.x;
+    const int n = a.rows * a.cols;
+    const bool flat = a.ld_in == a.cols;
+    double total = 0.0;
+    for (int e = tid; e < n; e += 16 * kSmThreads) {
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int i = e + j * kSmThreads;
+            x[j] = 0.f;
+            if (i < n) {
+                const int r = flat ? 0 : i / a.cols;
+                x[j] = to_f32(g[flat ? i : r * a.ld_in + (i - r * a.cols)]);
+            }
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s = fmaf(x[j], x[j], s);
+        total += s;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if ((tid & 31) == 0) sb.part[tid >> 5] = total;
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 1; i < kSmThreads / 32; ++i) total += sb.part[i];
+        sb.factor = (float)((double)a.held / (sqrt(total) + (double)a.eps));
+    }
+    __syncthreads();
+    const float k = sb.factor;
+    const int per_row = a.nb * 8, chunks = a.R * per_row;  // of 8 columns
+#pragma unroll 2
+    for (int i = tid; i < chunks; i += kSmThreads) {
+        // neighbouring threads read neighbouring elements of G
+        const int r = a.wide ? i / per_row : i % a.R, c8 = a.wide ? i - r * per_row : i / a.R;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = c8 * 8 + j;
+            v[j] = 0.f;
+            if (r < a.m && c < a.n) v[j] = to_f32(a.wide ? g[r * a.ld_in + c] : g[c * a.ld_in + r]);
+        }
+        Pack<__half, 8> p;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p.v[j] = __float2half_rn(v[j] * k);
+        *reinterpret_cast<Pack<__half, 8> *>(sx + box_at(a.R, r, c8)) = p;
+    }
+}
+
+// 32 values of row r as elements c .. c + 31 of boxes of R rows.
+template <typename H, int N>
+__device__ __forceinline__ void box_put(uint8_t *to, int R, int r, int c, const float (&v)[N]) {
+#pragma unroll
+    for (int q = 0; q < N / 8; ++q) {
+        Pack<H, 8> p;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p.v[e] = from_f32<H>(v[q * 8 + e]);
+        *reinterpret_cast<Pack<H, 8> *>(to + box_at(R, r, c / 8 + q)) = p;
+    }
+}
+
+// One thread's 32 results of row r: neighbouring threads hold neighbouring rows,
+// which lie side by side in a tall O.
+template <typename T>
+__device__ __forceinline__ void small_store(const SmArgs &a, T *o, const float (&v)[32], int r, int c0) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (c0 + j < a.n) o[a.wide ? r * a.ld_out + c0 + j : (c0 + j) * a.ld_out + r] = from_f32<T>(v[j]);
+}
+
+// A wide O's rows from the finished chunk, which the threads put back into its
+// boxes in O's 16-bit type: 8 elements at a time, neighbours side by side.
+template <typename T>
+__device__ __forceinline__ void small_copy(const SmArgs &a, T *o, const uint8_t *sx, int c80, int n8) {
+    const bool vec = aligned_to(o, 16) && a.ld_out % 8 == 0;
+    for (int i = threadIdx.x; i < a.m * n8; i += kSmThreads) {
+        const int r = i / n8, c8 = c80 + i - r * n8, c = c8 * 8;
+        const Pack<T, 8> p = *reinterpret_cast<const Pack<T, 8> *>(sx + box_at(a.R, r, c8));
+        T *to = o + r * a.ld_out + c;
+        if (vec && c + 8 <= a.n) {
+            *reinterpret_cast<Pack<T, 8> *>(to) = p;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < a.n) to[j] = p.v[j];
+        }
+    }
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) { ptx::tmem_ld16(t, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[32]) { ptx::tmem_ld32(t, v); }
+
+template <int R>
+__global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a) {
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    constexpr uint32_t box = R * 128;
+    uint8_t *sx = smem, *ss = sx + a.nb * box, *sc = ss + (R / 64) * box;
+    SmBars &sb = *reinterpret_cast<SmBars *>(sc + (R / 64) * box + (R == 64 ? 8192 : 0));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (uint64_t *b : {&sb.sq, &sb.x, &sb.drain}) ptx::mbar_init(ptx::smem_u32(b), 1);
+        sb.abort_flag = 0;
+        ptx::fence_mbar_init();
+        if (gridDim.x == 1) *a.status = 0;
+    }
+    if (warp == 0) {
+        ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    const long long b = blockIdx.x;
+    if (a.in_type == CBA_F32) small_load(a, static_cast<const float *>(a.G) + b * a.batch_in, sx, sb);
+    else if (a.in_type == CBA_F16) small_load(a, static_cast<const __half *>(a.G) + b * a.batch_in, sx, sb);
+    else small_load(a, static_cast<const __nv_bfloat16 *>(a.G) + b * a.batch_in, sx, sb);
+    // everything that the tensor cores read was written by these threads
+    auto publish = [&]() {
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncthreads();
+        ptx::tc_fence_after();
+    };
+    publish();
+    const uint32_t tmem = sb.tmem_base, uX = ptx::smem_u32(sx), uS = ptx::smem_u32(ss), uC = ptx::smem_u32(sc);
+    const uint32_t tS = tmem, tQ = tmem + 128, tX = tmem + 256;
+    constexpr uint32_t id_s = ptx::idesc_f16(128, R, false, false);
+    const int km = (a.m + 15) / 16, kn = (a.n + 15) / 16;
+    // 16 warps: the quarter of the rows that TMEM lets a warp read, and one of
+    // four column parts
+    const int quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const bool mine = quarter * 32 < R;  // this warp's rows exist
+    constexpr int CS = R / 4;            // S columns per thread
+    const int c_s = part * CS, nchunks = (a.nb + 3) / 4;
+    const float s_alpha = kNsSym / (a.held * a.held);
+    volatile int *ab = &sb.abort_flag;
+    uint32_t ph_sq = 0, ph_x = 0;
+    auto wait = [&](uint64_t *bar, uint32_t &phase) {
+        const bool ok = ptx::mbar_wait_bounded(ptx::smem_u32(bar), phase, ab, a.status, kNsLimitNs);
+        phase ^= 1;
+        ptx::tc_fence_after();
+        return __syncthreads_and(ok) != 0;
+    };
+    auto product = [&](uint32_t d, uint32_t u, int ksteps) {  // D = U U^T, R columns
+        for (int ks = 0; ks < ksteps; ++ks) {
+            const uint64_t de = ptx::smem_desc(u + (ks >> 2) * box + (ks & 3) * 32, 16, 1024, 2);
+            ptx::mma_f16(d, de, de, id_s, ks > 0);
+        }
+        ptx::mma_commit(ptx::smem_u32(&sb.sq));
+    };
+    auto apply = [&](int ch) {  // the 256 columns of X' from box 4 ch on
+        const uint32_t id = ptx::idesc_f16(128, 64 * min(4, a.nb - 4 * ch), false, true);
+        for (int ks = 0; ks < km; ++ks)
+            ptx::mma_f16(tX, ptx::smem_desc(uC + (ks >> 2) * box + (ks & 3) * 32, 16, 1024, 2),
+                         ptx::smem_desc(uX + 4 * ch * box + ks * 2048, box, 1024, 2), id, ks > 0);
+        ptx::mma_commit(ptx::smem_u32(&sb.x));
+    };
+    bool ok = true;
+    for (int step = 0; ok && step < a.steps; ++step) {
+        if (tid == 0) product(tS, uX, kn);
+        if (!(ok = wait(&sb.sq, ph_sq))) break;
+        float s[CS];
+        if (mine) {
+            tmem_ld(tS + lanes + c_s, s);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < CS; ++j) s[j] *= s_alpha;
+            box_put<__half>(ss, R, r, c_s, s);
+        }
+        publish();
+        if (tid == 0) product(tQ, uS, km);
+        if (!(ok = wait(&sb.sq, ph_sq))) break;
+        if (mine) {
+            float q[CS];
+            tmem_ld(tQ + lanes + c_s, q);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < CS; ++j) {
+                q[j] = fmaf(a.c / kNsSym, q[j], a.b * s[j]);
+                if (c_s + j == r) q[j] += a.a * kNsSym;
+            }
+            box_put<__half>(sc, R, r, c_s, q);
+        }
+        publish();
+        const bool last = step + 1 == a.steps;
+        const float alpha = (last ? a.scale / a.held : 1.f) / kNsSym;
+        for (int ch = 0; ok && ch < nchunks; ++ch) {
+            if (tid == 0) apply(ch);
+            if (!(ok = wait(&sb.x, ph_x))) break;
+            const int boxes = min(4, a.nb - 4 * ch);
+            if (mine && part < boxes)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c0 = ch * 256 + part * 64 + i * 32;
+                    float v[32];
+                    __syncwarp();
+                    ptx::tmem_ld32(tX + lanes + part * 64 + i * 32, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= alpha;
+                    if (!last) {
+                        box_put<__half>(sx, R, r, c0, v);
+                    } else if (a.out_type == CBA_F32) {
+                        if (r < a.m) small_store(a, static_cast<float *>(a.O) + b * a.batch_out, v, r, c0);
+                    } else if (a.out_type == CBA_F16) {
+                        if (a.wide) box_put<__half>(sx, R, r, c0, v);
+                        else if (r < a.m) small_store(a, static_cast<__half *>(a.O) + b * a.batch_out, v, r, c0);
+                    } else {
+                        if (a.wide) box_put<__nv_bfloat16>(sx, R, r, c0, v);
+                        else if (r < a.m) small_store(a, static_cast<__nv_bfloat16 *>(a.O) + b * a.batch_out, v, r, c0);
+                    }
+                }
+            publish();
+            if (last && a.wide && a.out_type != CBA_F32) {
+                if (a.out_type == CBA_F16)
+                    small_copy(a, static_cast<__half *>(a.O) + b * a.batch_out, sx, 32 * ch, 8 * boxes);
+                else
+                    small_copy(a, static_cast<__nv_bfloat16 *>(a.O) + b * a.batch_out, sx, 32 * ch, 8 * boxes);
+            }
+        }
+    }
+    // on a timeout MMAs may still be in flight: wait (bounded) for all of them
+    if (!ok && tid == 0) {
+        int no = 0;
+        ptx::mma_commit(ptx::smem_u32(&sb.drain));
+        ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kNsLimitNs);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
     }
 }
 
@@ -382,7 +710,7 @@ struct NsPlan {
     bool wide;                 // rows <= cols
     long long x_pitch, s_pitch;
     long long x_batch, s_batch;  // elements of one matrix
-    size_t off_part, off_x0, off_x1, off_s, off_b, total;
+    size_t off_part, off_x0, off_x1, off_s, off_c, total;
 };
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -416,8 +744,8 @@ int check_ns(const cba_orthogonalize_desc_t *d, NsPlan *p) {
     p->off_x0 = p->off_part + up256((size_t)d->batch * kNormBlocks * sizeof(double));
     p->off_x1 = p->off_x0 + xb;
     p->off_s = p->off_x1 + xb;
-    p->off_b = p->off_s + sb;
-    p->total = p->off_b + sb;
+    p->off_c = p->off_s + sb;
+    p->total = p->off_c + sb;
     return CBA_OK;
 }
 
@@ -442,7 +770,8 @@ cudaError_t ns_launch(const NsOperand &oa, const NsOperand &ob, NsArgs a, int ba
     using L = NsTile<CG, BN>;
     a.mt = (a.M + L::TM - 1) / L::TM;
     a.nt = (a.N + BN - 1) / BN;
-    a.units = a.mt * a.nt * batch;
+    a.sym = a.sym && L::TM == BN;  // needs square tiles
+    a.units = (a.sym ? a.mt * (a.mt + 1) / 2 : a.mt * a.nt) * batch;
     a.a_major = oa.major;
     a.b_major = ob.major;
     CUtensorMap ta, tb;
@@ -479,38 +808,79 @@ cudaError_t ns_gemm(const NsOperand &oa, const NsOperand &ob, const NsArgs &a, i
     return ns_launch<1, 64>(oa, ob, a, batch, st);
 }
 
-template <typename T>
-cudaError_t ns_start(const cba_orthogonalize_desc_t &d, const NsPlan &p, const void *G, void *ws, float held,
-                     cudaStream_t st) {
-    const long long ld = d.ld_in ? d.ld_in : d.cols, bs = d.batch_in ? d.batch_in : ld * d.rows;
+template <typename T, int VEC>
+cudaError_t ns_start_vec(const cba_orthogonalize_desc_t &d, const NsPlan &p, const T *G, long long ld, long long bs,
+                         void *ws, float held, cudaStream_t st) {
     const long long n = (long long)d.rows * d.cols;
-    const int parts = (int)std::max(1LL, std::min<long long>(kNormBlocks, n / 4096));
+    const int parts = (int)std::max(1LL, std::min<long long>(kNormBlocks, n / 8192));
     double *part = ws_at<double>(ws, p.off_part);
-    ns_norm_kernel<T><<<dim3(parts, d.batch), 256, 0, st>>>(static_cast<const T *>(G), d.rows, d.cols, ld, bs, part);
+    ns_norm_kernel<T, VEC><<<dim3(parts, d.batch), 256, 0, st>>>(G, d.rows, d.cols, ld, bs, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int blocks = std::max(1, std::min((d.rows + 7) / 8, 8 * kNumSMs / std::min(d.batch, 8 * kNumSMs)));
-    return launch_pdl(ns_cast_kernel<T>, dim3(blocks, d.batch), dim3(256), 0, st, static_cast<const T *>(G), d.rows,
-                      d.cols, ld, bs, static_cast<const double *>(part), parts, d.eps, held,
-                      ws_at<__half>(ws, p.off_x0), p.x_pitch, p.x_batch, static_cast<unsigned *>(ws));
+    return launch_pdl(ns_cast_kernel<T, VEC>, dim3(blocks, d.batch), dim3(256), 0, st, G, d.rows, d.cols, ld, bs,
+                      static_cast<const double *>(part), parts, d.eps, held, ws_at<__half>(ws, p.off_x0), p.x_pitch,
+                      p.x_batch, static_cast<unsigned *>(ws));
+}
+
+template <typename T>
+cudaError_t ns_start(const cba_orthogonalize_desc_t &d, const NsPlan &p, const void *G, void *ws, float held,
+                     cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const long long ld = d.ld_in ? d.ld_in : d.cols, bs = d.batch_in ? d.batch_in : ld * d.rows;
+    const T *g = static_cast<const T *>(G);
+    if (aligned_to(G, 16) && d.cols % V == 0 && ld % V == 0 && bs % V == 0)
+        return ns_start_vec<T, V>(d, p, g, ld, bs, ws, held, st);
+    return ns_start_vec<T, 1>(d, p, g, ld, bs, ws, held, st);
+}
+
+// All steps of a matrix in one block, where it fits.
+bool small_fits(const NsPlan &p) {
+    const int R = p.m <= 64 ? 64 : 128;
+    return p.m <= 128 && small_smem(R, (p.n + 63) / 64) <= kSmMax;
+}
+
+cudaError_t ns_small(const cba_orthogonalize_desc_t &d, const NsPlan &p, const void *G, void *O, void *ws, float held,
+                     cudaStream_t st) {
+    SmArgs a{};
+    a.G = G; a.O = O; a.rows = d.rows; a.cols = d.cols; a.m = p.m; a.n = p.n; a.steps = d.steps;
+    a.wide = p.wide; a.R = p.m <= 64 ? 64 : 128; a.nb = (p.n + 63) / 64;
+    a.in_type = d.in_type; a.out_type = d.out_type;
+    a.ld_in = d.ld_in ? d.ld_in : d.cols;
+    a.batch_in = d.batch_in ? d.batch_in : a.ld_in * d.rows;
+    a.ld_out = d.ld_out ? d.ld_out : d.cols;
+    a.batch_out = d.batch_out ? d.batch_out : a.ld_out * d.rows;
+    a.a = d.a; a.b = d.b; a.c = d.c; a.eps = d.eps; a.scale = d.scale; a.held = held;
+    a.status = static_cast<unsigned *>(ws);
+    const size_t smem = small_smem(a.R, a.nb);
+    auto kern = a.R == 64 ? ns_small_kernel<64> : ns_small_kernel<128>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmMax);
+    if (e != cudaSuccess) return e;
+    // one block clears the status word itself, several must not undo each other's
+    if (d.batch > 1) e = cudaMemsetAsync(ws, 0, 4, st);
+    if (e != cudaSuccess) return e;
+    kern<<<d.batch, kSmThreads, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const void *G, void *O, void *ws,
                    cudaStream_t st) {
     const float held = exp2f(roundf(0.5f * log2f((float)p.n)));
+    if (small_fits(p)) return ns_small(d, p, G, O, ws, held, st);
     cudaError_t e = d.in_type == CBA_F32   ? ns_start<float>(d, p, G, ws, held, st)
                     : d.in_type == CBA_F16 ? ns_start<__half>(d, p, G, ws, held, st)
                                            : ns_start<__nv_bfloat16>(d, p, G, ws, held, st);
     __half *x = ws_at<__half>(ws, p.off_x0), *xn = ws_at<__half>(ws, p.off_x1);
-    __half *S = ws_at<__half>(ws, p.off_s), *B = ws_at<__half>(ws, p.off_b);
+    __half *S = ws_at<__half>(ws, p.off_s), *C = ws_at<__half>(ws, p.off_c);
     NsArgs sq{};  // the products of m x m
     sq.M = sq.N = p.m;
     sq.out_ld = p.s_pitch;
     sq.out_batch = p.s_batch;
     sq.out_type = CBA_F16;
     sq.vec = 1;
+    sq.sym = 1;
     sq.status = static_cast<unsigned *>(ws);
-    const NsOperand so{S, p.m, p.m, p.s_pitch, 0}, bo{B, p.m, p.m, p.s_pitch, 0};
+    const NsOperand so{S, p.m, p.m, p.s_pitch, 0}, co{C, p.m, p.m, p.s_pitch, 0};
     for (int i = 0; e == cudaSuccess && i < d.steps; ++i) {
         // S: the contraction runs along X's rows (wide) or across them (tall)
         const NsOperand xs{x, d.rows, d.cols, p.x_pitch, p.wide ? 0 : 1};
@@ -524,10 +894,11 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
         g.K = p.m;
         g.alpha = d.c / kNsSym;
         g.beta = d.b;
+        g.diag = d.a * kNsSym;
         g.aux = S;
         g.aux_ld = p.s_pitch;
         g.aux_batch = p.s_batch;
-        g.out = B;
+        g.out = C;
         e = ns_gemm(so, so, g, d.batch, st);
         if (e != cudaSuccess) return e;
         g = NsArgs{};
@@ -535,10 +906,6 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
         g.N = d.cols;
         g.K = p.m;
         g.alpha = 1.f / kNsSym;
-        g.beta = d.a;
-        g.aux = x;
-        g.aux_ld = p.x_pitch;
-        g.aux_batch = p.x_batch;
         g.out = xn;
         g.out_ld = p.x_pitch;
         g.out_batch = p.x_batch;
@@ -547,7 +914,6 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
         g.status = sq.status;
         if (i + 1 == d.steps) {  // the last product writes the caller's matrix
             g.alpha *= d.scale / held;
-            g.beta *= d.scale / held;
             g.out = O;
             g.out_type = d.out_type;
             g.out_ld = d.ld_out ? d.ld_out : d.cols;
@@ -555,9 +921,9 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
             const long long v = 16 / (long long)dtype_bytes(d.out_type);
             g.vec = aligned_to(O, 16) && g.out_ld % v == 0 && g.out_batch % v == 0;
         }
-        // wide: X' = B X, X's rows contracted over; tall: X' = X B
+        // wide: X' = C X, X's rows contracted over; tall: X' = X C
         const NsOperand xk{x, d.rows, d.cols, p.x_pitch, 0}, xn_major{x, d.rows, d.cols, p.x_pitch, 1};
-        e = p.wide ? ns_gemm(bo, xn_major, g, d.batch, st) : ns_gemm(xk, bo, g, d.batch, st);
+        e = p.wide ? ns_gemm(co, xn_major, g, d.batch, st) : ns_gemm(xk, co, g, d.batch, st);
         std::swap(x, xn);
     }
     return e;

@@ -36,7 +36,7 @@ struct __align__(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
 
 inline size_t dtype_bytes(int t) { return t == CBA_F32 ? 4 : 2; }
 inline bool dtype_ok(int t) { return t == CBA_F32 || t == CBA_F16 || t == CBA_BF16; }
-inline bool aligned_to(const void *p, size_t a) {
+__host__ __device__ inline bool aligned_to(const void *p, size_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 

@@ -47,7 +47,11 @@ def draw(seed, *shape, scale=1e-3, dtype=torch.float32):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 9), (1, 9, 1), (2, 7, 5), (1, 50, 500), (1, 500, 50), (3, 64, 64), (1, 128, 576), (1, 130, 260),
-          (2, 255, 1024), (1, 1024, 255), (1, 129, 129), (1, 512, 2304), (5, 300, 200), (1, 260, 1100), (1, 1280, 1280)]
+          (2, 255, 1024), (1, 1024, 255), (1, 129, 129), (1, 512, 2304), (5, 300, 200), (1, 260, 1100), (1, 1280, 1280),
+          # one block per matrix: the largest that fit, with an odd number of 64-column boxes, and the first that do not
+          (2, 64, 1600), (1, 1, 1601), (3, 128, 640), (2, 65, 320), (1, 630, 127), (2, 128, 641), (1, 1290, 33),
+          # enough tiles for pairs of blocks and for the symmetric products' triangle, with ragged edges
+          (3, 900, 1300), (5, 1300, 1000)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
