@@ -27,7 +27,7 @@
 //
 // Roles of a block: warp 0 issues the TMA loads (and zeroes the rows of a
 // packed sequence's last tile that belong to its neighbour), warp 1 owns TMEM
-// and issues the MMAs, warps 4-11 compute P and dS (two warpgroups, 64 columns
+// and issues the MMAs, warps 4-19 compute P and dS (four warpgroups, 32 columns
 // of a tile each) and the epilogue.  Every wait is bounded (2 s); on a timeout
 // the block sets the workspace status bit, stops, waits (bounded) for its
 // copies in flight, frees its TMEM and returns.
@@ -45,7 +45,8 @@ namespace cba {
 namespace {
 
 constexpr uint64_t kAtLimitNs = 2000000000ull;
-constexpr int kAtThreads = 384;
+constexpr int kAtThreads = 640;
+constexpr int kAtWarps = 16;                  // that compute P and dS
 constexpr int kT = 128;                       // tile rows, of queries and of keys
 constexpr uint32_t kBoxBytes = kT * 128u;     // 128 rows x 64 16-bit elements
 constexpr float kLog2e = 1.4426950408889634f;
@@ -138,38 +139,48 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         if (u == 0 && t == 0 && BF16) *a.status = 0;  // f16: cleared with the maxima before
         if (tile * kT < s.lq) {
             const long long row0 = s.row0 + (long long)h * a.head_rows + tile * kT;
-            for (int r = t / LPR; r < kT; r += 256 / LPR) {
-                const int i = tile * kT + r;
-                float d = 0.f, n = 0.f;
-                if (i < s.lq && lane * 8 < a.dim) {
-                    const long long ob = b * a.so[0] + (s.q0 + i) * a.so[1] + h * a.so[2] + lane * 8;
-                    const long long db = b * a.sdo[0] + (s.q0 + i) * a.sdo[1] + h * a.sdo[2] + lane * 8;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + ob);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + db);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            constexpr int RPP = 256 / LPR, NR = 4;  // rows per pass; rows of a thread in flight
+            for (int r0 = t / LPR; r0 < kT; r0 += NR * RPP) {
+                uint4 x[NR], y[NR];
+                float l[NR];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 p = unpack2<BF16>(xs[j]), q = unpack2<BF16>(ys[j]);
+                for (int j = 0; j < NR; ++j) {
+                    const int i = tile * kT + r0 + j * RPP;
+                    x[j] = y[j] = make_uint4(0, 0, 0, 0);
+                    l[j] = INFINITY;  // a padding row: P = 0
+                    if (i < s.lq && lane * 8 < a.dim) {
+                        x[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.o) + b * a.so[0] +
+                                                                (s.q0 + i) * a.so[1] + h * a.so[2] + lane * 8);
+                        y[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.dout) + b * a.sdo[0] +
+                                                                (s.q0 + i) * a.sdo[1] + h * a.sdo[2] + lane * 8);
+                    }
+                    if (i < s.lq && lane == 0)
+                        l[j] = a.lse[a.cu_q ? (long long)h * a.total_q + s.q0 + i
+                                            : ((long long)b * a.hq + h) * a.len_q + i];
+                }
+#pragma unroll
+                for (int j = 0; j < NR; ++j) {
+                    float d = 0.f, n = 0.f;
+                    const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    const uint32_t ys[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 p = unpack2<BF16>(xs[e]), q = unpack2<BF16>(ys[e]);
                         d = fmaf(p.x, q.x, fmaf(p.y, q.y, d));
                         if (!BF16) n = fmaf(q.x, q.x, fmaf(q.y, q.y, n));
                     }
-                }
 #pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) {
-                    d += __shfl_xor_sync(0xffffffffu, d, o);
-                    if (!BF16) n += __shfl_xor_sync(0xffffffffu, n, o);
-                }
-                most = fmaxf(most, n);
-                if (lane == 0) {
-                    float l = INFINITY;  // a padding row, or one whose keys are all masked: P = 0
-                    if (i < s.lq) {
-                        const long long li = a.cu_q ? (long long)h * a.total_q + s.q0 + i
-                                                    : ((long long)b * a.hq + h) * a.len_q + i;
-                        l = a.lse[li];
-                        l = l == -INFINITY ? INFINITY : l * kLog2e - (BF16 ? 0.f : kPShift);
+                    for (int o = LPR / 2; o > 0; o >>= 1) {
+                        d += __shfl_xor_sync(0xffffffffu, d, o);
+                        if (!BF16) n += __shfl_xor_sync(0xffffffffu, n, o);
                     }
-                    a.lse2[row0 + r] = l;
-                    a.dsum[row0 + r] = d;
+                    most = fmaxf(most, n);
+                    if (lane == 0) {
+                        // a row whose keys are all masked has lse = -inf: P = 0 too
+                        const long long at = row0 + r0 + j * RPP;
+                        a.lse2[at] = l[j] == -INFINITY ? INFINITY : l[j] * kLog2e - (BF16 ? 0.f : kPShift);
+                        a.dsum[at] = d;
+                    }
                 }
             }
         }
@@ -260,26 +271,58 @@ __device__ __forceinline__ bool load_tile(uint32_t dst, const CUtensorMap *tm, l
     return true;
 }
 
-// D[128 x 128] = A[128 x dim] B[128 x dim]^T, both tiles row-major in 64-column boxes.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb, int dim,
+// D[128 x 128] = A[128 x dim] B[128 x dim]^T, both tiles row-major in 64-column
+// boxes.  (A descriptor counts 16-byte units: steps are additions to it.)
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb, int steps,
                                          uint32_t idesc) {
-    const int steps = (dim + 15) / 16;
-    for (int ks = 0; ks < steps; ++ks) {
-        const uint32_t off = (ks >> 2) * kBoxBytes + (ks & 3) * 32;
-        ptx::mma_f16(d, ptx::smem_desc(sa + off, 16, 1024, 2), ptx::smem_desc(sb + off, 16, 1024, 2),
-                     idesc, ks > 0);
+    const uint64_t da = ptx::smem_desc(sa, 16, 1024, 2), db = ptx::smem_desc(sb, 16, 1024, 2);
+#pragma unroll
+    for (int ks = 0; ks < DP / 16; ++ks) {
+        const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
+        if (ks < steps) ptx::mma_f16(d, da + off, db + off, idesc, ks > 0);
     }
 }
 
-// D[128 x DP] (+)= A[128 x 128] B[128 x DP]: A in TMEM (16-bit, the first 64
-// columns' 32 words at ta, the others' at ta + 64), B's rows contracted over.
+// D[128 x DP] (+)= A[128 x 128] B[128 x DP]: A in TMEM (16-bit; the 16 words of
+// each 32 columns at ta, ta + 32, ...), B's rows contracted over.
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t ta, uint32_t sb, uint32_t idesc,
                                         bool accumulate) {
+    const uint64_t db = ptx::smem_desc(sb, kBoxBytes, 1024, 2);
 #pragma unroll
     for (int ks = 0; ks < kT / 16; ++ks)
-        ptx::mma_f16_ts(d, ta + (ks >> 2) * 64 + (ks & 3) * 8,
-                        ptx::smem_desc(sb + ks * 2048, kBoxBytes, 1024, 2), idesc,
+        ptx::mma_f16_ts(d, ta + (ks >> 1) * 32 + (ks & 1) * 8, db + ks * (2048 >> 4), idesc,
                         accumulate || ks > 0);
+}
+
+// 2^(x cs - l) of 32 columns with an l of their own each.
+__device__ __forceinline__ void probabilities(float2 (&p)[16], float cs, const float *lse) {
+    const float2 c2 = make_float2(cs, cs);
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+        const float4 l = *reinterpret_cast<const float4 *>(lse + 2 * c);
+        p[c] = ptx::fma2(p[c], c2, make_float2(-l.x, -l.y));
+        p[c + 1] = ptx::fma2(p[c + 1], c2, make_float2(-l.z, -l.w));
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) p[c] = make_float2(ptx::ex2(p[c].x), ptx::ex2(p[c].y));
+}
+
+__device__ __forceinline__ void tmem_load(uint32_t t, float2 (&v)[16]) {
+    float x[32];
+    ptx::tmem_ld32(t, x);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = make_float2(x[2 * c], x[2 * c + 1]);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void tmem_store(uint32_t t, const float2 (&v)[16]) {
+    uint32_t w[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) w[c] = pack2<BF16>(v[c].x, v[c].y);
+    ptx::tmem_st16(t, w);
+    ptx::tmem_st_wait();
 }
 
 // One thread's row of a gradient tile: COLS fp32 columns of TMEM at `ta`,
@@ -288,15 +331,15 @@ template <int COLS, bool BF16>
 __device__ __forceinline__ void store_row(uint32_t ta, float scale, bool zero, bool live,
                                           uint16_t *out, int cols) {
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
-        float v[32];
+    for (int c = 0; c < COLS; c += 16) {
+        float v[16];
         __syncwarp();  // rows that are not stored skip the code below
         if (!zero) {
-            ptx::tmem_ld32(ta + c, v);
+            ptx::tmem_ld16(ta + c, v);
             ptx::tmem_ld_wait();
         }
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
+        for (int j = 0; j < 16; j += 8)
             if (live && c + j < cols) {
                 uint4 w;
                 uint32_t *u = &w.x;
@@ -345,11 +388,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at_init_bars(sb.b_full, kDoStages, 1);
         at_init_bars(sb.b_empty, kDoStages, 1);
         at_init_bars(sb.r_full, 2, 1);
-        at_init_bars(sb.r_empty, 2, 8);  // the 8 compute warps
+        at_init_bars(sb.r_empty, 2, kAtWarps);
         at_init_bars(&sb.s_full, 1, 1);
-        at_init_bars(&sb.p_ready, 1, 8);
+        at_init_bars(&sb.p_ready, 1, kAtWarps);
         at_init_bars(sb.dp_full, 2, 1);
-        at_init_bars(&sb.ds_ready, 1, 8);
+        at_init_bars(&sb.ds_ready, 1, kAtWarps);
         at_init_bars(&sb.fix, 3, 1);  // fix, acc, drain
         sb.abort_flag = 0;
         ptx::fence_mbar_init();
@@ -452,6 +495,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (lane == 0 && n > 0) {
             constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
             constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
+            const int steps = (a.dim + 15) / 16;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
                 ptx::tc_fence_after();
@@ -459,12 +503,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             };
             bool ok = wait(&sb.stat, 0) && wait(&sb.a_full[0], 0);
             if (ok) {
-                mma_rows(tS, sK, sQ, a.dim, id_s);
+                mma_rows<DP>(tS, sK, sQ, steps, id_s);
                 ptx::mma_commit(ptx::smem_u32(&sb.s_full));
                 ok = wait(&sb.b_full[0], 0);
             }
             if (ok) {
-                mma_rows(tDp, sV, sDo, a.dim, id_s);
+                mma_rows<DP>(tDp, sV, sDo, steps, id_s);
                 ptx::mma_commit(ptx::smem_u32(&sb.dp_full[0]));
             }
             for (int it = 0; ok && it < n; ++it) {
@@ -476,7 +520,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (nx < n) {
                     // S overwrites P: this thread's MMAs run in the order of issue
                     if (!(ok = wait(&sb.a_full[nx % kQStages], (uint32_t)(nx / kQStages)))) break;
-                    mma_rows(tS, sK, sQ + (nx % kQStages) * TILE, a.dim, id_s);
+                    mma_rows<DP>(tS, sK, sQ + (nx % kQStages) * TILE, steps, id_s);
                     ptx::mma_commit(ptx::smem_u32(&sb.s_full));
                 }
                 if (!(ok = wait(&sb.ds_ready, (uint32_t)it))) break;
@@ -484,7 +528,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 ptx::mma_commit(ptx::smem_u32(&sb.a_empty[st]));
                 if (nx < n) {
                     if (!(ok = wait(&sb.b_full[nx % kDoStages], (uint32_t)(nx / kDoStages)))) break;
-                    mma_rows(tDp, sV, sDo + (nx % kDoStages) * TILE, a.dim, id_s);
+                    mma_rows<DP>(tDp, sV, sDo + (nx % kDoStages) * TILE, steps, id_s);
                     ptx::mma_commit(ptx::smem_u32(&sb.dp_full[0]));
                 }
             }
@@ -509,67 +553,39 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         };
         for (int it = 0; it < n; ++it) {
             const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, sr = it & 1;
-            const float *lse = rows + sr * 2 * kT + wg * 64, *ds = lse + kT;
-            float p[64];
+            const float *lse = rows + sr * 2 * kT + wg * 32, *ds = lse + kT;
+            float2 p[16];
             if (!(ok = wait(&sb.r_full[sr], (uint32_t)(it / 2)) && wait(&sb.s_full, (uint32_t)it))) break;
             ptx::tc_fence_after();
-            {
-                float x[32], y[32];
-                ptx::tmem_ld32(tS + lanes + wg * 64, x);
-                ptx::tmem_ld32(tS + lanes + wg * 64 + 32, y);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 32; ++c) p[c] = x[c], p[32 + c] = y[c];
-            }
-#pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 l = *reinterpret_cast<const float4 *>(lse + c);
-                p[c] = ptx::ex2(fmaf(p[c], cs, -l.x));
-                p[c + 1] = ptx::ex2(fmaf(p[c + 1], cs, -l.y));
-                p[c + 2] = ptx::ex2(fmaf(p[c + 2], cs, -l.z));
-                p[c + 3] = ptx::ex2(fmaf(p[c + 3], cs, -l.w));
-            }
+            tmem_load(tS + lanes + wg * 32, p);
+            probabilities(p, cs, lse);
             if (a.causal && k0 + kT - 1 > q0 + off) {
-                const int first = j - off - q0 - wg * 64;  // columns before it do not see key j
+                const int first = j - off - q0 - wg * 32;  // columns before it do not see key j
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (c < first) p[c] = 0.f;
+                for (int c = 0; c < 16; ++c) {
+                    if (2 * c < first) p[c].x = 0.f;
+                    if (2 * c + 1 < first) p[c].y = 0.f;
+                }
             }
-            {
-                float w[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(pack2<BF16>(p[2 * c], p[2 * c + 1]));
-                ptx::tmem_st32(tS + lanes + wg * 64, w);
-                ptx::tmem_st_wait();
-            }
+            tmem_store<BF16>(tS + lanes + wg * 32, p);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
             if (!(ok = wait(&sb.dp_full[0], (uint32_t)it))) break;
             ptx::tc_fence_after();
-            float w[32];
+            float2 x[16];
+            tmem_load(tDp + lanes + wg * 32, x);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[32];
-                ptx::tmem_ld32(tDp + lanes + wg * 64 + half * 32, x);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    const float4 d = *reinterpret_cast<const float4 *>(ds + half * 32 + c);
-                    const float *pp = p + half * 32 + c;
-                    x[c] = pp[0] * (x[c] - d.x);
-                    x[c + 1] = pp[1] * (x[c + 1] - d.y);
-                    x[c + 2] = pp[2] * (x[c + 2] - d.z);
-                    x[c + 3] = pp[3] * (x[c + 3] - d.w);
-                    if constexpr (!BF16)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[c + e] *= pds;
-                    w[half * 16 + c / 2] = __uint_as_float(pack2<BF16>(x[c], x[c + 1]));
-                    w[half * 16 + c / 2 + 1] = __uint_as_float(pack2<BF16>(x[c + 2], x[c + 3]));
+            for (int c = 0; c < 16; c += 2) {
+                const float4 d = *reinterpret_cast<const float4 *>(ds + 2 * c);
+                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(-d.x, -d.y)));
+                x[c + 1] = ptx::mul2(p[c + 1], ptx::add2(x[c + 1], make_float2(-d.z, -d.w)));
+                if constexpr (!BF16) {
+                    x[c] = ptx::mul2(x[c], make_float2(pds, pds));
+                    x[c + 1] = ptx::mul2(x[c + 1], make_float2(pds, pds));
                 }
             }
-            ptx::tmem_st32(tDp + lanes + wg * 64, w);
-            ptx::tmem_st_wait();
+            tmem_store<BF16>(tDp + lanes + wg * 32, x);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -580,11 +596,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (n > 0 && ok) ok = wait(&sb.acc, 0);
         if (ok) {
             ptx::tc_fence_after();
-            // warpgroup 0 stores dv, warpgroup 1 dk
-            const long long *sg = wg ? a.sdk : a.sdv;
-            uint16_t *out = static_cast<uint16_t *>(wg ? a.dk : a.dv) + tb * sg[0] + (s.k0 + j) * sg[1] + h * sg[2];
-            const float f = wg ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
-            store_row<DP, BF16>((wg ? tDk : tDv) + lanes, f, n == 0, j < s.lk, out, a.dim);
+            // warpgroups 0 and 1 store dv, 2 and 3 dk, half of the columns each
+            const bool isk = wg >= 2;
+            const int c0 = (wg & 1) * (DP / 2);
+            const long long *sg = isk ? a.sdk : a.sdv;
+            uint16_t *out = static_cast<uint16_t *>(isk ? a.dk : a.dv) + tb * sg[0] + (s.k0 + j) * sg[1] + h * sg[2] + c0;
+            const float f = isk ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
+            store_row<DP / 2, BF16>((isk ? tDk : tDv) + lanes + c0, f, n == 0, j < s.lk, out, a.dim - c0);
         }
     }
     ptx::tc_fence_before();
@@ -627,9 +645,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at_init_bars(sb.b_full, kVStages, 1);
         at_init_bars(sb.b_empty, kVStages, 1);
         at_init_bars(&sb.s_full, 1, 1);
-        at_init_bars(&sb.p_ready, 1, 8);
+        at_init_bars(&sb.p_ready, 1, kAtWarps);
         at_init_bars(sb.dp_full, 2, 1);
-        at_init_bars(&sb.ds_ready, 1, 8);
+        at_init_bars(&sb.ds_ready, 1, kAtWarps);
         at_init_bars(&sb.fix, 3, 1);
         sb.abort_flag = 0;
         ptx::fence_mbar_init();
@@ -712,6 +730,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (lane == 0 && n > 0) {
             constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
             constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
+            const int steps = (a.dim + 15) / 16;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
                 ptx::tc_fence_after();
@@ -722,10 +741,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             // runs while the other's dS waits for its product
             auto scores = [&](int it) {
                 if (!wait(&sb.a_full[it % kKStages], (uint32_t)(it / kKStages))) return false;
-                mma_rows(tS, sQ, sK + (it % kKStages) * TILE, a.dim, id_s);
+                mma_rows<DP>(tS, sQ, sK + (it % kKStages) * TILE, steps, id_s);
                 ptx::mma_commit(ptx::smem_u32(&sb.s_full));
                 if (!wait(&sb.b_full[it % kVStages], (uint32_t)(it / kVStages))) return false;
-                mma_rows(tDp + (it & 1) * 128, sDo, sV + (it % kVStages) * TILE, a.dim, id_s);
+                mma_rows<DP>(tDp + (it & 1) * 128, sDo, sV + (it % kVStages) * TILE, steps, id_s);
                 ptx::mma_commit(ptx::smem_u32(&sb.dp_full[it & 1]));
                 ptx::mma_commit(ptx::smem_u32(&sb.b_empty[it % kVStages]));
                 return true;
@@ -761,51 +780,40 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return __all_sync(0xffffffffu, w);
         };
         for (int it = 0; it < n; ++it) {
-            float p[64];
+            float2 p[16];
             if (!(ok = wait(&sb.s_full, (uint32_t)it))) break;
             ptx::tc_fence_after();
-            {
-                float x[32], y[32];
-                ptx::tmem_ld32(tS + lanes + wg * 64, x);
-                ptx::tmem_ld32(tS + lanes + wg * 64 + 32, y);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 32; ++c) p[c] = x[c], p[32 + c] = y[c];
-            }
+            tmem_load(tS + lanes + wg * 32, p);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
 #pragma unroll
-            for (int c = 0; c < 64; ++c) p[c] = ptx::ex2(fmaf(p[c], cs, -lse));
+            for (int c = 0; c < 16; ++c) {
+                p[c] = ptx::fma2(p[c], make_float2(cs, cs), make_float2(-lse, -lse));
+                p[c] = make_float2(ptx::ex2(p[c].x), ptx::ex2(p[c].y));
+            }
             const int kb = it * kT;
             if (kb + kT > s.lk || (a.causal && kb + kT - 1 > q0 + off)) {
                 int lim = s.lk - kb;  // columns from it on are masked
                 if (a.causal) lim = min(lim, i + off - kb + 1);
-                lim -= wg * 64;
+                lim -= wg * 32;
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (c >= lim) p[c] = 0.f;
+                for (int c = 0; c < 16; ++c) {
+                    if (2 * c >= lim) p[c].x = 0.f;
+                    if (2 * c + 1 >= lim) p[c].y = 0.f;
+                }
             }
             if (!(ok = wait(&sb.dp_full[it & 1], (uint32_t)(it / 2)))) break;
             ptx::tc_fence_after();
-            const uint32_t td = tDp + (it & 1) * 128 + lanes + wg * 64;
-            float w[32];
+            const uint32_t td = tDp + (it & 1) * 128 + lanes + wg * 32;
+            float2 x[16];
+            tmem_load(td, x);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[32];
-                ptx::tmem_ld32(td + half * 32, x);
-                ptx::tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    x[c] = p[half * 32 + c] * (x[c] - dsum);
-                    if constexpr (!BF16) x[c] *= pds;
-                }
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    w[half * 16 + c] = __uint_as_float(pack2<BF16>(x[2 * c], x[2 * c + 1]));
+            for (int c = 0; c < 16; ++c) {
+                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(-dsum, -dsum)));
+                if constexpr (!BF16) x[c] = ptx::mul2(x[c], make_float2(pds, pds));
             }
-            ptx::tmem_st32(td, w);
-            ptx::tmem_st_wait();
+            tmem_store<BF16>(td, x);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready));
@@ -813,10 +821,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (n > 0 && ok) ok = wait(&sb.acc, 0);
         if (ok) {
             ptx::tc_fence_after();
-            // each warpgroup stores half of the columns
-            const int c0 = wg * (DP / 2);
+            // each warpgroup stores a quarter of the columns
+            const int c0 = wg * (DP / 4);
             uint16_t *out = static_cast<uint16_t *>(a.dq) + tb * a.sdq[0] + (s.q0 + i) * a.sdq[1] + h * a.sdq[2] + c0;
-            store_row<DP / 2, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < s.lq, out, a.dim - c0);
+            store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < s.lq, out, a.dim - c0);
         }
     }
     ptx::tc_fence_before();
