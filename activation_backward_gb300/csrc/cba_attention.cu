@@ -60,16 +60,16 @@ struct AtArgs {
     int causal, tiles, tile_slow;
     float scale;
     const float *lse;
-    float *lse2, *dsum;          // [head][padded rows] (dense: [batch][head][padded rows])
+    float *nlse, *ndsum;         // -lse / ln 2 and -D, [head][padded rows] (dense: [batch][head][padded rows])
     long long head_rows;         // padded rows of a head (dense: of a batch's head)
     unsigned *status, *maxima;   // maxima: bits of max |do|^2, max |v|^2 over rows (f16)
-    const void *o, *dout, *v;
+    const void *q, *o, *dout, *v;
     void *dq, *dk, *dv;
-    long long so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
+    long long sq[3], so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
 };
 
 // The sequence b: its first query and key token, its lengths, and the first
-// padded row of its lse2 / dsum.  Values of cu are clamped into the tensors, so
+// padded row of its statistics.  Values of cu are clamped into the tensors, so
 // that wrong ones give wrong results but no access out of bounds.
 struct AtSeq {
     long long q0, k0, row0;
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
                     if (lane == 0) {
                         // a row whose keys are all masked has lse = -inf: P = 0 too
                         const long long at = row0 + r0 + j * RPP;
-                        a.lse2[at] = l[j] == -INFINITY ? INFINITY : l[j] * kLog2e - (BF16 ? 0.f : kPShift);
-                        a.dsum[at] = d;
+                        a.nlse[at] = l[j] == -INFINITY ? -INFINITY : (BF16 ? 0.f : kPShift) - l[j] * kLog2e;
+                        a.ndsum[at] = -d;
                     }
                 }
             }
@@ -225,8 +225,8 @@ struct AtBars {
     uint64_t stat;                     // the block's own two tiles
     uint64_t a_full[NA], a_empty[NA];  // the ring used by the accumulating product
     uint64_t b_full[NB], b_empty[NB];
-    uint64_t r_full[2], r_empty[2];    // row statistics (kv kernel)
-    uint64_t s_full, p_ready;
+    uint64_t r_full[4], r_empty[4];    // row statistics (kv kernel)
+    uint64_t s_full[2], p_ready;
     uint64_t dp_full[2], ds_ready;
     uint64_t fix, acc, drain;
     uint32_t tmem_base;
@@ -275,34 +275,48 @@ __device__ __forceinline__ bool load_tile(uint32_t dst, const CUtensorMap *tm, l
 // boxes.  (A descriptor counts 16-byte units: steps are additions to it.)
 template <int DP>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb, int steps,
-                                         uint32_t idesc) {
+                                         uint32_t idesc, uint64_t *done, uint64_t *done2 = nullptr) {
     const uint64_t da = ptx::smem_desc(sa, 16, 1024, 2), db = ptx::smem_desc(sb, 16, 1024, 2);
+    if (ptx::elect_one()) {
+        auto step = [&](int ks) {
+            const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
+            ptx::mma_f16(d, da + off, db + off, idesc, ks > 0);
+        };
+        if (steps == DP / 16) {  // a condition in each step doubles its issue time
 #pragma unroll
-    for (int ks = 0; ks < DP / 16; ++ks) {
-        const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
-        if (ks < steps) ptx::mma_f16(d, da + off, db + off, idesc, ks > 0);
+            for (int ks = 0; ks < DP / 16; ++ks) step(ks);
+        } else {
+            for (int ks = 0; ks < steps; ++ks) step(ks);
+        }
+        ptx::mma_commit(ptx::smem_u32(done));
+        if (done2) ptx::mma_commit(ptx::smem_u32(done2));
     }
+    __syncwarp();
 }
 
 // D[128 x DP] (+)= A[128 x 128] B[128 x DP]: A in TMEM (16-bit; the 16 words of
 // each 32 columns at ta, ta + 32, ...), B's rows contracted over.
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t ta, uint32_t sb, uint32_t idesc,
-                                        bool accumulate) {
+                                        bool accumulate, uint64_t *done) {
     const uint64_t db = ptx::smem_desc(sb, kBoxBytes, 1024, 2);
+    if (ptx::elect_one()) {
 #pragma unroll
-    for (int ks = 0; ks < kT / 16; ++ks)
-        ptx::mma_f16_ts(d, ta + (ks >> 1) * 32 + (ks & 1) * 8, db + ks * (2048 >> 4), idesc,
-                        accumulate || ks > 0);
+        for (int ks = 0; ks < kT / 16; ++ks)
+            ptx::mma_f16_ts(d, ta + (ks >> 1) * 32 + (ks & 1) * 8, db + ks * (2048 >> 4), idesc,
+                            accumulate || ks > 0);
+        ptx::mma_commit(ptx::smem_u32(done));
+    }
+    __syncwarp();
 }
 
-// 2^(x cs - l) of 32 columns with an l of their own each.
-__device__ __forceinline__ void probabilities(float2 (&p)[16], float cs, const float *lse) {
+// 2^(x cs + nlse) of 32 columns with an nlse of their own each.
+__device__ __forceinline__ void probabilities(float2 (&p)[16], float cs, const float *nlse) {
     const float2 c2 = make_float2(cs, cs);
 #pragma unroll
     for (int c = 0; c < 16; c += 2) {
-        const float4 l = *reinterpret_cast<const float4 *>(lse + 2 * c);
-        p[c] = ptx::fma2(p[c], c2, make_float2(-l.x, -l.y));
-        p[c + 1] = ptx::fma2(p[c + 1], c2, make_float2(-l.z, -l.w));
+        const float4 l = *reinterpret_cast<const float4 *>(nlse + 2 * c);
+        p[c] = ptx::fma2(p[c], c2, make_float2(l.x, l.y));
+        p[c + 1] = ptx::fma2(p[c + 1], c2, make_float2(l.z, l.w));
     }
 #pragma unroll
     for (int c = 0; c < 16; ++c) p[c] = make_float2(ptx::ex2(p[c].x), ptx::ex2(p[c].y));
@@ -355,15 +369,49 @@ __device__ __forceinline__ void at_init_bars(uint64_t *first, int n, uint32_t co
     for (int i = 0; i < n; ++i) ptx::mbar_init(ptx::smem_u32(first + i), count);
 }
 
+// The MMA warp's wait for up to three barriers at once, some lanes on each: a wait
+// takes ~150 cycles even when its phase is over, in which no MMA is issued.
+struct AtWait {
+    uint64_t *bar;
+    uint32_t parity;
+};
+__device__ __forceinline__ bool wait_all(AtWait x, AtWait y, AtWait z, volatile int *abort, unsigned *status) {
+    const int lane = threadIdx.x & 31;
+    const AtWait w = lane < 10 ? x : lane < 20 ? y : z;
+    const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(w.bar), w.parity & 1u, abort, status, kAtLimitNs);
+    ptx::tc_fence_after();
+    return __all_sync(0xffffffffu, r) != 0;
+}
+
+// The end of the MMA warp's loop: the accumulators are handed over, and every
+// MMA issued has finished before TMEM is released.
+template <typename Bars>
+__device__ __forceinline__ void finish_mmas(bool ok, Bars &sb, unsigned *status) {
+    if (ptx::elect_one()) {
+        if (ok) ptx::mma_commit(ptx::smem_u32(&sb.acc));
+        else *reinterpret_cast<volatile int *>(&sb.abort_flag) = 1;
+        ptx::mma_commit(ptx::smem_u32(&sb.drain));
+    }
+    __syncwarp();
+    int no = 0;
+    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, status, kAtLimitNs);
+    __syncwarp();
+}
+
 // ---- dk, dv: one tile of keys, its queries in turn
 
-constexpr int kQStages = 3, kDoStages = 2;
-using KvBars = AtBars<kQStages, kDoStages>;
-
+// At dim 64 and less TMEM has room for two S tiles: S of the tile after next is
+// computed once dv has used P, so that the compute warps find the next S ready.
+// At larger dims S(i + 1) overwrites P(i) and the warps wait for it.
 template <int DP>
-constexpr uint32_t kv_smem_bytes() {
-    return (2 + kQStages + kDoStages) * (DP / 64) * kBoxBytes + 2 * 1024 + sizeof(KvBars);
-}
+struct Kv {
+    static constexpr int NS = DP == 64 ? 2 : 1;               // S buffers
+    // stages of q, of do, of the row statistics (dim 128 fills shared memory)
+    static constexpr int QST = DP == 64 ? 4 : 3, DOST = DP == 64 ? 4 : 2, RST = DP == 64 ? 4 : 2;
+    using Bars = AtBars<QST, DOST>;
+    static constexpr uint32_t TILES = (2 + QST + DOST) * (DP / 64) * kBoxBytes;
+    static constexpr uint32_t SMEM = TILES + RST * 1024 + sizeof(Bars);
+};
 
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kAtThreads, 1)
@@ -372,10 +420,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                    const AtArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t TILE = DP / 64 * kBoxBytes;
+    constexpr int NS = Kv<DP>::NS, kQStages = Kv<DP>::QST, kDoStages = Kv<DP>::DOST, kRStages = Kv<DP>::RST;
     const uint32_t sbase = ptx::smem_u32(smem);
     const uint32_t sK = sbase, sV = sK + TILE, sQ = sV + TILE, sDo = sQ + kQStages * TILE;
-    float *rows = reinterpret_cast<float *>(smem + (2 + kQStages + kDoStages) * TILE);
-    KvBars &sb = *reinterpret_cast<KvBars *>(smem + (2 + kQStages + kDoStages) * TILE + 2048);
+    float *rows = reinterpret_cast<float *>(smem + Kv<DP>::TILES);
+    auto &sb = *reinterpret_cast<typename Kv<DP>::Bars *>(smem + Kv<DP>::TILES + kRStages * 1024);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (sbase & 1023) {  // the swizzled tiles need it
         if (tid == 0) atomicOr(a.status, kStatusTimeout);
@@ -387,9 +436,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at_init_bars(sb.a_empty, kQStages, 1);
         at_init_bars(sb.b_full, kDoStages, 1);
         at_init_bars(sb.b_empty, kDoStages, 1);
-        at_init_bars(sb.r_full, 2, 1);
-        at_init_bars(sb.r_empty, 2, kAtWarps);
-        at_init_bars(&sb.s_full, 1, 1);
+        at_init_bars(sb.r_full, kRStages, 1);
+        at_init_bars(sb.r_empty, kRStages, kAtWarps);
+        at_init_bars(sb.s_full, 2, 1);
         at_init_bars(&sb.p_ready, 1, kAtWarps);
         at_init_bars(sb.dp_full, 2, 1);
         at_init_bars(&sb.ds_ready, 1, kAtWarps);
@@ -405,7 +454,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sb.tmem_base;
-    ptx::griddep_wait();  // lse2, dsum and the maxima come from the kernel before
+    ptx::griddep_wait();  // the row statistics and the maxima come from the kernel before
     ptx::griddep_launch_dependents();
 
     // this block's tile
@@ -425,7 +474,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int nq = qt_end - qt_begin;
     const bool live_tile = k0 < s.lk;
     const int n = live_tile ? nq * a.group : 0;
-    const uint32_t tS = tmem, tDp = tmem + 128, tDv = tmem + 256, tDk = tmem + 256 + DP;
+    const uint32_t tS = tmem, tDp = tmem + NS * 128, tDv = tDp + 128, tDk = tDv + DP;
     volatile int *ab = &sb.abort_flag;
     const int tb = a.cu_q ? 0 : b;  // the tensor maps' batch index
 
@@ -446,7 +495,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             int it = 0;
             for (; ok && it < n; ++it) {
                 const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, hq = h * a.group + g;
-                const int st = it % kQStages, sd = it % kDoStages, sr = it & 1;
+                const int st = it % kQStages, sd = it % kDoStages, sr = it % kRStages;
                 if (it >= kQStages)
                     ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_empty[st]),
                                                 (uint32_t)(it / kQStages - 1) & 1u, ab, a.status, kAtLimitNs);
@@ -455,8 +504,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int valid = min(kT, s.lq - q0);
                 ok = load_tile<DP>(sQ + st * TILE, &tq, s.q0 + q0, hq, tb, valid, a.cu_q != nullptr,
                                    ptx::smem_u32(&sb.a_full[st]), bfix, fphase, 0, ab, a.status);
-                if (ok && it >= 2)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_empty[sr]), (uint32_t)(it / 2 - 1) & 1u,
+                if (ok && it >= kRStages)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_empty[sr]), (uint32_t)(it / kRStages - 1) & 1u,
                                                 ab, a.status, kAtLimitNs);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -464,8 +513,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const uint32_t bar = ptx::smem_u32(&sb.r_full[sr]);
                     const long long r0 = s.row0 + (long long)hq * a.head_rows + q0;
                     ptx::mbar_arrive_expect_tx(bar, 2 * kT * 4);
-                    ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT), a.lse2 + r0, kT * 4, bar);
-                    ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT + kT), a.dsum + r0, kT * 4, bar);
+                    ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT), a.nlse + r0, kT * 4, bar);
+                    ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT + kT), a.ndsum + r0, kT * 4, bar);
                 }
                 if (it >= kDoStages)
                     ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_empty[sd]),
@@ -486,58 +535,46 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 for (int v = max(0, it - kDoStages); v <= it && v < n; ++v)
                     ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_full[v % kDoStages]),
                                            (uint32_t)(v / kDoStages) & 1u, &no, a.status, kAtLimitNs / 8);
-                for (int v = max(0, it - 2); v <= it && v < n; ++v)
-                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_full[v & 1]), (uint32_t)(v / 2) & 1u, &no,
+                for (int v = max(0, it - kRStages); v <= it && v < n; ++v)
+                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_full[v % kRStages]), (uint32_t)(v / kRStages) & 1u, &no,
                                            a.status, kAtLimitNs / 8);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && n > 0) {
+        // The whole warp walks the loop and one elected lane issues: descriptors and
+        // counters are then uniform over the warp, and an MMA takes a few cycles to
+        // issue instead of ~100 (more than the 64 that one of 128 columns runs).
+        if (n > 0) {
             constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
             constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
             const int steps = (a.dim + 15) / 16;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
-                ptx::tc_fence_after();
-                return r;
+            auto wait = [&](AtWait x, AtWait y, AtWait z) { return wait_all(x, y, z, ab, a.status); };
+            auto mma_s = [&](int it) {
+                mma_rows<DP>(tS + it % NS * 128, sK, sQ + (it % kQStages) * TILE, steps, id_s, &sb.s_full[it & 1]);
             };
-            bool ok = wait(&sb.stat, 0) && wait(&sb.a_full[0], 0);
-            if (ok) {
-                mma_rows<DP>(tS, sK, sQ, steps, id_s);
-                ptx::mma_commit(ptx::smem_u32(&sb.s_full));
-                ok = wait(&sb.b_full[0], 0);
-            }
-            if (ok) {
-                mma_rows<DP>(tDp, sV, sDo, steps, id_s);
-                ptx::mma_commit(ptx::smem_u32(&sb.dp_full[0]));
-            }
+            auto mma_dp = [&](int it) {
+                mma_rows<DP>(tDp, sV, sDo + (it % kDoStages) * TILE, steps, id_s, &sb.dp_full[0]);
+            };
+            auto full_q = [&](int it) { return AtWait{&sb.a_full[it % kQStages], (uint32_t)(it / kQStages)}; };
+            auto full_do = [&](int it) { return AtWait{&sb.b_full[it % kDoStages], (uint32_t)(it / kDoStages)}; };
+            const AtWait stat{&sb.stat, 0};
+            bool ok = wait(stat, full_q(0), n > 1 ? full_q(NS - 1) : stat);
+            if (ok) mma_s(0);
+            if (ok && NS == 2 && n > 1) mma_s(1);
+            ok = ok && wait(stat, stat, full_do(0));
+            if (ok) mma_dp(0);
             for (int it = 0; ok && it < n; ++it) {
-                const int st = it % kQStages, sd = it % kDoStages;
-                const int nx = it + 1;
-                if (!(ok = wait(&sb.p_ready, (uint32_t)it))) break;
-                mma_acc(tDv, tS, sDo + sd * TILE, id_a, it > 0);
-                ptx::mma_commit(ptx::smem_u32(&sb.b_empty[sd]));
-                if (nx < n) {
-                    // S overwrites P: this thread's MMAs run in the order of issue
-                    if (!(ok = wait(&sb.a_full[nx % kQStages], (uint32_t)(nx / kQStages)))) break;
-                    mma_rows<DP>(tS, sK, sQ + (nx % kQStages) * TILE, steps, id_s);
-                    ptx::mma_commit(ptx::smem_u32(&sb.s_full));
-                }
-                if (!(ok = wait(&sb.ds_ready, (uint32_t)it))) break;
-                mma_acc(tDk, tDp, sQ + st * TILE, id_a, it > 0);
-                ptx::mma_commit(ptx::smem_u32(&sb.a_empty[st]));
-                if (nx < n) {
-                    if (!(ok = wait(&sb.b_full[nx % kDoStages], (uint32_t)(nx / kDoStages)))) break;
-                    mma_rows<DP>(tDp, sV, sDo + (nx % kDoStages) * TILE, steps, id_s);
-                    ptx::mma_commit(ptx::smem_u32(&sb.dp_full[0]));
-                }
+                const int ns = it + NS, nd = it + 1;  // the next tiles of S and of dP
+                const AtWait pr{&sb.p_ready, (uint32_t)it}, dr{&sb.ds_ready, (uint32_t)it};
+                if (!(ok = wait(pr, pr, ns < n ? full_q(ns) : pr))) break;
+                mma_acc(tDv, tS + it % NS * 128, sDo + (it % kDoStages) * TILE, id_a, it > 0, &sb.b_empty[it % kDoStages]);
+                // S overwrites P, dP overwrites dS: this thread's MMAs run in the order of issue
+                if (ns < n) mma_s(ns);
+                if (!(ok = wait(dr, dr, nd < n ? full_do(nd) : dr))) break;
+                mma_acc(tDk, tDp, sQ + (it % kQStages) * TILE, id_a, it > 0, &sb.a_empty[it % kQStages]);
+                if (nd < n) mma_dp(nd);
             }
-            if (ok) ptx::mma_commit(ptx::smem_u32(&sb.acc));
-            else *ab = 1;
-            // every MMA issued has finished before TMEM is released
-            ptx::mma_commit(ptx::smem_u32(&sb.drain));
-            int no = 0;
-            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kAtLimitNs);
+            finish_mmas(ok, sb, a.status);
         }
     } else if (warp >= 4 && live_tile) {
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
@@ -552,13 +589,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return __all_sync(0xffffffffu, r);
         };
         for (int it = 0; it < n; ++it) {
-            const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, sr = it & 1;
-            const float *lse = rows + sr * 2 * kT + wg * 32, *ds = lse + kT;
+            const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, sr = it % kRStages;
+            const float *nl = rows + sr * 2 * kT + wg * 32, *nd = nl + kT;
             float2 p[16];
-            if (!(ok = wait(&sb.r_full[sr], (uint32_t)(it / 2)) && wait(&sb.s_full, (uint32_t)it))) break;
+            if (!(ok = wait(&sb.r_full[sr], (uint32_t)(it / kRStages)) && wait(&sb.s_full[it & 1], (uint32_t)(it / 2)))) break;
             ptx::tc_fence_after();
-            tmem_load(tS + lanes + wg * 32, p);
-            probabilities(p, cs, lse);
+            const uint32_t ts = tS + it % NS * 128 + lanes + wg * 32;
+            tmem_load(ts, p);
+            probabilities(p, cs, nl);
             if (a.causal && k0 + kT - 1 > q0 + off) {
                 const int first = j - off - q0 - wg * 32;  // columns before it do not see key j
 #pragma unroll
@@ -567,7 +605,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (2 * c + 1 < first) p[c].y = 0.f;
                 }
             }
-            tmem_store<BF16>(tS + lanes + wg * 32, p);
+            tmem_store<BF16>(ts, p);
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
@@ -577,9 +615,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             tmem_load(tDp + lanes + wg * 32, x);
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-                const float4 d = *reinterpret_cast<const float4 *>(ds + 2 * c);
-                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(-d.x, -d.y)));
-                x[c + 1] = ptx::mul2(p[c + 1], ptx::add2(x[c + 1], make_float2(-d.z, -d.w)));
+                const float4 d = *reinterpret_cast<const float4 *>(nd + 2 * c);
+                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(d.x, d.y)));
+                x[c + 1] = ptx::mul2(p[c + 1], ptx::add2(x[c + 1], make_float2(d.z, d.w)));
                 if constexpr (!BF16) {
                     x[c] = ptx::mul2(x[c], make_float2(pds, pds));
                     x[c + 1] = ptx::mul2(x[c + 1], make_float2(pds, pds));
@@ -615,36 +653,78 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
 // ---- dq: one tile of queries, its keys in turn
 
-constexpr int kKStages = 3, kVStages = 2;
+// The block's q and do rows are A operands of every tile's products, so they lie
+// in TMEM (16-bit, 32 or 64 columns each): the products then read one operand
+// from shared memory instead of two, whose 128 bytes per cycle are what an MMA
+// of 128 columns with both operands there waits for (81 against 55 cycles each,
+// dq of 1x8192 h32/8 d128 758 against 628 us).  At dim 128 that leaves room for one dP,
+// below it for two, of which one is computed while the other's dS is used.
+constexpr int kKStages = 4, kVStages = 3;
 using QBars = AtBars<kKStages, kVStages>;
 
 template <int DP>
 constexpr uint32_t q_smem_bytes() {
-    return (2 + kKStages + kVStages) * (DP / 64) * kBoxBytes + sizeof(QBars);
+    return (kKStages + kVStages) * (DP / 64) * kBoxBytes + sizeof(QBars);
+}
+
+// D[128 x 128] = A[128 x dim] B[128 x dim]^T, A in TMEM.
+template <int DP>
+__device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t ta, uint32_t sb, int steps, uint32_t idesc,
+                                            uint64_t *done, uint64_t *done2 = nullptr) {
+    const uint64_t db = ptx::smem_desc(sb, 16, 1024, 2);
+    if (ptx::elect_one()) {
+        auto step = [&](int ks) {
+            ptx::mma_f16_ts(d, ta + ks * 8, db + (((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4), idesc, ks > 0);
+        };
+        if (steps == DP / 16) {
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) step(ks);
+        } else {
+            for (int ks = 0; ks < steps; ++ks) step(ks);
+        }
+        ptx::mma_commit(ptx::smem_u32(done));
+        if (done2) ptx::mma_commit(ptx::smem_u32(done2));
+    }
+    __syncwarp();
+}
+
+// WORDS 32-bit words (pairs of elements) of a row into TMEM; zeros past `dim`.
+template <int WORDS>
+__device__ __forceinline__ void row_to_tmem(uint32_t t, const uint16_t *row, bool live, int dim, int first) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < WORDS; j += 4) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (live && 2 * (first + j) < dim) v = *reinterpret_cast<const uint4 *>(row + 2 * (first + j));
+        w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
+    }
+    __syncwarp();
+    if constexpr (WORDS == 16) ptx::tmem_st16(t + first, w);
+    else ptx::tmem_st8(t + first, w);
 }
 
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kAtThreads, 1)
-    attn_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
+    attn_q_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                   const AtArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t TILE = DP / 64 * kBoxBytes;
     const uint32_t sbase = ptx::smem_u32(smem);
-    const uint32_t sQ = sbase, sDo = sQ + TILE, sK = sDo + TILE, sV = sK + kKStages * TILE;
-    QBars &sb = *reinterpret_cast<QBars *>(smem + (2 + kKStages + kVStages) * TILE);
+    constexpr int NB = DP == 64 ? 2 : 1;  // dP buffers
+    const uint32_t sK = sbase, sV = sK + kKStages * TILE;
+    QBars &sb = *reinterpret_cast<QBars *>(smem + (kKStages + kVStages) * TILE);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (sbase & 1023) {
         if (tid == 0) atomicOr(a.status, kStatusTimeout);
         return;
     }
     if (tid == 0) {
-        at_init_bars(&sb.stat, 1, 1);
+        at_init_bars(&sb.stat, 1, kAtWarps);  // the rows in TMEM
         at_init_bars(sb.a_full, kKStages, 1);
         at_init_bars(sb.a_empty, kKStages, 1);
         at_init_bars(sb.b_full, kVStages, 1);
         at_init_bars(sb.b_empty, kVStages, 1);
-        at_init_bars(&sb.s_full, 1, 1);
+        at_init_bars(sb.s_full, 2, 1);
         at_init_bars(&sb.p_ready, 1, kAtWarps);
         at_init_bars(sb.dp_full, 2, 1);
         at_init_bars(&sb.ds_ready, 1, kAtWarps);
@@ -678,7 +758,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int last = min(q0 + kT, s.lq) - 1 + off;  // the last key any of its queries sees
         n = last < 0 ? 0 : min(n, last / kT + 1);
     }
-    const uint32_t tS = tmem, tDp = tmem + 128, tDq = tmem + 384;
+    const uint32_t tS = tmem, tDp = tmem + 128, tDq = tDp + NB * 128, tQ = tDq + DP, tDo = tQ + DP / 2;
     volatile int *ab = &sb.abort_flag;
     const int tb = a.cu_q ? 0 : b;
 
@@ -686,15 +766,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         if (n > 0) {
             uint32_t fphase = 0;
             const uint32_t bfix = ptx::smem_u32(&sb.fix);
-            if (lane == 0) {
-                const uint32_t bar = ptx::smem_u32(&sb.stat);
-                ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
-#pragma unroll
-                for (int j = 0; j < DP / 64; ++j) {
-                    ptx::tma_load_4d(sQ + j * kBoxBytes, &tq, j * 64, (int)s.q0 + q0, h, tb, bar);
-                    ptx::tma_load_4d(sDo + j * kBoxBytes, &tdo, j * 64, (int)s.q0 + q0, h, tb, bar);
-                }
-            }
             bool ok = true;
             int it = 0;
             for (; ok && it < n; ++it) {
@@ -717,7 +788,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             if (!ok) {
                 int no = 0;
-                ptx::mbar_wait_bounded(ptx::smem_u32(&sb.stat), 0, &no, a.status, kAtLimitNs);
                 for (int v = max(0, it - kKStages); v <= it && v < n; ++v)
                     ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_full[v % kKStages]),
                                            (uint32_t)(v / kKStages) & 1u, &no, a.status, kAtLimitNs / 8);
@@ -727,50 +797,47 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && n > 0) {
+        // The whole warp walks the loop and one elected lane issues: descriptors and
+        // counters are then uniform over the warp, and an MMA takes a few cycles to
+        // issue instead of ~100 (more than the 64 that one of 128 columns runs).
+        if (n > 0) {
             constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
             constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
             const int steps = (a.dim + 15) / 16;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
-                ptx::tc_fence_after();
-                return r;
+            auto wait = [&](AtWait x, AtWait y, AtWait z) { return wait_all(x, y, z, ab, a.status); };
+            auto mma_s = [&](int it) {
+                mma_rows_ts<DP>(tS, tQ, sK + (it % kKStages) * TILE, steps, id_s, &sb.s_full[it & 1]);
             };
-            bool ok = wait(&sb.stat, 0);
-            // S and dP of tile it; dP alternates between two buffers, so that it
-            // runs while the other's dS waits for its product
-            auto scores = [&](int it) {
-                if (!wait(&sb.a_full[it % kKStages], (uint32_t)(it / kKStages))) return false;
-                mma_rows<DP>(tS, sQ, sK + (it % kKStages) * TILE, steps, id_s);
-                ptx::mma_commit(ptx::smem_u32(&sb.s_full));
-                if (!wait(&sb.b_full[it % kVStages], (uint32_t)(it / kVStages))) return false;
-                mma_rows<DP>(tDp + (it & 1) * 128, sDo, sV + (it % kVStages) * TILE, steps, id_s);
-                ptx::mma_commit(ptx::smem_u32(&sb.dp_full[it & 1]));
-                ptx::mma_commit(ptx::smem_u32(&sb.b_empty[it % kVStages]));
-                return true;
+            auto mma_dp = [&](int it) {
+                mma_rows_ts<DP>(tDp + it % NB * 128, tDo, sV + (it % kVStages) * TILE, steps, id_s,
+                                &sb.dp_full[it & 1], &sb.b_empty[it % kVStages]);
             };
-            if (ok) ok = scores(0);
+            auto full_k = [&](int it) { return AtWait{&sb.a_full[it % kKStages], (uint32_t)(it / kKStages)}; };
+            auto full_v = [&](int it) { return AtWait{&sb.b_full[it % kVStages], (uint32_t)(it / kVStages)}; };
+            bool ok = wait({&sb.stat, 0}, full_k(0), full_v(0));
+            if (ok) mma_s(0);
+            if (ok) mma_dp(0);
             for (int it = 0; ok && it < n; ++it) {
-                if (it + 1 < n) {
-                    if (!(ok = wait(&sb.p_ready, (uint32_t)it))) break;  // S(it) is in registers
-                    if (!(ok = scores(it + 1))) break;
-                }
-                if (!(ok = wait(&sb.ds_ready, (uint32_t)it))) break;
-                mma_acc(tDq, tDp + (it & 1) * 128, sK + (it % kKStages) * TILE, id_a, it > 0);
-                ptx::mma_commit(ptx::smem_u32(&sb.a_empty[it % kKStages]));
+                const int nx = it + 1;
+                const bool more = nx < n;
+                const AtWait pr{&sb.p_ready, (uint32_t)it}, dr{&sb.ds_ready, (uint32_t)it};  // pr: S is in registers
+                if (!(ok = wait(pr, more ? full_k(nx) : pr, more && NB == 2 ? full_v(nx) : pr))) break;
+                if (more) mma_s(nx);
+                if (NB == 2 && more) mma_dp(nx);
+                if (!(ok = wait(dr, dr, more && NB == 1 ? full_v(nx) : dr))) break;
+                mma_acc(tDq, tDp + it % NB * 128, sK + (it % kKStages) * TILE, id_a, it > 0,
+                        &sb.a_empty[it % kKStages]);
+                // with one buffer dP overwrites dS: this thread's MMAs run in the order of issue
+                if (NB == 1 && more) mma_dp(nx);
             }
-            if (ok) ptx::mma_commit(ptx::smem_u32(&sb.acc));
-            else *ab = 1;
-            ptx::mma_commit(ptx::smem_u32(&sb.drain));
-            int no = 0;
-            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kAtLimitNs);
+            finish_mmas(ok, sb, a.status);
         }
     } else if (warp >= 4 && live_tile) {
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const int r = quarter * 32 + lane, i = q0 + r;  // this thread's query
         const long long row = s.row0 + (long long)h * a.head_rows + i;
-        const float lse = __ldcg(a.lse2 + row), dsum = __ldcg(a.dsum + row);
+        const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row);
         const float cs = a.scale * kLog2e;
         const float sds = BF16 ? 1.f : ds_scale(a.maxima);
         const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);
@@ -779,9 +846,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const bool w = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
             return __all_sync(0xffffffffu, w);
         };
+        if (n > 0) {
+            constexpr int WORDS = DP / 8;  // of each tensor's DP / 2 words, per warpgroup
+            const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + tb * a.sq[0] + (s.q0 + i) * a.sq[1] + h * a.sq[2];
+            const uint16_t *drow = static_cast<const uint16_t *>(a.dout) + tb * a.sdo[0] + (s.q0 + i) * a.sdo[1] + h * a.sdo[2];
+            row_to_tmem<WORDS>(tQ + lanes, qrow, i < s.lq, a.dim, wg * WORDS);
+            row_to_tmem<WORDS>(tDo + lanes, drow, i < s.lq, a.dim, wg * WORDS);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.stat));
+        }
         for (int it = 0; it < n; ++it) {
             float2 p[16];
-            if (!(ok = wait(&sb.s_full, (uint32_t)it))) break;
+            if (!(ok = wait(&sb.s_full[it & 1], (uint32_t)(it / 2)))) break;
             ptx::tc_fence_after();
             tmem_load(tS + lanes + wg * 32, p);
             ptx::tc_fence_before();
@@ -789,7 +867,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                p[c] = ptx::fma2(p[c], make_float2(cs, cs), make_float2(-lse, -lse));
+                p[c] = ptx::fma2(p[c], make_float2(cs, cs), make_float2(nl, nl));
                 p[c] = make_float2(ptx::ex2(p[c].x), ptx::ex2(p[c].y));
             }
             const int kb = it * kT;
@@ -805,12 +883,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             if (!(ok = wait(&sb.dp_full[it & 1], (uint32_t)(it / 2)))) break;
             ptx::tc_fence_after();
-            const uint32_t td = tDp + (it & 1) * 128 + lanes + wg * 32;
+            const uint32_t td = tDp + it % NB * 128 + lanes + wg * 32;
             float2 x[16];
             tmem_load(td, x);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(-dsum, -dsum)));
+                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(nd, nd)));
                 if constexpr (!BF16) x[c] = ptx::mul2(x[c], make_float2(pds, pds));
             }
             tmem_store<BF16>(td, x);
@@ -843,7 +921,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 struct AtPlan {
     int dp, q_tiles, k_tiles;
     long long head_rows;   // padded rows of one head
-    size_t off_lse2, off_dsum, total;
+    size_t off_nlse, off_ndsum, total;
 };
 
 void fill_strides(const cba_attn_strides_t &s, int heads, int dim, long long len, long long *out) {
@@ -899,9 +977,9 @@ int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
     }
     const long long grid = std::max((long long)p->k_tiles * d->heads_kv, (long long)p->q_tiles * d->heads_q);
     if (grid * d->batch >= (1LL << 30) || rows >= (1LL << 40)) return CBA_ERR_UNSUPPORTED;
-    p->off_lse2 = 256;
-    p->off_dsum = p->off_lse2 + ((size_t)rows * 4 + 255) / 256 * 256;
-    p->total = p->off_dsum + ((size_t)rows * 4 + 255) / 256 * 256;
+    p->off_nlse = 256;
+    p->off_ndsum = p->off_nlse + ((size_t)rows * 4 + 255) / 256 * 256;
+    p->total = p->off_ndsum + ((size_t)rows * 4 + 255) / 256 * 256;
     return CBA_OK;
 }
 
@@ -929,7 +1007,7 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(attn_kv_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kv_smem_bytes<DP>());
+                             (int)Kv<DP>::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_q_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)q_smem_bytes<DP>());
@@ -937,17 +1015,17 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     if (p.k_tiles > 0) {
         a.tiles = p.k_tiles;
         e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)((long long)p.k_tiles * d.heads_kv * d.batch)),
-                       dim3(kAtThreads), kv_smem_bytes<DP>(), st, tm[0], tm[1], tm[2], tm[3], a);
+                       dim3(kAtThreads), Kv<DP>::SMEM, st, tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
     }
     if (p.q_tiles > 0) {
         a.tiles = p.q_tiles;
         // without keys there is no launch between this one and the preparation
         if (p.k_tiles > 0)
-            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(qgrid), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[0],
-                           tm[1], tm[2], tm[3], a);
+            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(qgrid), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[1],
+                           tm[2], a);
         else
-            attn_q_kernel<DP, BF16><<<qgrid, kAtThreads, q_smem_bytes<DP>(), st>>>(tm[0], tm[1], tm[2], tm[3], a);
+            attn_q_kernel<DP, BF16><<<qgrid, kAtThreads, q_smem_bytes<DP>(), st>>>(tm[1], tm[2], a);
         if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
@@ -993,12 +1071,12 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.lse = lse;
     a.status = static_cast<unsigned *>(workspace);
     a.maxima = a.status + 4;
-    a.lse2 = ws_at<float>(workspace, p.off_lse2);
-    a.dsum = ws_at<float>(workspace, p.off_dsum);
+    a.nlse = ws_at<float>(workspace, p.off_nlse);
+    a.ndsum = ws_at<float>(workspace, p.off_ndsum);
     a.head_rows = p.head_rows;
-    a.o = o; a.dout = dout; a.v = v; a.dq = dq; a.dk = dk; a.dv = dv;
-    long long sq[3], sk[3];
-    fill_strides(d->q, d->heads_q, d->dim, tq, sq);
+    a.q = q; a.o = o; a.dout = dout; a.v = v; a.dq = dq; a.dk = dk; a.dv = dv;
+    long long sk[3];
+    fill_strides(d->q, d->heads_q, d->dim, tq, a.sq);
     fill_strides(d->k, d->heads_kv, d->dim, tk, sk);
     fill_strides(d->v, d->heads_kv, d->dim, tk, a.sv);
     fill_strides(d->o, d->heads_q, d->dim, tq, a.so);
@@ -1009,7 +1087,7 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     // without queries (or keys) the main kernels load nothing of them
     CUtensorMap tm[4] = {};
     if (tq > 0 && tk > 0 &&
-        (!attn_map(&tm[0], q, *d, d->heads_q, tq, sq) || !attn_map(&tm[1], k, *d, d->heads_kv, tk, sk) ||
+        (!attn_map(&tm[0], q, *d, d->heads_q, tq, a.sq) || !attn_map(&tm[1], k, *d, d->heads_kv, tk, sk) ||
          !attn_map(&tm[2], v, *d, d->heads_kv, tk, a.sv) || !attn_map(&tm[3], dout, *d, d->heads_q, tq, a.sdo)))
         return CBA_ERR_UNSUPPORTED;
     cudaGetLastError();
