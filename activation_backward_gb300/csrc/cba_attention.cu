@@ -26,8 +26,8 @@
 // values stay clear of f16's subnormals and none can overflow.
 //
 // Roles of a block: warp 0 issues the TMA loads (and zeroes the rows of a
-// packed sequence's last tile that belong to its neighbour), warp 1 owns TMEM
-// and issues the MMAs, warps 4-19 compute P and dS (four warpgroups, 32 columns
+// packed sequence's last tile that belong to its neighbour) and hands out the
+// work, warp 1 owns TMEM and issues the MMAs, warps 4-19 compute P and dS (four warpgroups, 32 columns
 // of a tile each) and the epilogue.  Every wait is bounded (2 s); on a timeout
 // the block sets the workspace status bit, stops, waits (bounded) for its
 // copies in flight, frees its TMEM and returns.
@@ -47,6 +47,10 @@ namespace {
 constexpr uint64_t kAtLimitNs = 2000000000ull;
 constexpr int kAtThreads = 640;
 constexpr int kAtWarps = 16;                  // that compute P and dS
+// Registers per thread: 96 at launch (of 640 threads), then moved from the load
+// and MMA warps' warpgroup to the four that compute.
+constexpr int kCtlRegs = 64, kCompRegs = 104;
+static_assert(128 * kCtlRegs + 512 * kCompRegs <= 640 * 96);
 constexpr int kT = 128;                       // tile rows, of queries and of keys
 constexpr uint32_t kBoxBytes = kT * 128u;     // 128 rows x 64 16-bit elements
 constexpr float kLog2e = 1.4426950408889634f;
@@ -63,6 +67,8 @@ struct AtArgs {
     float *nlse, *ndsum;         // -lse / ln 2 and -D, [head][padded rows] (dense: [batch][head][padded rows])
     long long head_rows;         // padded rows of a head (dense: of a batch's head)
     unsigned *status, *maxima;   // maxima: bits of max |do|^2, max |v|^2 over rows (f16)
+    unsigned *next;              // work items handed out, of the two main kernels
+    int items;                   // this launch's
     const void *q, *o, *dout, *v;
     void *dq, *dk, *dv;
     long long sq[3], so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
@@ -136,7 +142,10 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         const int u = (int)blockIdx.x - v_blocks;
         const int tile = u % q_tiles, h = u / q_tiles % a.hq, b = u / q_tiles / a.hq;
         const AtSeq s = at_seq(a, b);
-        if (u == 0 && t == 0 && BF16) *a.status = 0;  // f16: cleared with the maxima before
+        if (u == 0 && t == 0) {
+            if (BF16) *a.status = 0;  // f16: cleared with the maxima before
+            a.next[0] = a.next[1] = 0;
+        }
         if (tile * kT < s.lq) {
             const long long row0 = s.row0 + (long long)h * a.head_rows + tile * kT;
             constexpr int RPP = 256 / LPR, NR = 4;  // rows per pass; rows of a thread in flight
@@ -220,15 +229,21 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
 
 // ---- shared pieces of the two main kernels
 
+// A barrier that the compute warps arrive on has two instances, used in turn,
+// where a warp can be a tile ahead of another (the next S or dP is computed
+// early): its arrival for the next tile must not count for this one.
 template <int NA, int NB>
 struct AtBars {
-    uint64_t stat;                     // the block's own two tiles
+    uint64_t stat;                     // the item's own two tiles
     uint64_t a_full[NA], a_empty[NA];  // the ring used by the accumulating product
     uint64_t b_full[NB], b_empty[NB];
     uint64_t r_full[4], r_empty[4];    // row statistics (kv kernel)
-    uint64_t s_full[2], p_ready;
-    uint64_t dp_full[2], ds_ready;
-    uint64_t fix, acc, drain;
+    uint64_t s_full[2], p_ready[2];
+    uint64_t dp_full[2], ds_ready[2];
+    uint64_t fix, drain, acc, stat_empty;
+    uint64_t acc_empty;                // the epilogue has read the accumulators
+    uint64_t i_full[2], i_empty[2];    // work items handed out
+    int item[2];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -242,13 +257,13 @@ struct AtBars {
 template <int DP>
 __device__ __forceinline__ bool load_tile(uint32_t dst, const CUtensorMap *tm, long long token,
                                           int head, int b, int valid, bool packed, uint32_t bar,
-                                          uint32_t fix, uint32_t &fix_phase, uint32_t extra,
-                                          volatile int *abort, unsigned *status) {
+                                          uint32_t fix, uint32_t &fix_phase, volatile int *abort,
+                                          unsigned *status) {
     const int lane = threadIdx.x & 31;
     const bool tail = packed && valid < kT;
     if (lane == 0) {
         const uint32_t on = tail ? fix : bar;
-        ptx::mbar_arrive_expect_tx(on, DP / 64 * kBoxBytes + (tail ? 0u : extra));
+        ptx::mbar_arrive_expect_tx(on, DP / 64 * kBoxBytes);
 #pragma unroll
         for (int j = 0; j < DP / 64; ++j)
             ptx::tma_load_4d(dst + j * kBoxBytes, tm, j * 64, (int)token, head, b, on);
@@ -265,7 +280,7 @@ __device__ __forceinline__ bool load_tile(uint32_t dst, const CUtensorMap *tm, l
                              : "memory");
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, extra);
+        if (lane == 0) ptx::mbar_arrive(bar);
     }
     __syncwarp();
     return true;
@@ -369,33 +384,120 @@ __device__ __forceinline__ void at_init_bars(uint64_t *first, int n, uint32_t co
     for (int i = 0; i < n; ++i) ptx::mbar_init(ptx::smem_u32(first + i), count);
 }
 
-// The MMA warp's wait for up to three barriers at once, some lanes on each: a wait
-// takes ~150 cycles even when its phase is over, in which no MMA is issued.
+// A ring's stage and the parity of its phase.
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void step(int stages) {
+        if (++s == stages) s = 0, ph ^= 1;
+    }
+};
+
+// The MMA warp's wait for two barriers at once, half of the lanes on each: a wait
+// takes ~150 cycles even when its phase is over, in which no MMA is issued.  (Two
+// warps that issue in turn hide that, but their MMAs then alternate between
+// accumulators and run at half the rate: kv 666 -> 975 us on 1x8192 h32/8 d128.)
 struct AtWait {
     uint64_t *bar;
     uint32_t parity;
 };
-__device__ __forceinline__ bool wait_all(AtWait x, AtWait y, AtWait z, volatile int *abort, unsigned *status) {
-    const int lane = threadIdx.x & 31;
-    const AtWait w = lane < 10 ? x : lane < 20 ? y : z;
+__device__ __forceinline__ bool wait_both(AtWait x, AtWait y, volatile int *abort, unsigned *status) {
+    const AtWait w = threadIdx.x & 1 ? y : x;
     const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(w.bar), w.parity & 1u, abort, status, kAtLimitNs);
     ptx::tc_fence_after();
     return __all_sync(0xffffffffu, r) != 0;
 }
 
-// The end of the MMA warp's loop: the accumulators are handed over, and every
-// MMA issued has finished before TMEM is released.
+// The end of the MMA warp's work: every MMA issued has finished before TMEM is
+// released.
 template <typename Bars>
 __device__ __forceinline__ void finish_mmas(bool ok, Bars &sb, unsigned *status) {
     if (ptx::elect_one()) {
-        if (ok) ptx::mma_commit(ptx::smem_u32(&sb.acc));
-        else *reinterpret_cast<volatile int *>(&sb.abort_flag) = 1;
+        if (!ok) *reinterpret_cast<volatile int *>(&sb.abort_flag) = 1;
         ptx::mma_commit(ptx::smem_u32(&sb.drain));
     }
     __syncwarp();
     int no = 0;
     ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, status, kAtLimitNs);
     __syncwarp();
+}
+
+// ---- work items
+
+// Both main kernels are persistent, one block per SM: a block takes its first
+// item by its index and the others from a counter, in the order of falling work
+// where the mask makes it fall.  The load warp takes the next item when it has
+// begun the last loads of one (earlier, and the items would be dealt out before
+// it is known who is done first); the loads and first products of the next item
+// then run under the last products and the epilogue of the one before (of
+// 32x676 h8 d64, six query tiles per item, more than half of a block's life was
+// its start and end when it had one item).
+
+// Load warp: hands item number k to the other warps.  False past the last item.
+template <typename Bars>
+__device__ __forceinline__ bool hand_out(const AtArgs &a, int k, int item, Bars &sb, bool &ok) {
+    if (k >= 2)
+        ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(&sb.i_empty[k & 1]), (uint32_t)(k / 2 - 1) & 1u,
+                                          &sb.abort_flag, a.status, kAtLimitNs);
+    ok = __all_sync(0xffffffffu, ok) != 0;
+    if (!ok) return false;
+    if ((threadIdx.x & 31) == 0) {
+        *const_cast<volatile int *>(&sb.item[k & 1]) = item;
+        ptx::mbar_arrive(ptx::smem_u32(&sb.i_full[k & 1]));
+    }
+    __syncwarp();
+    return item < a.items;
+}
+__device__ __forceinline__ int next_item(unsigned *next) {
+    unsigned v = 0;
+    if ((threadIdx.x & 31) == 0) v = atomicAdd(next, 1u);
+    return (int)gridDim.x + (int)__shfl_sync(0xffffffffu, v, 0);
+}
+
+// The k-th item of this block, or -1 past the last (or on a timeout).  Called by
+// whole warps.
+template <typename Bars>
+__device__ __forceinline__ int take_item(const AtArgs &a, int k, Bars &sb, bool &ok) {
+    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.i_full[k & 1]), (uint32_t)(k / 2) & 1u, &sb.abort_flag, a.status,
+                                kAtLimitNs);
+    ok = __all_sync(0xffffffffu, ok) != 0;
+    if (!ok) return -1;
+    const int item = *const_cast<volatile int *>(&sb.item[k & 1]);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.i_empty[k & 1]));
+    return item < a.items ? item : -1;
+}
+constexpr int kItemReaders = 1 + kAtWarps;  // the MMA and compute warps
+
+// The same number, computed with anew: what is derived from it after a long loop
+// is not kept in registers through it.
+__device__ __forceinline__ int afresh(int v) {
+    int r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Bars of one pipeline stage's ring: initialised by one thread.
+template <typename Bars>
+__device__ __forceinline__ void init_common(Bars &sb) {
+    at_init_bars(sb.s_full, 2, 1);
+    at_init_bars(sb.p_ready, 2, kAtWarps);
+    at_init_bars(sb.dp_full, 2, 1);
+    at_init_bars(sb.ds_ready, 2, kAtWarps);
+    at_init_bars(&sb.fix, 4, 1);  // fix, drain, acc, stat_empty
+    at_init_bars(&sb.acc_empty, 1, kAtWarps);
+    at_init_bars(sb.i_full, 2, 1);
+    at_init_bars(sb.i_empty, 2, kItemReaders);
+    sb.abort_flag = 0;
+}
+
+// After a timeout the load warp waits (bounded) for the copies it has begun: the
+// last `stages` of `count` phases of a ring.
+__device__ __forceinline__ void drain_ring(uint64_t *bars, int stages, int count, unsigned *status) {
+    int no = 0;
+    for (int v = max(0, count - stages); v < count; ++v)
+        ptx::mbar_wait_bounded(ptx::smem_u32(bars + v % stages), (uint32_t)(v / stages) & 1u, &no, status,
+                               kAtLimitNs / 8);
 }
 
 // ---- dk, dv: one tile of keys, its queries in turn
@@ -412,6 +514,33 @@ struct Kv {
     static constexpr uint32_t TILES = (2 + QST + DOST) * (DP / 64) * kBoxBytes;
     static constexpr uint32_t SMEM = TILES + RST * 1024 + sizeof(Bars);
 };
+
+struct KvItem {
+    AtSeq s;
+    int b, h, k0, off, qt_begin, nq, n;
+    bool live;  // the tile has keys; n: query tiles, over the group's heads in turn
+};
+
+__device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
+    KvItem w;
+    int tile;
+    if (a.tile_slow) {
+        w.b = u % a.batch, u /= a.batch;
+        w.h = u % a.hkv, tile = u / a.hkv;
+    } else {
+        tile = u % a.tiles, u /= a.tiles;
+        w.h = u % a.hkv, w.b = u / a.hkv;
+    }
+    w.s = at_seq(a, w.b);
+    w.k0 = tile * kT;
+    w.off = w.s.lk - w.s.lq;  // causal: key j is seen by the queries i >= j - off
+    const int qt_end = (w.s.lq + kT - 1) / kT;
+    w.qt_begin = a.causal ? min(max(w.k0 - w.off, 0) / kT, qt_end) : 0;
+    w.nq = qt_end - w.qt_begin;
+    w.live = w.k0 < w.s.lk;
+    w.n = w.live ? w.nq * a.group : 0;
+    return w;
+}
 
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kAtThreads, 1)
@@ -438,12 +567,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at_init_bars(sb.b_empty, kDoStages, 1);
         at_init_bars(sb.r_full, kRStages, 1);
         at_init_bars(sb.r_empty, kRStages, kAtWarps);
-        at_init_bars(sb.s_full, 2, 1);
-        at_init_bars(&sb.p_ready, 1, kAtWarps);
-        at_init_bars(sb.dp_full, 2, 1);
-        at_init_bars(&sb.ds_ready, 1, kAtWarps);
-        at_init_bars(&sb.fix, 3, 1);  // fix, acc, drain
-        sb.abort_flag = 0;
+        init_common(sb);
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
@@ -456,191 +580,212 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t tmem = sb.tmem_base;
     ptx::griddep_wait();  // the row statistics and the maxima come from the kernel before
     ptx::griddep_launch_dependents();
-
-    // this block's tile
-    int u = (int)blockIdx.x, tile, h, b;
-    if (a.tile_slow) {
-        b = u % a.batch, u /= a.batch;
-        h = u % a.hkv, tile = u / a.hkv;
-    } else {
-        tile = u % a.tiles, u /= a.tiles;
-        h = u % a.hkv, b = u / a.hkv;
-    }
-    const AtSeq s = at_seq(a, b);
-    const int k0 = tile * kT;
-    const int off = s.lk - s.lq;  // causal: key j is seen by the queries i >= j - off
-    const int qt_end = (s.lq + kT - 1) / kT;
-    const int qt_begin = a.causal ? min(max(k0 - off, 0) / kT, qt_end) : 0;
-    const int nq = qt_end - qt_begin;
-    const bool live_tile = k0 < s.lk;
-    const int n = live_tile ? nq * a.group : 0;
     const uint32_t tS = tmem, tDp = tmem + NS * 128, tDv = tDp + 128, tDk = tDv + DP;
     volatile int *ab = &sb.abort_flag;
-    const int tb = a.cu_q ? 0 : b;  // the tensor maps' batch index
+    const bool packed = a.cu_q != nullptr;
+    bool ok = true;
 
+    if (warp < 4) {
+    ptx::regs_dec<kCtlRegs>();
     if (warp == 0) {
-        if (n > 0) {
-            uint32_t fphase = 0;
-            const uint32_t bfix = ptx::smem_u32(&sb.fix);
+        uint32_t fphase = 0;
+        const uint32_t bfix = ptx::smem_u32(&sb.fix);
+        int gt = 0, nq_begun = 0, nr_begun = 0, ndo_begun = 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+            ok = __all_sync(0xffffffffu, ok) != 0;
+            return ok;
+        };
+        for (int k = 0, item = (int)blockIdx.x; hand_out(a, k, item, sb, ok); ++k, item = next_item(a.next)) {
+            const KvItem w = kv_item(a, item);
+            if (w.n == 0) continue;
+            const int tb = packed ? 0 : w.b;
+            if (gt > 0 && !wait(&sb.stat_empty, (uint32_t)(gt - 1))) break;
             if (lane == 0) {
                 const uint32_t bar = ptx::smem_u32(&sb.stat);
                 ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
 #pragma unroll
                 for (int j = 0; j < DP / 64; ++j) {
-                    ptx::tma_load_4d(sK + j * kBoxBytes, &tk, j * 64, (int)s.k0 + k0, h, tb, bar);
-                    ptx::tma_load_4d(sV + j * kBoxBytes, &tv, j * 64, (int)s.k0 + k0, h, tb, bar);
+                    ptx::tma_load_4d(sK + j * kBoxBytes, &tk, j * 64, (int)w.s.k0 + w.k0, w.h, tb, bar);
+                    ptx::tma_load_4d(sV + j * kBoxBytes, &tv, j * 64, (int)w.s.k0 + w.k0, w.h, tb, bar);
                 }
             }
-            bool ok = true;
-            int it = 0;
-            for (; ok && it < n; ++it) {
-                const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, hq = h * a.group + g;
-                const int st = it % kQStages, sd = it % kDoStages, sr = it % kRStages;
-                if (it >= kQStages)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_empty[st]),
-                                                (uint32_t)(it / kQStages - 1) & 1u, ab, a.status, kAtLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
+            ++gt;
+            for (int it = 0; ok && it < w.n; ++it) {
+                const int g = it / w.nq, q0 = (w.qt_begin + it - g * w.nq) * kT, hq = w.h * a.group + g;
+                const int valid = min(kT, w.s.lq - q0);
+                const int st = nq_begun % kQStages, sd = ndo_begun % kDoStages, sr = nr_begun % kRStages;
+                if (nq_begun >= kQStages && !wait(&sb.a_empty[st], (uint32_t)(nq_begun / kQStages - 1))) break;
+                ++nq_begun;
+                ok = load_tile<DP>(sQ + st * TILE, &tq, w.s.q0 + q0, hq, tb, valid, packed,
+                                   ptx::smem_u32(&sb.a_full[st]), bfix, fphase, ab, a.status);
                 if (!ok) break;
-                const int valid = min(kT, s.lq - q0);
-                ok = load_tile<DP>(sQ + st * TILE, &tq, s.q0 + q0, hq, tb, valid, a.cu_q != nullptr,
-                                   ptx::smem_u32(&sb.a_full[st]), bfix, fphase, 0, ab, a.status);
-                if (ok && it >= kRStages)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_empty[sr]), (uint32_t)(it / kRStages - 1) & 1u,
-                                                ab, a.status, kAtLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                if (nr_begun >= kRStages && !wait(&sb.r_empty[sr], (uint32_t)(nr_begun / kRStages - 1))) break;
+                ++nr_begun;
                 if (lane == 0) {
                     const uint32_t bar = ptx::smem_u32(&sb.r_full[sr]);
-                    const long long r0 = s.row0 + (long long)hq * a.head_rows + q0;
+                    const long long r0 = w.s.row0 + (long long)hq * a.head_rows + q0;
                     ptx::mbar_arrive_expect_tx(bar, 2 * kT * 4);
                     ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT), a.nlse + r0, kT * 4, bar);
                     ptx::bulk_load(ptx::smem_u32(rows + sr * 2 * kT + kT), a.ndsum + r0, kT * 4, bar);
                 }
-                if (it >= kDoStages)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_empty[sd]),
-                                                (uint32_t)(it / kDoStages - 1) & 1u, ab, a.status, kAtLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                ok = load_tile<DP>(sDo + sd * TILE, &tdo, s.q0 + q0, hq, tb, valid, a.cu_q != nullptr,
-                                   ptx::smem_u32(&sb.b_full[sd]), bfix, fphase, 0, ab, a.status);
+                if (ndo_begun >= kDoStages && !wait(&sb.b_empty[sd], (uint32_t)(ndo_begun / kDoStages - 1))) break;
+                ++ndo_begun;
+                ok = load_tile<DP>(sDo + sd * TILE, &tdo, w.s.q0 + q0, hq, tb, valid, packed,
+                                   ptx::smem_u32(&sb.b_full[sd]), bfix, fphase, ab, a.status);
             }
-            if (!ok) {
-                // no copy may be in flight when the block exits: the barriers of
-                // the last stages' phases that were begun
-                int no = 0;
-                ptx::mbar_wait_bounded(ptx::smem_u32(&sb.stat), 0, &no, a.status, kAtLimitNs);
-                for (int v = max(0, it - kQStages); v <= it && v < n; ++v)
-                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_full[v % kQStages]),
-                                           (uint32_t)(v / kQStages) & 1u, &no, a.status, kAtLimitNs / 8);
-                for (int v = max(0, it - kDoStages); v <= it && v < n; ++v)
-                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_full[v % kDoStages]),
-                                           (uint32_t)(v / kDoStages) & 1u, &no, a.status, kAtLimitNs / 8);
-                for (int v = max(0, it - kRStages); v <= it && v < n; ++v)
-                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.r_full[v % kRStages]), (uint32_t)(v / kRStages) & 1u, &no,
-                                           a.status, kAtLimitNs / 8);
-            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            drain_ring(&sb.stat, 1, gt, a.status);
+            drain_ring(sb.a_full, kQStages, nq_begun, a.status);
+            drain_ring(sb.b_full, kDoStages, ndo_begun, a.status);
+            drain_ring(sb.r_full, kRStages, nr_begun, a.status);
         }
     } else if (warp == 1) {
         // The whole warp walks the loop and one elected lane issues: descriptors and
-        // counters are then uniform over the warp, and an MMA takes a few cycles to
+        // counters are then uniform over the warp, and an MMA takes ~50 cycles to
         // issue instead of ~100 (more than the 64 that one of 128 columns runs).
-        if (n > 0) {
-            constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
-            constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
-            const int steps = (a.dim + 15) / 16;
-            auto wait = [&](AtWait x, AtWait y, AtWait z) { return wait_all(x, y, z, ab, a.status); };
-            auto mma_s = [&](int it) {
-                mma_rows<DP>(tS + it % NS * 128, sK, sQ + (it % kQStages) * TILE, steps, id_s, &sb.s_full[it & 1]);
-            };
-            auto mma_dp = [&](int it) {
-                mma_rows<DP>(tDp, sV, sDo + (it % kDoStages) * TILE, steps, id_s, &sb.dp_full[0]);
-            };
-            auto full_q = [&](int it) { return AtWait{&sb.a_full[it % kQStages], (uint32_t)(it / kQStages)}; };
-            auto full_do = [&](int it) { return AtWait{&sb.b_full[it % kDoStages], (uint32_t)(it / kDoStages)}; };
-            const AtWait stat{&sb.stat, 0};
-            bool ok = wait(stat, full_q(0), n > 1 ? full_q(NS - 1) : stat);
-            if (ok) mma_s(0);
-            if (ok && NS == 2 && n > 1) mma_s(1);
-            ok = ok && wait(stat, stat, full_do(0));
-            if (ok) mma_dp(0);
-            for (int it = 0; ok && it < n; ++it) {
-                const int ns = it + NS, nd = it + 1;  // the next tiles of S and of dP
-                const AtWait pr{&sb.p_ready, (uint32_t)it}, dr{&sb.ds_ready, (uint32_t)it};
-                if (!(ok = wait(pr, pr, ns < n ? full_q(ns) : pr))) break;
-                mma_acc(tDv, tS + it % NS * 128, sDo + (it % kDoStages) * TILE, id_a, it > 0, &sb.b_empty[it % kDoStages]);
-                // S overwrites P, dP overwrites dS: this thread's MMAs run in the order of issue
-                if (ns < n) mma_s(ns);
-                if (!(ok = wait(dr, dr, nd < n ? full_do(nd) : dr))) break;
-                mma_acc(tDk, tDp, sQ + (it % kQStages) * TILE, id_a, it > 0, &sb.a_empty[it % kQStages]);
-                if (nd < n) mma_dp(nd);
+        constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
+        constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
+        const int steps = (a.dim + 15) / 16;
+        auto wait = [&](AtWait x, AtWait y) { return ok = wait_both(x, y, ab, a.status); };
+        auto full_q = [&](Ring r) { return AtWait{&sb.a_full[r.s], r.ph}; };
+        auto full_do = [&](Ring r) { return AtWait{&sb.b_full[r.s], r.ph}; };
+        Ring rs, rk, rp, rv;   // q's ring for S and for dk, do's for dP and for dv
+        int gt = 0, js = 0, jp = 0;  // items; tiles of S, tiles of dv so far
+        auto mma_s = [&]() {
+            mma_rows<DP>(tS + js % NS * 128, sK, sQ + rs.s * TILE, steps, id_s, &sb.s_full[js & 1]);
+            rs.step(kQStages);
+            ++js;
+        };
+        auto mma_dp = [&](bool last) {  // the item's last product of K's and V's tiles
+            mma_rows<DP>(tDp, sV, sDo + rp.s * TILE, steps, id_s, &sb.dp_full[0], last ? &sb.stat_empty : nullptr);
+            rp.step(kDoStages);
+        };
+        for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
+            const int n = kv_item(a, item).n;
+            if (n == 0) continue;
+            const AtWait stat{&sb.stat, (uint32_t)gt}, freed{&sb.acc_empty, (uint32_t)(gt - 1)};
+            if (!wait(stat, full_q(rs))) break;
+            mma_s();
+            if (NS == 2 && n > 1) {
+                if (!wait(full_q(rs), full_q(rs))) break;
+                mma_s();
             }
-            finish_mmas(ok, sb, a.status);
+            // dv and dk overwrite the accumulators of the item before
+            if (!wait(full_do(rp), gt > 0 ? freed : stat)) break;
+            mma_dp(n == 1);
+            for (int it = 0; it < n; ++it, ++jp) {
+                const bool ms = it + NS < n, md = it + 1 < n;  // more S, more dP to come
+                const AtWait pr{&sb.p_ready[jp & 1], (uint32_t)(jp / 2)}, dr{&sb.ds_ready[jp & 1], (uint32_t)(jp / 2)};
+                if (!wait(pr, ms ? full_q(rs) : pr)) break;
+                mma_acc(tDv, tS + jp % NS * 128, sDo + rv.s * TILE, id_a, it > 0, &sb.b_empty[rv.s]);
+                rv.step(kDoStages);
+                // S overwrites P, dP overwrites dS: this warp's MMAs run in the order of issue
+                if (ms) mma_s();
+                if (!wait(dr, md ? full_do(rp) : dr)) break;
+                mma_acc(tDk, tDp, sQ + rk.s * TILE, id_a, it > 0, &sb.a_empty[rk.s]);
+                rk.step(kQStages);
+                if (md) mma_dp(it + 2 == n);
+            }
+            if (!ok) break;
+            if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&sb.acc));
+            __syncwarp();
+            ++gt;
         }
-    } else if (warp >= 4 && live_tile) {
+        finish_mmas(ok, sb, a.status);
+    }
+    } else {
+        ptx::regs_inc<kCompRegs>();
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const int j = k0 + quarter * 32 + lane;  // this thread's key
         const float cs = a.scale * kLog2e;
         const float sds = BF16 ? 1.f : ds_scale(a.maxima);       // dS is held times sds
         const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);    // from the held P
-        bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
-            return __all_sync(0xffffffffu, r);
+            return ok = __all_sync(0xffffffffu, r) != 0;
         };
-        for (int it = 0; it < n; ++it) {
-            const int g = it / nq, q0 = (qt_begin + it - g * nq) * kT, sr = it % kRStages;
-            const float *nl = rows + sr * 2 * kT + wg * 32, *nd = nl + kT;
-            float2 p[16];
-            if (!(ok = wait(&sb.r_full[sr], (uint32_t)(it / kRStages)) && wait(&sb.s_full[it & 1], (uint32_t)(it / 2)))) break;
-            ptx::tc_fence_after();
-            const uint32_t ts = tS + it % NS * 128 + lanes + wg * 32;
-            tmem_load(ts, p);
-            probabilities(p, cs, nl);
-            if (a.causal && k0 + kT - 1 > q0 + off) {
-                const int first = j - off - q0 - wg * 32;  // columns before it do not see key j
+        int gt = 0, g0 = 0;
+        for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
+            int n;
+            {
+                const KvItem w = kv_item(a, item);
+                if (!w.live) continue;
+                n = w.n;
+                const int begin = w.qt_begin * kT, end = begin + w.nq * kT;
+                // this thread's key is seen by the queries from here on, the tile's last one by those from `all` on
+                const int sees = w.k0 + quarter * 32 + lane - w.off, all = w.k0 + kT - 1 - w.off;
+                int q0 = begin;  // the step's first query, over the group's heads in turn
+                for (int it = 0; it < n; ++it) {
+                    const int i = g0 + it, sr = i % kRStages;
+                    const float *nl = rows + sr * 2 * kT + wg * 32, *nd = nl + kT;
+                    float2 p[16];
+                    if (!(wait(&sb.r_full[sr], (uint32_t)(i / kRStages)) && wait(&sb.s_full[i & 1], (uint32_t)(i / 2))))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint32_t ts = tS + i % NS * 128 + lanes + wg * 32;
+                    tmem_load(ts, p);
+                    probabilities(p, cs, nl);
+                    if (a.causal && q0 < all) {
+                        const int first = sees - q0 - wg * 32;  // columns before it do not see the key
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (2 * c < first) p[c].x = 0.f;
-                    if (2 * c + 1 < first) p[c].y = 0.f;
+                        for (int c = 0; c < 16; ++c) {
+                            if (2 * c < first) p[c].x = 0.f;
+                            if (2 * c + 1 < first) p[c].y = 0.f;
+                        }
+                    }
+                    q0 += kT;
+                    if (q0 == end) q0 = begin;
+                    tmem_store<BF16>(ts, p);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[i & 1]));
+                    if (!wait(&sb.dp_full[0], (uint32_t)i)) break;
+                    ptx::tc_fence_after();
+                    float2 x[16];
+                    tmem_load(tDp + lanes + wg * 32, x);
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        const float4 d = *reinterpret_cast<const float4 *>(nd + 2 * c);
+                        x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(d.x, d.y)));
+                        x[c + 1] = ptx::mul2(p[c + 1], ptx::add2(x[c + 1], make_float2(d.z, d.w)));
+                        if constexpr (!BF16) {
+                            x[c] = ptx::mul2(x[c], make_float2(pds, pds));
+                            x[c + 1] = ptx::mul2(x[c + 1], make_float2(pds, pds));
+                        }
+                    }
+                    tmem_store<BF16>(tDp + lanes + wg * 32, x);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready[i & 1]));
+                        ptx::mbar_arrive(ptx::smem_u32(&sb.r_empty[sr]));
+                    }
                 }
             }
-            tmem_store<BF16>(ts, p);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
-            if (!(ok = wait(&sb.dp_full[0], (uint32_t)it))) break;
+            if (!ok) break;
+            if (n > 0 && !wait(&sb.acc, (uint32_t)gt)) break;
             ptx::tc_fence_after();
-            float2 x[16];
-            tmem_load(tDp + lanes + wg * 32, x);
-#pragma unroll
-            for (int c = 0; c < 16; c += 2) {
-                const float4 d = *reinterpret_cast<const float4 *>(nd + 2 * c);
-                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(d.x, d.y)));
-                x[c + 1] = ptx::mul2(p[c + 1], ptx::add2(x[c + 1], make_float2(d.z, d.w)));
-                if constexpr (!BF16) {
-                    x[c] = ptx::mul2(x[c], make_float2(pds, pds));
-                    x[c + 1] = ptx::mul2(x[c + 1], make_float2(pds, pds));
-                }
+            {
+                // warpgroups 0 and 1 store dv, 2 and 3 dk, half of the columns each
+                const KvItem w = kv_item(a, afresh(item));
+                const bool isk = wg >= 2;
+                const int c0 = (wg & 1) * (DP / 2), j = w.k0 + quarter * 32 + lane;  // this thread's key
+                const long long *sg = isk ? a.sdk : a.sdv;
+                uint16_t *out = static_cast<uint16_t *>(isk ? a.dk : a.dv) + (packed ? 0 : w.b) * sg[0] +
+                                (w.s.k0 + j) * sg[1] + w.h * sg[2] + c0;
+                const float f = isk ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
+                store_row<DP / 2, BF16>((isk ? tDk : tDv) + lanes + c0, f, n == 0, j < w.s.lk, out, a.dim - c0);
             }
-            tmem_store<BF16>(tDp + lanes + wg * 32, x);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready));
-                ptx::mbar_arrive(ptx::smem_u32(&sb.r_empty[sr]));
+            if (n > 0) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
+                ++gt;
             }
-        }
-        if (n > 0 && ok) ok = wait(&sb.acc, 0);
-        if (ok) {
-            ptx::tc_fence_after();
-            // warpgroups 0 and 1 store dv, 2 and 3 dk, half of the columns each
-            const bool isk = wg >= 2;
-            const int c0 = (wg & 1) * (DP / 2);
-            const long long *sg = isk ? a.sdk : a.sdv;
-            uint16_t *out = static_cast<uint16_t *>(isk ? a.dk : a.dv) + tb * sg[0] + (s.k0 + j) * sg[1] + h * sg[2] + c0;
-            const float f = isk ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
-            store_row<DP / 2, BF16>((isk ? tDk : tDv) + lanes + c0, f, n == 0, j < s.lk, out, a.dim - c0);
+            g0 += n;
         }
     }
     ptx::tc_fence_before();
@@ -653,12 +798,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
 // ---- dq: one tile of queries, its keys in turn
 
-// The block's q and do rows are A operands of every tile's products, so they lie
+// The item's q and do rows are A operands of every tile's products, so they lie
 // in TMEM (16-bit, 32 or 64 columns each): the products then read one operand
 // from shared memory instead of two, whose 128 bytes per cycle are what an MMA
-// of 128 columns with both operands there waits for (81 against 55 cycles each,
-// dq of 1x8192 h32/8 d128 758 against 628 us).  At dim 128 that leaves room for one dP,
-// below it for two, of which one is computed while the other's dS is used.
+// of 128 columns with both operands there waits for (one tile of dim 128: 2230 cycles
+// against 2270, and 64 KB more for the rings).  At dim 128 that leaves room for one
+// dP, below it for two, of which one is computed while the other's dS is used.
 constexpr int kKStages = 4, kVStages = 3;
 using QBars = AtBars<kKStages, kVStages>;
 
@@ -688,19 +833,43 @@ __device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t ta, uint32_t sb
     __syncwarp();
 }
 
-// WORDS 32-bit words (pairs of elements) of a row into TMEM; zeros past `dim`.
+// WORDS 32-bit words (pairs of elements) of a row from `first` on; zeros past `dim`.
 template <int WORDS>
-__device__ __forceinline__ void row_to_tmem(uint32_t t, const uint16_t *row, bool live, int dim, int first) {
-    uint32_t w[16];
+__device__ __forceinline__ void row_words(uint32_t (&w)[16], const uint16_t *row, bool live, int dim, int first) {
 #pragma unroll
     for (int j = 0; j < WORDS; j += 4) {
         uint4 v = make_uint4(0, 0, 0, 0);
         if (live && 2 * (first + j) < dim) v = *reinterpret_cast<const uint4 *>(row + 2 * (first + j));
         w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
     }
-    __syncwarp();
-    if constexpr (WORDS == 16) ptx::tmem_st16(t + first, w);
-    else ptx::tmem_st8(t + first, w);
+}
+
+struct QItem {
+    AtSeq s;
+    int b, h, q0, off, n;
+    bool live;  // the tile has queries; n: key tiles that any of them sees
+};
+
+__device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
+    QItem w;
+    int tile;
+    if (a.tile_slow) {  // causal: the tiles with the most keys first
+        w.b = u % a.batch, u /= a.batch;
+        w.h = u % a.hq, tile = a.tiles - 1 - u / a.hq;
+    } else {
+        tile = u % a.tiles, u /= a.tiles;
+        w.h = u % a.hq, w.b = u / a.hq;
+    }
+    w.s = at_seq(a, w.b);
+    w.q0 = tile * kT;
+    w.off = w.s.lk - w.s.lq;
+    w.live = w.q0 < w.s.lq;
+    w.n = w.live ? (w.s.lk + kT - 1) / kT : 0;
+    if (a.causal && w.live) {
+        const int last = min(w.q0 + kT, w.s.lq) - 1 + w.off;  // the last key any of its queries sees
+        w.n = last < 0 ? 0 : min(w.n, last / kT + 1);
+    }
+    return w;
 }
 
 template <int DP, bool BF16>
@@ -724,12 +893,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         at_init_bars(sb.a_empty, kKStages, 1);
         at_init_bars(sb.b_full, kVStages, 1);
         at_init_bars(sb.b_empty, kVStages, 1);
-        at_init_bars(sb.s_full, 2, 1);
-        at_init_bars(&sb.p_ready, 1, kAtWarps);
-        at_init_bars(sb.dp_full, 2, 1);
-        at_init_bars(&sb.ds_ready, 1, kAtWarps);
-        at_init_bars(&sb.fix, 3, 1);
-        sb.abort_flag = 0;
+        init_common(sb);
         ptx::fence_mbar_init();
     }
     if (warp == 1) {
@@ -740,169 +904,217 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sb.tmem_base;
-
-    int u = (int)blockIdx.x, tile, h, b;
-    if (a.tile_slow) {  // causal: the tiles with the most keys first
-        b = u % a.batch, u /= a.batch;
-        h = u % a.hq, tile = a.tiles - 1 - u / a.hq;
-    } else {
-        tile = u % a.tiles, u /= a.tiles;
-        h = u % a.hq, b = u / a.hq;
-    }
-    const AtSeq s = at_seq(a, b);
-    const int q0 = tile * kT, hk = h / a.group;
-    const int off = s.lk - s.lq;
-    const bool live_tile = q0 < s.lq;
-    int n = live_tile ? (s.lk + kT - 1) / kT : 0;
-    if (a.causal && live_tile) {
-        const int last = min(q0 + kT, s.lq) - 1 + off;  // the last key any of its queries sees
-        n = last < 0 ? 0 : min(n, last / kT + 1);
-    }
     const uint32_t tS = tmem, tDp = tmem + 128, tDq = tDp + NB * 128, tQ = tDq + DP, tDo = tQ + DP / 2;
     volatile int *ab = &sb.abort_flag;
-    const int tb = a.cu_q ? 0 : b;
+    const bool packed = a.cu_q != nullptr;
+    bool ok = true;
 
+    if (warp < 4) {
+    ptx::regs_dec<kCtlRegs>();
     if (warp == 0) {
-        if (n > 0) {
-            uint32_t fphase = 0;
-            const uint32_t bfix = ptx::smem_u32(&sb.fix);
-            bool ok = true;
-            int it = 0;
-            for (; ok && it < n; ++it) {
-                const int st = it % kKStages, sv = it % kVStages;
-                const int valid = min(kT, s.lk - it * kT);
-                if (it >= kKStages)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_empty[st]),
-                                                (uint32_t)(it / kKStages - 1) & 1u, ab, a.status, kAtLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
+        uint32_t fphase = 0;
+        const uint32_t bfix = ptx::smem_u32(&sb.fix);
+        int nk_begun = 0, nv_begun = 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+            ok = __all_sync(0xffffffffu, ok) != 0;
+            return ok;
+        };
+        for (int k = 0, item = (int)blockIdx.x; hand_out(a, k, item, sb, ok); ++k, item = next_item(a.next + 1)) {
+            const QItem w = q_item(a, item);
+            const int tb = packed ? 0 : w.b, hk = w.h / a.group;
+            for (int it = 0; ok && it < w.n; ++it) {
+                const int st = nk_begun % kKStages, sv = nv_begun % kVStages;
+                const int valid = min(kT, w.s.lk - it * kT);
+                if (nk_begun >= kKStages && !wait(&sb.a_empty[st], (uint32_t)(nk_begun / kKStages - 1))) break;
+                ++nk_begun;
+                ok = load_tile<DP>(sK + st * TILE, &tk, w.s.k0 + it * kT, hk, tb, valid, packed,
+                                   ptx::smem_u32(&sb.a_full[st]), bfix, fphase, ab, a.status);
                 if (!ok) break;
-                ok = load_tile<DP>(sK + st * TILE, &tk, s.k0 + it * kT, hk, tb, valid, a.cu_q != nullptr,
-                                   ptx::smem_u32(&sb.a_full[st]), bfix, fphase, 0, ab, a.status);
-                if (ok && it >= kVStages)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_empty[sv]),
-                                                (uint32_t)(it / kVStages - 1) & 1u, ab, a.status, kAtLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                ok = load_tile<DP>(sV + sv * TILE, &tv, s.k0 + it * kT, hk, tb, valid, a.cu_q != nullptr,
-                                   ptx::smem_u32(&sb.b_full[sv]), bfix, fphase, 0, ab, a.status);
+                if (nv_begun >= kVStages && !wait(&sb.b_empty[sv], (uint32_t)(nv_begun / kVStages - 1))) break;
+                ++nv_begun;
+                ok = load_tile<DP>(sV + sv * TILE, &tv, w.s.k0 + it * kT, hk, tb, valid, packed,
+                                   ptx::smem_u32(&sb.b_full[sv]), bfix, fphase, ab, a.status);
             }
-            if (!ok) {
-                int no = 0;
-                for (int v = max(0, it - kKStages); v <= it && v < n; ++v)
-                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.a_full[v % kKStages]),
-                                           (uint32_t)(v / kKStages) & 1u, &no, a.status, kAtLimitNs / 8);
-                for (int v = max(0, it - kVStages); v <= it && v < n; ++v)
-                    ptx::mbar_wait_bounded(ptx::smem_u32(&sb.b_full[v % kVStages]),
-                                           (uint32_t)(v / kVStages) & 1u, &no, a.status, kAtLimitNs / 8);
-            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            drain_ring(sb.a_full, kKStages, nk_begun, a.status);
+            drain_ring(sb.b_full, kVStages, nv_begun, a.status);
         }
     } else if (warp == 1) {
-        // The whole warp walks the loop and one elected lane issues: descriptors and
-        // counters are then uniform over the warp, and an MMA takes a few cycles to
-        // issue instead of ~100 (more than the 64 that one of 128 columns runs).
-        if (n > 0) {
-            constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
-            constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
-            const int steps = (a.dim + 15) / 16;
-            auto wait = [&](AtWait x, AtWait y, AtWait z) { return wait_all(x, y, z, ab, a.status); };
-            auto mma_s = [&](int it) {
-                mma_rows_ts<DP>(tS, tQ, sK + (it % kKStages) * TILE, steps, id_s, &sb.s_full[it & 1]);
-            };
-            auto mma_dp = [&](int it) {
-                mma_rows_ts<DP>(tDp + it % NB * 128, tDo, sV + (it % kVStages) * TILE, steps, id_s,
-                                &sb.dp_full[it & 1], &sb.b_empty[it % kVStages]);
-            };
-            auto full_k = [&](int it) { return AtWait{&sb.a_full[it % kKStages], (uint32_t)(it / kKStages)}; };
-            auto full_v = [&](int it) { return AtWait{&sb.b_full[it % kVStages], (uint32_t)(it / kVStages)}; };
-            bool ok = wait({&sb.stat, 0}, full_k(0), full_v(0));
-            if (ok) mma_s(0);
-            if (ok) mma_dp(0);
-            for (int it = 0; ok && it < n; ++it) {
-                const int nx = it + 1;
-                const bool more = nx < n;
-                const AtWait pr{&sb.p_ready, (uint32_t)it}, dr{&sb.ds_ready, (uint32_t)it};  // pr: S is in registers
-                if (!(ok = wait(pr, more ? full_k(nx) : pr, more && NB == 2 ? full_v(nx) : pr))) break;
-                if (more) mma_s(nx);
-                if (NB == 2 && more) mma_dp(nx);
-                if (!(ok = wait(dr, dr, more && NB == 1 ? full_v(nx) : dr))) break;
-                mma_acc(tDq, tDp + it % NB * 128, sK + (it % kKStages) * TILE, id_a, it > 0,
-                        &sb.a_empty[it % kKStages]);
-                // with one buffer dP overwrites dS: this thread's MMAs run in the order of issue
-                if (NB == 1 && more) mma_dp(nx);
+        constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
+        constexpr uint32_t id_a = ptx::idesc_f16(128, DP, BF16, true);
+        const int steps = (a.dim + 15) / 16;
+        auto wait = [&](AtWait x, AtWait y) { return ok = wait_both(x, y, ab, a.status); };
+        auto full_k = [&](Ring r) { return AtWait{&sb.a_full[r.s], r.ph}; };
+        auto full_v = [&](Ring r) { return AtWait{&sb.b_full[r.s], r.ph}; };
+        Ring rs, rv, rq;  // k's ring for S and for dq, v's
+        int gt = 0, js = 0, jp = 0;  // items; tiles of S and dP, tiles of dq so far
+        auto mma_s = [&]() {
+            mma_rows_ts<DP>(tS, tQ, sK + rs.s * TILE, steps, id_s, &sb.s_full[js & 1]);
+            rs.step(kKStages);
+        };
+        auto mma_dp = [&]() {
+            mma_rows_ts<DP>(tDp + js % NB * 128, tDo, sV + rv.s * TILE, steps, id_s, &sb.dp_full[js & 1],
+                            &sb.b_empty[rv.s]);
+            rv.step(kVStages);
+            ++js;
+        };
+        for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
+            const int n = q_item(a, item).n;
+            if (n == 0) continue;
+            const AtWait stat{&sb.stat, (uint32_t)gt}, freed{&sb.acc_empty, (uint32_t)(gt - 1)};
+            if (!wait(stat, full_k(rs))) break;
+            mma_s();
+            // dq overwrites the accumulator of the item before
+            if (!wait(full_v(rv), gt > 0 ? freed : stat)) break;
+            mma_dp();
+            for (int it = 0; it < n; ++it, ++jp) {
+                const bool more = it + 1 < n;
+                const AtWait pr{&sb.p_ready[jp & 1], (uint32_t)(jp / 2)}, dr{&sb.ds_ready[jp & 1], (uint32_t)(jp / 2)};
+                if (!wait(pr, more ? full_k(rs) : pr)) break;  // S is in registers
+                if (more) mma_s();
+                if (NB == 2 && more) {
+                    if (!wait(full_v(rv), full_v(rv))) break;
+                    mma_dp();
+                }
+                if (!wait(dr, more && NB == 1 ? full_v(rv) : dr)) break;
+                mma_acc(tDq, tDp + jp % NB * 128, sK + rq.s * TILE, id_a, it > 0, &sb.a_empty[rq.s]);
+                rq.step(kKStages);
+                // with one buffer dP overwrites dS: this warp's MMAs run in the order of issue
+                if (NB == 1 && more) mma_dp();
             }
-            finish_mmas(ok, sb, a.status);
+            if (!ok) break;
+            if (ptx::elect_one()) ptx::mma_commit(ptx::smem_u32(&sb.acc));
+            __syncwarp();
+            ++gt;
         }
-    } else if (warp >= 4 && live_tile) {
+        finish_mmas(ok, sb, a.status);
+    }
+    } else {
+        ptx::regs_inc<kCompRegs>();
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const int r = quarter * 32 + lane, i = q0 + r;  // this thread's query
-        const long long row = s.row0 + (long long)h * a.head_rows + i;
-        const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row);
+        const int r = quarter * 32 + lane;
         const float cs = a.scale * kLog2e;
         const float sds = BF16 ? 1.f : ds_scale(a.maxima);
         const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);
-        bool ok = true;
+        constexpr int WORDS = DP / 8;  // of each tensor's DP / 2 words, per warpgroup
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            const bool w = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
-            return __all_sync(0xffffffffu, w);
+            const bool x = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+            return ok = __all_sync(0xffffffffu, x) != 0;
         };
-        if (n > 0) {
-            constexpr int WORDS = DP / 8;  // of each tensor's DP / 2 words, per warpgroup
-            const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + tb * a.sq[0] + (s.q0 + i) * a.sq[1] + h * a.sq[2];
-            const uint16_t *drow = static_cast<const uint16_t *>(a.dout) + tb * a.sdo[0] + (s.q0 + i) * a.sdo[1] + h * a.sdo[2];
-            row_to_tmem<WORDS>(tQ + lanes, qrow, i < s.lq, a.dim, wg * WORDS);
-            row_to_tmem<WORDS>(tDo + lanes, drow, i < s.lq, a.dim, wg * WORDS);
+        int gt = 0, g0 = 0, k = 0;
+        // the next item's rows are read before the epilogue of the one before and
+        // put into TMEM once its products are done
+        auto read_rows = [&](const QItem &w, uint32_t (&wq)[16], uint32_t (&wd)[16]) {
+            const int tb = packed ? 0 : w.b, i = w.q0 + r;
+            const uint16_t *qr = static_cast<const uint16_t *>(a.q) + tb * a.sq[0] + (w.s.q0 + i) * a.sq[1] + w.h * a.sq[2];
+            const uint16_t *dr = static_cast<const uint16_t *>(a.dout) + tb * a.sdo[0] + (w.s.q0 + i) * a.sdo[1] + w.h * a.sdo[2];
+            row_words<WORDS>(wq, qr, i < w.s.lq, a.dim, wg * WORDS);
+            row_words<WORDS>(wd, dr, i < w.s.lq, a.dim, wg * WORDS);
+        };
+        auto put_rows = [&](const uint32_t (&wq)[16], const uint32_t (&wd)[16]) {
+            __syncwarp();
+            if constexpr (WORDS == 16) {
+                ptx::tmem_st16(tQ + lanes + wg * WORDS, wq);
+                ptx::tmem_st16(tDo + lanes + wg * WORDS, wd);
+            } else {
+                ptx::tmem_st8(tQ + lanes + wg * WORDS, wq);
+                ptx::tmem_st8(tDo + lanes + wg * WORDS, wd);
+            }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.stat));
-        }
-        for (int it = 0; it < n; ++it) {
-            float2 p[16];
-            if (!(ok = wait(&sb.s_full[it & 1], (uint32_t)(it / 2)))) break;
-            ptx::tc_fence_after();
-            tmem_load(tS + lanes + wg * 32, p);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready));
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                p[c] = ptx::fma2(p[c], make_float2(cs, cs), make_float2(nl, nl));
-                p[c] = make_float2(ptx::ex2(p[c].x), ptx::ex2(p[c].y));
+        };
+        int item = take_item(a, k, sb, ok), n = 0;
+        if (item >= 0) {
+            const QItem w = q_item(a, item);
+            n = w.n;
+            if (n > 0) {
+                uint32_t wq[16], wd[16];
+                read_rows(w, wq, wd);
+                put_rows(wq, wd);
             }
-            const int kb = it * kT;
-            if (kb + kT > s.lk || (a.causal && kb + kT - 1 > q0 + off)) {
-                int lim = s.lk - kb;  // columns from it on are masked
-                if (a.causal) lim = min(lim, i + off - kb + 1);
-                lim -= wg * 32;
+        }
+        while (item >= 0) {
+            if (n > 0) {
+                const QItem w = q_item(a, afresh(item));
+                const long long row = w.s.row0 + (long long)w.h * a.head_rows + w.q0 + r;
+                const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row);
+                // this thread's query sees the keys before `sees`; tiles that end by `all` need no mask
+                const int sees = a.causal ? min(w.s.lk, w.q0 + r + w.off + 1) : w.s.lk;
+                const int all = a.causal ? min(w.s.lk, w.q0 + w.off + 1) : w.s.lk;
+                for (int it = 0; it < n; ++it) {
+                    const int i = g0 + it;
+                    float2 p[16];
+                    if (!wait(&sb.s_full[i & 1], (uint32_t)(i / 2))) break;
+                    ptx::tc_fence_after();
+                    tmem_load(tS + lanes + wg * 32, p);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[i & 1]));
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    if (2 * c >= lim) p[c].x = 0.f;
-                    if (2 * c + 1 >= lim) p[c].y = 0.f;
+                    for (int c = 0; c < 16; ++c) {
+                        p[c] = ptx::fma2(p[c], make_float2(cs, cs), make_float2(nl, nl));
+                        p[c] = make_float2(ptx::ex2(p[c].x), ptx::ex2(p[c].y));
+                    }
+                    if (it * kT + kT > all) {
+                        const int lim = sees - it * kT - wg * 32;  // columns from it on are masked
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            if (2 * c >= lim) p[c].x = 0.f;
+                            if (2 * c + 1 >= lim) p[c].y = 0.f;
+                        }
+                    }
+                    if (!wait(&sb.dp_full[i & 1], (uint32_t)(i / 2))) break;
+                    ptx::tc_fence_after();
+                    const uint32_t td = tDp + i % NB * 128 + lanes + wg * 32;
+                    float2 x[16];
+                    tmem_load(td, x);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(nd, nd)));
+                        if constexpr (!BF16) x[c] = ptx::mul2(x[c], make_float2(pds, pds));
+                    }
+                    tmem_store<BF16>(td, x);
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready[i & 1]));
                 }
+                if (!ok) break;
             }
-            if (!(ok = wait(&sb.dp_full[it & 1], (uint32_t)(it / 2)))) break;
-            ptx::tc_fence_after();
-            const uint32_t td = tDp + it % NB * 128 + lanes + wg * 32;
-            float2 x[16];
-            tmem_load(td, x);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(nd, nd)));
-                if constexpr (!BF16) x[c] = ptx::mul2(x[c], make_float2(pds, pds));
+            const int next = take_item(a, ++k, sb, ok);
+            if (!ok) break;
+            int next_n = 0;
+            uint32_t wq[16] = {}, wd[16] = {};
+            if (next >= 0) {
+                const QItem w = q_item(a, next);
+                next_n = w.n;
+                if (next_n > 0) read_rows(w, wq, wd);
             }
-            tmem_store<BF16>(td, x);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.ds_ready));
-        }
-        if (n > 0 && ok) ok = wait(&sb.acc, 0);
-        if (ok) {
+            if (n > 0 && !wait(&sb.acc, (uint32_t)gt)) break;
             ptx::tc_fence_after();
-            // each warpgroup stores a quarter of the columns
-            const int c0 = wg * (DP / 4);
-            uint16_t *out = static_cast<uint16_t *>(a.dq) + tb * a.sdq[0] + (s.q0 + i) * a.sdq[1] + h * a.sdq[2] + c0;
-            store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < s.lq, out, a.dim - c0);
+            if (next_n > 0) put_rows(wq, wd);
+            const QItem w = q_item(a, afresh(item));
+            if (w.live) {
+                // each warpgroup stores a quarter of the columns
+                const int c0 = wg * (DP / 4), i = w.q0 + r;
+                uint16_t *out = static_cast<uint16_t *>(a.dq) + (packed ? 0 : w.b) * a.sdq[0] + (w.s.q0 + i) * a.sdq[1] +
+                                w.h * a.sdq[2] + c0;
+                store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < w.s.lq, out, a.dim - c0);
+            }
+            if (n > 0) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
+                ++gt;
+            }
+            g0 += n;
+            n = next_n;
+            item = next;
         }
     }
     ptx::tc_fence_before();
@@ -1014,18 +1226,21 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     if (e != cudaSuccess) return e;
     if (p.k_tiles > 0) {
         a.tiles = p.k_tiles;
-        e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)((long long)p.k_tiles * d.heads_kv * d.batch)),
+        a.items = (int)((long long)p.k_tiles * d.heads_kv * d.batch);
+        e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)std::min(a.items, kNumSMs)),
                        dim3(kAtThreads), Kv<DP>::SMEM, st, tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
     }
     if (p.q_tiles > 0) {
         a.tiles = p.q_tiles;
+        a.items = (int)qgrid;
+        const unsigned blocks = std::min(qgrid, (unsigned)kNumSMs);
         // without keys there is no launch between this one and the preparation
         if (p.k_tiles > 0)
-            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(qgrid), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[1],
+            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(blocks), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[1],
                            tm[2], a);
         else
-            attn_q_kernel<DP, BF16><<<qgrid, kAtThreads, q_smem_bytes<DP>(), st>>>(tm[1], tm[2], a);
+            attn_q_kernel<DP, BF16><<<blocks, kAtThreads, q_smem_bytes<DP>(), st>>>(tm[1], tm[2], a);
         if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
@@ -1070,6 +1285,7 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.causal = d->causal; a.tile_slow = d->causal; a.scale = d->scale;
     a.lse = lse;
     a.status = static_cast<unsigned *>(workspace);
+    a.next = a.status + 2;
     a.maxima = a.status + 4;
     a.nlse = ws_at<float>(workspace, p.off_nlse);
     a.ndsum = ws_at<float>(workspace, p.off_ndsum);

@@ -118,6 +118,30 @@ def test_lengths(cuda_lib, len_q, len_k, dim, dtype, causal):
     compare(args, run(*args, dim ** -0.5, causal), dim ** -0.5, causal, dtype)
 
 
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, BF), (64, F16), (128, F16)], ids=str)
+def test_more_tiles_than_blocks(cuda_lib, dim, dtype, causal):
+    """Several tiles per block, of unlike work: 320 of keys, 640 of queries, ragged, repeated."""
+    rng = np.random.default_rng(dim)
+    args = make(rng, 32, 330, 200, 10, 5, dim, dtype, "bshd", 0.1, causal)
+    first = [t.clone() for t in run(*args, 0.1, causal)]
+    compare(args, first, 0.1, causal, dtype)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, run(*args, 0.1, causal)))
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, F16)], ids=str)
+def test_many_packed_sequences(cuda_lib, dim, dtype):
+    rng = np.random.default_rng(dim)
+    lens = [int(x) for x in rng.integers(0, 420, size=60)]
+    parts, args, cu = pack(rng, lens, lens, 4, 2, dim, dtype, 0.1, True)
+    outs = run(*args, 0.1, True, cu_q=cu[0], cu_k=cu[1], sequences=60, max_q=max(lens), max_k=max(lens))
+    at = 0
+    for p, n in zip(parts, lens):
+        compare(p, [g[None, at:at + n] for g in outs], 0.1, True, dtype)
+        at += n
+
+
 @pytest.mark.parametrize("dtype", [BF, F16], ids=str)
 @pytest.mark.parametrize("dim", [8, 16, 40, 72, 80, 96, 120])
 def test_head_dimensions(cuda_lib, dim, dtype):
