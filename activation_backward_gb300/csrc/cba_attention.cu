@@ -69,6 +69,10 @@ struct AtArgs {
     unsigned *status, *maxima;   // maxima: bits of max |do|^2, max |v|^2 over rows (f16)
     unsigned *next;              // work items handed out, of the two main kernels
     int items;                   // this launch's
+    int chunk, chunks;           // steps of an item at most; items per tile at most
+    int cnt_kv, cnt_q;           // tiles that have an arrival counter
+    unsigned *arrived;           // this launch's counters (kv's lie before q's)
+    float *part;                 // fp32 tiles of the items of a tile
     const void *q, *o, *dout, *v;
     void *dq, *dk, *dv;
     long long sq[3], so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
@@ -146,6 +150,8 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
             if (BF16) *a.status = 0;  // f16: cleared with the maxima before
             a.next[0] = a.next[1] = 0;
         }
+        if (u == 0)
+            for (int i = t; i < a.cnt_kv + a.cnt_q; i += 256) a.arrived[i] = 0;
         if (tile * kT < s.lq) {
             const long long row0 = s.row0 + (long long)h * a.head_rows + tile * kT;
             constexpr int RPP = 256 / LPR, NR = 4;  // rows per pass; rows of a thread in flight
@@ -243,7 +249,8 @@ struct AtBars {
     uint64_t fix, drain, acc, stat_empty;
     uint64_t acc_empty;                // the epilogue has read the accumulators
     uint64_t i_full[2], i_empty[2];    // work items handed out
-    int item[2];
+    uint64_t join;                     // the compute warps, around an arrival
+    int item[2], last;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -291,11 +298,11 @@ __device__ __forceinline__ bool load_tile(uint32_t dst, const CUtensorMap *tm, l
 template <int DP>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb, int steps,
                                          uint32_t idesc, uint64_t *done, uint64_t *done2 = nullptr) {
-    const uint64_t da = ptx::smem_desc(sa, 16, 1024, 2), db = ptx::smem_desc(sb, 16, 1024, 2);
+    const ptx::Desc da = ptx::desc_of(sa, 16, 1024, 2), db = ptx::desc_of(sb, 16, 1024, 2);
     if (ptx::elect_one()) {
         auto step = [&](int ks) {
             const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
-            ptx::mma_f16(d, da + off, db + off, idesc, ks > 0);
+            ptx::mma_f16(d, da, off, db, off, idesc, ks > 0);
         };
         if (steps == DP / 16) {  // a condition in each step doubles its issue time
 #pragma unroll
@@ -313,11 +320,11 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t sa, uint32_t sb, i
 // each 32 columns at ta, ta + 32, ...), B's rows contracted over.
 __device__ __forceinline__ void mma_acc(uint32_t d, uint32_t ta, uint32_t sb, uint32_t idesc,
                                         bool accumulate, uint64_t *done) {
-    const uint64_t db = ptx::smem_desc(sb, kBoxBytes, 1024, 2);
+    const ptx::Desc db = ptx::desc_of(sb, kBoxBytes, 1024, 2);
     if (ptx::elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < kT / 16; ++ks)
-            ptx::mma_f16_ts(d, ta + (ks >> 1) * 32 + (ks & 1) * 8, db + ks * (2048 >> 4), idesc,
+            ptx::mma_f16_ts(d, ta + (ks >> 1) * 32 + (ks & 1) * 8, db, ks * (2048 >> 4), idesc,
                             accumulate || ks > 0);
         ptx::mma_commit(ptx::smem_u32(done));
     }
@@ -433,6 +440,11 @@ __device__ __forceinline__ void finish_mmas(bool ok, Bars &sb, unsigned *status)
 // 32x676 h8 d64, six query tiles per item, more than half of a block's life was
 // its start and end when it had one item).
 
+// Few tiles with many steps each are cut into items of at most `chunk` steps.
+// Such an item writes its fp32 sums to memory and arrives on the tile's counter;
+// the one that arrives last adds all of them in the order of the steps, so the
+// result does not depend on who that is.
+
 // Load warp: hands item number k to the other warps.  False past the last item.
 template <typename Bars>
 __device__ __forceinline__ bool hand_out(const AtArgs &a, int k, int item, Bars &sb, bool &ok) {
@@ -469,6 +481,82 @@ __device__ __forceinline__ int take_item(const AtArgs &a, int k, Bars &sb, bool 
 }
 constexpr int kItemReaders = 1 + kAtWarps;  // the MMA and compute warps
 
+// The first step and the number of steps of a tile's item c, of n in all; `used`:
+// the items that the tile is cut into.
+__device__ __forceinline__ void cut(const AtArgs &a, int c, int &it0, int &n, int &used) {
+    used = 1;
+    it0 = 0;
+    if (a.chunks == 1) return;
+    used = max(1, (n + a.chunk - 1) / a.chunk);
+    it0 = c * a.chunk;
+    n = min(a.chunk, n - it0);
+}
+
+// The compute warps' arrival on a tile's counter with their sums in memory.  True
+// in all of them if theirs was the last of `used` (ok: false on a timeout).
+template <typename Bars>
+__device__ __forceinline__ bool arrive_last(const AtArgs &a, int tile, int used, Bars &sb, uint32_t &phase, bool &ok) {
+    auto meet = [&]() {
+        __threadfence();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.join));
+        const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.join), phase, &sb.abort_flag, a.status, kAtLimitNs);
+        phase ^= 1;
+        return ok = __all_sync(0xffffffffu, r) != 0;
+    };
+    if (!meet()) return false;
+    if (threadIdx.x == 128)
+        *const_cast<volatile int *>(&sb.last) = atomicAdd(a.arrived + tile, 1u) + 1 == (unsigned)used;
+    if (!meet()) return false;
+    return *const_cast<volatile int *>(&sb.last) != 0;
+}
+
+// COLS columns of a thread's row of accumulators in memory: 16 bytes of 32 rows
+// side by side.  `at`: the item's sums plus the thread's row.
+template <int COLS>
+__device__ __forceinline__ void sums_to_memory(uint32_t ta, float4 *at) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 16) {
+        float v[16];
+        ptx::tmem_ld16(ta + c, v);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+            __stcg(at + (c + j) / 4 * kT, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+    }
+}
+// The same of `used` items, `stride` float4 apart, added, scaled and stored as
+// store_row does.
+template <int COLS, bool BF16>
+__device__ __forceinline__ void store_sums(const float4 *at, int used, long long stride, float scale, bool live,
+                                           uint16_t *out, int cols) {
+    constexpr int C = 16;  // columns at a time
+    if (!live) return;
+    for (int c = 0; c < COLS && c < cols; c += C) {
+        float4 x[C / 4];
+#pragma unroll
+        for (int j = 0; j < C / 4; ++j) x[j] = __ldcg(at + (c / 4 + j) * kT);
+        for (int i = 1; i < used; ++i) {
+            float4 y[C / 4];
+#pragma unroll
+            for (int j = 0; j < C / 4; ++j) y[j] = __ldcg(at + i * stride + (c / 4 + j) * kT);
+#pragma unroll
+            for (int j = 0; j < C / 4; ++j)
+                x[j] = make_float4(x[j].x + y[j].x, x[j].y + y[j].y, x[j].z + y[j].z, x[j].w + y[j].w);
+        }
+#pragma unroll
+        for (int j = 0; j < C / 4; j += 2)
+            if (c + 4 * j < cols) {
+                uint4 w;
+                w.x = pack2<BF16>(x[j].x * scale, x[j].y * scale);
+                w.y = pack2<BF16>(x[j].z * scale, x[j].w * scale);
+                w.z = pack2<BF16>(x[j + 1].x * scale, x[j + 1].y * scale);
+                w.w = pack2<BF16>(x[j + 1].z * scale, x[j + 1].w * scale);
+                *reinterpret_cast<uint4 *>(out + c + 4 * j) = w;
+            }
+    }
+}
+
 // The same number, computed with anew: what is derived from it after a long loop
 // is not kept in registers through it.
 __device__ __forceinline__ int afresh(int v) {
@@ -486,6 +574,7 @@ __device__ __forceinline__ void init_common(Bars &sb) {
     at_init_bars(sb.ds_ready, 2, kAtWarps);
     at_init_bars(&sb.fix, 4, 1);  // fix, drain, acc, stat_empty
     at_init_bars(&sb.acc_empty, 1, kAtWarps);
+    at_init_bars(&sb.join, 1, kAtWarps);
     at_init_bars(sb.i_full, 2, 1);
     at_init_bars(sb.i_empty, 2, kItemReaders);
     sb.abort_flag = 0;
@@ -517,12 +606,17 @@ struct Kv {
 
 struct KvItem {
     AtSeq s;
-    int b, h, k0, off, qt_begin, nq, n;
-    bool live;  // the tile has keys; n: query tiles, over the group's heads in turn
+    int b, h, k0, off, qt_begin, nq;
+    int it0, n;      // steps: query tiles, over the group's heads in turn
+    int tile, c, used;
+    bool live;       // there are keys, and steps or zeros to be stored
 };
 
 __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
     KvItem w;
+    w.c = 0;
+    if (a.chunks > 1) w.c = u % a.chunks, u /= a.chunks;
+    w.tile = u;
     int tile;
     if (a.tile_slow) {
         w.b = u % a.batch, u /= a.batch;
@@ -539,6 +633,9 @@ __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
     w.nq = qt_end - w.qt_begin;
     w.live = w.k0 < w.s.lk;
     w.n = w.live ? w.nq * a.group : 0;
+    cut(a, w.c, w.it0, w.n, w.used);
+    w.live = w.live && w.c < w.used;
+    if (!w.live) w.n = 0;
     return w;
 }
 
@@ -596,7 +693,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ok = __all_sync(0xffffffffu, ok) != 0;
             return ok;
         };
-        for (int k = 0, item = (int)blockIdx.x; hand_out(a, k, item, sb, ok); ++k, item = next_item(a.next)) {
+        auto live = [&](int item) {  // the first item from this one on with anything to do
+            while ((packed || a.chunks > 1) && item < a.items && !kv_item(a, item).live) item = next_item(a.next);
+            return item;
+        };
+        for (int k = 0, item = live((int)blockIdx.x); hand_out(a, k, item, sb, ok); ++k, item = live(next_item(a.next))) {
             const KvItem w = kv_item(a, item);
             if (w.n == 0) continue;
             const int tb = packed ? 0 : w.b;
@@ -612,7 +713,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             ++gt;
             for (int it = 0; ok && it < w.n; ++it) {
-                const int g = it / w.nq, q0 = (w.qt_begin + it - g * w.nq) * kT, hq = w.h * a.group + g;
+                const int t = w.it0 + it, g = t / w.nq, q0 = (w.qt_begin + t - g * w.nq) * kT, hq = w.h * a.group + g;
                 const int valid = min(kT, w.s.lq - q0);
                 const int st = nq_begun % kQStages, sd = ndo_begun % kDoStages, sr = nr_begun % kRStages;
                 if (nq_begun >= kQStages && !wait(&sb.a_empty[st], (uint32_t)(nq_begun / kQStages - 1))) break;
@@ -708,16 +809,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return ok = __all_sync(0xffffffffu, r) != 0;
         };
         int gt = 0, g0 = 0;
+        uint32_t joined = 0;
         for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
             int n;
             {
                 const KvItem w = kv_item(a, item);
-                if (!w.live) continue;
                 n = w.n;
                 const int begin = w.qt_begin * kT, end = begin + w.nq * kT;
                 // this thread's key is seen by the queries from here on, the tile's last one by those from `all` on
                 const int sees = w.k0 + quarter * 32 + lane - w.off, all = w.k0 + kT - 1 - w.off;
-                int q0 = begin;  // the step's first query, over the group's heads in turn
+                // the step's first query, over the group's heads in turn
+                int q0 = n > 0 ? begin + w.it0 % w.nq * kT : 0;
                 for (int it = 0; it < n; ++it) {
                     const int i = g0 + it, sr = i % kRStages;
                     const float *nl = rows + sr * 2 * kT + wg * 32, *nd = nl + kT;
@@ -777,13 +879,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 uint16_t *out = static_cast<uint16_t *>(isk ? a.dk : a.dv) + (packed ? 0 : w.b) * sg[0] +
                                 (w.s.k0 + j) * sg[1] + w.h * sg[2] + c0;
                 const float f = isk ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
-                store_row<DP / 2, BF16>((isk ? tDk : tDv) + lanes + c0, f, n == 0, j < w.s.lk, out, a.dim - c0);
-            }
-            if (n > 0) {
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
-                ++gt;
+                const uint32_t acc = (isk ? tDk : tDv) + lanes + c0;
+                constexpr long long ITEM = 2 * DP * kT / 4;  // float4 of an item's sums
+                float4 *at = reinterpret_cast<float4 *>(a.part) + w.tile * a.chunks * ITEM + wg * (DP / 2) / 4 * kT +
+                             quarter * 32 + lane;
+                if (w.used == 1) store_row<DP / 2, BF16>(acc, f, n == 0, j < w.s.lk, out, a.dim - c0);
+                else sums_to_memory<DP / 2>(acc, at + w.c * ITEM);
+                if (n > 0) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
+                    ++gt;
+                }
+                if (w.used > 1) {
+                    const bool last = arrive_last(a, w.tile, w.used, sb, joined, ok);
+                    if (!ok) break;
+                    if (last) store_sums<DP / 2, BF16>(at, w.used, ITEM, f, j < w.s.lk, out, a.dim - c0);
+                }
             }
             g0 += n;
         }
@@ -816,10 +928,10 @@ constexpr uint32_t q_smem_bytes() {
 template <int DP>
 __device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t ta, uint32_t sb, int steps, uint32_t idesc,
                                             uint64_t *done, uint64_t *done2 = nullptr) {
-    const uint64_t db = ptx::smem_desc(sb, 16, 1024, 2);
+    const ptx::Desc db = ptx::desc_of(sb, 16, 1024, 2);
     if (ptx::elect_one()) {
         auto step = [&](int ks) {
-            ptx::mma_f16_ts(d, ta + ks * 8, db + (((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4), idesc, ks > 0);
+            ptx::mma_f16_ts(d, ta + ks * 8, db, ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4, idesc, ks > 0);
         };
         if (steps == DP / 16) {
 #pragma unroll
@@ -846,12 +958,17 @@ __device__ __forceinline__ void row_words(uint32_t (&w)[16], const uint16_t *row
 
 struct QItem {
     AtSeq s;
-    int b, h, q0, off, n;
-    bool live;  // the tile has queries; n: key tiles that any of them sees
+    int b, h, q0, off;
+    int it0, n;      // steps: key tiles that any of the tile's queries sees
+    int tile, c, used;
+    bool live;       // there are queries, and steps or zeros to be stored
 };
 
 __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
     QItem w;
+    w.c = 0;
+    if (a.chunks > 1) w.c = u % a.chunks, u /= a.chunks;
+    w.tile = u;
     int tile;
     if (a.tile_slow) {  // causal: the tiles with the most keys first
         w.b = u % a.batch, u /= a.batch;
@@ -869,6 +986,9 @@ __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
         const int last = min(w.q0 + kT, w.s.lq) - 1 + w.off;  // the last key any of its queries sees
         w.n = last < 0 ? 0 : min(w.n, last / kT + 1);
     }
+    cut(a, w.c, w.it0, w.n, w.used);
+    w.live = w.live && w.c < w.used;
+    if (!w.live) w.n = 0;
     return w;
 }
 
@@ -920,20 +1040,25 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ok = __all_sync(0xffffffffu, ok) != 0;
             return ok;
         };
-        for (int k = 0, item = (int)blockIdx.x; hand_out(a, k, item, sb, ok); ++k, item = next_item(a.next + 1)) {
+        auto live = [&](int item) {
+            while ((packed || a.chunks > 1) && item < a.items && !q_item(a, item).live) item = next_item(a.next + 1);
+            return item;
+        };
+        for (int k = 0, item = live((int)blockIdx.x); hand_out(a, k, item, sb, ok);
+             ++k, item = live(next_item(a.next + 1))) {
             const QItem w = q_item(a, item);
             const int tb = packed ? 0 : w.b, hk = w.h / a.group;
             for (int it = 0; ok && it < w.n; ++it) {
                 const int st = nk_begun % kKStages, sv = nv_begun % kVStages;
-                const int valid = min(kT, w.s.lk - it * kT);
+                const int key = (w.it0 + it) * kT, valid = min(kT, w.s.lk - key);
                 if (nk_begun >= kKStages && !wait(&sb.a_empty[st], (uint32_t)(nk_begun / kKStages - 1))) break;
                 ++nk_begun;
-                ok = load_tile<DP>(sK + st * TILE, &tk, w.s.k0 + it * kT, hk, tb, valid, packed,
+                ok = load_tile<DP>(sK + st * TILE, &tk, w.s.k0 + key, hk, tb, valid, packed,
                                    ptx::smem_u32(&sb.a_full[st]), bfix, fphase, ab, a.status);
                 if (!ok) break;
                 if (nv_begun >= kVStages && !wait(&sb.b_empty[sv], (uint32_t)(nv_begun / kVStages - 1))) break;
                 ++nv_begun;
-                ok = load_tile<DP>(sV + sv * TILE, &tv, w.s.k0 + it * kT, hk, tb, valid, packed,
+                ok = load_tile<DP>(sV + sv * TILE, &tv, w.s.k0 + key, hk, tb, valid, packed,
                                    ptx::smem_u32(&sb.b_full[sv]), bfix, fphase, ab, a.status);
             }
             if (!ok) break;
@@ -1006,6 +1131,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return ok = __all_sync(0xffffffffu, x) != 0;
         };
         int gt = 0, g0 = 0, k = 0;
+        uint32_t joined = 0;
         // the next item's rows are read before the epilogue of the one before and
         // put into TMEM once its products are done
         auto read_rows = [&](const QItem &w, uint32_t (&wq)[16], uint32_t (&wd)[16]) {
@@ -1044,9 +1170,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const QItem w = q_item(a, afresh(item));
                 const long long row = w.s.row0 + (long long)w.h * a.head_rows + w.q0 + r;
                 const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row);
-                // this thread's query sees the keys before `sees`; tiles that end by `all` need no mask
-                const int sees = a.causal ? min(w.s.lk, w.q0 + r + w.off + 1) : w.s.lk;
-                const int all = a.causal ? min(w.s.lk, w.q0 + w.off + 1) : w.s.lk;
+                // counted from the first step: this thread's query sees the keys before `sees`; tiles
+                // that end by `all` need no mask
+                const int sees = (a.causal ? min(w.s.lk, w.q0 + r + w.off + 1) : w.s.lk) - w.it0 * kT;
+                const int all = (a.causal ? min(w.s.lk, w.q0 + w.off + 1) : w.s.lk) - w.it0 * kT;
                 for (int it = 0; it < n; ++it) {
                     const int i = g0 + it;
                     float2 p[16];
@@ -1098,19 +1225,27 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (n > 0 && !wait(&sb.acc, (uint32_t)gt)) break;
             ptx::tc_fence_after();
             if (next_n > 0) put_rows(wq, wd);
-            const QItem w = q_item(a, afresh(item));
-            if (w.live) {
+            {
                 // each warpgroup stores a quarter of the columns
+                const QItem w = q_item(a, afresh(item));
                 const int c0 = wg * (DP / 4), i = w.q0 + r;
                 uint16_t *out = static_cast<uint16_t *>(a.dq) + (packed ? 0 : w.b) * a.sdq[0] + (w.s.q0 + i) * a.sdq[1] +
                                 w.h * a.sdq[2] + c0;
-                store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < w.s.lq, out, a.dim - c0);
-            }
-            if (n > 0) {
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
-                ++gt;
+                constexpr long long ITEM = DP * kT / 4;
+                float4 *at = reinterpret_cast<float4 *>(a.part) + w.tile * a.chunks * ITEM + c0 / 4 * kT + r;
+                if (w.used == 1) store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < w.s.lq, out, a.dim - c0);
+                else sums_to_memory<DP / 4>(tDq + lanes + c0, at + w.c * ITEM);
+                if (n > 0) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
+                    ++gt;
+                }
+                if (w.used > 1) {
+                    const bool last = arrive_last(a, w.tile, w.used, sb, joined, ok);
+                    if (!ok) break;
+                    if (last) store_sums<DP / 4, BF16>(at, w.used, ITEM, a.scale / sds, i < w.s.lq, out, a.dim - c0);
+                }
             }
             g0 += n;
             n = next_n;
@@ -1130,11 +1265,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
 // ---- host side
 
+struct AtCut {
+    int chunk, chunks, tiles;  // steps per item, items per tile, tiles with a counter (0: not cut)
+};
 struct AtPlan {
     int dp, q_tiles, k_tiles;
     long long head_rows;   // padded rows of one head
-    size_t off_nlse, off_ndsum, total;
+    AtCut kv, q;
+    size_t off_nlse, off_ndsum, off_arrived, off_part, total;
 };
+
+// Whether tiles of `steps` steps at most, `tiles` of them with `all` steps
+// together, are cut into items: where the longest is more than `most` times an
+// SM's share, into items of about that share, but of 8 steps at least (some 10
+// us; an item that is joined costs 3-5 more).
+AtCut plan_cut(long long tiles, long long steps, double all, double most) {
+    const double share = all / kNumSMs;
+    const long long chunk = std::max(8LL, (long long)share + 1);
+    AtCut c{(int)std::max(1LL, steps), 1, 0};
+    if (steps <= most * share || steps < chunk + chunk / 4 || tiles > 1024) return c;
+    c.chunk = (int)chunk;
+    c.chunks = (int)((steps + chunk - 1) / chunk);
+    c.tiles = (int)tiles;
+    return c;
+}
 
 void fill_strides(const cba_attn_strides_t &s, int heads, int dim, long long len, long long *out) {
     if (s.batch == 0 && s.token == 0 && s.head == 0) {
@@ -1189,9 +1343,24 @@ int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
     }
     const long long grid = std::max((long long)p->k_tiles * d->heads_kv, (long long)p->q_tiles * d->heads_q);
     if (grid * d->batch >= (1LL << 30) || rows >= (1LL << 40)) return CBA_ERR_UNSUPPORTED;
+    {
+        // steps of all tiles together; packed: as if all sequences were the longest
+        const double seqs = !d->packed ? d->batch
+                                       : std::min((double)d->batch, std::max((double)d->total_q / std::max(1, d->len_q),
+                                                                             (double)d->total_k / std::max(1, d->len_k)));
+        const double all = seqs * d->heads_q * p->q_tiles * p->k_tiles * (d->causal ? 0.5 : 1.0);
+        // SMs that are done with dk and dv go on to dq, so there a tile may take longer
+        p->kv = plan_cut((long long)p->k_tiles * d->heads_kv * d->batch,
+                         (long long)p->q_tiles * (d->heads_q / d->heads_kv), all, 1.75);
+        p->q = plan_cut((long long)p->q_tiles * d->heads_q * d->batch, p->k_tiles, all, 1.25);
+    }
     p->off_nlse = 256;
     p->off_ndsum = p->off_nlse + ((size_t)rows * 4 + 255) / 256 * 256;
-    p->total = p->off_ndsum + ((size_t)rows * 4 + 255) / 256 * 256;
+    p->off_arrived = p->off_ndsum + ((size_t)rows * 4 + 255) / 256 * 256;
+    p->off_part = p->off_arrived + ((size_t)(p->kv.tiles + p->q.tiles) * 4 + 255) / 256 * 256;
+    // the two kernels run at the same time where one ends: sums of their own
+    p->total = p->off_part + (size_t)kT * p->dp * 4 *
+                                 (2 * (size_t)p->kv.tiles * p->kv.chunks + (size_t)p->q.tiles * p->q.chunks);
     return CBA_OK;
 }
 
@@ -1212,8 +1381,9 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     cudaError_t e = cudaSuccess;
     if (!BF16) e = cudaMemsetAsync(a.status, 0, 256, st);  // the status word and the maxima
     if (e != cudaSuccess) return e;
-    // f16: the blocks that look for v's largest row
-    const int vb = BF16 ? 0 : kNumSMs;
+    // f16: the blocks that look for v's largest row, 256 rows or more each
+    const long long vrows = (d.packed ? d.total_k : (long long)d.batch * d.len_k) * d.heads_kv;
+    const int vb = BF16 ? 0 : (int)std::max(1LL, std::min<long long>(vrows / 256, 16 * kNumSMs));
     const unsigned qgrid = (unsigned)((long long)p.q_tiles * d.heads_q * d.batch);
     attn_prep_kernel<DP, BF16><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), vb);
     e = cudaGetLastError();
@@ -1226,15 +1396,21 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     if (e != cudaSuccess) return e;
     if (p.k_tiles > 0) {
         a.tiles = p.k_tiles;
-        a.items = (int)((long long)p.k_tiles * d.heads_kv * d.batch);
+        a.chunk = p.kv.chunk;
+        a.chunks = p.kv.chunks;
+        a.items = (int)((long long)p.k_tiles * d.heads_kv * d.batch) * a.chunks;
         e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)std::min(a.items, kNumSMs)),
                        dim3(kAtThreads), Kv<DP>::SMEM, st, tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
     }
     if (p.q_tiles > 0) {
         a.tiles = p.q_tiles;
-        a.items = (int)qgrid;
-        const unsigned blocks = std::min(qgrid, (unsigned)kNumSMs);
+        a.chunk = p.q.chunk;
+        a.chunks = p.q.chunks;
+        a.items = (int)qgrid * a.chunks;
+        a.arrived += p.kv.tiles;
+        a.part += 2 * (size_t)kT * p.dp * p.kv.tiles * p.kv.chunks;
+        const unsigned blocks = (unsigned)std::min(a.items, kNumSMs);
         // without keys there is no launch between this one and the preparation
         if (p.k_tiles > 0)
             e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(blocks), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[1],
@@ -1286,6 +1462,10 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.lse = lse;
     a.status = static_cast<unsigned *>(workspace);
     a.next = a.status + 2;
+    a.cnt_kv = p.kv.tiles;
+    a.cnt_q = p.q.tiles;
+    a.arrived = ws_at<unsigned>(workspace, p.off_arrived);
+    a.part = ws_at<float>(workspace, p.off_part);
     a.maxima = a.status + 4;
     a.nlse = ws_at<float>(workspace, p.off_nlse);
     a.ndsum = ws_at<float>(workspace, p.off_ndsum);

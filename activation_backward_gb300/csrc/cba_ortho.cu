@@ -217,48 +217,57 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        // the whole warp walks the loop and one elected lane issues (descriptors and
+        // counters are then uniform over the warp: half the issue time per MMA)
+        if (rank == 0) {
             const uint32_t idesc = ptx::idesc_f16(L::TM, BN, false, a.b_major != 0, a.a_major != 0);
-            // bytes of one K = 16 step, and between the 64-row boxes
-            const uint32_t sa = a.a_major ? 2048 : 32, sbk = a.b_major ? 2048 : 32;
+            // 16-byte units of one K = 16 step
+            const uint32_t sa = a.a_major ? 2048 >> 4 : 32 >> 4, sbk = a.b_major ? 2048 >> 4 : 32 >> 4;
             auto commit = [&](uint64_t *bar) {
                 if constexpr (CG == 2) ptx::mma_commit_pair(ptx::smem_u32(bar));
                 else ptx::mma_commit(ptx::smem_u32(bar));
             };
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity, ab, a.status, kNsLimitNs);
+                ptx::tc_fence_after();
+                return __all_sync(0xffffffffu, r) != 0;
+            };
             bool ok = true;
-            int gs = 0;
+            int s = 0;
+            uint32_t ph = 0;
             for (int i = 0; ok && i < mine; ++i) {
                 const int ac = i & 1;
-                if (i >= 2)
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.acc_empty[ac]), (uint32_t)(i / 2 - 1) & 1u,
-                                                ab, a.status, kNsLimitNs);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                for (int kb = 0; kb < nk; ++kb, ++gs) {
-                    const int s = gs % kNsStages;
-                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.full[s]), (uint32_t)(gs / kNsStages) & 1u, ab,
-                                                a.status, kNsLimitNs);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
+                if (i >= 2 && !(ok = wait(&sb.acc_empty[ac], (uint32_t)(i / 2 - 1) & 1u))) break;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!(ok = wait(&sb.full[s], ph))) break;
                     const uint32_t at = ptx::smem_u32(smem + s * L::STAGE);
+                    const ptx::Desc da = ptx::desc_of(at, a.a_major ? 8192 : 16, 1024, 2);
+                    const ptx::Desc db = ptx::desc_of(at + L::A_BYTES, a.b_major ? 8192 : 16, 1024, 2);
+                    if (ptx::elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < kNsBK / 16; ++ks) {
-                        const uint64_t da = ptx::smem_desc(at + ks * sa, a.a_major ? 8192 : 16, 1024, 2);
-                        const uint64_t db = ptx::smem_desc(at + L::A_BYTES + ks * sbk, a.b_major ? 8192 : 16, 1024, 2);
-                        const uint32_t acc = (kb > 0 || ks > 0) ? 1u : 0u;
-                        if constexpr (CG == 2) ptx::mma_f16_pair(tmem + ac * BN, da, db, idesc, acc);
-                        else ptx::mma_f16(tmem + ac * BN, da, db, idesc, acc);
+                        for (int ks = 0; ks < kNsBK / 16; ++ks) {
+                            const uint32_t acc = (kb > 0 || ks > 0) ? 1u : 0u;
+                            if constexpr (CG == 2)
+                                ptx::mma_f16_pair(tmem + ac * BN, da, ks * sa, db, ks * sbk, idesc, acc);
+                            else
+                                ptx::mma_f16(tmem + ac * BN, da, ks * sa, db, ks * sbk, idesc, acc);
+                        }
+                        commit(&sb.empty[s]);
+                        if (kb + 1 == nk) commit(&sb.acc_full[ac]);
                     }
-                    commit(&sb.empty[s]);
+                    __syncwarp();
+                    if (++s == kNsStages) s = 0, ph ^= 1;
                 }
-                if (ok) commit(&sb.acc_full[ac]);
             }
-            if (!ok) *ab = 1;
             // every MMA issued has finished before TMEM is released
-            if constexpr (CG == 2) ptx::mma_commit_pair(ptx::smem_u32(&sb.drain));
-            else ptx::mma_commit(ptx::smem_u32(&sb.drain));
+            if (ptx::elect_one()) {
+                if (!ok) *ab = 1;
+                commit(&sb.drain);
+            }
+            __syncwarp();
             int no = 0;
             ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kNsLimitNs);
+            __syncwarp();
         }
     } else {
         const int quarter = warp & 3;
@@ -611,22 +620,30 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
         return __syncthreads_and(ok) != 0;
     };
     auto product = [&](uint32_t d, uint32_t u, int ksteps) {  // D = U U^T, R columns
-        for (int ks = 0; ks < ksteps; ++ks) {
-            const uint64_t de = ptx::smem_desc(u + (ks >> 2) * box + (ks & 3) * 32, 16, 1024, 2);
-            ptx::mma_f16(d, de, de, id_s, ks > 0);
+        const ptx::Desc de = ptx::desc_of(u, 16, 1024, 2);
+        if (ptx::elect_one()) {
+#pragma unroll 4
+            for (int ks = 0; ks < ksteps; ++ks) {
+                const uint32_t off = ((ks >> 2) * box + (ks & 3) * 32) >> 4;
+                ptx::mma_f16(d, de, off, de, off, id_s, ks > 0);
+            }
+            ptx::mma_commit(ptx::smem_u32(&sb.sq));
         }
-        ptx::mma_commit(ptx::smem_u32(&sb.sq));
+        __syncwarp();
     };
     auto apply = [&](int ch) {  // the 256 columns of X' from box 4 ch on
         const uint32_t id = ptx::idesc_f16(128, 64 * min(4, a.nb - 4 * ch), false, true);
-        for (int ks = 0; ks < km; ++ks)
-            ptx::mma_f16(tX, ptx::smem_desc(uC + (ks >> 2) * box + (ks & 3) * 32, 16, 1024, 2),
-                         ptx::smem_desc(uX + 4 * ch * box + ks * 2048, box, 1024, 2), id, ks > 0);
-        ptx::mma_commit(ptx::smem_u32(&sb.x));
+        const ptx::Desc dc = ptx::desc_of(uC, 16, 1024, 2), dx = ptx::desc_of(uX + 4 * ch * box, box, 1024, 2);
+        if (ptx::elect_one()) {
+            for (int ks = 0; ks < km; ++ks)
+                ptx::mma_f16(tX, dc, ((ks >> 2) * box + (ks & 3) * 32) >> 4, dx, ks * (2048 >> 4), id, ks > 0);
+            ptx::mma_commit(ptx::smem_u32(&sb.x));
+        }
+        __syncwarp();
     };
     bool ok = true;
     for (int step = 0; ok && step < a.steps; ++step) {
-        if (tid == 0) product(tS, uX, kn);
+        if (warp == 0) product(tS, uX, kn);
         if (!(ok = wait(&sb.sq, ph_sq))) break;
         float s[CS];
         if (mine) {
@@ -637,7 +654,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
             box_put<__half>(ss, R, r, c_s, s);
         }
         publish();
-        if (tid == 0) product(tQ, uS, km);
+        if (warp == 0) product(tQ, uS, km);
         if (!(ok = wait(&sb.sq, ph_sq))) break;
         if (mine) {
             float q[CS];
@@ -654,7 +671,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
         const bool last = step + 1 == a.steps;
         const float alpha = (last ? a.scale / a.held : 1.f) / kNsSym;
         for (int ch = 0; ok && ch < nchunks; ++ch) {
-            if (tid == 0) apply(ch);
+            if (warp == 0) apply(ch);
             if (!(ok = wait(&sb.x, ph_x))) break;
             const int boxes = min(4, a.nb - 4 * ch);
             if (mine && part < boxes)

@@ -392,26 +392,40 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b
            ((a_mmajor ? 1u : 0u) << 15) | ((b_nmajor ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16, one CTA.
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+// A shared-memory matrix descriptor as two words: the low one holds the address
+// in 16-byte units (steps are additions to it) and the leading offset, the high
+// one the stride offset and the modes.
+struct Desc {
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc desc_of(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes, uint32_t swizzle) {
+    const uint64_t d = smem_desc(saddr, lbo_bytes, sbo_bytes, swizzle);
+    return Desc{(uint32_t)d, (uint32_t)(d >> 32)};
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f16, one CTA; the operands' addresses
+// moved on by da and db 16-byte units.
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, Desc a, uint32_t da, Desc b, uint32_t db, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo + da), "r"(a.hi), "r"(b.lo + db), "r"(b.hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
 // The same with A in TMEM: 128 lanes x 8 columns of two packed 16-bit values
 // (the even k in the low half) per K = 16 step.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t db, uint32_t idesc,
+                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b.lo + db), "r"(b.hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -463,13 +477,14 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 // As mma_f16, over both blocks' tensor cores: A's rows and B's rows are split
 // between the two blocks' shared memory (the descriptors hold for both).
-__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, Desc a, uint32_t da, Desc b, uint32_t db,
                                              uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo + da), "r"(a.hi), "r"(b.lo + db), "r"(b.hi), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // Arrives on the barrier at this offset in both blocks of the pair once all

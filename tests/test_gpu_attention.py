@@ -130,6 +130,30 @@ def test_more_tiles_than_blocks(cuda_lib, dim, dtype, causal):
         assert all(torch.equal(a, b) for a, b in zip(first, run(*args, 0.1, causal)))
 
 
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF)], ids=str)
+@pytest.mark.parametrize("len_q,len_k,hq,hk", [(1100, 1500, 4, 1), (3, 2700, 2, 1), (2700, 3, 2, 2), (1500, 1100, 8, 1)])
+def test_few_tiles_cut_into_items(cuda_lib, len_q, len_k, hq, hk, dim, dtype, causal):
+    """Too few tiles for the SMs: their steps are shared out and the sums joined, with the same bits every time."""
+    rng = np.random.default_rng(len_q + hq)
+    args = make(rng, 1, len_q, len_k, hq, hk, dim, dtype, "bshd", 0.1, causal)
+    first = [t.clone() for t in run(*args, 0.1, causal)]
+    compare(args, first, 0.1, causal, dtype)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, run(*args, 0.1, causal)))
+
+
+def test_packed_tiles_cut_into_items(cuda_lib):
+    rng = np.random.default_rng(11)
+    lens = [0, 1700, 5, 900, 130]
+    parts, args, cu = pack(rng, lens, lens, 4, 1, 128, BF, 0.1, True)
+    outs = run(*args, 0.1, True, cu_q=cu[0], cu_k=cu[1], sequences=5, max_q=1700, max_k=1700)
+    at = 0
+    for p, n in zip(parts, lens):
+        compare(p, [g[None, at:at + n] for g in outs], 0.1, True, BF)
+        at += n
+
+
 @pytest.mark.parametrize("dim,dtype", [(64, BF), (128, F16)], ids=str)
 def test_many_packed_sequences(cuda_lib, dim, dtype):
     rng = np.random.default_rng(dim)
