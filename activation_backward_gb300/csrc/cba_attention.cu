@@ -73,9 +73,9 @@ struct AtArgs {
     int cnt_kv, cnt_q;           // tiles that have an arrival counter
     unsigned *arrived;           // this launch's counters (kv's lie before q's)
     float *part;                 // fp32 tiles of the items of a tile
-    const void *q, *o, *dout, *v;
+    const void *o, *dout, *v;
     void *dq, *dk, *dv;
-    long long sq[3], so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
+    long long so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
 };
 
 // The sequence b: its first query and key token, its lengths, and the first
@@ -240,17 +240,16 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
 // early): its arrival for the next tile must not count for this one.
 template <int NA, int NB>
 struct AtBars {
-    uint64_t stat;                     // the item's own two tiles
+    uint64_t stat[2];                  // the item's own two tiles
     uint64_t a_full[NA], a_empty[NA];  // the ring used by the accumulating product
     uint64_t b_full[NB], b_empty[NB];
     uint64_t r_full[4], r_empty[4];    // row statistics (kv kernel)
     uint64_t s_full[2], p_ready[2];
     uint64_t dp_full[2], ds_ready[2];
-    uint64_t fix, drain, acc, stat_empty;
-    uint64_t acc_empty;                // the epilogue has read the accumulators
+    uint64_t fix, drain, acc, stat_empty[2];
     uint64_t i_full[2], i_empty[2];    // work items handed out
     uint64_t join;                     // the compute warps, around an arrival
-    int item[2], last;
+    int last;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -387,6 +386,39 @@ __device__ __forceinline__ void store_row(uint32_t ta, float scale, bool zero, b
     }
 }
 
+// 32 rows x 32 columns of a warp's accumulators, stored through 2 KB of shared
+// memory of its own: row = lane, its 16-byte chunk j at j ^ ((row >> 1) & 3); then
+// four lanes store a row's 64 bytes.
+template <bool BF16>
+__device__ __forceinline__ void store_rows_staged(uint32_t ta, float scale, bool zero, int live, uint16_t *out,
+                                                  long long stride, int cols, uint8_t *stage) {
+    const int lane = threadIdx.x & 31;
+    float v[32];
+    if (!zero) {
+        ptx::tmem_ld32(ta, v);
+        ptx::tmem_ld_wait();
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint4 w;
+        uint32_t *u = &w.x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            u[e] = zero ? 0u : pack2<BF16>(v[8 * j + 2 * e] * scale, v[8 * j + 2 * e + 1] * scale);
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+    }
+    __syncwarp();
+    const int j = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        if (r < live && j * 8 < cols)
+            *reinterpret_cast<uint4 *>(out + r * stride + j * 8) =
+                *reinterpret_cast<const uint4 *>(stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+    }
+    __syncwarp();
+}
+
 __device__ __forceinline__ void at_init_bars(uint64_t *first, int n, uint32_t count) {
     for (int i = 0; i < n; ++i) ptx::mbar_init(ptx::smem_u32(first + i), count);
 }
@@ -445,20 +477,20 @@ __device__ __forceinline__ void finish_mmas(bool ok, Bars &sb, unsigned *status)
 // the one that arrives last adds all of them in the order of the steps, so the
 // result does not depend on who that is.
 
-// Load warp: hands item number k to the other warps.  False past the last item.
-template <typename Bars>
-__device__ __forceinline__ bool hand_out(const AtArgs &a, int k, int item, Bars &sb, bool &ok) {
+// Load warp: hands item number k to the other warps (tile < 0: there is none).
+template <typename Item, typename Bars>
+__device__ __forceinline__ bool hand_out(const AtArgs &a, int k, const Item &w, Item *slots, Bars &sb, bool &ok) {
     if (k >= 2)
         ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(&sb.i_empty[k & 1]), (uint32_t)(k / 2 - 1) & 1u,
                                           &sb.abort_flag, a.status, kAtLimitNs);
     ok = __all_sync(0xffffffffu, ok) != 0;
     if (!ok) return false;
     if ((threadIdx.x & 31) == 0) {
-        *const_cast<volatile int *>(&sb.item[k & 1]) = item;
+        slots[k & 1] = w;
         ptx::mbar_arrive(ptx::smem_u32(&sb.i_full[k & 1]));
     }
     __syncwarp();
-    return item < a.items;
+    return w.tile >= 0;
 }
 __device__ __forceinline__ int next_item(unsigned *next) {
     unsigned v = 0;
@@ -466,18 +498,19 @@ __device__ __forceinline__ int next_item(unsigned *next) {
     return (int)gridDim.x + (int)__shfl_sync(0xffffffffu, v, 0);
 }
 
-// The k-th item of this block, or -1 past the last (or on a timeout).  Called by
-// whole warps.
-template <typename Bars>
-__device__ __forceinline__ int take_item(const AtArgs &a, int k, Bars &sb, bool &ok) {
+// The k-th item of this block, or NULL past the last (or on a timeout); it stays
+// until all readers are done with it.  Called by whole warps.
+template <typename Item, typename Bars>
+__device__ __forceinline__ const Item *take_item(const AtArgs &a, int k, const Item *slots, Bars &sb, bool &ok) {
     ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.i_full[k & 1]), (uint32_t)(k / 2) & 1u, &sb.abort_flag, a.status,
                                 kAtLimitNs);
     ok = __all_sync(0xffffffffu, ok) != 0;
-    if (!ok) return -1;
-    const int item = *const_cast<volatile int *>(&sb.item[k & 1]);
+    return ok && slots[k & 1].tile >= 0 ? slots + (k & 1) : nullptr;
+}
+template <typename Bars>
+__device__ __forceinline__ void done_item(int k, Bars &sb) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.i_empty[k & 1]));
-    return item < a.items ? item : -1;
 }
 constexpr int kItemReaders = 1 + kAtWarps;  // the MMA and compute warps
 
@@ -557,14 +590,6 @@ __device__ __forceinline__ void store_sums(const float4 *at, int used, long long
     }
 }
 
-// The same number, computed with anew: what is derived from it after a long loop
-// is not kept in registers through it.
-__device__ __forceinline__ int afresh(int v) {
-    int r;
-    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
 // Bars of one pipeline stage's ring: initialised by one thread.
 template <typename Bars>
 __device__ __forceinline__ void init_common(Bars &sb) {
@@ -572,8 +597,7 @@ __device__ __forceinline__ void init_common(Bars &sb) {
     at_init_bars(sb.p_ready, 2, kAtWarps);
     at_init_bars(sb.dp_full, 2, 1);
     at_init_bars(sb.ds_ready, 2, kAtWarps);
-    at_init_bars(&sb.fix, 4, 1);  // fix, drain, acc, stat_empty
-    at_init_bars(&sb.acc_empty, 1, kAtWarps);
+    at_init_bars(&sb.fix, 3, 1);  // fix, drain, acc
     at_init_bars(&sb.join, 1, kAtWarps);
     at_init_bars(sb.i_full, 2, 1);
     at_init_bars(sb.i_empty, 2, kItemReaders);
@@ -593,15 +617,21 @@ __device__ __forceinline__ void drain_ring(uint64_t *bars, int stages, int count
 
 // At dim 64 and less TMEM has room for two S tiles: S of the tile after next is
 // computed once dv has used P, so that the compute warps find the next S ready.
-// At larger dims S(i + 1) overwrites P(i) and the warps wait for it.
+// At larger dims S(i + 1) overwrites P(i) and the warps wait for it.  Shared
+// memory there is full with one K and V tile; below, the next item's come while
+// this one's are in use, and the results pass through a stage so that a warp
+// stores 64 bytes of 8 rows at a time instead of 16 bytes of 32.
 template <int DP>
 struct Kv {
     static constexpr int NS = DP == 64 ? 2 : 1;               // S buffers
-    // stages of q, of do, of the row statistics (dim 128 fills shared memory)
-    static constexpr int QST = DP == 64 ? 4 : 3, DOST = DP == 64 ? 4 : 2, RST = DP == 64 ? 4 : 2;
+    static constexpr int KVB = DP == 64 ? 2 : 1;              // K and V tiles
+    // stages of q, of do, of the row statistics
+    static constexpr int QST = DP == 64 ? 4 : 3, DOST = DP == 64 ? 3 : 2, RST = DP == 64 ? 4 : 2;
     using Bars = AtBars<QST, DOST>;
-    static constexpr uint32_t TILES = (2 + QST + DOST) * (DP / 64) * kBoxBytes;
-    static constexpr uint32_t SMEM = TILES + RST * 1024 + sizeof(Bars);
+    static constexpr uint32_t TILES = (2 * KVB + QST + DOST) * (DP / 64) * kBoxBytes;
+    static constexpr uint32_t STAGE = DP == 64 ? kAtWarps * 2048 : 0;
+    static constexpr uint32_t ROWS = TILES + STAGE, BARS = ROWS + RST * 1024;
+    static constexpr uint32_t SMEM = BARS + sizeof(Bars) + 2 * 128;  // and the items
 };
 
 struct KvItem {
@@ -611,6 +641,7 @@ struct KvItem {
     int tile, c, used;
     bool live;       // there are keys, and steps or zeros to be stored
 };
+static_assert(sizeof(KvItem) <= 128);
 
 __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
     KvItem w;
@@ -646,18 +677,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                    const AtArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t TILE = DP / 64 * kBoxBytes;
-    constexpr int NS = Kv<DP>::NS, kQStages = Kv<DP>::QST, kDoStages = Kv<DP>::DOST, kRStages = Kv<DP>::RST;
+    constexpr int NS = Kv<DP>::NS, KVB = Kv<DP>::KVB, kQStages = Kv<DP>::QST, kDoStages = Kv<DP>::DOST, kRStages = Kv<DP>::RST;
     const uint32_t sbase = ptx::smem_u32(smem);
-    const uint32_t sK = sbase, sV = sK + TILE, sQ = sV + TILE, sDo = sQ + kQStages * TILE;
-    float *rows = reinterpret_cast<float *>(smem + Kv<DP>::TILES);
-    auto &sb = *reinterpret_cast<typename Kv<DP>::Bars *>(smem + Kv<DP>::TILES + kRStages * 1024);
+    const uint32_t sK = sbase, sV = sK + KVB * TILE, sQ = sV + KVB * TILE, sDo = sQ + kQStages * TILE;
+    float *rows = reinterpret_cast<float *>(smem + Kv<DP>::ROWS);
+    auto &sb = *reinterpret_cast<typename Kv<DP>::Bars *>(smem + Kv<DP>::BARS);
+    KvItem *slots = reinterpret_cast<KvItem *>(&sb + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (sbase & 1023) {  // the swizzled tiles need it
         if (tid == 0) atomicOr(a.status, kStatusTimeout);
         return;
     }
     if (tid == 0) {
-        at_init_bars(&sb.stat, 1, 1);
+        at_init_bars(sb.stat, KVB, 1);
+        at_init_bars(sb.stat_empty, KVB, 1);
         at_init_bars(sb.a_full, kQStages, 1);
         at_init_bars(sb.a_empty, kQStages, 1);
         at_init_bars(sb.b_full, kDoStages, 1);
@@ -693,25 +726,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ok = __all_sync(0xffffffffu, ok) != 0;
             return ok;
         };
-        auto live = [&](int item) {  // the first item from this one on with anything to do
-            while ((packed || a.chunks > 1) && item < a.items && !kv_item(a, item).live) item = next_item(a.next);
-            return item;
-        };
-        for (int k = 0, item = live((int)blockIdx.x); hand_out(a, k, item, sb, ok); ++k, item = live(next_item(a.next))) {
-            const KvItem w = kv_item(a, item);
-            if (w.n == 0) continue;
-            const int tb = packed ? 0 : w.b;
-            if (gt > 0 && !wait(&sb.stat_empty, (uint32_t)(gt - 1))) break;
-            if (lane == 0) {
-                const uint32_t bar = ptx::smem_u32(&sb.stat);
-                ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
-#pragma unroll
-                for (int j = 0; j < DP / 64; ++j) {
-                    ptx::tma_load_4d(sK + j * kBoxBytes, &tk, j * 64, (int)w.s.k0 + w.k0, w.h, tb, bar);
-                    ptx::tma_load_4d(sV + j * kBoxBytes, &tv, j * 64, (int)w.s.k0 + w.k0, w.h, tb, bar);
-                }
+        // the next item from `item` on with anything to do
+        auto live = [&](int item) {
+            KvItem w{};
+            w.tile = -1;
+            for (; item < a.items; item = next_item(a.next)) {
+                w = kv_item(a, item);
+                if (w.live) break;
+                w.tile = -1;
             }
-            ++gt;
+            return w;
+        };
+        KvItem w = live((int)blockIdx.x);
+        for (int k = 0; hand_out(a, k, w, slots, sb, ok); ++k, w = live(next_item(a.next))) {
+            const int tb = packed ? 0 : w.b;
             for (int it = 0; ok && it < w.n; ++it) {
                 const int t = w.it0 + it, g = t / w.nq, q0 = (w.qt_begin + t - g * w.nq) * kT, hq = w.h * a.group + g;
                 const int valid = min(kT, w.s.lq - q0);
@@ -734,11 +762,29 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 ++ndo_begun;
                 ok = load_tile<DP>(sDo + sd * TILE, &tdo, w.s.q0 + q0, hq, tb, valid, packed,
                                    ptx::smem_u32(&sb.b_full[sd]), bfix, fphase, ab, a.status);
+                if (!ok) break;
+                if (it == 0) {  // K and V, once the item that used their tiles before is through with them:
+                                // the last to be free
+                    const int sk = gt % KVB;
+                    if (gt >= KVB && !wait(&sb.stat_empty[sk], (uint32_t)(gt / KVB - 1))) break;
+                    ++gt;
+                    if (lane == 0) {
+                        const uint32_t bar = ptx::smem_u32(&sb.stat[sk]);
+                        ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
+#pragma unroll
+                        for (int j = 0; j < DP / 64; ++j) {
+                            const uint32_t to = sk * TILE + j * kBoxBytes;
+                            ptx::tma_load_4d(sK + to, &tk, j * 64, (int)w.s.k0 + w.k0, w.h, tb, bar);
+                            ptx::tma_load_4d(sV + to, &tv, j * 64, (int)w.s.k0 + w.k0, w.h, tb, bar);
+                        }
+                    }
+                    __syncwarp();
+                }
             }
             if (!ok) break;
         }
         if (!ok) {
-            drain_ring(&sb.stat, 1, gt, a.status);
+            drain_ring(sb.stat, KVB, gt, a.status);
             drain_ring(sb.a_full, kQStages, nq_begun, a.status);
             drain_ring(sb.b_full, kDoStages, ndo_begun, a.status);
             drain_ring(sb.r_full, kRStages, nr_begun, a.status);
@@ -756,26 +802,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         Ring rs, rk, rp, rv;   // q's ring for S and for dk, do's for dP and for dv
         int gt = 0, js = 0, jp = 0;  // items; tiles of S, tiles of dv so far
         auto mma_s = [&]() {
-            mma_rows<DP>(tS + js % NS * 128, sK, sQ + rs.s * TILE, steps, id_s, &sb.s_full[js & 1]);
+            mma_rows<DP>(tS + js % NS * 128, sK + gt % KVB * TILE, sQ + rs.s * TILE, steps, id_s, &sb.s_full[js & 1]);
             rs.step(kQStages);
             ++js;
         };
         auto mma_dp = [&](bool last) {  // the item's last product of K's and V's tiles
-            mma_rows<DP>(tDp, sV, sDo + rp.s * TILE, steps, id_s, &sb.dp_full[0], last ? &sb.stat_empty : nullptr);
+            mma_rows<DP>(tDp, sV + gt % KVB * TILE, sDo + rp.s * TILE, steps, id_s, &sb.dp_full[0],
+                         last ? &sb.stat_empty[gt % KVB] : nullptr);
             rp.step(kDoStages);
         };
-        for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
-            const int n = kv_item(a, item).n;
+        const KvItem *w;
+        for (int k = 0; (w = take_item(a, k, slots, sb, ok)) != nullptr; ++k) {
+            const int n = w->n;
+            done_item(k, sb);
             if (n == 0) continue;
-            const AtWait stat{&sb.stat, (uint32_t)gt}, freed{&sb.acc_empty, (uint32_t)(gt - 1)};
+            const AtWait stat{&sb.stat[gt % KVB], (uint32_t)(gt / KVB)};
             if (!wait(stat, full_q(rs))) break;
             mma_s();
             if (NS == 2 && n > 1) {
                 if (!wait(full_q(rs), full_q(rs))) break;
                 mma_s();
             }
-            // dv and dk overwrite the accumulators of the item before
-            if (!wait(full_do(rp), gt > 0 ? freed : stat)) break;
+            if (!wait(full_do(rp), stat)) break;
             mma_dp(n == 1);
             for (int it = 0; it < n; ++it, ++jp) {
                 const bool ms = it + NS < n, md = it + 1 < n;  // more S, more dP to come
@@ -783,7 +831,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (!wait(pr, ms ? full_q(rs) : pr)) break;
                 mma_acc(tDv, tS + jp % NS * 128, sDo + rv.s * TILE, id_a, it > 0, &sb.b_empty[rv.s]);
                 rv.step(kDoStages);
-                // S overwrites P, dP overwrites dS: this warp's MMAs run in the order of issue
+                // S overwrites P, dP overwrites dS: this warp's MMAs run in the order of issue.
+                // (The first dv and dk overwrite the item before's, which the compute warps
+                // have stored before the P that they follow.)
                 if (ms) mma_s();
                 if (!wait(dr, md ? full_do(rp) : dr)) break;
                 mma_acc(tDk, tDp, sQ + rk.s * TILE, id_a, it > 0, &sb.a_empty[rk.s]);
@@ -810,16 +860,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         };
         int gt = 0, g0 = 0;
         uint32_t joined = 0;
-        for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
-            int n;
+        const KvItem *w;
+        for (int k = 0; (w = take_item(a, k, slots, sb, ok)) != nullptr; ++k) {
+            const int n = w->n;
             {
-                const KvItem w = kv_item(a, item);
-                n = w.n;
-                const int begin = w.qt_begin * kT, end = begin + w.nq * kT;
+                const int begin = w->qt_begin * kT, end = begin + w->nq * kT;
                 // this thread's key is seen by the queries from here on, the tile's last one by those from `all` on
-                const int sees = w.k0 + quarter * 32 + lane - w.off, all = w.k0 + kT - 1 - w.off;
+                const int sees = w->k0 + quarter * 32 + lane - w->off, all = w->k0 + kT - 1 - w->off;
                 // the step's first query, over the group's heads in turn
-                int q0 = n > 0 ? begin + w.it0 % w.nq * kT : 0;
+                int q0 = n > 0 ? begin + w->it0 % w->nq * kT : 0;
                 for (int it = 0; it < n; ++it) {
                     const int i = g0 + it, sr = i % kRStages;
                     const float *nl = rows + sr * 2 * kT + wg * 32, *nd = nl + kT;
@@ -872,31 +921,34 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ptx::tc_fence_after();
             {
                 // warpgroups 0 and 1 store dv, 2 and 3 dk, half of the columns each
-                const KvItem w = kv_item(a, afresh(item));
                 const bool isk = wg >= 2;
-                const int c0 = (wg & 1) * (DP / 2), j = w.k0 + quarter * 32 + lane;  // this thread's key
+                const int c0 = (wg & 1) * (DP / 2), row = w->k0 + quarter * 32;  // the warp's first key
                 const long long *sg = isk ? a.sdk : a.sdv;
-                uint16_t *out = static_cast<uint16_t *>(isk ? a.dk : a.dv) + (packed ? 0 : w.b) * sg[0] +
-                                (w.s.k0 + j) * sg[1] + w.h * sg[2] + c0;
+                uint16_t *out = static_cast<uint16_t *>(isk ? a.dk : a.dv) + (packed ? 0 : w->b) * sg[0] +
+                                (w->s.k0 + row) * sg[1] + w->h * sg[2] + c0;
                 const float f = isk ? a.scale / sds : (BF16 ? 1.f : exp2f(-kPShift));
                 const uint32_t acc = (isk ? tDk : tDv) + lanes + c0;
                 constexpr long long ITEM = 2 * DP * kT / 4;  // float4 of an item's sums
-                float4 *at = reinterpret_cast<float4 *>(a.part) + w.tile * a.chunks * ITEM + wg * (DP / 2) / 4 * kT +
+                float4 *at = reinterpret_cast<float4 *>(a.part) + w->tile * a.chunks * ITEM + wg * (DP / 2) / 4 * kT +
                              quarter * 32 + lane;
-                if (w.used == 1) store_row<DP / 2, BF16>(acc, f, n == 0, j < w.s.lk, out, a.dim - c0);
-                else sums_to_memory<DP / 2>(acc, at + w.c * ITEM);
-                if (n > 0) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
-                    ++gt;
-                }
-                if (w.used > 1) {
-                    const bool last = arrive_last(a, w.tile, w.used, sb, joined, ok);
+                const int live = w->s.lk - row;  // of the warp's rows
+                if (w->used > 1)
+                    sums_to_memory<DP / 2>(acc, at + w->c * ITEM);
+                else if constexpr (Kv<DP>::STAGE > 0)
+                    store_rows_staged<BF16>(acc, f, n == 0, live, out, sg[1], a.dim - c0,
+                                            smem + Kv<DP>::TILES + (warp - 4) * 2048);
+                else
+                    store_row<DP / 2, BF16>(acc, f, n == 0, lane < live, out + lane * sg[1], a.dim - c0);
+                ptx::tc_fence_before();
+                if (n > 0) ++gt;
+                if (w->used > 1) {
+                    const bool last = arrive_last(a, w->tile, w->used, sb, joined, ok);
                     if (!ok) break;
-                    if (last) store_sums<DP / 2, BF16>(at, w.used, ITEM, f, j < w.s.lk, out, a.dim - c0);
+                    if (last)
+                        store_sums<DP / 2, BF16>(at, w->used, ITEM, f, lane < live, out + lane * sg[1], a.dim - c0);
                 }
             }
+            done_item(k, sb);
             g0 += n;
         }
     }
@@ -913,16 +965,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 // The item's q and do rows are A operands of every tile's products, so they lie
 // in TMEM (16-bit, 32 or 64 columns each): the products then read one operand
 // from shared memory instead of two, whose 128 bytes per cycle are what an MMA
-// of 128 columns with both operands there waits for (one tile of dim 128: 2230 cycles
-// against 2270, and 64 KB more for the rings).  At dim 128 that leaves room for one
-// dP, below it for two, of which one is computed while the other's dS is used.
-constexpr int kKStages = 4, kVStages = 3;
-using QBars = AtBars<kKStages, kVStages>;
-
+// of 128 columns with both operands there waits for.  They come there through
+// shared memory, where the next item's wait while this one runs.  At dim 128 TMEM
+// has room for one dP, below it for two, of which one is computed while the
+// other's dS is used.
 template <int DP>
-constexpr uint32_t q_smem_bytes() {
-    return (kKStages + kVStages) * (DP / 64) * kBoxBytes + sizeof(QBars);
-}
+struct Qk {
+    static constexpr int NB = DP == 64 ? 2 : 1;   // dP buffers
+    static constexpr int KST = DP == 64 ? 4 : 3, VST = DP == 64 ? 3 : 2;
+    using Bars = AtBars<KST, VST>;
+    static constexpr uint32_t TILES = (2 + KST + VST) * (DP / 64) * kBoxBytes;
+    static constexpr uint32_t SMEM = TILES + sizeof(Bars) + 2 * 128;  // and the items
+};
 
 // D[128 x 128] = A[128 x dim] B[128 x dim]^T, A in TMEM.
 template <int DP>
@@ -945,17 +999,6 @@ __device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t ta, uint32_t sb
     __syncwarp();
 }
 
-// WORDS 32-bit words (pairs of elements) of a row from `first` on; zeros past `dim`.
-template <int WORDS>
-__device__ __forceinline__ void row_words(uint32_t (&w)[16], const uint16_t *row, bool live, int dim, int first) {
-#pragma unroll
-    for (int j = 0; j < WORDS; j += 4) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live && 2 * (first + j) < dim) v = *reinterpret_cast<const uint4 *>(row + 2 * (first + j));
-        w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
-    }
-}
-
 struct QItem {
     AtSeq s;
     int b, h, q0, off;
@@ -963,6 +1006,7 @@ struct QItem {
     int tile, c, used;
     bool live;       // there are queries, and steps or zeros to be stored
 };
+static_assert(sizeof(QItem) <= 128);
 
 __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
     QItem w;
@@ -994,21 +1038,25 @@ __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
 
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(kAtThreads, 1)
-    attn_q_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+    attn_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                   const AtArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr uint32_t TILE = DP / 64 * kBoxBytes;
     const uint32_t sbase = ptx::smem_u32(smem);
-    constexpr int NB = DP == 64 ? 2 : 1;  // dP buffers
-    const uint32_t sK = sbase, sV = sK + kKStages * TILE;
-    QBars &sb = *reinterpret_cast<QBars *>(smem + (kKStages + kVStages) * TILE);
+    constexpr int NB = Qk<DP>::NB, kKStages = Qk<DP>::KST, kVStages = Qk<DP>::VST;
+    const uint32_t sQ = sbase, sDo = sQ + TILE, sK = sDo + TILE, sV = sK + kKStages * TILE;
+    auto &sb = *reinterpret_cast<typename Qk<DP>::Bars *>(smem + Qk<DP>::TILES);
+    QItem *slots = reinterpret_cast<QItem *>(&sb + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (sbase & 1023) {
         if (tid == 0) atomicOr(a.status, kStatusTimeout);
         return;
     }
     if (tid == 0) {
-        at_init_bars(&sb.stat, 1, kAtWarps);  // the rows in TMEM
+        at_init_bars(&sb.stat[0], 1, kAtWarps);  // the rows in TMEM
+        at_init_bars(&sb.stat[1], 1, 1);         // in shared memory
+        at_init_bars(sb.stat_empty, 1, kAtWarps);
         at_init_bars(sb.a_full, kKStages, 1);
         at_init_bars(sb.a_empty, kKStages, 1);
         at_init_bars(sb.b_full, kVStages, 1);
@@ -1041,13 +1089,33 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return ok;
         };
         auto live = [&](int item) {
-            while ((packed || a.chunks > 1) && item < a.items && !q_item(a, item).live) item = next_item(a.next + 1);
-            return item;
+            QItem w{};
+            w.tile = -1;
+            for (; item < a.items; item = next_item(a.next + 1)) {
+                w = q_item(a, item);
+                if (w.live) break;
+                w.tile = -1;
+            }
+            return w;
         };
-        for (int k = 0, item = live((int)blockIdx.x); hand_out(a, k, item, sb, ok);
-             ++k, item = live(next_item(a.next + 1))) {
-            const QItem w = q_item(a, item);
+        QItem w = live((int)blockIdx.x);
+        int gt = 0;
+        for (int k = 0; hand_out(a, k, w, slots, sb, ok); ++k, w = live(next_item(a.next + 1))) {
             const int tb = packed ? 0 : w.b, hk = w.h / a.group;
+            if (w.n == 0) continue;
+            // rows past a packed sequence's last are its neighbour's: their results are not stored
+            if (gt > 0 && !wait(sb.stat_empty, (uint32_t)(gt - 1))) break;
+            ++gt;
+            if (lane == 0) {
+                const uint32_t bar = ptx::smem_u32(&sb.stat[1]);
+                ptx::mbar_arrive_expect_tx(bar, 2 * TILE);
+#pragma unroll
+                for (int j = 0; j < DP / 64; ++j) {
+                    ptx::tma_load_4d(sQ + j * kBoxBytes, &tq, j * 64, (int)w.s.q0 + w.q0, w.h, tb, bar);
+                    ptx::tma_load_4d(sDo + j * kBoxBytes, &tdo, j * 64, (int)w.s.q0 + w.q0, w.h, tb, bar);
+                }
+            }
+            __syncwarp();
             for (int it = 0; ok && it < w.n; ++it) {
                 const int st = nk_begun % kKStages, sv = nv_begun % kVStages;
                 const int key = (w.it0 + it) * kT, valid = min(kT, w.s.lk - key);
@@ -1064,6 +1132,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (!ok) break;
         }
         if (!ok) {
+            drain_ring(&sb.stat[1], 1, gt, a.status);
             drain_ring(sb.a_full, kKStages, nk_begun, a.status);
             drain_ring(sb.b_full, kVStages, nv_begun, a.status);
         }
@@ -1086,14 +1155,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             rv.step(kVStages);
             ++js;
         };
-        for (int k = 0, item; (item = take_item(a, k, sb, ok)) >= 0; ++k) {
-            const int n = q_item(a, item).n;
+        const QItem *w;
+        for (int k = 0; (w = take_item(a, k, slots, sb, ok)) != nullptr; ++k) {
+            const int n = w->n;
+            done_item(k, sb);
             if (n == 0) continue;
-            const AtWait stat{&sb.stat, (uint32_t)gt}, freed{&sb.acc_empty, (uint32_t)(gt - 1)};
+            const AtWait stat{&sb.stat[0], (uint32_t)gt};
             if (!wait(stat, full_k(rs))) break;
             mma_s();
-            // dq overwrites the accumulator of the item before
-            if (!wait(full_v(rv), gt > 0 ? freed : stat)) break;
+            if (!wait(full_v(rv), stat)) break;
             mma_dp();
             for (int it = 0; it < n; ++it, ++jp) {
                 const bool more = it + 1 < n;
@@ -1107,7 +1177,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (!wait(dr, more && NB == 1 ? full_v(rv) : dr)) break;
                 mma_acc(tDq, tDp + jp % NB * 128, sK + rq.s * TILE, id_a, it > 0, &sb.a_empty[rq.s]);
                 rq.step(kKStages);
-                // with one buffer dP overwrites dS: this warp's MMAs run in the order of issue
+                // with one buffer dP overwrites dS: this warp's MMAs run in the order of issue.
+                // (The first dq overwrites the item before's, stored before the dS it follows.)
                 if (NB == 1 && more) mma_dp();
             }
             if (!ok) break;
@@ -1125,55 +1196,51 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const float cs = a.scale * kLog2e;
         const float sds = BF16 ? 1.f : ds_scale(a.maxima);
         const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);
-        constexpr int WORDS = DP / 8;  // of each tensor's DP / 2 words, per warpgroup
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             const bool x = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
             return ok = __all_sync(0xffffffffu, x) != 0;
         };
         int gt = 0, g0 = 0, k = 0;
         uint32_t joined = 0;
-        // the next item's rows are read before the epilogue of the one before and
-        // put into TMEM once its products are done
-        auto read_rows = [&](const QItem &w, uint32_t (&wq)[16], uint32_t (&wd)[16]) {
-            const int tb = packed ? 0 : w.b, i = w.q0 + r;
-            const uint16_t *qr = static_cast<const uint16_t *>(a.q) + tb * a.sq[0] + (w.s.q0 + i) * a.sq[1] + w.h * a.sq[2];
-            const uint16_t *dr = static_cast<const uint16_t *>(a.dout) + tb * a.sdo[0] + (w.s.q0 + i) * a.sdo[1] + w.h * a.sdo[2];
-            row_words<WORDS>(wq, qr, i < w.s.lq, a.dim, wg * WORDS);
-            row_words<WORDS>(wd, dr, i < w.s.lq, a.dim, wg * WORDS);
-        };
-        auto put_rows = [&](const uint32_t (&wq)[16], const uint32_t (&wd)[16]) {
-            __syncwarp();
-            if constexpr (WORDS == 16) {
-                ptx::tmem_st16(tQ + lanes + wg * WORDS, wq);
-                ptx::tmem_st16(tDo + lanes + wg * WORDS, wd);
-            } else {
-                ptx::tmem_st8(tQ + lanes + wg * WORDS, wq);
-                ptx::tmem_st8(tDo + lanes + wg * WORDS, wd);
+        int gr = 0;  // rows put into TMEM so far
+        // the warpgroup's DP / 8 words of this thread's rows of q and do, from the
+        // swizzled tiles (chunk j of row r at j ^ (r & 7)) into TMEM
+        auto put_rows = [&]() {
+            if (!wait(&sb.stat[1], (uint32_t)gr)) return;
+            ++gr;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint8_t *tile = smem + half * TILE + r * 128;
+                uint32_t x[DP / 8];
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    const int c = wg * (DP / 32) + j;  // 16-byte chunk of the row
+                    const uint4 v = *reinterpret_cast<const uint4 *>(tile + (c >> 3) * kBoxBytes + (((c & 7) ^ (r & 7)) << 4));
+                    x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+                }
+                const uint32_t to = (half ? tDo : tQ) + lanes + wg * (DP / 8);
+                if constexpr (DP == 128) ptx::tmem_st16(to, x);
+                else ptx::tmem_st8(to, x);
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.stat));
-        };
-        int item = take_item(a, k, sb, ok), n = 0;
-        if (item >= 0) {
-            const QItem w = q_item(a, item);
-            n = w.n;
-            if (n > 0) {
-                uint32_t wq[16], wd[16];
-                read_rows(w, wq, wd);
-                put_rows(wq, wd);
+            if (lane == 0) {
+                ptx::mbar_arrive(ptx::smem_u32(&sb.stat[0]));
+                ptx::mbar_arrive(ptx::smem_u32(sb.stat_empty));
             }
-        }
-        while (item >= 0) {
+        };
+        const QItem *w = take_item(a, k, slots, sb, ok);
+        if (w && w->n > 0) put_rows();
+        while (ok && w) {
+            const int n = w->n;
             if (n > 0) {
-                const QItem w = q_item(a, afresh(item));
-                const long long row = w.s.row0 + (long long)w.h * a.head_rows + w.q0 + r;
+                const long long row = w->s.row0 + (long long)w->h * a.head_rows + w->q0 + r;
                 const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row);
                 // counted from the first step: this thread's query sees the keys before `sees`; tiles
                 // that end by `all` need no mask
-                const int sees = (a.causal ? min(w.s.lk, w.q0 + r + w.off + 1) : w.s.lk) - w.it0 * kT;
-                const int all = (a.causal ? min(w.s.lk, w.q0 + w.off + 1) : w.s.lk) - w.it0 * kT;
+                const int lk = w->s.lk - w->it0 * kT, diag = w->q0 + w->off + 1 - w->it0 * kT;
+                const int sees = a.causal ? min(lk, diag + r) : lk, all = a.causal ? min(lk, diag) : lk;
                 for (int it = 0; it < n; ++it) {
                     const int i = g0 + it;
                     float2 p[16];
@@ -1213,43 +1280,36 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
                 if (!ok) break;
             }
-            const int next = take_item(a, ++k, sb, ok);
-            if (!ok) break;
-            int next_n = 0;
-            uint32_t wq[16] = {}, wd[16] = {};
-            if (next >= 0) {
-                const QItem w = q_item(a, next);
-                next_n = w.n;
-                if (next_n > 0) read_rows(w, wq, wd);
-            }
-            if (n > 0 && !wait(&sb.acc, (uint32_t)gt)) break;
+            const QItem *next = take_item(a, k + 1, slots, sb, ok);
+            if (!ok || (n > 0 && !wait(&sb.acc, (uint32_t)gt))) break;
             ptx::tc_fence_after();
-            if (next_n > 0) put_rows(wq, wd);
+            // the products that read this item's rows are done
+            if (next && next->n > 0) put_rows();
+            if (!ok) break;
             {
                 // each warpgroup stores a quarter of the columns
-                const QItem w = q_item(a, afresh(item));
-                const int c0 = wg * (DP / 4), i = w.q0 + r;
-                uint16_t *out = static_cast<uint16_t *>(a.dq) + (packed ? 0 : w.b) * a.sdq[0] + (w.s.q0 + i) * a.sdq[1] +
-                                w.h * a.sdq[2] + c0;
+                const int c0 = wg * (DP / 4), i = w->q0 + r;
+                uint16_t *out = static_cast<uint16_t *>(a.dq) + (packed ? 0 : w->b) * a.sdq[0] + (w->s.q0 + i) * a.sdq[1] +
+                                w->h * a.sdq[2] + c0;
                 constexpr long long ITEM = DP * kT / 4;
-                float4 *at = reinterpret_cast<float4 *>(a.part) + w.tile * a.chunks * ITEM + c0 / 4 * kT + r;
-                if (w.used == 1) store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < w.s.lq, out, a.dim - c0);
-                else sums_to_memory<DP / 4>(tDq + lanes + c0, at + w.c * ITEM);
-                if (n > 0) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty));
-                    ++gt;
-                }
-                if (w.used > 1) {
-                    const bool last = arrive_last(a, w.tile, w.used, sb, joined, ok);
+                float4 *at = reinterpret_cast<float4 *>(a.part) + w->tile * a.chunks * ITEM + c0 / 4 * kT + r;
+                if (w->used == 1)
+                    store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < w->s.lq, out, a.dim - c0);
+                else
+                    sums_to_memory<DP / 4>(tDq + lanes + c0, at + w->c * ITEM);
+                ptx::tc_fence_before();
+                if (n > 0) ++gt;
+                if (w->used > 1) {
+                    const bool last = arrive_last(a, w->tile, w->used, sb, joined, ok);
                     if (!ok) break;
-                    if (last) store_sums<DP / 4, BF16>(at, w.used, ITEM, a.scale / sds, i < w.s.lq, out, a.dim - c0);
+                    if (last)
+                        store_sums<DP / 4, BF16>(at, w->used, ITEM, a.scale / sds, i < w->s.lq, out, a.dim - c0);
                 }
             }
+            done_item(k, sb);
+            ++k;
             g0 += n;
-            n = next_n;
-            item = next;
+            w = next;
         }
     }
     ptx::tc_fence_before();
@@ -1392,7 +1452,7 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
                              (int)Kv<DP>::SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_q_kernel<DP, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)q_smem_bytes<DP>());
+                                 (int)Qk<DP>::SMEM);
     if (e != cudaSuccess) return e;
     if (p.k_tiles > 0) {
         a.tiles = p.k_tiles;
@@ -1413,10 +1473,10 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
         const unsigned blocks = (unsigned)std::min(a.items, kNumSMs);
         // without keys there is no launch between this one and the preparation
         if (p.k_tiles > 0)
-            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(blocks), dim3(kAtThreads), q_smem_bytes<DP>(), st, tm[1],
-                           tm[2], a);
+            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(blocks), dim3(kAtThreads), Qk<DP>::SMEM, st, tm[0],
+                           tm[1], tm[2], tm[3], a);
         else
-            attn_q_kernel<DP, BF16><<<blocks, kAtThreads, q_smem_bytes<DP>(), st>>>(tm[1], tm[2], a);
+            attn_q_kernel<DP, BF16><<<blocks, kAtThreads, Qk<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
@@ -1470,9 +1530,9 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.nlse = ws_at<float>(workspace, p.off_nlse);
     a.ndsum = ws_at<float>(workspace, p.off_ndsum);
     a.head_rows = p.head_rows;
-    a.q = q; a.o = o; a.dout = dout; a.v = v; a.dq = dq; a.dk = dk; a.dv = dv;
-    long long sk[3];
-    fill_strides(d->q, d->heads_q, d->dim, tq, a.sq);
+    a.o = o; a.dout = dout; a.v = v; a.dq = dq; a.dk = dk; a.dv = dv;
+    long long sq[3], sk[3];
+    fill_strides(d->q, d->heads_q, d->dim, tq, sq);
     fill_strides(d->k, d->heads_kv, d->dim, tk, sk);
     fill_strides(d->v, d->heads_kv, d->dim, tk, a.sv);
     fill_strides(d->o, d->heads_q, d->dim, tq, a.so);
@@ -1483,7 +1543,7 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     // without queries (or keys) the main kernels load nothing of them
     CUtensorMap tm[4] = {};
     if (tq > 0 && tk > 0 &&
-        (!attn_map(&tm[0], q, *d, d->heads_q, tq, a.sq) || !attn_map(&tm[1], k, *d, d->heads_kv, tk, sk) ||
+        (!attn_map(&tm[0], q, *d, d->heads_q, tq, sq) || !attn_map(&tm[1], k, *d, d->heads_kv, tk, sk) ||
          !attn_map(&tm[2], v, *d, d->heads_kv, tk, a.sv) || !attn_map(&tm[3], dout, *d, d->heads_q, tq, a.sdo)))
         return CBA_ERR_UNSUPPORTED;
     cudaGetLastError();
