@@ -647,10 +647,12 @@ cudaError_t fwd_ring(const LnArgs &a, cudaStream_t st) {
     auto kern = ln_fwd_ring_kernel<T, P, TPR, EPT, ring>;
     static const int per_sm = [&] {
         int n = 0;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+        if (allow_smem<ln_fwd_ring_kernel<T, P, TPR, EPT, ring>>(smem) != cudaSuccess) return 0;
         return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, block, smem) == cudaSuccess ? n : 0;
     }();
     if (per_sm == 0) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = allow_smem<ln_fwd_ring_kernel<T, P, TPR, EPT, ring>>(smem);
+    if (e != cudaSuccess) return e;
     const long long blocks = std::min<long long>((a.rows + rpb - 1) / rpb, (long long)kNumSMs * per_sm);
     kern<<<(unsigned)blocks, block, smem, st>>>(a);
     return cudaGetLastError();
@@ -691,10 +693,9 @@ template <typename T, typename P, int TPR, int EPT, bool RES>
 cudaError_t bwd_ring(const LnArgs &a, const LnPlan &p, cudaStream_t st) {
     constexpr int block = ring_block(TPR), smem = kRing * (RES ? 3 : 2) * block * EPT * (int)sizeof(T);
     static_assert((block / TPR - 1) * TPR * EPT * 4 <= smem, "the groups' sums fit the ring");
-    auto kern = ln_bwd_ring_kernel<T, P, TPR, EPT, RES>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<ln_bwd_ring_kernel<T, P, TPR, EPT, RES>>(smem);
     if (e != cudaSuccess) return e;
-    kern<<<p.nblk, block, smem, st>>>(a);
+    ln_bwd_ring_kernel<T, P, TPR, EPT, RES><<<p.nblk, block, smem, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -24,8 +24,9 @@
 // a pair of blocks computes 256 x 256 tiles (each holds half of A's and of B's
 // rows, which halves the traffic of both per product), with CG = 1 a block
 // computes 128 x BN.  Persistent: two accumulators in TMEM, so the epilogue of
-// one tile runs under the products of the next.  Warp 0 issues the TMA loads,
-// warp 1 the MMAs, warps 2-5 the epilogue.  Every wait is bounded (2 s); on a
+// one tile runs under the products of the next.  Where S has too few tiles for
+// the SMs, a cluster of blocks shares a tile's contraction (ns_split_kernel).
+// Warp 0 issues the TMA loads, warp 1 the MMAs, warps 2-9 the epilogue.  Every wait is bounded (2 s); on a
 // timeout the block sets the workspace status bit, stops, waits (bounded) for
 // copies and MMAs in flight, frees its TMEM and returns.
 #include <cuda.h>
@@ -42,7 +43,8 @@ namespace cba {
 namespace {
 
 constexpr uint64_t kNsLimitNs = 2000000000ull;
-constexpr int kNsThreads = 192;
+constexpr int kNsEpiWarps = 8;                 // two per quarter of a tile's rows
+constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;
 constexpr int kNsStages = 6;
 constexpr int kNsBK = 64;                      // contraction elements per stage (128 bytes)
 constexpr float kNsSym = 4096.f;               // S and C are held times 2^12
@@ -100,14 +102,13 @@ __device__ __forceinline__ void ns_load(uint32_t dst, const CUtensorMap *tm, int
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void ns_store(void *out, long long at, const float (&v)[32], int n,
-                                         int vec) {
+template <typename T, int N>
+__device__ __forceinline__ void ns_store(void *out, long long at, const float (&v)[N], int n, int vec) {
     T *o = static_cast<T *>(out) + at;
-    if (vec && n >= 32) {
+    if (vec && n >= N) {
         constexpr int V = 16 / sizeof(T);
 #pragma unroll
-        for (int i = 0; i < 32; i += V) {
+        for (int i = 0; i < N; i += V) {
             Pack<T, V> p;
 #pragma unroll
             for (int j = 0; j < V; ++j) p.v[j] = from_f32<T>(v[i + j]);
@@ -115,9 +116,60 @@ __device__ __forceinline__ void ns_store(void *out, long long at, const float (&
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < N; ++i)
             if (i < n) o[i] = from_f32<T>(v[i]);
     }
+}
+
+// Tile u of the triangle on and above the diagonal: column j holds rows 0 .. j.
+__device__ __forceinline__ void triangle(int u, int &i, int &j) {
+    j = (int)((sqrtf(8.f * u + 1.f) - 1.f) * 0.5f);
+    while (j * (j + 1) / 2 > u) --j;
+    while ((j + 1) * (j + 2) / 2 <= u) ++j;
+    i = u - j * (j + 1) / 2;
+}
+
+// 16 bytes at a time, a chunk of N aux values ahead of their use.
+template <int N>
+__device__ __forceinline__ void aux_load(Pack<__half, 8> (&p)[N / 8], const __half *aux, int n) {
+#pragma unroll
+    for (int j = 0; j < N / 8; ++j)
+        if (8 * j < n) p[j] = *reinterpret_cast<const Pack<__half, 8> *>(aux + 8 * j);  // rows are 16-byte multiples
+}
+
+// N results of one row from column `col` on (n of them in the matrix; live: the
+// row is): out = alpha v + beta aux + diag I, stored, and on tiles above the
+// diagonal of a symmetric matrix (mirror) also as a column.  Called by whole warps
+// whose lanes hold neighbouring rows, an even one in an even lane.
+template <int N>
+__device__ __forceinline__ void ns_result(const NsArgs &a, float (&v)[N], const Pack<__half, 8> *aux, int b, int row,
+                                          int col, bool mirror) {
+    const int n = a.N - col;
+    if (n <= 0) return;
+    const bool live = row < a.M;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        v[j] *= a.alpha;
+        if (a.aux) v[j] = fmaf(a.beta, __half2float(aux[j / 8].v[j & 7]), v[j]);
+        if (a.diag != 0.f && col + j == row) v[j] += a.diag;
+    }
+    if (mirror) {
+        // two rows of a column are 4 bytes side by side: even lanes store even
+        // columns, odd lanes odd ones (a row past M falls on the pitch's padding)
+        __half *o = static_cast<__half *>(a.out) + b * a.out_batch + (row & ~1);
+        const bool odd = row & 1;
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const __half2 h = odd ? __floats2half2_rn(got, v[j + 1]) : __floats2half2_rn(v[j], got);
+            if ((row & ~1) < a.M && j + odd < n) *reinterpret_cast<__half2 *>(o + (col + j + odd) * a.out_ld) = h;
+        }
+    }
+    if (!live) return;
+    const long long at = b * a.out_batch + row * a.out_ld + col;
+    if (a.out_type == CBA_F16) ns_store<__half>(a.out, at, v, n, a.vec);
+    else if (a.out_type == CBA_BF16) ns_store<__nv_bfloat16>(a.out, at, v, n, a.vec);
+    else ns_store<float>(a.out, at, v, n, a.vec);
 }
 
 template <int CG, int BN>
@@ -139,7 +191,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_u32(&sb.acc_full[i]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sb.acc_empty[i]), 4 * CG);  // the epilogue warps
+            ptx::mbar_init(ptx::smem_u32(&sb.acc_empty[i]), kNsEpiWarps * CG);
         }
         ptx::mbar_init(ptx::smem_u32(&sb.drain), 1);
         sb.abort_flag = 0;
@@ -169,15 +221,14 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     // running together share B's rows in L2
     auto where = [&](int i, int &b, int &m0, int &n0) {
         int u = g0 + i * gstep;
-        if (a.sym) {  // column j of the triangle holds tiles 0 .. j
+        if (a.sym) {
             const int tri = a.mt * (a.mt + 1) / 2;
             b = u / tri;
             u -= b * tri;
-            int j = (int)((sqrtf(8.f * u + 1.f) - 1.f) * 0.5f);
-            while (j * (j + 1) / 2 > u) --j;
-            while ((j + 1) * (j + 2) / 2 <= u) ++j;
-            m0 = (u - j * (j + 1) / 2) * L::TM;
-            n0 = j * BN;
+            int ti, tj;
+            triangle(u, ti, tj);
+            m0 = ti * L::TM;
+            n0 = tj * BN;
             return;
         }
         m0 = u % a.mt * L::TM;
@@ -270,27 +321,29 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             __syncwarp();
         }
     } else {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, c0 = (warp - 2) / 4 * (BN / 2);
         bool ok = true;
         for (int i = 0; ok && i < mine; ++i) {
             const int ac = i & 1;
+            int b, m0, n0;
+            where(i, b, m0, n0);
+            const int row = m0 + (int)rank * 128 + quarter * 32 + lane;
+            const __half *aux = a.aux ? a.aux + b * a.aux_batch + min(row, a.M - 1) * a.aux_ld + n0 + c0 : nullptr;
+            Pack<__half, 8> ax[4];
+            if (aux) aux_load<32>(ax, aux, a.N - n0 - c0);
             ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.acc_full[ac]), (uint32_t)(i / 2) & 1u, ab, a.status,
                                         kNsLimitNs);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            int b, m0, n0;
-            where(i, b, m0, n0);
-            const int row = m0 + (int)rank * 128 + quarter * 32 + lane;
-            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + ac * BN;
-            const __half *aux = a.aux ? a.aux + b * a.aux_batch + row * a.aux_ld : nullptr;
-            const long long at = b * a.out_batch + row * a.out_ld;
-            for (int c = 0; c < BN; c += 32) {
+            const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + ac * BN + c0;
+#pragma unroll 1
+            for (int c = 0; c < BN / 2; c += 32) {
                 float v[32];
-                __syncwarp();  // rows past M skip the stores below
+                __syncwarp();  // rows past M skip the stores
                 ptx::tmem_ld32(t0 + c, v);
                 ptx::tmem_ld_wait();
-                if (c + 32 == BN) {  // the accumulator is read: the MMAs may reuse it
+                if (c + 32 == BN / 2) {  // the accumulator is read: the MMAs may reuse it
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -300,38 +353,8 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                             ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty[ac]));
                     }
                 }
-                const int col = n0 + c, n = a.N - col;
-                if (row >= a.M || n <= 0) continue;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= a.alpha;
-                if (aux) {
-                    if (n >= 32) {  // aux rows are 16-byte multiples
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            const Pack<__half, 8> p = *reinterpret_cast<const Pack<__half, 8> *>(aux + col + j);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[j + e] = fmaf(a.beta, __half2float(p.v[e]), v[j + e]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < n) v[j] = fmaf(a.beta, __half2float(aux[col + j]), v[j]);
-                    }
-                }
-                if (a.diag != 0.f) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (col + j == row) v[j] += a.diag;
-                }
-                if (a.sym && m0 < n0) {  // 32 rows of a column side by side
-                    __half *o = static_cast<__half *>(a.out) + b * a.out_batch + row;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j < n) o[(col + j) * a.out_ld] = __float2half_rn(v[j]);
-                }
-                if (a.out_type == CBA_F16) ns_store<__half>(a.out, at + col, v, n, a.vec);
-                else if (a.out_type == CBA_BF16) ns_store<__nv_bfloat16>(a.out, at + col, v, n, a.vec);
-                else ns_store<float>(a.out, at + col, v, n, a.vec);
+                ns_result<32>(a, v, ax, b, row, n0 + c0 + c, a.sym && m0 < n0);
+                if (aux && c + 32 < BN / 2) aux_load<32>(ax, aux + c + 32, a.N - n0 - c0 - c - 32);
             }
         }
     }
@@ -343,6 +366,146 @@ __global__ void __launch_bounds__(kNsThreads, 1)
         ptx::tc_fence_after();
         if constexpr (CG == 2) ptx::tmem_dealloc_pair(tmem, L::TMEM_COLS);
         else ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+// ---- a tile's contraction shared by a cluster
+
+// D[128 x 128] of a symmetric product: block `rank` of a cluster of SK contracts
+// every SK-th part, leaves its fp32 sums in its shared memory ([column / 4][row]
+// float4), and adds up 128 / SK of the columns of all blocks, in the order of
+// the ranks.  (S of 512 x 2304: ten tiles, whose 36 stages a block alone loads at
+// ~100 GB/s in 9 us.)
+template <int SK>
+__global__ void __launch_bounds__(kNsThreads, 1)
+    ns_split_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                    const NsArgs a) {
+    using L = NsTile<1, 128>;
+    extern __shared__ uint8_t smem_dyn[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+    NsBars &sb = *reinterpret_cast<NsBars *>(smem + kNsStages * L::STAGE);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)ptx::cluster_ctarank();
+    if (tid == 0) {
+        for (int i = 0; i < kNsStages; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&sb.full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sb.empty[i]), 1);
+        }
+        ptx::mbar_init(ptx::smem_u32(&sb.acc_full[0]), 1);
+        sb.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 128);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sb.tmem_base;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    int u = (int)blockIdx.x / SK;
+    const int tri = a.mt * (a.mt + 1) / 2, b = u / tri;
+    int ti, tj;
+    triangle(u - b * tri, ti, tj);
+    const int m0 = ti * 128, n0 = tj * 128;
+    const int nk = (a.K + kNsBK - 1) / kNsBK, k0 = nk * rank / SK, k1 = nk * (rank + 1) / SK;
+    volatile int *ab = &sb.abort_flag;
+    bool ok = true;
+    int begun = 0;  // stages that lane 0 of the load warp has begun to fill
+    if (warp == 0) {
+        if (lane == 0)
+            for (int kb = k0; kb < k1; ++kb, ++begun) {
+                const int s = begun % kNsStages;
+                if (begun >= kNsStages)
+                    ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.empty[s]), (uint32_t)(begun / kNsStages - 1) & 1u, ab,
+                                                a.status, kNsLimitNs);
+                if (!ok) break;
+                const uint32_t bar = ptx::smem_u32(&sb.full[s]), to = ptx::smem_u32(smem + s * L::STAGE);
+                ptx::mbar_arrive_expect_tx(bar, L::STAGE);
+                ns_load<1>(to, &ta, a.a_major, 128, m0, kb * kNsBK, b, bar);
+                ns_load<1>(to + L::A_BYTES, &tb, a.b_major, 128, n0, kb * kNsBK, b, bar);
+            }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t idesc = ptx::idesc_f16(128, 128, false, a.b_major != 0, a.a_major != 0);
+        const uint32_t sa = a.a_major ? 2048 >> 4 : 32 >> 4, sbk = a.b_major ? 2048 >> 4 : 32 >> 4;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int kb = k0; kb < k1; ++kb) {
+            const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.full[s]), ph, ab, a.status, kNsLimitNs);
+            ptx::tc_fence_after();
+            if (!(ok = __all_sync(0xffffffffu, r))) break;
+            const uint32_t at = ptx::smem_u32(smem + s * L::STAGE);
+            const ptx::Desc da = ptx::desc_of(at, a.a_major ? 8192 : 16, 1024, 2);
+            const ptx::Desc db = ptx::desc_of(at + L::A_BYTES, a.b_major ? 8192 : 16, 1024, 2);
+            if (ptx::elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < kNsBK / 16; ++ks)
+                    ptx::mma_f16(tmem, da, ks * sa, db, ks * sbk, idesc, kb > k0 || ks > 0);
+                ptx::mma_commit(ptx::smem_u32(&sb.empty[s]));
+            }
+            __syncwarp();
+            if (++s == kNsStages) s = 0, ph ^= 1;
+        }
+        if (ptx::elect_one()) {
+            if (!ok) *ab = 1;
+            ptx::mma_commit(ptx::smem_u32(&sb.acc_full[0]));
+        }
+        __syncwarp();
+    }
+    // every thread: the products are done (and with them the copies), so that the
+    // stages may hold the sums; a block that timed out leaves nothing to be added
+    int no = 0;
+    bool done = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.acc_full[0]), 0, &no, a.status, kNsLimitNs);
+    done = __syncthreads_and(done && *ab == 0) != 0;
+    ptx::tc_fence_after();
+    if (!done)  // copies that no product waited for
+        for (int v = max(0, begun - kNsStages); v < begun; ++v)
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.full[v % kNsStages]), (uint32_t)(v / kNsStages) & 1u, &no, a.status,
+                                   kNsLimitNs / 8);
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    float4 *sums = reinterpret_cast<float4 *>(smem);
+    if (warp >= 2 && done) {
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) {
+            float v[16];
+            ptx::tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + half * 64 + c, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                sums[(half * 64 + c + j) / 4 * 128 + quarter * 32 + lane] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+    }
+    ptx::cluster_sync();
+    if (warp >= 2) {
+        constexpr int COLS = 128 / SK, PER = COLS / 2 < 8 ? 8 : COLS / 2;  // of a rank, of a warp
+        const int c0 = rank * COLS + half * PER, row = quarter * 32 + lane;
+        if (half * PER < COLS) {
+#pragma unroll
+            for (int c = 0; c < PER; c += 8) {
+                float v[8] = {};
+#pragma unroll
+                for (int q = 0; q < SK; ++q) {
+                    const uint32_t from = ptx::mapa(ptx::smem_u32(sums + (c0 + c) / 4 * 128 + row), (uint32_t)q);
+                    const float4 x = ptx::ld_cluster(from), y = ptx::ld_cluster(from + 128 * 16);
+                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+                }
+                __syncwarp();
+                ns_result<8>(a, v, nullptr, b, m0 + row, n0 + c0 + c, m0 < n0);
+            }
+        }
+    }
+    ptx::cluster_sync();  // the others have read this block's sums
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 128);
     }
 }
 
@@ -782,47 +945,71 @@ struct NsOperand {
     int major;
 };
 
-template <int CG, int BN>
-cudaError_t ns_launch(const NsOperand &oa, const NsOperand &ob, NsArgs a, int batch, cudaStream_t st) {
-    using L = NsTile<CG, BN>;
-    a.mt = (a.M + L::TM - 1) / L::TM;
-    a.nt = (a.N + BN - 1) / BN;
-    a.sym = a.sym && L::TM == BN;  // needs square tiles
-    a.units = (a.sym ? a.mt * (a.mt + 1) / 2 : a.mt * a.nt) * batch;
-    a.a_major = oa.major;
-    a.b_major = ob.major;
+// A product's kernel and the tensor maps of its operands, made once per call and
+// operand buffer.
+struct NsProduct {
+    int cg, bn, sk;  // blocks per tile (pair), tile columns, blocks that share a contraction
     CUtensorMap ta, tb;
-    if (!ns_map(&ta, oa.base, batch, oa.rows, oa.cols, oa.pitch, oa.major, 128) ||
-        !ns_map(&tb, ob.base, batch, ob.rows, ob.cols, ob.pitch, ob.major, L::ROWS_B))
-        return cudaErrorInvalidValue;
-    auto kern = ns_gemm_kernel<CG, BN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
+};
+
+// The tile: 256 x 256 by pairs of blocks once they fill half of the SMs; below
+// that smaller ones, which spread the product over more SMs; and where `split` (a
+// symmetric product without aux) has a long contraction and few tiles, clusters
+// that share it.
+bool ns_product(NsProduct *p, const NsOperand &oa, const NsOperand &ob, int M, int N, int K, bool split, int batch) {
+    const long long t256 = (long long)((M + 255) / 256) * ((N + 255) / 256) * batch;
+    const long long t128 = (long long)((M + 127) / 128) * ((N + 127) / 128) * batch;
+    *p = NsProduct{1, 64, 1, {}, {}};
+    if (t256 >= kNumSMs / 4) *p = NsProduct{2, 256, 1, {}, {}};
+    else if (t128 >= kNumSMs / 2) *p = NsProduct{1, 128, 1, {}, {}};
+    const int nk = (K + kNsBK - 1) / kNsBK, mt = (M + 127) / 128;
+    if (split && p->cg == 1) {
+        // 128 blocks in clusters of 8 fit the GPU at once; at least 4 stages each
+        const long long tiles = (long long)mt * (mt + 1) / 2 * batch;
+        for (int sk = 8; sk >= 2; sk /= 2)
+            if (tiles * sk <= 128 && nk >= 4 * sk) {
+                *p = NsProduct{1, 128, sk, {}, {}};
+                break;
+            }
+    }
+    return ns_map(&p->ta, oa.base, batch, oa.rows, oa.cols, oa.pitch, oa.major, 128) &&
+           ns_map(&p->tb, ob.base, batch, ob.rows, ob.cols, ob.pitch, ob.major, p->bn / p->cg);
+}
+
+template <auto Kern>
+cudaError_t ns_launch(unsigned grid, int cluster, uint32_t smem, const NsProduct &p, const NsArgs &a, cudaStream_t st) {
+    cudaError_t e = allow_smem<Kern>((int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CG * std::min(a.units, kNumSMs / CG)));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kNsThreads);
-    cfg.dynamicSmemBytes = L::SMEM;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, ta, tb, a);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, Kern, p.ta, p.tb, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// The tile: 256 x 256 by pairs of blocks once they fill half of the SMs; below
-// that smaller ones, which spread the product over more SMs.
-cudaError_t ns_gemm(const NsOperand &oa, const NsOperand &ob, const NsArgs &a, int batch, cudaStream_t st) {
-    const long long t256 = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256) * batch;
-    const long long t128 = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128) * batch;
-    if (t256 >= kNumSMs / 4) return ns_launch<2, 256>(oa, ob, a, batch, st);
-    if (t128 >= kNumSMs / 2) return ns_launch<1, 128>(oa, ob, a, batch, st);
-    return ns_launch<1, 64>(oa, ob, a, batch, st);
+cudaError_t ns_gemm(const NsProduct &p, NsArgs a, int batch, cudaStream_t st) {
+    const int tm = 128 * p.cg;
+    a.mt = (a.M + tm - 1) / tm;
+    a.nt = (a.N + p.bn - 1) / p.bn;
+    a.sym = a.sym && tm == p.bn;  // needs square tiles
+    a.units = (a.sym ? a.mt * (a.mt + 1) / 2 : a.mt * a.nt) * batch;
+    const unsigned grid = (unsigned)(p.cg * std::min(a.units, kNumSMs / p.cg)), parts = (unsigned)(a.units * p.sk);
+    if (p.sk == 8) return ns_launch<ns_split_kernel<8>>(parts, 8, NsTile<1, 128>::SMEM, p, a, st);
+    if (p.sk == 4) return ns_launch<ns_split_kernel<4>>(parts, 4, NsTile<1, 128>::SMEM, p, a, st);
+    if (p.sk == 2) return ns_launch<ns_split_kernel<2>>(parts, 2, NsTile<1, 128>::SMEM, p, a, st);
+    if (p.cg == 2) return ns_launch<ns_gemm_kernel<2, 256>>(grid, 2, NsTile<2, 256>::SMEM, p, a, st);
+    if (p.bn == 128) return ns_launch<ns_gemm_kernel<1, 128>>(grid, 1, NsTile<1, 128>::SMEM, p, a, st);
+    return ns_launch<ns_gemm_kernel<1, 64>>(grid, 1, NsTile<1, 64>::SMEM, p, a, st);
 }
 
 template <typename T, int VEC>
@@ -871,7 +1058,7 @@ cudaError_t ns_small(const cba_orthogonalize_desc_t &d, const NsPlan &p, const v
     a.status = static_cast<unsigned *>(ws);
     const size_t smem = small_smem(a.R, a.nb);
     auto kern = a.R == 64 ? ns_small_kernel<64> : ns_small_kernel<128>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmMax);
+    cudaError_t e = a.R == 64 ? allow_smem<ns_small_kernel<64>>((int)kSmMax) : allow_smem<ns_small_kernel<128>>((int)kSmMax);
     if (e != cudaSuccess) return e;
     // one block clears the status word itself, several must not undo each other's
     if (d.batch > 1) e = cudaMemsetAsync(ws, 0, 4, st);
@@ -887,63 +1074,65 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
     cudaError_t e = d.in_type == CBA_F32   ? ns_start<float>(d, p, G, ws, held, st)
                     : d.in_type == CBA_F16 ? ns_start<__half>(d, p, G, ws, held, st)
                                            : ns_start<__nv_bfloat16>(d, p, G, ws, held, st);
-    __half *x = ws_at<__half>(ws, p.off_x0), *xn = ws_at<__half>(ws, p.off_x1);
+    if (e != cudaSuccess) return e;
+    __half *x[2] = {ws_at<__half>(ws, p.off_x0), ws_at<__half>(ws, p.off_x1)};
     __half *S = ws_at<__half>(ws, p.off_s), *C = ws_at<__half>(ws, p.off_c);
-    NsArgs sq{};  // the products of m x m
-    sq.M = sq.N = p.m;
-    sq.out_ld = p.s_pitch;
-    sq.out_batch = p.s_batch;
-    sq.out_type = CBA_F16;
-    sq.vec = 1;
-    sq.sym = 1;
-    sq.status = static_cast<unsigned *>(ws);
+    unsigned *status = static_cast<unsigned *>(ws);
     const NsOperand so{S, p.m, p.m, p.s_pitch, 0}, co{C, p.m, p.m, p.s_pitch, 0};
-    for (int i = 0; e == cudaSuccess && i < d.steps; ++i) {
-        // S: the contraction runs along X's rows (wide) or across them (tall)
-        const NsOperand xs{x, d.rows, d.cols, p.x_pitch, p.wide ? 0 : 1};
-        NsArgs g = sq;
-        g.K = p.n;
-        g.alpha = kNsSym / (held * held);
-        g.out = S;
-        e = ns_gemm(xs, xs, g, d.batch, st);
-        if (e != cudaSuccess) return e;
-        g = sq;
-        g.K = p.m;
-        g.alpha = d.c / kNsSym;
-        g.beta = d.b;
-        g.diag = d.a * kNsSym;
-        g.aux = S;
-        g.aux_ld = p.s_pitch;
-        g.aux_batch = p.s_batch;
-        g.out = C;
-        e = ns_gemm(so, so, g, d.batch, st);
-        if (e != cudaSuccess) return e;
-        g = NsArgs{};
-        g.M = d.rows;
-        g.N = d.cols;
-        g.K = p.m;
-        g.alpha = 1.f / kNsSym;
-        g.out = xn;
-        g.out_ld = p.x_pitch;
-        g.out_batch = p.x_batch;
-        g.out_type = CBA_F16;
-        g.vec = 1;
-        g.status = sq.status;
-        if (i + 1 == d.steps) {  // the last product writes the caller's matrix
-            g.alpha *= d.scale / held;
-            g.out = O;
-            g.out_type = d.out_type;
-            g.out_ld = d.ld_out ? d.ld_out : d.cols;
-            g.out_batch = d.batch_out ? d.batch_out : g.out_ld * d.rows;
-            const long long v = 16 / (long long)dtype_bytes(d.out_type);
-            g.vec = aligned_to(O, 16) && g.out_ld % v == 0 && g.out_batch % v == 0;
-        }
-        // wide: X' = C X, X's rows contracted over; tall: X' = X C
-        const NsOperand xk{x, d.rows, d.cols, p.x_pitch, 0}, xn_major{x, d.rows, d.cols, p.x_pitch, 1};
-        e = p.wide ? ns_gemm(co, xn_major, g, d.batch, st) : ns_gemm(xk, co, g, d.batch, st);
-        std::swap(x, xn);
+    // S: the contraction runs along X's rows (wide) or across them (tall); X': wide
+    // C X, X's rows contracted over, tall X C
+    NsProduct ps[2], pc, px[2];
+    const int bufs = d.steps > 1 ? 2 : 1;
+    bool ok = ns_product(&pc, so, so, p.m, p.m, p.m, false, d.batch);
+    NsArgs as{}, ac{}, ax{};
+    as.a_major = as.b_major = p.wide ? 0 : 1;
+    ax.b_major = p.wide ? 1 : 0;
+    for (int i = 0; i < bufs && ok; ++i) {
+        const NsOperand xs{x[i], d.rows, d.cols, p.x_pitch, as.a_major}, xk{x[i], d.rows, d.cols, p.x_pitch, 0},
+            xn{x[i], d.rows, d.cols, p.x_pitch, 1};
+        ok = ns_product(&ps[i], xs, xs, p.m, p.m, p.n, true, d.batch) &&
+             (p.wide ? ns_product(&px[i], co, xn, d.rows, d.cols, p.m, false, d.batch)
+                     : ns_product(&px[i], xk, co, d.rows, d.cols, p.m, false, d.batch));
     }
-    return e;
+    if (!ok) return cudaErrorInvalidValue;
+    as.M = as.N = ac.M = ac.N = ac.K = ax.K = p.m;
+    as.K = p.n;
+    as.out_ld = ac.out_ld = ac.aux_ld = p.s_pitch;
+    as.out_batch = ac.out_batch = ac.aux_batch = p.s_batch;
+    as.out_type = ac.out_type = ax.out_type = CBA_F16;
+    as.vec = ac.vec = ax.vec = 1;
+    as.sym = ac.sym = 1;
+    as.status = ac.status = ax.status = status;
+    as.alpha = kNsSym / (held * held);
+    as.out = S;
+    ac.alpha = d.c / kNsSym;
+    ac.beta = d.b;
+    ac.diag = d.a * kNsSym;
+    ac.aux = S;
+    ac.out = C;
+    ax.M = d.rows;
+    ax.N = d.cols;
+    ax.alpha = 1.f / kNsSym;
+    ax.out_ld = p.x_pitch;
+    ax.out_batch = p.x_batch;
+    for (int i = 0; i < d.steps; ++i) {
+        e = ns_gemm(ps[i & 1], as, d.batch, st);
+        if (e == cudaSuccess) e = ns_gemm(pc, ac, d.batch, st);
+        if (e != cudaSuccess) return e;
+        ax.out = x[~i & 1];
+        if (i + 1 == d.steps) {  // the last product writes the caller's matrix
+            ax.alpha *= d.scale / held;
+            ax.out = O;
+            ax.out_type = d.out_type;
+            ax.out_ld = d.ld_out ? d.ld_out : d.cols;
+            ax.out_batch = d.batch_out ? d.batch_out : ax.out_ld * d.rows;
+            const long long v = 16 / (long long)dtype_bytes(d.out_type);
+            ax.vec = aligned_to(O, 16) && ax.out_ld % v == 0 && ax.out_batch % v == 0;
+        }
+        e = ns_gemm(px[i & 1], ax, d.batch, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace

@@ -3,6 +3,7 @@
 // vector loads and stores, and the host-side checks they share.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -38,6 +39,21 @@ inline size_t dtype_bytes(int t) { return t == CBA_F32 ? 4 : 2; }
 inline bool dtype_ok(int t) { return t == CBA_F32 || t == CBA_F16 || t == CBA_BF16; }
 __host__ __device__ inline bool aligned_to(const void *p, size_t a) {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory: set once per device (the
+// call costs about as much as a launch's arguments).
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // The device that holds `ptr` becomes current for this library's runtime

@@ -51,7 +51,9 @@ SHAPES = [(1, 1, 1), (1, 1, 9), (1, 9, 1), (2, 7, 5), (1, 50, 500), (1, 500, 50)
           # one block per matrix: the largest that fit, with an odd number of 64-column boxes, and the first that do not
           (2, 64, 1600), (1, 1, 1601), (3, 128, 640), (2, 65, 320), (1, 630, 127), (2, 128, 641), (1, 1290, 33),
           # enough tiles for pairs of blocks and for the symmetric products' triangle, with ragged edges
-          (3, 900, 1300), (5, 1300, 1000)]
+          (3, 900, 1300), (5, 1300, 1000),
+          # contractions shared by clusters of 2, 4 and 8 blocks, with ragged tiles, from either side
+          (1, 385, 4099), (2, 260, 5000), (6, 300, 1023), (1, 3001, 391), (8, 200, 2000), (1, 1100, 1300)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
