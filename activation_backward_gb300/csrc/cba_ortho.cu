@@ -812,8 +812,10 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
         if (mine) {
             tmem_ld(tS + lanes + c_s, s);
             ptx::tmem_ld_wait();
+            // b S takes S as rounded too: C is then the polynomial of one matrix, and near 1 an
+            // error of S moves it by b + 2 c = -0.7 of itself instead of b (50x500: 2.1e-3 -> 1e-3)
 #pragma unroll
-            for (int j = 0; j < CS; ++j) s[j] *= s_alpha;
+            for (int j = 0; j < CS; ++j) s[j] = __half2float(__float2half_rn(s[j] * s_alpha));
             box_put<__half>(ss, R, r, c_s, s);
         }
         publish();
