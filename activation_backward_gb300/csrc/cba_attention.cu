@@ -432,9 +432,9 @@ struct Ring {
     }
 };
 
-// The MMA warp's wait for two barriers at once, half of the lanes on each: a wait
-// takes ~150 cycles even when its phase is over, in which no MMA is issued.  (Two
-// warps that issue in turn hide that, but their MMAs then alternate between
+// A warp's wait for two barriers at once, half of the lanes on each: a wait takes
+// ~150 cycles even when its phase is over, in which the MMA warp issues none.  (Two
+// warps that issue MMAs in turn hide that, but their MMAs then alternate between
 // accumulators and run at half the rate: kv 666 -> 975 us on 1x8192 h32/8 d128.)
 struct AtWait {
     uint64_t *bar;
@@ -874,9 +874,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int i = g0 + it, sr = i % kRStages;
                     const float *nl = rows + sr * 2 * kT + wg * 32, *nd = nl + kT;
                     float2 p[16];
-                    if (!(wait(&sb.r_full[sr], (uint32_t)(i / kRStages)) && wait(&sb.s_full[i & 1], (uint32_t)(i / 2))))
+                    if (!(ok = wait_both({&sb.r_full[sr], (uint32_t)(i / kRStages)},
+                                         {&sb.s_full[i & 1], (uint32_t)(i / 2)}, ab, a.status)))
                         break;
-                    ptx::tc_fence_after();
                     const uint32_t ts = tS + i % NS * 128 + lanes + wg * 32;
                     tmem_load(ts, p);
                     probabilities(p, cs, nl);
@@ -1237,7 +1237,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const int n = w->n;
             if (n > 0) {
                 const long long row = w->s.row0 + (long long)w->h * a.head_rows + w->q0 + r;
-                const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row);
+                const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row) * pds;
                 // counted from the first step: this thread's query sees the keys before `sees`; tiles
                 // that end by `all` need no mask
                 const int lk = w->s.lk - w->it0 * kT, diag = w->q0 + w->off + 1 - w->it0 * kT;
@@ -1271,8 +1271,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     tmem_load(td, x);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        x[c] = ptx::mul2(p[c], ptx::add2(x[c], make_float2(nd, nd)));
-                        if constexpr (!BF16) x[c] = ptx::mul2(x[c], make_float2(pds, pds));
+                        if constexpr (BF16) x[c] = ptx::add2(x[c], make_float2(nd, nd));
+                        else x[c] = ptx::fma2(x[c], make_float2(pds, pds), make_float2(nd, nd));
+                        x[c] = ptx::mul2(p[c], x[c]);
                     }
                     tmem_store<BF16>(td, x);
                     ptx::tc_fence_before();

@@ -9,6 +9,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "../../include/cba.h"
 
 namespace cba {
@@ -34,6 +36,33 @@ template <typename T, int VEC>
 struct __align__(sizeof(T) * VEC < 16 ? sizeof(T) * VEC : 16) Pack {
     T v[VEC];
 };
+
+// Elements 2 j and 2 j + 1 of a pack as fp32, and the other way.
+template <typename T, int VEC>
+__device__ __forceinline__ float2 pair_of(const Pack<T, VEC> &p, int j) {
+    if constexpr (sizeof(T) == 4) {
+        return make_float2(p.v[2 * j], p.v[2 * j + 1]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+        return __half22float2(__halves2half2(p.v[2 * j], p.v[2 * j + 1]));
+    } else {
+        return __bfloat1622float2(__halves2bfloat162(p.v[2 * j], p.v[2 * j + 1]));
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void set_pair(Pack<T, VEC> &p, int j, float2 v) {
+    if constexpr (sizeof(T) == 4) {
+        p.v[2 * j] = v.x;
+        p.v[2 * j + 1] = v.y;
+    } else if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __float22half2_rn(v);
+        p.v[2 * j] = h.x;
+        p.v[2 * j + 1] = h.y;
+    } else {
+        const __nv_bfloat162 h = __float22bfloat162_rn(v);
+        p.v[2 * j] = h.x;
+        p.v[2 * j + 1] = h.y;
+    }
+}
 
 inline size_t dtype_bytes(int t) { return t == CBA_F32 ? 4 : 2; }
 inline bool dtype_ok(int t) { return t == CBA_F32 || t == CBA_F16 || t == CBA_BF16; }
