@@ -249,6 +249,7 @@ struct AtBars {
     uint64_t fix, drain, acc, stat_empty[2];
     uint64_t i_full[2], i_empty[2];    // work items handed out
     uint64_t join;                     // the compute warps, around an arrival
+    uint64_t staged;                   // the results have passed through q's ring (kv kernel, dim 128)
     int last;
     uint32_t tmem_base;
     int abort_flag;
@@ -386,37 +387,39 @@ __device__ __forceinline__ void store_row(uint32_t ta, float scale, bool zero, b
     }
 }
 
-// 32 rows x 32 columns of a warp's accumulators, stored through 2 KB of shared
-// memory of its own: row = lane, its 16-byte chunk j at j ^ ((row >> 1) & 3); then
-// four lanes store a row's 64 bytes.
-template <bool BF16>
-__device__ __forceinline__ void store_rows_staged(uint32_t ta, float scale, bool zero, int live, uint16_t *out,
+// 32 rows x COLS columns of a warp's accumulators, stored through 2 KB of shared
+// memory of its own, 32 columns at a time: row = lane, its 16-byte chunk j at
+// j ^ ((row >> 1) & 3); then four lanes store a row's 64 bytes (16 bytes of 32 rows
+// at a time, as store_row does, take 8300 cycles of an item at dim 128).
+template <int COLS, bool BF16>
+__device__ __forceinline__ void store_rows_staged(uint32_t ta, float scale, int live, uint16_t *out,
                                                   long long stride, int cols, uint8_t *stage) {
     const int lane = threadIdx.x & 31;
-    float v[32];
-    if (!zero) {
-        ptx::tmem_ld32(ta, v);
+    auto slot = [&](int r, int j) { return stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4); };
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+        float v[32];
+        ptx::tmem_ld32(ta + c, v);
         ptx::tmem_ld_wait();
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint4 w;
-        uint32_t *u = &w.x;
+        for (int j = 0; j < 4; ++j) {
+            uint4 w;
+            w.x = pack2<BF16>(v[8 * j] * scale, v[8 * j + 1] * scale);
+            w.y = pack2<BF16>(v[8 * j + 2] * scale, v[8 * j + 3] * scale);
+            w.z = pack2<BF16>(v[8 * j + 4] * scale, v[8 * j + 5] * scale);
+            w.w = pack2<BF16>(v[8 * j + 6] * scale, v[8 * j + 7] * scale);
+            *reinterpret_cast<uint4 *>(slot(lane, j)) = w;
+        }
+        __syncwarp();
+        const int j = lane & 3;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            u[e] = zero ? 0u : pack2<BF16>(v[8 * j + 2 * e] * scale, v[8 * j + 2 * e + 1] * scale);
-        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + (lane >> 2);
+            if (r < live && c + j * 8 < cols)
+                *reinterpret_cast<uint4 *>(out + r * stride + c + j * 8) = *reinterpret_cast<const uint4 *>(slot(r, j));
+        }
+        __syncwarp();
     }
-    __syncwarp();
-    const int j = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2);
-        if (r < live && j * 8 < cols)
-            *reinterpret_cast<uint4 *>(out + r * stride + j * 8) =
-                *reinterpret_cast<const uint4 *>(stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
-    }
-    __syncwarp();
 }
 
 __device__ __forceinline__ void at_init_bars(uint64_t *first, int n, uint32_t count) {
@@ -559,8 +562,8 @@ __device__ __forceinline__ void sums_to_memory(uint32_t ta, float4 *at) {
             __stcg(at + (c + j) / 4 * kT, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
     }
 }
-// The same of `used` items, `stride` float4 apart, added, scaled and stored as
-// store_row does.
+// The same of `used` items, `stride` float4 apart, added, scaled, rounded and
+// stored 16 bytes at a time.
 template <int COLS, bool BF16>
 __device__ __forceinline__ void store_sums(const float4 *at, int used, long long stride, float scale, bool live,
                                            uint16_t *out, int cols) {
@@ -599,7 +602,7 @@ __device__ __forceinline__ void init_common(Bars &sb) {
     at_init_bars(sb.dp_full, 2, 1);
     at_init_bars(sb.ds_ready, 2, kAtWarps);
     at_init_bars(&sb.fix, 3, 1);  // fix, drain, acc
-    at_init_bars(&sb.join, 1, kAtWarps);
+    at_init_bars(&sb.join, 2, kAtWarps);  // join, staged
     at_init_bars(sb.i_full, 2, 1);
     at_init_bars(sb.i_empty, 2, kItemReaders);
     sb.abort_flag = 0;
@@ -619,9 +622,9 @@ __device__ __forceinline__ void drain_ring(uint64_t *bars, int stages, int count
 // At dim 64 and less TMEM has room for two S tiles: S of the tile after next is
 // computed once dv has used P, so that the compute warps find the next S ready.
 // At larger dims S(i + 1) overwrites P(i) and the warps wait for it.  Shared
-// memory there is full with one K and V tile; below, the next item's come while
-// this one's are in use, and the results pass through a stage so that a warp
-// stores 64 bytes of 8 rows at a time instead of 16 bytes of 32.
+// memory there is full with one K and V tile, and the results pass through a stage
+// of q's ring that the load warp keeps free for them; below, the next item's K and
+// V come while this one's are in use, and the results have a stage of their own.
 template <int DP>
 struct Kv {
     static constexpr int NS = DP == 64 ? 2 : 1;               // S buffers
@@ -721,7 +724,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (warp == 0) {
         uint32_t fphase = 0;
         const uint32_t bfix = ptx::smem_u32(&sb.fix);
-        int gt = 0, nq_begun = 0, nr_begun = 0, ndo_begun = 0;
+        int gt = 0, nq_begun = 0, nr_begun = 0, ndo_begun = 0, staged = 0;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
             ok = __all_sync(0xffffffffu, ok) != 0;
@@ -745,6 +748,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int t = w.it0 + it, g = t / w.nq, q0 = (w.qt_begin + t - g * w.nq) * kT, hq = w.h * a.group + g;
                 const int valid = min(kT, w.s.lq - q0);
                 const int st = nq_begun % kQStages, sd = ndo_begun % kDoStages, sr = nr_begun % kRStages;
+                // dim 128: the stage after an item's first q holds the results of the item before
+                // until they are stored (gt: items whose K and V have been asked for)
+                if (Kv<DP>::STAGE == 0 && it < 2 && staged < gt - 1) {
+                    if (!wait(&sb.staged, (uint32_t)staged)) break;
+                    ++staged;
+                }
                 if (nq_begun >= kQStages && !wait(&sb.a_empty[st], (uint32_t)(nq_begun / kQStages - 1))) break;
                 ++nq_begun;
                 ok = load_tile<DP>(sQ + st * TILE, &tq, w.s.q0 + q0, hq, tb, valid, packed,
@@ -935,13 +944,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int live = w->s.lk - row;  // of the warp's rows
                 if (w->used > 1)
                     sums_to_memory<DP / 2>(acc, at + w->c * ITEM);
-                else if constexpr (Kv<DP>::STAGE > 0)
-                    store_rows_staged<BF16>(acc, f, n == 0, live, out, sg[1], a.dim - c0,
-                                            smem + Kv<DP>::TILES + (warp - 4) * 2048);
+                else if (n == 0)
+                    store_row<DP / 2, BF16>(acc, f, true, lane < live, out + lane * sg[1], a.dim - c0);
                 else
-                    store_row<DP / 2, BF16>(acc, f, n == 0, lane < live, out + lane * sg[1], a.dim - c0);
+                    store_rows_staged<DP / 2, BF16>(acc, f, live, out, sg[1], a.dim - c0,
+                                                    smem + (Kv<DP>::STAGE ? Kv<DP>::TILES
+                                                                          : (2 * KVB + (g0 + n + 1) % kQStages) * TILE) +
+                                                        (warp - 4) * 2048);
                 ptx::tc_fence_before();
                 if (n > 0) ++gt;
+                if (Kv<DP>::STAGE == 0 && n > 0) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.staged));
+                }
                 if (w->used > 1) {
                     const bool last = arrive_last(a, w->tile, w->used, sb, joined, ok);
                     if (!ok) break;
@@ -1226,13 +1242,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(ptx::smem_u32(&sb.stat[0]));
-                ptx::mbar_arrive(ptx::smem_u32(sb.stat_empty));
-            }
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.stat[0]));
+        };
+        // the tiles may be filled again
+        auto free_rows = [&]() {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(sb.stat_empty));
         };
         const QItem *w = take_item(a, k, slots, sb, ok);
-        if (w && w->n > 0) put_rows();
+        if (w && w->n > 0) {
+            put_rows();
+            free_rows();
+        }
         while (ok && w) {
             const int n = w->n;
             if (n > 0) {
@@ -1286,26 +1308,38 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (!ok || (n > 0 && !wait(&sb.acc, (uint32_t)gt))) break;
             ptx::tc_fence_after();
             // the products that read this item's rows are done
-            if (next && next->n > 0) put_rows();
-            if (!ok) break;
+            const bool more = next && next->n > 0;
+            if (more) {
+                put_rows();
+                // at dim 128 the results pass through the tile of q: all warps have read it
+                if (ok && DP == 128) wait(&sb.stat[0], (uint32_t)(gr - 1));
+                if (!ok) break;
+                if (DP == 64) free_rows();
+            }
             {
                 // each warpgroup stores a quarter of the columns
-                const int c0 = wg * (DP / 4), i = w->q0 + r;
-                uint16_t *out = static_cast<uint16_t *>(a.dq) + (packed ? 0 : w->b) * a.sdq[0] + (w->s.q0 + i) * a.sdq[1] +
-                                w->h * a.sdq[2] + c0;
+                const int c0 = wg * (DP / 4), first = w->q0 + quarter * 32, live = w->s.lq - first;
+                uint16_t *out = static_cast<uint16_t *>(a.dq) + (packed ? 0 : w->b) * a.sdq[0] +
+                                (w->s.q0 + first) * a.sdq[1] + w->h * a.sdq[2] + c0;
                 constexpr long long ITEM = DP * kT / 4;
                 float4 *at = reinterpret_cast<float4 *>(a.part) + w->tile * a.chunks * ITEM + c0 / 4 * kT + r;
-                if (w->used == 1)
-                    store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, i < w->s.lq, out, a.dim - c0);
+                if (w->used == 1 && (DP == 64 || n == 0))
+                    store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, lane < live, out + lane * a.sdq[1],
+                                            a.dim - c0);
+                else if (w->used == 1)
+                    store_rows_staged<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, live, out, a.sdq[1], a.dim - c0,
+                                                    smem + (warp - 4) * 2048);
                 else
                     sums_to_memory<DP / 4>(tDq + lanes + c0, at + w->c * ITEM);
+                if (DP == 128 && more) free_rows();
                 ptx::tc_fence_before();
                 if (n > 0) ++gt;
                 if (w->used > 1) {
                     const bool last = arrive_last(a, w->tile, w->used, sb, joined, ok);
                     if (!ok) break;
                     if (last)
-                        store_sums<DP / 4, BF16>(at, w->used, ITEM, a.scale / sds, i < w->s.lq, out, a.dim - c0);
+                        store_sums<DP / 4, BF16>(at, w->used, ITEM, a.scale / sds, lane < live, out + lane * a.sdq[1],
+                                                 a.dim - c0);
                 }
             }
             done_item(k, sb);
