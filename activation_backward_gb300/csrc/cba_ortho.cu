@@ -525,7 +525,7 @@ __device__ __forceinline__ double block_sum(double v, double *sm) {
 
 // Partial sums of squares: block (p, b) takes the p-th part of matrix b's 16-byte
 // vectors (VEC elements; 1 where rows are not whole vectors), summed in a fixed
-// order: 4 vectors in fp32, their sums in fp64.
+// order: 4 vectors in fp32, their a thread's sum in fp32 too.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
     ns_norm_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, double *part) {
@@ -601,14 +601,16 @@ __global__ void __launch_bounds__(256)
 // memory in boxes of R rows x 64 columns with the 128-byte swizzle: as rows it
 // is the K-major operand of S = X X^T, as columns the N-major operand of C X.
 // Each 256-column chunk of X' depends on that chunk of X alone, so X is replaced
-// chunk by chunk.  The MMAs have M = 128 rows; with R = 64 the upper 64 lanes
+// chunk by chunk.  TMEM holds two accumulators of a chunk: the next chunk's product
+// runs while one is read back, and the one that the last chunk leaves free takes
+// the next step's S, begun over the finished chunks.  The MMAs have M = 128 rows; with R = 64 the upper 64 lanes
 // compute with whatever lies behind the operand and are not read.  A tall
 // matrix is transposed on its way in and out.
 constexpr int kSmThreads = 512;
 constexpr size_t kSmMax = 227 * 1024;
 
 struct SmBars {
-    uint64_t sq, x, drain;
+    uint64_t sq, x[2], drain;
     uint32_t tmem_base;
     int abort_flag;
     float factor;
@@ -635,51 +637,94 @@ __device__ __forceinline__ uint32_t box_at(int R, int r, int c8) {
     return (uint32_t)((c8 >> 3) * R * 128 + r * 128 + (((c8 & 7) ^ (r & 7)) << 4));
 }
 
-// |G|^2 and the scaled, zero-padded f16 copy.  G is read twice (the second time
-// from L2); 16 loads of a thread are in flight at a time.
+// The sum of squares of a thread's share of `n` packs of VEC elements, `per_row`
+// packs to a row (flat: one row), 8 loads in flight.
+template <typename T, int VEC>
+__device__ __forceinline__ float small_squares(const T *g, int n, int per_row, long long ld, bool flat) {
+    float s = 0.f;
+    for (int e = threadIdx.x; e < n; e += 8 * kSmThreads) {
+        Pack<T, VEC> p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = e + j * kSmThreads;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) p[j].v[k] = from_f32<T>(0.f);
+            if (i < n) {
+                const int r = flat ? 0 : i / per_row;
+                p[j] = *reinterpret_cast<const Pack<T, VEC> *>(g + r * ld + (long long)(i - r * per_row) * VEC);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) s = fmaf(to_f32(p[j].v[k]), to_f32(p[j].v[k]), s);
+    }
+    return s;
+}
+
+// Rows of a wide G, scaled, as the boxes' rows: a warp per row, W elements a time,
+// 8 loads in flight.
+template <typename T, int W>
+__device__ __forceinline__ void small_rows(const SmArgs &a, const T *g, uint8_t *sx, float k) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int c0 = lane * W; c0 < a.nb * 64; c0 += 64 * W)
+        for (int r0 = warp; r0 < a.R; r0 += kSmThreads / 8) {
+            Pack<T, W> v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + (i >> 1) * (kSmThreads / 32), c = c0 + (i & 1) * 32 * W;
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[i].v[j] = from_f32<T>(0.f);
+                if (r < a.m && c < a.n) v[i] = *reinterpret_cast<const Pack<T, W> *>(g + r * a.ld_in + c);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // R is a multiple of the 64 rows that a pass covers
+                const int r = r0 + (i >> 1) * (kSmThreads / 32), c = c0 + (i & 1) * 32 * W;
+                Pack<__half, W> p;
+#pragma unroll
+                for (int j = 0; j < W; ++j) p.v[j] = __float2half_rn(to_f32(v[i].v[j]) * k);
+                if (c < a.nb * 64)
+                    *reinterpret_cast<Pack<__half, W> *>(sx + box_at(a.R, r, c >> 3) + (c & 7) * 2) = p;
+            }
+        }
+}
+
+// |G|^2 and the scaled, zero-padded f16 copy.  G is read twice, the second time
+// from L1 or L2.
 template <typename T>
 __device__ __forceinline__ void small_load(const SmArgs &a, const T *g, uint8_t *sx, SmBars &sb) {
     const int tid = threadIdx.x;
     const int n = a.rows * a.cols;
     const bool flat = a.ld_in == a.cols;
-    double total = 0.0;
-    for (int e = tid; e < n; e += 16 * kSmThreads) {
-        float x[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const int i = e + j * kSmThreads;
-            x[j] = 0.f;
-            if (i < n) {
-                const int r = flat ? 0 : i / a.cols;
-                x[j] = to_f32(g[flat ? i : r * a.ld_in + (i - r * a.cols)]);
-            }
-        }
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s = fmaf(x[j], x[j], s);
-        total += s;
-    }
+    constexpr int V = 16 / sizeof(T);
+    float total = flat && n % V == 0 && aligned_to(g, 16) ? small_squares<T, V>(g, n / V, n / V, 0, true)
+                                                           : small_squares<T, 1>(g, n, a.cols, a.ld_in, flat);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if ((tid & 31) == 0) sb.part[tid >> 5] = total;
     __syncthreads();
-    if (tid == 0) {
-        for (int i = 1; i < kSmThreads / 32; ++i) total += sb.part[i];
-        sb.factor = (float)((double)a.held / (sqrt(total) + (double)a.eps));
+    if (tid < 32) {
+        double s = tid < kSmThreads / 32 ? sb.part[tid] : 0.0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (tid == 0) sb.factor = (float)((double)a.held / (sqrt(s) + (double)a.eps));
     }
     __syncthreads();
     const float k = sb.factor;
-    const int per_row = a.nb * 8, chunks = a.R * per_row;  // of 8 columns
+    // neighbouring threads read neighbouring elements of G
+    if (a.wide) {
+        if (aligned_to(g, 4 * sizeof(T)) && a.ld_in % 4 == 0 && a.n % 4 == 0) small_rows<T, 4>(a, g, sx, k);
+        else small_rows<T, 1>(a, g, sx, k);
+        return;
+    }
 #pragma unroll 2
-    for (int i = tid; i < chunks; i += kSmThreads) {
-        // neighbouring threads read neighbouring elements of G
-        const int r = a.wide ? i / per_row : i % a.R, c8 = a.wide ? i - r * per_row : i / a.R;
+    for (int i = tid; i < a.R * a.nb * 8; i += kSmThreads) {  // 8 of a column of G
+        const int r = i % a.R, c8 = i / a.R;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = c8 * 8 + j;
-            v[j] = 0.f;
-            if (r < a.m && c < a.n) v[j] = to_f32(a.wide ? g[r * a.ld_in + c] : g[c * a.ld_in + r]);
+            v[j] = r < a.m && c < a.n ? to_f32(g[c * a.ld_in + r]) : 0.f;
         }
         Pack<__half, 8> p;
 #pragma unroll
@@ -710,26 +755,24 @@ __device__ __forceinline__ void small_store(const SmArgs &a, T *o, const float (
 }
 
 // A wide O's rows from the finished chunk, which the threads put back into its
-// boxes in O's 16-bit type: 8 elements at a time, neighbours side by side.
+// boxes in O's 16-bit type: a warp per row, W elements at a time.
+template <typename T, int W>
+__device__ __forceinline__ void small_copy_by(const SmArgs &a, T *o, const uint8_t *sx, int c0, int cols) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = warp; r < a.m; r += kSmThreads / 32)
+#pragma unroll 2
+        for (int c = c0 + lane * W; c < c0 + cols; c += 32 * W)
+            *reinterpret_cast<Pack<T, W> *>(o + r * a.ld_out + c) =
+                *reinterpret_cast<const Pack<T, W> *>(sx + box_at(a.R, r, c >> 3) + (c & 7) * 2);
+}
 template <typename T>
-__device__ __forceinline__ void small_copy(const SmArgs &a, T *o, const uint8_t *sx, int c80, int n8) {
-    const bool vec = aligned_to(o, 16) && a.ld_out % 8 == 0;
-    for (int i = threadIdx.x; i < a.m * n8; i += kSmThreads) {
-        const int r = i / n8, c8 = c80 + i - r * n8, c = c8 * 8;
-        const Pack<T, 8> p = *reinterpret_cast<const Pack<T, 8> *>(sx + box_at(a.R, r, c8));
-        T *to = o + r * a.ld_out + c;
-        if (vec && c + 8 <= a.n) {
-            *reinterpret_cast<Pack<T, 8> *>(to) = p;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c + j < a.n) to[j] = p.v[j];
-        }
-    }
+__device__ __forceinline__ void small_copy(const SmArgs &a, T *o, const uint8_t *sx, int c0, int cols) {
+    if (aligned_to(o, 8) && a.ld_out % 4 == 0 && cols % 4 == 0) small_copy_by<T, 4>(a, o, sx, c0, cols);
+    else small_copy_by<T, 1>(a, o, sx, c0, cols);
 }
 
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) { ptx::tmem_ld16(t, v); }
 __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[32]) { ptx::tmem_ld32(t, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) { ptx::tmem_ld16(t, v); }
 
 template <int R>
 __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a) {
@@ -741,7 +784,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
     SmBars &sb = *reinterpret_cast<SmBars *>(sc + (R / 64) * box + (R == 64 ? 8192 : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (uint64_t *b : {&sb.sq, &sb.x, &sb.drain}) ptx::mbar_init(ptx::smem_u32(b), 1);
+        for (uint64_t *b : {&sb.sq, &sb.x[0], &sb.x[1], &sb.drain}) ptx::mbar_init(ptx::smem_u32(b), 1);
         sb.abort_flag = 0;
         ptx::fence_mbar_init();
         if (gridDim.x == 1) *a.status = 0;
@@ -754,16 +797,18 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
     if (a.in_type == CBA_F32) small_load(a, static_cast<const float *>(a.G) + b * a.batch_in, sx, sb);
     else if (a.in_type == CBA_F16) small_load(a, static_cast<const __half *>(a.G) + b * a.batch_in, sx, sb);
     else small_load(a, static_cast<const __nv_bfloat16 *>(a.G) + b * a.batch_in, sx, sb);
-    // everything that the tensor cores read was written by these threads
+    // Everything that the tensor cores read was written by these threads.  A wait
+    // that ran out shows at the next publish, to all threads at once.
+    bool ok = true;
     auto publish = [&]() {
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        __syncthreads();
+        ok = __syncthreads_and(ok) != 0;
         ptx::tc_fence_after();
+        return ok;
     };
     publish();
     const uint32_t tmem = sb.tmem_base, uX = ptx::smem_u32(sx), uS = ptx::smem_u32(ss), uC = ptx::smem_u32(sc);
-    const uint32_t tS = tmem, tQ = tmem + 128, tX = tmem + 256;
     constexpr uint32_t id_s = ptx::idesc_f16(128, R, false, false);
     const int km = (a.m + 15) / 16, kn = (a.n + 15) / 16;
     // 16 warps: the quarter of the rows that TMEM lets a warp read, and one of
@@ -771,26 +816,27 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
     const int quarter = warp & 3, part = warp >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const bool mine = quarter * 32 < R;  // this warp's rows exist
+    constexpr int issuer = R == 64 ? 2 : 0;  // of the MMAs: a warp without rows, if there is one
     constexpr int CS = R / 4;            // S columns per thread
     const int c_s = part * CS, nchunks = (a.nb + 3) / 4;
+    const uint32_t tS = tmem + (nchunks & 1) * 256, tQ = tS + 128;
     const float s_alpha = kNsSym / (a.held * a.held);
     volatile int *ab = &sb.abort_flag;
-    uint32_t ph_sq = 0, ph_x = 0;
-    auto wait = [&](uint64_t *bar, uint32_t &phase) {
-        const bool ok = ptx::mbar_wait_bounded(ptx::smem_u32(bar), phase, ab, a.status, kNsLimitNs);
-        phase ^= 1;
+    uint32_t ph_x = 0;  // a bit for each chunk in flight
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+        ok = ptx::mbar_wait_bounded(ptx::smem_u32(bar), phase, ab, a.status, kNsLimitNs) && ok;
         ptx::tc_fence_after();
-        return __syncthreads_and(ok) != 0;
     };
-    auto product = [&](uint32_t d, uint32_t u, int ksteps) {  // D = U U^T, R columns
+    // D (+)= U U^T, R columns, the K steps k0 .. k1 - 1 of U's ksteps
+    auto product = [&](uint32_t d, uint32_t u, int k0, int k1, int ksteps) {
         const ptx::Desc de = ptx::desc_of(u, 16, 1024, 2);
         if (ptx::elect_one()) {
 #pragma unroll 4
-            for (int ks = 0; ks < ksteps; ++ks) {
+            for (int ks = k0; ks < min(k1, ksteps); ++ks) {
                 const uint32_t off = ((ks >> 2) * box + (ks & 3) * 32) >> 4;
                 ptx::mma_f16(d, de, off, de, off, id_s, ks > 0);
             }
-            ptx::mma_commit(ptx::smem_u32(&sb.sq));
+            if (k1 >= ksteps) ptx::mma_commit(ptx::smem_u32(&sb.sq));
         }
         __syncwarp();
     };
@@ -798,16 +844,17 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
         const uint32_t id = ptx::idesc_f16(128, 64 * min(4, a.nb - 4 * ch), false, true);
         const ptx::Desc dc = ptx::desc_of(uC, 16, 1024, 2), dx = ptx::desc_of(uX + 4 * ch * box, box, 1024, 2);
         if (ptx::elect_one()) {
+#pragma unroll 4
             for (int ks = 0; ks < km; ++ks)
-                ptx::mma_f16(tX, dc, ((ks >> 2) * box + (ks & 3) * 32) >> 4, dx, ks * (2048 >> 4), id, ks > 0);
-            ptx::mma_commit(ptx::smem_u32(&sb.x));
+                ptx::mma_f16(tmem + (ch & 1) * 256, dc, ((ks >> 2) * box + (ks & 3) * 32) >> 4, dx, ks * (2048 >> 4),
+                             id, ks > 0);
+            ptx::mma_commit(ptx::smem_u32(&sb.x[ch & 1]));
         }
         __syncwarp();
     };
-    bool ok = true;
-    for (int step = 0; ok && step < a.steps; ++step) {
-        if (warp == 0) product(tS, uX, kn);
-        if (!(ok = wait(&sb.sq, ph_sq))) break;
+    if (warp == issuer) product(tS, uX, 0, kn, kn);
+    for (int step = 0; step < a.steps; ++step) {
+        wait(&sb.sq, 0);
         float s[CS];
         if (mine) {
             tmem_ld(tS + lanes + c_s, s);
@@ -818,9 +865,9 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
             for (int j = 0; j < CS; ++j) s[j] = __half2float(__float2half_rn(s[j] * s_alpha));
             box_put<__half>(ss, R, r, c_s, s);
         }
-        publish();
-        if (warp == 0) product(tQ, uS, km);
-        if (!(ok = wait(&sb.sq, ph_sq))) break;
+        if (!publish()) break;
+        if (warp == issuer) product(tQ, uS, 0, km, km);
+        wait(&sb.sq, 1);
         if (mine) {
             float q[CS];
             tmem_ld(tQ + lanes + c_s, q);
@@ -832,20 +879,19 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
             }
             box_put<__half>(sc, R, r, c_s, q);
         }
-        publish();
+        if (!publish()) break;
         const bool last = step + 1 == a.steps;
         const float alpha = (last ? a.scale / a.held : 1.f) / kNsSym;
-        for (int ch = 0; ok && ch < nchunks; ++ch) {
-            if (warp == 0) apply(ch);
-            if (!(ok = wait(&sb.x, ph_x))) break;
-            const int boxes = min(4, a.nb - 4 * ch);
-            if (mine && part < boxes)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c0 = ch * 256 + part * 64 + i * 32;
+        if (warp == issuer)
+            for (int ch = 0; ch < min(2, nchunks); ++ch) apply(ch);
+        for (int ch = 0; ch < nchunks; ++ch) {
+            wait(&sb.x[ch & 1], ph_x >> (ch & 1) & 1);
+            ph_x ^= 1u << (ch & 1);
+            if (mine)
+                for (int i = part; i < 2 * min(4, a.nb - 4 * ch); i += 4) {
+                    const int c0 = ch * 256 + i * 32;
                     float v[32];
-                    __syncwarp();
-                    ptx::tmem_ld32(tX + lanes + part * 64 + i * 32, v);
+                    ptx::tmem_ld32(tmem + (ch & 1) * 256 + lanes + i * 32, v);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] *= alpha;
@@ -861,17 +907,23 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
                         else if (r < a.m) small_store(a, static_cast<__nv_bfloat16 *>(a.O) + b * a.batch_out, v, r, c0);
                     }
                 }
-            publish();
+            if (!publish()) break;
+            if (warp == issuer) {
+                if (ch + 2 < nchunks) apply(ch + 2);
+                else if (!last) product(tS, uX, ch + 1 < nchunks || nchunks == 1 ? 0 : 16 * ch, 16 * ch + 16, kn);
+            }
             if (last && a.wide && a.out_type != CBA_F32) {
+                const int cols = min(256, a.n - 256 * ch);
                 if (a.out_type == CBA_F16)
-                    small_copy(a, static_cast<__half *>(a.O) + b * a.batch_out, sx, 32 * ch, 8 * boxes);
+                    small_copy(a, static_cast<__half *>(a.O) + b * a.batch_out, sx, 256 * ch, cols);
                 else
-                    small_copy(a, static_cast<__nv_bfloat16 *>(a.O) + b * a.batch_out, sx, 32 * ch, 8 * boxes);
+                    small_copy(a, static_cast<__nv_bfloat16 *>(a.O) + b * a.batch_out, sx, 256 * ch, cols);
             }
         }
+        if (!ok) break;
     }
     // on a timeout MMAs may still be in flight: wait (bounded) for all of them
-    if (!ok && tid == 0) {
+    if (!ok && tid == issuer * 32) {
         int no = 0;
         ptx::mma_commit(ptx::smem_u32(&sb.drain));
         ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kNsLimitNs);
