@@ -1006,22 +1006,31 @@ struct NsProduct {
     CUtensorMap ta, tb;
 };
 
-// The tile: 256 x 256 by pairs of blocks once they fill half of the SMs; below
-// that smaller ones, which spread the product over more SMs; and where `split` (a
-// symmetric product without aux) has a long contraction and few tiles, clusters
-// that share it.
-bool ns_product(NsProduct *p, const NsOperand &oa, const NsOperand &ob, int M, int N, int K, bool split, int batch) {
-    const long long t256 = (long long)((M + 255) / 256) * ((N + 255) / 256) * batch;
+// The tile: 256 x 256 by pairs of blocks once they fill half of the SMs (a
+// symmetric product counts the tiles that it computes); below that smaller ones,
+// which spread the product over more SMs; and where `split` (a symmetric product
+// without aux) has a long contraction and few tiles, clusters that share it.
+// Five steps in us, the rule's side first:
+//   pairs from a quarter of the SMs on  1024x2048 154, from an eighth on 168; 1024x4096 196, from a half on 205
+//   symmetric tiles counted once        2048x2048 256, as if all were computed 309; 2048x8192 557, 611
+//   128 columns from half of the SMs    1024x2048 154, from a quarter on 167, from all 166
+//   contractions shared                 512x2304 109, not 128; 256x8192 117, not 235; 1024x4096 196, not 215
+//   by two only where of 48 stages  1024x1024 124, also below 132
+bool ns_product(NsProduct *p, const NsOperand &oa, const NsOperand &ob, int M, int N, int K, bool sym, bool split,
+                int batch) {
+    const long long m256 = (M + 255) / 256;
+    const long long t256 = (sym ? m256 * (m256 + 1) / 2 : m256 * ((N + 255) / 256)) * batch;
     const long long t128 = (long long)((M + 127) / 128) * ((N + 127) / 128) * batch;
     *p = NsProduct{1, 64, 1, {}, {}};
     if (t256 >= kNumSMs / 4) *p = NsProduct{2, 256, 1, {}, {}};
     else if (t128 >= kNumSMs / 2) *p = NsProduct{1, 128, 1, {}, {}};
     const int nk = (K + kNsBK - 1) / kNsBK, mt = (M + 127) / 128;
     if (split && p->cg == 1) {
-        // 128 blocks in clusters of 8 fit the GPU at once; at least 4 stages each
+        // 128 blocks in clusters of 8 fit the GPU at once; at least 4 stages each, and
+        // more where few share: joining costs them as much as it saves otherwise
         const long long tiles = (long long)mt * (mt + 1) / 2 * batch;
         for (int sk = 8; sk >= 2; sk /= 2)
-            if (tiles * sk <= 128 && nk >= 4 * sk) {
+            if (tiles * sk <= 128 && nk >= 4 * sk && nk * sk >= 96) {
                 *p = NsProduct{1, 128, sk, {}, {}};
                 break;
             }
@@ -1092,7 +1101,8 @@ cudaError_t ns_start(const cba_orthogonalize_desc_t &d, const NsPlan &p, const v
     return ns_start_vec<T, 1>(d, p, g, ld, bs, ws, held, st);
 }
 
-// All steps of a matrix in one block, where it fits.
+// All steps of a matrix in one block, where it fits (in us, and as launches of their
+// own: 50x500 24, 87; 128x576 44, 86; 64 of 64x256 25, 100; 304 of 128x512 86, 402).
 bool small_fits(const NsPlan &p) {
     const int R = p.m <= 64 ? 64 : 128;
     return p.m <= 128 && small_smem(R, (p.n + 63) / 64) <= kSmMax;
@@ -1137,16 +1147,16 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
     // C X, X's rows contracted over, tall X C
     NsProduct ps[2], pc, px[2];
     const int bufs = d.steps > 1 ? 2 : 1;
-    bool ok = ns_product(&pc, so, so, p.m, p.m, p.m, false, d.batch);
+    bool ok = ns_product(&pc, so, so, p.m, p.m, p.m, true, false, d.batch);
     NsArgs as{}, ac{}, ax{};
     as.a_major = as.b_major = p.wide ? 0 : 1;
     ax.b_major = p.wide ? 1 : 0;
     for (int i = 0; i < bufs && ok; ++i) {
         const NsOperand xs{x[i], d.rows, d.cols, p.x_pitch, as.a_major}, xk{x[i], d.rows, d.cols, p.x_pitch, 0},
             xn{x[i], d.rows, d.cols, p.x_pitch, 1};
-        ok = ns_product(&ps[i], xs, xs, p.m, p.m, p.n, true, d.batch) &&
-             (p.wide ? ns_product(&px[i], co, xn, d.rows, d.cols, p.m, false, d.batch)
-                     : ns_product(&px[i], xk, co, d.rows, d.cols, p.m, false, d.batch));
+        ok = ns_product(&ps[i], xs, xs, p.m, p.m, p.n, true, true, d.batch) &&
+             (p.wide ? ns_product(&px[i], co, xn, d.rows, d.cols, p.m, false, false, d.batch)
+                     : ns_product(&px[i], xk, co, d.rows, d.cols, p.m, false, false, d.batch));
     }
     if (!ok) return cudaErrorInvalidValue;
     as.M = as.N = ac.M = ac.N = ac.K = ax.K = p.m;
