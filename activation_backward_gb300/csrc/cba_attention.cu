@@ -573,13 +573,20 @@ __device__ __forceinline__ void store_sums(const float4 *at, int used, long long
         float4 x[C / 4];
 #pragma unroll
         for (int j = 0; j < C / 4; ++j) x[j] = __ldcg(at + (c / 4 + j) * kT);
-        for (int i = 1; i < used; ++i) {
-            float4 y[C / 4];
+        for (int i = 1; i < used; i += 2) {  // two items' loads in flight
+            float4 y[2][C / 4];
 #pragma unroll
-            for (int j = 0; j < C / 4; ++j) y[j] = __ldcg(at + i * stride + (c / 4 + j) * kT);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < C / 4; ++j)
-                x[j] = make_float4(x[j].x + y[j].x, x[j].y + y[j].y, x[j].z + y[j].z, x[j].w + y[j].w);
+                for (int j = 0; j < C / 4; ++j) {
+                    y[h][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i + h < used) y[h][j] = __ldcg(at + (i + h) * stride + (c / 4 + j) * kT);
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < C / 4; ++j)
+                    x[j] = make_float4(x[j].x + y[h][j].x, x[j].y + y[h][j].y, x[j].z + y[h][j].z, x[j].w + y[h][j].w);
         }
 #pragma unroll
         for (int j = 0; j < C / 4; j += 2)
@@ -1372,14 +1379,18 @@ struct AtPlan {
 };
 
 // Whether tiles of `steps` steps at most, `tiles` of them with `all` steps
-// together, are cut into items: where the longest is more than `most` times an
-// SM's share, into items of about half of it, but of 8 steps at least (some 10
-// us; an item that is joined costs 3-5 more).
+// together, are cut into items: where the longest is more than 12 steps above
+// `most` times an SM's share, into items of about half of it, but of 8 steps at
+// least.  (A step takes 1 to 1.5 us; an item that is joined costs 4 us, and its
+// tile 1.5 us more per item.  Causal, dim 128, whole / cut: 4096 tokens with 4
+// heads 59 / 80 us, 2048 with 8 / 1 heads 186 / 47, 1024 with 32 / 4 heads 111 / 50,
+// 8192 with 8 / 2 heads 413 / 302.  Items of 0.4 or 0.9 of the share: 3 to 8% slower
+// on the last and on 3 documents of 8192 tokens; of 4 steps at least: 74 us where 50.)
 AtCut plan_cut(long long tiles, long long steps, double all, double most) {
     const double share = all / kNumSMs;
     const long long chunk = std::max(8LL, (long long)(0.6 * share) + 1);
     AtCut c{(int)std::max(1LL, steps), 1, 0};
-    if (steps <= most * share || steps < chunk + chunk / 4 || tiles > 1024) return c;
+    if (steps <= most * share + 12 || steps < chunk + chunk / 4 || tiles > 1024) return c;
     c.chunk = (int)chunk;
     c.chunks = (int)((steps + chunk - 1) / chunk);
     c.tiles = (int)tiles;
@@ -1445,11 +1456,13 @@ int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
                                        : std::min((double)d->batch, std::max((double)d->total_q / std::max(1, d->len_q),
                                                                              (double)d->total_k / std::max(1, d->len_k)));
         const double all = seqs * d->heads_q * p->q_tiles * p->k_tiles * (d->causal ? 0.5 : 1.0);
-        // SMs that are done with dk and dv go on to dq, so there a tile may take longer (packed 8192
-        // h16/4: 176 us with its longest tile at 1.2 times the share whole, 184 us with it cut)
+        // SMs that are done with dk and dv go on to dq, so a tile of dk and dv may take the time
+        // of both shares, and where those are whole a tile of dq that of what is left beside them
+        // (packed 8192 h16/4: 176 us with its longest tile at 1.2 times the share whole, 184 us cut;
+        // dq cut beside whole dk and dv, 4096 tokens, 4 heads: 75 us, whole 59)
         p->kv = plan_cut((long long)p->k_tiles * d->heads_kv * d->batch,
                          (long long)p->q_tiles * (d->heads_q / d->heads_kv), all, 1.75);
-        p->q = plan_cut((long long)p->q_tiles * d->heads_q * d->batch, p->k_tiles, all, 1.25);
+        p->q = plan_cut((long long)p->q_tiles * d->heads_q * d->batch, p->k_tiles, all, p->kv.tiles ? 1.25 : 2.3);
     }
     p->off_nlse = 256;
     p->off_ndsum = p->off_nlse + ((size_t)rows * 4 + 255) / 256 * 256;
