@@ -617,21 +617,23 @@ int bwd_tpr(int cols) {
     return 0;
 }
 
-// Whether a call's rows move as 16-byte vectors and are enough for the ring:
-// with fewer than 4 rows per group it has nothing to run ahead of.  (In us, ring
-// and rows held in registers: bf16 forward 65536x2048 98, 128; 4864x2048 13.9, 14.8;
-// 2432x2048 8.9, 8.7; backward 32768x4096 142, 243; 4864x4096 37, 53; 608x4096
-// 15.4, 14.8; 304x4096 18.9, 14.9; 9728x512 12.7, 20.9.)
+// Whether a call's rows move as 16-byte vectors and are enough for the ring: a
+// row for every group of a block per SM.  (In us, ring and rows held in registers:
+// bf16 forward 65536x2048 98, 128; 4864x2048 13.9, 14.8; 2432x512 3.4, 4.6;
+// backward 32768x4096 142, 243; 608x4096 16.9, 18.8; 304x4096 13.1, 14.8; 2432x512
+// 7.7, 11.0.  The one size found where it loses: forward 65536x512 31, 29.)
 bool ring_rows(long long rows, int tpr) {
     const int groups = tpr < 256 ? 256 / tpr : 1;
-    return rows >= 4LL * groups * kNumSMs;
+    return rows >= (long long)groups * kNumSMs;
 }
 
 // The plan of a backward call whose rows move as 16-byte vectors or not.  Blocks:
 // a row per group while that needs no more than a block per SM; past that at
 // least 4 rows per group, so that the partial rows stay small beside the data
 // they come from.  (fp32, 255 columns, us with at least 1, 4, 16 rows: 8192 rows
-// 11.1, 10.3, 16.5; 1000 rows 7.6, 6.6, 7.0; bf16 2000x1024 13.6, 11.8, 14.0.)
+// 11.1, 10.3, 16.5; 1000 rows 7.6, 6.6, 7.0; the ring, bf16, a block per SM and two
+// of fewer rows: 608x4096 16.9, 21.0; 1216x2048 12.2, 14.1; 304x4096 13.1 and with
+// half of the blocks 14.4.)
 LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d, bool vec) {
     LnPlan p{};
     p.tpr = bwd_tpr(d.cols);
@@ -641,18 +643,15 @@ LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d, bool vec) {
             if (d.cols <= t * e) p.ring_tpr = t;
         if (p.ring_tpr && !ring_rows(d.rows, p.ring_tpr)) p.ring_tpr = 0;
     }
-    if (p.ring_tpr) {
-        p.nblk = kNumSMs * ring_bwd_per_sm(p.ring_tpr);
-    } else {
-        const int groups = p.tpr && p.tpr < 128 ? 128 / p.tpr : 1;
-        const int per_sm = p.tpr == 0 ? 1 : p.tpr >= 512 ? 1 : p.tpr == 256 ? 2 : 4;
-        long long most = (long long)kNumSMs * per_sm;
-        if (p.tpr == 0) most = std::max(1LL, most * 6 / ((d.cols + kWideCols - 1) / kWideCols));
-        const long long one = std::min<long long>(kNumSMs, (d.rows + groups - 1) / groups);
-        const long long four = (d.rows + 4LL * groups - 1) / (4LL * groups);
-        p.nblk = (int)std::max(1LL, std::min(most, std::max(one, four)));
-        if (d.rows == 0) p.nblk = 0;
-    }
+    const int tpr = p.ring_tpr ? p.ring_tpr : p.tpr, block = p.ring_tpr ? 256 : 128;
+    const int groups = tpr && tpr < block ? block / tpr : 1;
+    const int per_sm = p.ring_tpr ? ring_bwd_per_sm(tpr) : tpr == 0 ? 1 : tpr >= 512 ? 1 : tpr == 256 ? 2 : 4;
+    long long most = (long long)kNumSMs * per_sm;
+    if (tpr == 0) most = std::max(1LL, most * 6 / ((d.cols + kWideCols - 1) / kWideCols));
+    const long long one = std::min<long long>(kNumSMs, (d.rows + groups - 1) / groups);
+    const long long four = (d.rows + 4LL * groups - 1) / (4LL * groups);
+    p.nblk = (int)std::max(1LL, std::min(most, std::max(one, four)));
+    if (d.rows == 0) p.nblk = 0;
     p.part_bytes = ((size_t)p.nblk * 2 * d.cols * sizeof(float) + 255) / 256 * 256;
     p.off_rowc = p.part_bytes;
     p.total = p.part_bytes;
