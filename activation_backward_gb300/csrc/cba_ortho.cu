@@ -1006,31 +1006,36 @@ struct NsProduct {
     CUtensorMap ta, tb;
 };
 
-// The tile: 256 x 256 by pairs of blocks once they fill half of the SMs (a
-// symmetric product counts the tiles that it computes); below that smaller ones,
-// which spread the product over more SMs; and where `split` (a symmetric product
-// without aux) has a long contraction and few tiles, clusters that share it.
-// Five steps in us, the rule's side first:
-//   pairs from a quarter of the SMs on  1024x2048 154, from an eighth on 168; 1024x4096 196, from a half on 205
-//   symmetric tiles counted once        2048x2048 256, as if all were computed 309; 2048x8192 557, 611
-//   128 columns from half of the SMs    1024x2048 154, from a quarter on 167, from all 166
-//   contractions shared                 512x2304 109, not 128; 256x8192 117, not 235; 1024x4096 196, not 215
-//   by two only where of 48 stages  1024x1024 124, also below 132
+// The tile whose rounds over the SMs take least: a round of 256 x 256 by pairs of
+// blocks takes 1, of 128 x 128 0.8, of 128 x 64 0.55 of the time (a smaller tile
+// moves more bytes per product); 128 x 64 computes all of a symmetric product.
+// And where `split` (a symmetric product without aux) has a long contraction and
+// few tiles, clusters share it.  Five steps in us, the rule's side first:
+//   128 columns, not pairs   1024x2048 154, 168; symmetric ones of 2048x2048 256, 309, of 8 of 1024x1024 279, 368
+//   pairs, not 128 columns   1024x4096 196, 205; symmetric ones of 2 of 8192x2048 857, 1033
+//   64 columns, not 128      symmetric ones of 1024x1024 124, 152
+//   128 columns, not 64      1024x2048 154, 166
+//   contractions shared      512x2304 109, not 128; 256x8192 117, not 235; 1024x4096 196, not 215
+//   by two only where long   1024x1024 124, also below 48 stages 132
 bool ns_product(NsProduct *p, const NsOperand &oa, const NsOperand &ob, int M, int N, int K, bool sym, bool split,
                 int batch) {
-    const long long m256 = (M + 255) / 256;
-    const long long t256 = (sym ? m256 * (m256 + 1) / 2 : m256 * ((N + 255) / 256)) * batch;
-    const long long t128 = (long long)((M + 127) / 128) * ((N + 127) / 128) * batch;
-    *p = NsProduct{1, 64, 1, {}, {}};
-    if (t256 >= kNumSMs / 4) *p = NsProduct{2, 256, 1, {}, {}};
-    else if (t128 >= kNumSMs / 2) *p = NsProduct{1, 128, 1, {}, {}};
-    const int nk = (K + kNsBK - 1) / kNsBK, mt = (M + 127) / 128;
+    auto tiles = [&](int tm, int tn, bool half) {
+        const long long mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
+        return (half ? mt * (mt + 1) / 2 : mt * nt) * batch;
+    };
+    auto cost = [](long long tiles, int at_once, int round) { return (tiles + at_once - 1) / at_once * round; };
+    const long long c256 = cost(tiles(256, 256, sym), kNumSMs / 2, 20), c128 = cost(tiles(128, 128, sym), kNumSMs, 16),
+                    c64 = cost(tiles(128, 64, false), kNumSMs, 11);
+    if (c256 < c128 && c256 < c64) *p = NsProduct{2, 256, 1, {}, {}};
+    else if (c128 <= c64) *p = NsProduct{1, 128, 1, {}, {}};
+    else *p = NsProduct{1, 64, 1, {}, {}};
+    const int nk = (K + kNsBK - 1) / kNsBK;
     if (split && p->cg == 1) {
         // 128 blocks in clusters of 8 fit the GPU at once; at least 4 stages each, and
         // more where few share: joining costs them as much as it saves otherwise
-        const long long tiles = (long long)mt * (mt + 1) / 2 * batch;
+        const long long t128 = tiles(128, 128, true);
         for (int sk = 8; sk >= 2; sk /= 2)
-            if (tiles * sk <= 128 && nk >= 4 * sk && nk * sk >= 96) {
+            if (t128 * sk <= 128 && nk >= 4 * sk && nk * sk >= 96) {
                 *p = NsProduct{1, 128, sk, {}, {}};
                 break;
             }
