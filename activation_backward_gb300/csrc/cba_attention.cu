@@ -206,30 +206,51 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         const long long rows = (a.cu_k ? 1 : (long long)a.batch) * tokens * a.hkv;
         const long long per = (rows + v_blocks - 1) / v_blocks;
         const long long r1 = min(rows, (blockIdx.x + 1LL) * per);
-        for (long long r0 = blockIdx.x * per; r0 < r1; r0 += 256 / LPR) {
-            const long long r = r0 + t / LPR;
-            float n = 0.f;
-            if (r < r1 && lane * 8 < a.dim) {
-                const int h = (int)(r % a.hkv);
-                const long long tok = r / a.hkv % tokens, b = r / a.hkv / tokens;
-                const uint4 x = *reinterpret_cast<const uint4 *>(
-                    static_cast<const uint16_t *>(a.v) + b * a.sv[0] + tok * a.sv[1] + h * a.sv[2] + lane * 8);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        long long r = blockIdx.x * per + t / LPR;
+        int h = (int)(r % a.hkv);
+        long long tok = rows ? r / a.hkv % tokens : 0, b = rows ? r / a.hkv / tokens : 0;
+        constexpr int NR = 4;  // rows of a thread in flight
+        while (r - t / LPR < r1) {  // the same for all of the block
+            uint4 x[NR];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 p = unpack2<false>(xs[j]);
-                    n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
-                }
+            for (int j = 0; j < NR; ++j) {
+                x[j] = make_uint4(0, 0, 0, 0);
+                if (r < r1 && lane * 8 < a.dim)
+                    x[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.v) + b * a.sv[0] +
+                                                            tok * a.sv[1] + h * a.sv[2] + lane * 8);
+                r += 256 / LPR;
+                h += 256 / LPR;
+                tok += h / a.hkv;
+                h %= a.hkv;
+                while (tok >= tokens) tok -= tokens, ++b;
             }
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            most = fmaxf(most, n);
+            for (int j = 0; j < NR; ++j) {
+                float n = 0.f;
+                const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 p = unpack2<false>(xs[e]);
+                    n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                most = fmaxf(most, n);
+            }
         }
     }
     if constexpr (!BF16) {  // a maximum does not depend on the order
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        if ((t & 31) == 0) atomicMax(a.maxima + which, __float_as_uint(most));
+        __shared__ float warps[8];
+        if ((t & 31) == 0) warps[t >> 5] = most;
+        __syncthreads();
+        if (t == 0) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i) most = fmaxf(most, warps[i]);
+            // thousands of blocks on one word: most of them see that it is no less already
+            if (__float_as_uint(most) > __ldcg(a.maxima + which)) atomicMax(a.maxima + which, __float_as_uint(most));
+        }
     }
 }
 

@@ -525,7 +525,7 @@ __device__ __forceinline__ double block_sum(double v, double *sm) {
 
 // Partial sums of squares: block (p, b) takes the p-th part of matrix b's 16-byte
 // vectors (VEC elements; 1 where rows are not whole vectors), summed in a fixed
-// order: 4 vectors in fp32, their a thread's sum in fp32 too.
+// order: 4 vectors in fp32, their sums in fp64.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
     ns_norm_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, double *part) {
