@@ -294,3 +294,27 @@ def test_gradients_match_differences_of_the_forward(cuda_lib):
         # directional sum's 2-norm
         bar = 16 * 2.0 ** -11 * np.sqrt(((g * step) ** 2).sum()) + 16 * 2.0 ** -11 * np.abs(g).max() * np.sqrt(g.size) / 8
         assert abs((g * step).sum() - want) <= bar, (i, (g * step).sum(), want, bar)
+
+
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("dim,dtype", [(64, F16), (128, BF)], ids=str)
+@pytest.mark.parametrize("len_q,len_k,hq,hk", [(2100, 3900, 2, 1), (1900, 300, 8, 1), (2050, 2050, 4, 4)])
+def test_many_items_of_a_tile(cuda_lib, len_q, len_k, hq, hk, dim, dtype, causal):
+    """Both sides cut, tiles of up to 15 items, and tiles that stay whole although some SMs go without."""
+    rng = np.random.default_rng(len_q + hq)
+    args = make(rng, 1, len_q, len_k, hq, hk, dim, dtype, "bshd", 0.1, causal)
+    first = [t.clone() for t in run(*args, 0.1, causal)]
+    compare(args, first, 0.1, causal, dtype)
+    assert all(torch.equal(a, b) for a, b in zip(first, run(*args, 0.1, causal)))
+
+
+@pytest.mark.parametrize("hk,len_k", [(1, 3), (3, 700), (7, 129)])
+def test_the_row_of_v_that_sets_the_scale(cuda_lib, hk, len_k):
+    """f16: one row of v a thousand times the rest, the last of all rows; nothing overflows."""
+    rng = np.random.default_rng(hk)
+    q, k, v, o, lse, do = make(rng, 3, 140, len_k, 2 * hk, hk, 64, F16, "bshd", 0.1, False)
+    v[-1, -1, -1] *= 1000.0
+    o2, lse2 = T.attention_forward(f8(q[-1]), f8(k[-1]), f8(v[-1]), 0.1, False)
+    o[-1] = torch.from_numpy(o2).to("cuda", F16)
+    args = (q, k, v, o, lse, do)
+    compare(args, run(*args, 0.1, False), 0.1, False, F16)

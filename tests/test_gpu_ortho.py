@@ -137,3 +137,16 @@ def test_same_bits_and_graph(cuda_lib):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(first, out)
+
+
+@pytest.mark.parametrize("shape", [
+    # clusters of two blocks on a long contraction; tiles of 128 columns beside pairs of blocks; both sides tall
+    (6, 300, 3201), (8, 1000, 1010), (3, 5000, 300), (1, 1999, 2050),
+    # one block per matrix, from one chunk of columns to seven, in rows that are and are not whole vectors
+    (2, 64, 256), (2, 40, 260), (1, 77, 513), (2, 513, 77), (2, 33, 1030), (1, 128, 600),
+], ids=str)
+def test_tiles_and_chunks(cuda_lib, shape):
+    G = draw(sum(shape), *shape)
+    first = call(G, torch.full(shape, 9.0, device="cuda", dtype=torch.float16)).clone()
+    check(first, G)
+    assert torch.equal(first, call(G, torch.empty_like(first)))
