@@ -87,7 +87,9 @@ struct NsTile {
     static constexpr int ROWS_B = BN / CG;  // B rows a block loads
     static constexpr uint32_t A_BYTES = 128u * 128u, B_BYTES = ROWS_B * 128u;
     static constexpr uint32_t STAGE = A_BYTES + B_BYTES;
-    static constexpr uint32_t SMEM = kNsStages * STAGE + 1024 + sizeof(NsBars);
+    static constexpr uint32_t STAGED = kNsStages * STAGE;  // 32 rows x 32 columns of 16 bits per epilogue warp
+    static constexpr uint32_t BARS = STAGED + kNsEpiWarps * 2048;
+    static constexpr uint32_t SMEM = BARS + 1024 + sizeof(NsBars);
     static constexpr int TM = 128 * CG;     // tile rows
     static constexpr uint32_t TMEM_COLS = 2 * BN;
 };
@@ -136,7 +138,38 @@ __device__ __forceinline__ void triangle(int u, int &i, int &j) {
     i = u - j * (j + 1) / 2;
 }
 
-// 16 bytes at a time, a chunk of N aux values ahead of their use.
+// 32 columns of a warp's 32 rows, through its 2 KB of shared memory, so that four
+// lanes store 64 bytes of a row side by side: 32 lanes that store 16 bytes of their
+// own rows take a line each (5 of 700x700 208, 264 us; 3500x4000 811, 839; 2048x2048
+// alike).  `at`: of the first row; n columns, `live` rows exist.
+template <typename T>
+__device__ __forceinline__ void ns_store_staged(void *out, long long at, long long ld, const float (&v)[32], int live,
+                                                int n, uint8_t *stage) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        Pack<T, 8> p;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p.v[e] = from_f32<T>(v[8 * j + e]);
+        *reinterpret_cast<Pack<T, 8> *>(stage + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = p;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4, c = lane & 3;
+        const Pack<T, 8> p = *reinterpret_cast<const Pack<T, 8> *>(stage + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+        T *o = static_cast<T *>(out) + at + r * ld + 8 * c;
+        if (r >= live) continue;
+        if (8 * c + 8 <= n) *reinterpret_cast<Pack<T, 8> *>(o) = p;
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * c + e < n) o[e] = p.v[e];
+    }
+    __syncwarp();  // read before the next columns are written
+}
+
+// N aux values of a row, 16 bytes at a time.
 template <int N>
 __device__ __forceinline__ void aux_load(Pack<__half, 8> (&p)[N / 8], const __half *aux, int n) {
 #pragma unroll
@@ -147,10 +180,11 @@ __device__ __forceinline__ void aux_load(Pack<__half, 8> (&p)[N / 8], const __ha
 // N results of one row from column `col` on (n of them in the matrix; live: the
 // row is): out = alpha v + beta aux + diag I, stored, and on tiles above the
 // diagonal of a symmetric matrix (mirror) also as a column.  Called by whole warps
-// whose lanes hold neighbouring rows, an even one in an even lane.
+// whose lanes hold neighbouring rows, an even one in an even lane.  `stage`: the
+// warp's shared memory for 32 columns, or NULL.
 template <int N>
 __device__ __forceinline__ void ns_result(const NsArgs &a, float (&v)[N], const Pack<__half, 8> *aux, int b, int row,
-                                          int col, bool mirror) {
+                                          int col, bool mirror, uint8_t *stage) {
     const int n = a.N - col;
     if (n <= 0) return;
     const bool live = row < a.M;
@@ -172,6 +206,15 @@ __device__ __forceinline__ void ns_result(const NsArgs &a, float (&v)[N], const 
             if ((row & ~1) < a.M && j + odd < n) *reinterpret_cast<__half2 *>(o + (col + j + odd) * a.out_ld) = h;
         }
     }
+    if constexpr (N == 32) {
+        if (stage && a.vec && a.out_type != CBA_F32) {
+            const int first = row - (int)(threadIdx.x & 31);
+            const long long at = b * a.out_batch + first * a.out_ld + col;
+            if (a.out_type == CBA_F16) ns_store_staged<__half>(a.out, at, a.out_ld, v, a.M - first, n, stage);
+            else ns_store_staged<__nv_bfloat16>(a.out, at, a.out_ld, v, a.M - first, n, stage);
+            return;
+        }
+    }
     if (!live) return;
     const long long at = b * a.out_batch + row * a.out_ld + col;
     if (a.out_type == CBA_F16) ns_store<__half>(a.out, at, v, n, a.vec);
@@ -188,7 +231,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
     // both blocks of a pair round up alike: the same kernel, the same layout
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-    NsBars &sb = *reinterpret_cast<NsBars *>(smem + kNsStages * L::STAGE);
+    NsBars &sb = *reinterpret_cast<NsBars *>(smem + L::BARS);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = CG == 2 ? ptx::cluster_ctarank() : 0;
     if (tid == 0) {
@@ -336,7 +379,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
             where(i, b, m0, n0);
             const int row = m0 + (int)rank * 128 + quarter * 32 + lane;
             const __half *aux = a.aux ? a.aux + b * a.aux_batch + min(row, a.M - 1) * a.aux_ld + n0 + c0 : nullptr;
-            Pack<__half, 8> ax[4];
+            Pack<__half, 8> ax[4];  // 32 columns ahead (all of them while the products run: C 1 us slower)
             if (aux) aux_load<32>(ax, aux, a.N - n0 - c0);
             ok = ptx::mbar_wait_bounded(ptx::smem_u32(&sb.acc_full[ac]), (uint32_t)(i / 2) & 1u, ab, a.status,
                                         kNsLimitNs);
@@ -360,7 +403,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                             ptx::mbar_arrive(ptx::smem_u32(&sb.acc_empty[ac]));
                     }
                 }
-                ns_result<32>(a, v, ax, b, row, n0 + c0 + c, a.sym && m0 < n0);
+                ns_result<32>(a, v, ax, b, row, n0 + c0 + c, a.sym && m0 < n0, smem + L::STAGED + (warp - 2) * 2048);
                 if (aux && c + 32 < BN / 2) aux_load<32>(ax, aux + c + 32, a.N - n0 - c0 - c - 32);
             }
         }
@@ -502,7 +545,7 @@ __global__ void __launch_bounds__(kNsThreads, 1)
                     v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
                 }
                 __syncwarp();
-                ns_result<8>(a, v, nullptr, b, m0 + row, n0 + c0 + c, m0 < n0);
+                ns_result<8>(a, v, nullptr, b, m0 + row, n0 + c0 + c, m0 < n0, nullptr);
             }
         }
     }
