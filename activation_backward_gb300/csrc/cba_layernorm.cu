@@ -84,8 +84,10 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) {
 
 // ---- forward: one row per group of TPR threads
 
+// (64 registers from 128 threads a row on, 1024 threads on an SM: 10000x9001 bf16
+// 165 us, with the 69 that the compiler takes 305.)
 template <typename T, typename P, int VEC, int TPR, int EPT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR < 128 ? 0 : 1024 / TPR)
     ln_fwd_kernel(const LnArgs a) {
     constexpr int NV = EPT / VEC;
     constexpr int BLOCK = TPR < 128 ? 128 : TPR;
@@ -125,22 +127,34 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     }
     T *y = static_cast<T *>(a.y) + row * a.ld_y;
     const P *ga = static_cast<const P *>(a.gamma), *be = static_cast<const P *>(a.beta);
+    // 8 columns' parameters at a time: no load of theirs moves ahead of a store to y by itself
+    // (20000x1001 bf16: 46 -> 32 us)
+    constexpr int CH = VEC < 8 ? 8 / VEC : 1;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * TPR + t) * VEC;
-        if (c < a.cols) {
-            Pack<P, VEC> g, b;
-            if (ga) g = load_pack<P, VEC>(ga + c);
-            if (be) b = load_pack<P, VEC>(be + c);
-            Pack<T, VEC> o;
+    for (int i0 = 0; i0 < NV; i0 += CH) {
+        Pack<P, VEC> g[CH], b[CH];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float h = (v[i * VEC + j] - mean) * rstd;
-                if (ga) h *= to_f32(g.v[j]);
-                if (be) h += to_f32(b.v[j]);
-                o.v[j] = from_f32<T>(h);
+        for (int k = 0; k < CH; ++k) {
+            const int c = ((i0 + k) * TPR + t) * VEC;
+            if (c < a.cols) {
+                if (ga) g[k] = load_pack<P, VEC>(ga + c);
+                if (be) b[k] = load_pack<P, VEC>(be + c);
             }
-            *reinterpret_cast<Pack<T, VEC> *>(y + c) = o;
+        }
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int i = i0 + k, c = (i * TPR + t) * VEC;
+            if (c < a.cols) {
+                Pack<T, VEC> o;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    float h = (v[i * VEC + j] - mean) * rstd;
+                    if (ga) h *= to_f32(g[k].v[j]);
+                    if (be) h += to_f32(b[k].v[j]);
+                    o.v[j] = from_f32<T>(h);
+                }
+                *reinterpret_cast<Pack<T, VEC> *>(y + c) = o;
+            }
         }
     }
 }
@@ -155,10 +169,12 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnArgs a) {
     const P *ga = static_cast<const P *>(a.gamma), *be = static_cast<const P *>(a.beta);
     int half = 0;
     float s[1] = {0.f};
+#pragma unroll 8
     for (int c = threadIdx.x; c < a.cols; c += 1024) s[0] += to_f32(x[c]);
     row_sum<1024, 1>(s, buf, half, 0, threadIdx.x);
     const float mean = s[0] * a.inv_cols;
     s[0] = 0.f;
+#pragma unroll 8
     for (int c = threadIdx.x; c < a.cols; c += 1024) {
         const float d = to_f32(x[c]) - mean;
         s[0] = fmaf(d, d, s[0]);
@@ -169,11 +185,18 @@ __global__ void __launch_bounds__(1024) ln_fwd_long_kernel(const LnArgs a) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
     }
-    for (int c = threadIdx.x; c < a.cols; c += 1024) {
-        float h = (to_f32(x[c]) - mean) * rstd;
-        if (ga) h *= to_f32(ga[c]);
-        if (be) h += to_f32(be[c]);
-        y[c] = from_f32<T>(h);
+    for (int c0 = threadIdx.x; c0 < a.cols; c0 += 4 * 1024) {  // loads of four columns ahead of their stores
+        float h[4], g[4], b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = min(c0 + k * 1024, a.cols - 1);
+            h[k] = to_f32(x[c]);
+            g[k] = ga ? to_f32(ga[c]) : 1.f;
+            b[k] = be ? to_f32(be[c]) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c0 + k * 1024 < a.cols) y[c0 + k * 1024] = from_f32<T>(fmaf((h[k] - mean) * rstd, g[k], b[k]));
     }
 }
 
@@ -210,8 +233,15 @@ __device__ __forceinline__ void write_partials(const LnArgs &a, float (&dg)[EPT]
 
 // ---- backward: a group of TPR threads walks rows; threads own columns
 
+// Blocks per SM, and registers for as many (20000x1001 bf16 49 us; where the compiler
+// took more, and the fourth block waited, 69).  A residual takes more of them:
+// 60000x257 with three blocks 55 us, with four, which spill, 106; 20000x1001 59, 106.
+__host__ __device__ constexpr int bwd_per_sm(int tpr, bool res) {
+    return tpr >= 512 ? 1 : tpr == 256 ? 2 : res ? 3 : 4;
+}
+
 template <typename T, typename P, int VEC, int TPR, int EPT, bool RES>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, bwd_per_sm(TPR, RES))
     ln_bwd_kernel(const LnArgs a) {
     constexpr int NV = EPT / VEC;
     constexpr int BLOCK = TPR < 128 ? 128 : TPR;
@@ -529,6 +559,7 @@ __global__ void __launch_bounds__(512) ln_bwd_rowsums_kernel(const LnArgs a) {
     const float mean = a.mean_in[row], rstd = a.rstd_in[row];
     int half = 0;
     float s[2] = {0.f, 0.f};
+#pragma unroll 8
     for (int c = threadIdx.x; c < a.cols; c += 512) {
         const float g = to_f32(dy[c]) * (ga ? to_f32(ga[c]) : 1.f);
         s[0] += g;
@@ -552,23 +583,45 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_kernel(const LnArgs a) {
         dg[e] = db[e] = 0.f;
         ga[e] = gp && c < a.cols ? to_f32(gp[c]) : 1.f;
     }
-    for (long long row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        const float mean = a.mean_in[row], rstd = a.rstd_in[row];
-        const float2 m = a.rowc[row];
+    // a row's loads before the stores of the row before: none would move ahead of them by itself
+    // (10000x9001 bf16, with the row sums: 573 -> 238 us)
+    T px[E], pd[E], pr[E];
+    float mean = 0.f, rstd = 0.f;
+    float2 m = make_float2(0.f, 0.f);
+    auto fetch = [&](long long row) {
+        if (row >= a.rows) return;
         const T *x = xb + row * a.ld_x, *dy = dyb + row * a.ld_dy;
-        T *dx = static_cast<T *>(a.dx) + row * a.ld_dx;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const int c = c0 + e * 256;
             if (c < a.cols) {
-                const float h = (to_f32(x[c]) - mean) * rstd, d = to_f32(dy[c]);
-                dg[e] = fmaf(d, h, dg[e]);
-                db[e] += d;
-                float v = rstd * (d * ga[e] - fmaf(h, m.y, m.x));
-                if (rb) v += to_f32(rb[row * a.ld_res + c]);
-                dx[c] = from_f32<T>(v);
+                px[e] = x[c];
+                pd[e] = dy[c];
+                if (rb) pr[e] = rb[row * a.ld_res + c];
             }
         }
+        mean = a.mean_in[row];
+        rstd = a.rstd_in[row];
+        m = a.rowc[row];
+    };
+    fetch(blockIdx.y);
+    for (long long row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        T *dx = static_cast<T *>(a.dx) + row * a.ld_dx;
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (c0 + e * 256 < a.cols) {
+                const float h = (to_f32(px[e]) - mean) * rstd, d = to_f32(pd[e]);
+                dg[e] = fmaf(d, h, dg[e]);
+                db[e] += d;
+                v[e] = rstd * (d * ga[e] - fmaf(h, m.y, m.x));
+                if (rb) v[e] += to_f32(pr[e]);
+            }
+        }
+        fetch(row + gridDim.y);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (c0 + e * 256 < a.cols) dx[c0 + e * 256] = from_f32<T>(v[e]);
     }
     float *part = a.part + (size_t)blockIdx.y * 2 * a.cols;
 #pragma unroll
@@ -642,7 +695,7 @@ bool ring_rows(long long rows, int tpr) {
 // 11.1, 10.3, 16.5; 1000 rows 7.6, 6.6, 7.0; the ring, bf16, a block per SM and two
 // of fewer rows: 608x4096 16.9, 21.0; 1216x2048 12.2, 14.1; 304x4096 13.1 and with
 // half of the blocks 14.4.)
-LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d, bool vec) {
+LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d, bool vec, bool res) {
     LnPlan p{};
     p.tpr = bwd_tpr(d.cols);
     if (vec) {
@@ -653,7 +706,7 @@ LnPlan ln_bwd_plan(const cba_layernorm_desc_t &d, bool vec) {
     }
     const int tpr = p.ring_tpr ? p.ring_tpr : p.tpr, block = p.ring_tpr ? 256 : 128;
     const int groups = tpr && tpr < block ? block / tpr : 1;
-    const int per_sm = p.ring_tpr ? ring_bwd_per_sm(tpr) : tpr == 0 ? 1 : tpr >= 512 ? 1 : tpr == 256 ? 2 : 4;
+    const int per_sm = p.ring_tpr ? ring_bwd_per_sm(tpr) : tpr == 0 ? 1 : bwd_per_sm(tpr, res);
     long long most = (long long)kNumSMs * per_sm;
     if (tpr == 0) most = std::max(1LL, most * 6 / ((d.cols + kWideCols - 1) / kWideCols));
     const long long one = std::min<long long>(kNumSMs, (d.rows + groups - 1) / groups);
@@ -841,8 +894,9 @@ int cba_layernorm_forward(const cba_layernorm_desc_t *d, const void *x, const vo
 
 size_t cba_layernorm_workspace_bytes(const cba_layernorm_desc_t *d) {
     if (check_desc(d) != CBA_OK) return 0;
-    // whether rows move as vectors depends on the call's pointers: room for both
-    return std::max(ln_bwd_plan(*d, false).total, ln_bwd_plan(*d, true).total);
+    // whether rows move as vectors depends on the call's pointers: room for both (and with a
+    // residual there are no more blocks)
+    return std::max(ln_bwd_plan(*d, false, false).total, ln_bwd_plan(*d, true, false).total);
 }
 
 int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const void *dy,
@@ -871,7 +925,7 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = select_device_of(workspace);
     const bool v = vector_ok(*d, {x, dy, gamma, residual, dx}, {a.ld_x, a.ld_dy, a.ld_dx, residual ? a.ld_res : 0});
-    const LnPlan p = ln_bwd_plan(*d, v);
+    const LnPlan p = ln_bwd_plan(*d, v, residual != nullptr);
     a.rowc = ws_at<float2>(workspace, p.off_rowc);
     if (e == cudaSuccess && d->rows > 0) {
         e = with_types(*d, [&](auto t, auto pt) {
