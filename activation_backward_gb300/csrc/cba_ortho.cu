@@ -144,7 +144,7 @@ __device__ __forceinline__ void triangle(int u, int &i, int &j) {
 // alike).  `at`: of the first row; n columns, `live` rows exist.
 template <typename T>
 __device__ __forceinline__ void ns_store_staged(void *out, long long at, long long ld, const float (&v)[32], int live,
-                                                int n, uint8_t *stage) {
+                                                int n, bool vec, uint8_t *stage) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -154,6 +154,15 @@ __device__ __forceinline__ void ns_store_staged(void *out, long long at, long lo
         *reinterpret_cast<Pack<T, 8> *>(stage + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)) = p;
     }
     __syncwarp();
+    if (!vec) {  // rows on any address: 32 lanes store 32 elements of one (1000x2001 203 -> 180 us)
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            const T x = *reinterpret_cast<const T *>(stage + r * 64 + (((lane >> 3) ^ (r >> 1 & 3)) << 4) + (lane & 7) * 2);
+            if (r < live && lane < n) static_cast<T *>(out)[at + r * ld + lane] = x;
+        }
+        __syncwarp();
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + lane / 4, c = lane & 3;
@@ -207,11 +216,11 @@ __device__ __forceinline__ void ns_result(const NsArgs &a, float (&v)[N], const 
         }
     }
     if constexpr (N == 32) {
-        if (stage && a.vec && a.out_type != CBA_F32) {
+        if (stage && a.out_type != CBA_F32) {
             const int first = row - (int)(threadIdx.x & 31);
             const long long at = b * a.out_batch + first * a.out_ld + col;
-            if (a.out_type == CBA_F16) ns_store_staged<__half>(a.out, at, a.out_ld, v, a.M - first, n, stage);
-            else ns_store_staged<__nv_bfloat16>(a.out, at, a.out_ld, v, a.M - first, n, stage);
+            if (a.out_type == CBA_F16) ns_store_staged<__half>(a.out, at, a.out_ld, v, a.M - first, n, a.vec, stage);
+            else ns_store_staged<__nv_bfloat16>(a.out, at, a.out_ld, v, a.M - first, n, a.vec, stage);
             return;
         }
     }
@@ -634,13 +643,22 @@ __global__ void __launch_bounds__(256)
     for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
         const T *src = g + b * batch_stride + r * ld;
         __half *dst = x + b * x_batch + r * pitch;
-#pragma unroll 4
-        for (int c = lane * VEC; c < cols; c += 32 * VEC) {
-            const Pack<T, VEC> p = *reinterpret_cast<const Pack<T, VEC> *>(src + c);
-            Pack<__half, VEC> o;
+        constexpr int N = VEC == 1 ? 8 : 4;  // loads ahead of the stores
+        for (int c0 = lane * VEC; c0 < cols; c0 += N * 32 * VEC) {
+            Pack<T, VEC> p[N];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) o.v[j] = __float2half_rn(to_f32(p.v[j]) * k);
-            *reinterpret_cast<Pack<__half, VEC> *>(dst + c) = o;
+            for (int i = 0; i < N; ++i) {
+                const int c = c0 + i * 32 * VEC;
+                if (c < cols) p[i] = *reinterpret_cast<const Pack<T, VEC> *>(src + c);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = c0 + i * 32 * VEC;
+                Pack<__half, VEC> o;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) o.v[j] = __float2half_rn(to_f32(p[i].v[j]) * k);
+                if (c < cols) *reinterpret_cast<Pack<__half, VEC> *>(dst + c) = o;
+            }
         }
     }
 }
