@@ -27,7 +27,7 @@
 //
 // Measured (us; launches overlap, so a call takes less than their sum; rates count
 // the formulas' 5 products):
-//   8192 tokens, 32/8 heads of 128, causal, bf16   27 + 655 + 504, call 1125 (1225 where calls
+//   8192 tokens, 32/8 heads of 128, causal, bf16   27 + 655 + 504, call 1125 (1221 where calls
 //       follow each other without a pause): 1.22 PFLOP/s, 1.7 with the 7 products that run.
 //       The tensor cores bound it, at the clock that the power limit leaves them
 //   9 documents of 8192 tokens, 16/4 heads of 128  15 + 103 + 92, call 166: the longest tile

@@ -22,7 +22,7 @@
 //   backward 43264 x 255 fp32                    29: 4.6 TB/s, 0.68 (26 + 3.5; rows that are not
 //       whole vectors move 4 bytes a thread)
 //   169 x 512 fp32                               3 and 5.4 on the device; a call from Python takes
-//       5.2 and 8.6, the time in which the host issues it
+//       5.1 and 8.0, the time in which the host issues it
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
