@@ -17,6 +17,9 @@ def _rows(t):
         raise ValueError("the leading axes of the tensor do not fold into one")
     if t.numel() and t.shape[-1] > 1 and r.stride(1) != 1:
         raise ValueError("the innermost axis is not contiguous")
+    # (an expanded tensor's stride of 0 would read as the descriptor's "contiguous")
+    if t.numel() and r.shape[0] > 1 and r.stride(0) < r.shape[1]:
+        raise ValueError("rows of the tensor lie on one another (it is expanded): make it contiguous")
     return r
 
 

@@ -1,0 +1,63 @@
+"""What the torch-tensor calls read from their tensors and refuse (no GPU): the library's entry points are replaced by
+recorders, so nothing is launched and no pointer is read."""
+import pytest
+import torch
+
+from activation_backward_gb300 import _binding as B
+from activation_backward_gb300 import transformer as tr
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The arguments of the library calls that were made."""
+    seen = []
+    for name in ("cba_layernorm_forward", "cba_layernorm_backward", "cba_attention_backward", "cba_orthogonalize"):
+        monkeypatch.setattr(B, name, lambda *a, _n=name, **kw: seen.append((_n, *a)))
+    for name in ("cba_layernorm_workspace_bytes", "cba_attention_workspace_bytes", "cba_orthogonalize_workspace_bytes"):
+        monkeypatch.setattr(B, name, lambda d: 256)
+    return seen
+
+
+# ---- layer norm
+
+def norm_args(*shape):
+    rows = torch.zeros(shape).numel() // shape[-1]
+    return dict(x=torch.randn(shape), dy=torch.randn(shape), gamma=torch.ones(shape[-1]), mean=torch.zeros(rows), rstd=torch.ones(rows))
+
+
+@pytest.mark.parametrize("name", ["x", "dy", "residual"])
+@pytest.mark.parametrize("stored", [(1, 1, 32), (4, 1, 32), (1, 10, 32)], ids=str)
+def test_layer_norm_refuses_rows_that_lie_on_one_another(calls, name, stored):
+    """An expanded tensor (the gradient of a sum over positions is one) holds fewer elements than its shape says."""
+    a = norm_args(4, 10, 32)
+    a[name] = torch.randn(stored).expand(4, 10, 32)
+    with pytest.raises(ValueError):
+        tr.layer_norm_backward(**a)
+    if name == "x":
+        with pytest.raises(ValueError):
+            tr.layer_norm(a["x"])
+    assert not calls
+
+
+def test_layer_norm_refuses_the_gradient_of_a_sum(calls):
+    y, got = torch.randn(6, 8, requires_grad=True), []
+    z = y * 1.0
+    z.register_hook(got.append)
+    z.sum(0).backward(torch.ones(8))
+    dy = got[0]
+    assert dy.shape == (6, 8) and dy.stride() == (0, 1)
+    with pytest.raises(ValueError):
+        tr.layer_norm_backward(torch.randn(6, 8), dy, None, torch.zeros(6), torch.ones(6))
+    with pytest.raises(ValueError):  # rows that overlap in part
+        tr.layer_norm(torch.randn(20).as_strided((6, 8), (2, 1)))
+    assert not calls
+
+
+@pytest.mark.parametrize("t,ld", [(torch.zeros(1, 8).expand(1, 8), 0), (torch.zeros(6, 12)[:, :8], 12), (torch.zeros(6, 8), 8),
+                                  (torch.zeros(6, 3)[:, 1:2], 3), (torch.zeros(2, 3, 2, 8)[:, :, 0], 16), (torch.zeros(0, 8), 0)],
+                         ids=lambda v: str(tuple(v.shape)) if torch.is_tensor(v) else "")
+def test_layer_norm_takes_the_rows_stride(calls, t, ld):
+    tr.layer_norm(t)
+    (name, d, x, *_), = calls
+    assert name == "cba_layernorm_forward" and (d.rows, d.cols) == (t.numel() // t.shape[-1], t.shape[-1])
+    assert d.ld_x == ld and x.data_ptr() == t.data_ptr()
