@@ -467,6 +467,9 @@ def make_attention_desc(q, k, v, o, dout, dq, dk, dv, causal=False, scale=None, 
             raise ValueError(f"{name}: shape, type or device differs from {'k' if want is k else 'q'}'s")
         if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name}: the innermost axis is not contiguous")
+        # (strides of 0 on every axis would read as the descriptor's "contiguous")
+        if t.numel() and any(n > 1 and s < t.shape[-1] for n, s in zip(t.shape[:-1], t.stride())):
+            raise ValueError(f"{name}: indices of an axis lie on one another (it is expanded): make it contiguous")
     d = cba_attention_desc_t()
     d.heads_q, d.heads_kv, d.dim = q.shape[-2], k.shape[-2], q.shape[-1]
     d.type, d.causal, d.packed = dtype_code(q.dtype), int(causal), int(packed)

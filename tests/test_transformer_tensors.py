@@ -61,3 +61,47 @@ def test_layer_norm_takes_the_rows_stride(calls, t, ld):
     (name, d, x, *_), = calls
     assert name == "cba_layernorm_forward" and (d.rows, d.cols) == (t.numel() // t.shape[-1], t.shape[-1])
     assert d.ld_x == ld and x.data_ptr() == t.data_ptr()
+
+
+# ---- attention's backward pass
+
+def attn_args(shape=(2, 16, 4, 64), dtype=torch.bfloat16):
+    a = {n: torch.randn(shape).to(dtype) for n in ("q", "k", "v", "o", "dout")}
+    a["lse"] = torch.zeros(*shape[:-3], shape[-2], shape[-3])
+    return a
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "o", "dout"])
+@pytest.mark.parametrize("stored", [(1, 1, 1, 64), (2, 1, 1, 64), (1, 16, 1, 64), (1, 1, 4, 64), (1, 16, 4, 64), (2, 1, 4, 64),
+                                    (2, 16, 1, 64)], ids=str)
+def test_attention_refuses_expanded_tensors(calls, name, stored):
+    a = attn_args()
+    a[name] = torch.randn(stored).bfloat16().expand(2, 16, 4, 64)
+    with pytest.raises(ValueError, match=name):
+        tr.attention_backward(**a)
+    assert not calls
+
+
+def test_packed_attention_refuses_expanded_tensors(calls):
+    a = attn_args((16, 4, 64))
+    cu = torch.tensor([0, 9, 16], dtype=torch.int32)
+    tr.attention_backward(**a, cu_q=cu)
+    assert len(calls) == 1
+    for stored in ((1, 1, 64), (16, 1, 64), (1, 4, 64)):
+        a["dout"] = torch.randn(stored).bfloat16().expand(16, 4, 64)
+        with pytest.raises(ValueError, match="dout"):
+            tr.attention_backward(**a, cu_q=cu)
+    assert len(calls) == 1
+
+
+def test_attention_axes_of_one_index_may_have_any_stride(calls):
+    """Of such an axis only index 0 is used: expanding it changes nothing."""
+    a = attn_args((1, 16, 1, 64))
+    a["dout"] = torch.randn(16, 64).bfloat16().as_strided((1, 16, 1, 64), (0, 64, 0, 1))
+    tr.attention_backward(**a)
+    d = calls[0][1]
+    assert (d.dout.batch, d.dout.token, d.dout.head) == (0, 64, 0) and (d.q.batch, d.q.token, d.q.head) == (0, 64, 0)
+    one = attn_args((1, 1, 1, 64))
+    tr.attention_backward(**one)
+    d = calls[1][1]
+    assert (d.q.batch, d.q.token, d.q.head) == (0, 0, 0)
