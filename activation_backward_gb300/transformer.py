@@ -65,6 +65,9 @@ def layer_norm_backward(x, dy, gamma, mean, rstd, residual=None, dgamma=None, db
     if (dgamma is None) != (dbeta is None):
         raise ValueError("dgamma and dbeta come together")
     rows, drows = _rows(x), _rows(dy)
+    for t in (mean, rstd):
+        if t.dtype != torch.float32 or t.numel() != rows.shape[0] or not t.is_contiguous():
+            raise ValueError("mean and rstd are contiguous fp32, one element per row of x")
     rrows = None if residual is None else _rows(residual)
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     add = dgamma is not None

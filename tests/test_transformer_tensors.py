@@ -63,6 +63,27 @@ def test_layer_norm_takes_the_rows_stride(calls, t, ld):
     assert d.ld_x == ld and x.data_ptr() == t.data_ptr()
 
 
+@pytest.mark.parametrize("name", ["mean", "rstd"])
+@pytest.mark.parametrize("bad", [lambda t: t.bfloat16(), lambda t: t.double(), lambda t: t[:3], lambda t: t[:, None].expand(40, 2),
+                                 lambda t: torch.zeros(80)[::2], lambda t: t.new_zeros(1).expand(40)],
+                         ids=["bf16", "fp64", "short", "wide", "every second", "expanded"])
+def test_layer_norm_backward_refuses_other_statistics(calls, name, bad):
+    a = norm_args(4, 10, 32)
+    tr.layer_norm_backward(**a)
+    assert len(calls) == 1
+    a[name] = bad(a[name])
+    with pytest.raises(ValueError, match="mean and rstd"):
+        tr.layer_norm_backward(**a)
+    assert len(calls) == 1
+
+
+def test_layer_norm_backward_takes_statistics_in_the_shape_of_the_rows(calls):
+    a = norm_args(4, 10, 32)
+    a["mean"], a["rstd"] = a["mean"].view(4, 10), a["rstd"].view(4, 10, 1)
+    tr.layer_norm_backward(**a)
+    assert len(calls) == 1
+
+
 # ---- attention's backward pass
 
 def attn_args(shape=(2, 16, 4, 64), dtype=torch.bfloat16):
