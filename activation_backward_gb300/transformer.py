@@ -23,6 +23,12 @@ def _rows(t):
     return r
 
 
+def _on_device_of(x, **others):
+    for name, t in others.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, not on {x.device}")
+
+
 def _workspace(nbytes, what, device):
     if nbytes == 0:
         raise B.CbaError(B.CBA_ERR_ARG, what)
@@ -48,6 +54,7 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-5):
     """(y, mean, rstd) over the last axis of x; mean and rstd (fp32, one per
     row) are what the backward pass takes."""
     rows = _rows(x)
+    _on_device_of(x, gamma=gamma, beta=beta)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     mean, rstd = (torch.empty(rows.shape[0], device=x.device) for _ in range(2))
     d = _norm_desc(rows, gamma, beta, eps, ld_x=_ld(rows))
@@ -64,6 +71,7 @@ def layer_norm_backward(x, dy, gamma, mean, rstd, residual=None, dgamma=None, db
         raise ValueError("residual has another shape or type than x")
     if (dgamma is None) != (dbeta is None):
         raise ValueError("dgamma and dbeta come together")
+    _on_device_of(x, dy=dy, gamma=gamma, mean=mean, rstd=rstd, residual=residual, dgamma=dgamma, dbeta=dbeta)
     rows, drows = _rows(x), _rows(dy)
     for t in (mean, rstd):
         if t.dtype != torch.float32 or t.numel() != rows.shape[0] or not t.is_contiguous():
@@ -92,6 +100,7 @@ def attention_backward(q, k, v, o, lse, dout, causal=False, scale=None, cu_q=Non
     of the sequences, one more than there are; cu_k defaults to cu_q) and lse
     [heads, tokens]."""
     outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+    _on_device_of(q, lse=lse, cu_q=cu_q, cu_k=cu_k)
     sequences = None
     if cu_q is not None:
         cu_k = cu_q if cu_k is None else cu_k

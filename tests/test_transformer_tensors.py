@@ -126,3 +126,37 @@ def test_attention_axes_of_one_index_may_have_any_stride(calls):
     tr.attention_backward(**one)
     d = calls[1][1]
     assert (d.q.batch, d.q.token, d.q.head) == (0, 0, 0)
+
+
+# ---- devices
+
+@pytest.mark.parametrize("name", ["dy", "gamma", "mean", "rstd", "residual", "dgamma", "dbeta"])
+def test_layer_norm_backward_refuses_tensors_of_another_device(calls, name):
+    a = dict(norm_args(6, 32), residual=torch.zeros(6, 32), dgamma=torch.zeros(32), dbeta=torch.zeros(32))
+    tr.layer_norm_backward(**a)
+    assert len(calls) == 1
+    a[name] = a[name].to("meta")
+    with pytest.raises(ValueError, match=f"{name} is on meta"):
+        tr.layer_norm_backward(**a)
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("name", ["gamma", "beta"])
+def test_layer_norm_refuses_tensors_of_another_device(calls, name):
+    with pytest.raises(ValueError, match=f"{name} is on meta"):
+        tr.layer_norm(torch.zeros(6, 32), **{name: torch.zeros(32, device="meta")})
+    assert not calls
+
+
+@pytest.mark.parametrize("name", ["lse", "cu_q", "cu_k", "o"])
+def test_attention_refuses_tensors_of_another_device(calls, name):
+    """Sequence starts often live on the host; the kernels read them on the GPU."""
+    a = attn_args((16, 4, 64))
+    a["cu_q"] = torch.tensor([0, 9, 16], dtype=torch.int32)
+    a["cu_k"] = a["cu_q"].clone()
+    tr.attention_backward(**a)
+    assert len(calls) == 1
+    a[name] = a[name].to("meta")
+    with pytest.raises(ValueError, match=name):
+        tr.attention_backward(**a)
+    assert len(calls) == 1
