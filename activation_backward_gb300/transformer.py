@@ -56,7 +56,7 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-5):
     rows = _rows(x)
     _on_device_of(x, gamma=gamma, beta=beta)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    mean, rstd = (torch.empty(rows.shape[0], device=x.device) for _ in range(2))
+    mean, rstd = (torch.empty(rows.shape[0], dtype=torch.float32, device=x.device) for _ in range(2))
     d = _norm_desc(rows, gamma, beta, eps, ld_x=_ld(rows))
     B.cba_layernorm_forward(d, rows, gamma, beta, y, mean, rstd)
     return y, mean, rstd
@@ -80,7 +80,7 @@ def layer_norm_backward(x, dy, gamma, mean, rstd, residual=None, dgamma=None, db
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     add = dgamma is not None
     if not add:
-        dgamma, dbeta = (torch.empty(x.shape[-1], device=x.device) for _ in range(2))
+        dgamma, dbeta = (torch.empty(x.shape[-1], dtype=torch.float32, device=x.device) for _ in range(2))
     for g in (dgamma, dbeta):
         if g.dtype != torch.float32 or g.shape != x.shape[-1:] or not g.is_contiguous():
             raise ValueError("dgamma and dbeta are contiguous fp32 vectors of x's last axis")

@@ -160,3 +160,23 @@ def test_attention_refuses_tensors_of_another_device(calls, name):
     with pytest.raises(ValueError, match=name):
         tr.attention_backward(**a)
     assert len(calls) == 1
+
+
+# ---- torch's defaults
+
+@pytest.fixture(params=[torch.bfloat16, torch.float64], ids=str)
+def default_type(request):
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(request.param)
+    yield request.param
+    torch.set_default_dtype(before)
+
+
+def test_statistics_and_parameter_gradients_are_fp32_whatever_the_default_type(calls, default_type):
+    """The kernels write 4 bytes an element."""
+    x = torch.zeros(6, 32, dtype=torch.bfloat16)
+    y, mean, rstd = tr.layer_norm(x)
+    assert y.dtype == torch.bfloat16 and mean.dtype == rstd.dtype == torch.float32
+    dx, dgamma, dbeta = tr.layer_norm_backward(x, x, None, mean, rstd)
+    assert dx.dtype == torch.bfloat16 and dgamma.dtype == dbeta.dtype == torch.float32
+    assert [c[0] for c in calls] == ["cba_layernorm_forward", "cba_layernorm_backward"]
