@@ -1366,7 +1366,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                 (w->s.q0 + first) * a.sdq[1] + w->h * a.sdq[2] + c0;
                 constexpr long long ITEM = DP * kT / 4;
                 float4 *at = reinterpret_cast<float4 *>(a.part) + w->tile * a.chunks * ITEM + c0 / 4 * kT + r;
-                if (w->used == 1 && (DP == 64 || n == 0))
+                // The staged store needs the tile of q, which is free once the next item's rows have been
+                // read from it, or where no item follows.  An item without keys in between leaves in it
+                // (now or soon) the rows of the one after.
+                if (w->used == 1 && (DP == 64 || n == 0 || (next && !more)))
                     store_row<DP / 4, BF16>(tDq + lanes + c0, a.scale / sds, n == 0, lane < live, out + lane * a.sdq[1],
                                             a.dim - c0);
                 else if (w->used == 1)
