@@ -160,14 +160,16 @@ int fail_cuda(cudaError_t e) {
 // to the same device) current for this library's runtime, which keeps its own
 // per-thread current device.  Without a pointer, the stream's device.  The
 // pointer query is also legal while the stream is being captured into a CUDA
-// graph, where asking the stream for its device is not.
-cudaError_t select_device(cudaStream_t stream, const void *ptr) {
+// graph, where asking the stream for its device is not.  `known`: memory that CUDA
+// has not allocated or registered is refused.
+cudaError_t select_device(cudaStream_t stream, const void *ptr, bool known = false) {
     int dev = -1;
     cudaError_t e = cudaSuccess;
     if (ptr) {
         cudaPointerAttributes a;
         e = cudaPointerGetAttributes(&a, ptr);
         if (e == cudaSuccess) dev = a.device;
+        if (e == cudaSuccess && known && a.type == cudaMemoryTypeUnregistered) e = cudaErrorInvalidValue;
     } else if (stream) {
         e = cudaStreamGetDevice(stream, &dev);
     }
@@ -183,7 +185,7 @@ cudaError_t select_device(cudaStream_t stream, const void *ptr) {
 
 namespace cba {
 int report_cuda_error(cudaError_t e) { return fail_cuda(e); }
-cudaError_t select_device_of(const void *ptr) { return select_device(nullptr, ptr); }
+cudaError_t select_device_of(const void *ptr) { return select_device(nullptr, ptr, true); }
 }  // namespace cba
 
 extern "C" {

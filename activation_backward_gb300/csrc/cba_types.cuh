@@ -86,7 +86,7 @@ cudaError_t allow_smem(int bytes) {
 }
 
 // The device that holds `ptr` becomes current for this library's runtime
-// (cba_api.cu).
+// (cba_api.cu); ordinary host memory is an error.
 cudaError_t select_device_of(const void *ptr);
 
 }  // namespace cba
