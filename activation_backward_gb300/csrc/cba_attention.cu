@@ -23,7 +23,10 @@
 // TMEM, which the MMAs read as their A operand, and never to shared memory.
 // In f16 both are scaled by powers of two first (P by 2^12, dS by a power that
 // puts the bound 2 max|do| max|v| of |dP - D| at 2^15), so that their small
-// values stay clear of f16's subnormals and none can overflow.
+// values stay clear of f16's subnormals and none can overflow.  The maxima are
+// those of a sequence's rows under one key/value head, rows with infinities or
+// NaN left out: neither another sequence's values nor an infinity among one's own
+// costs the others bits.
 //
 // Measured (us; launches overlap, so a call takes less than their sum; rates count
 // the formulas' 5 products):
@@ -78,7 +81,9 @@ struct AtArgs {
     const float *lse;
     float *nlse, *ndsum;         // -lse / ln 2 and -D, [head][padded rows] (dense: [batch][head][padded rows])
     long long head_rows;         // padded rows of a head (dense: of a batch's head)
-    unsigned *status, *maxima;   // maxima: bits of max |do|^2, max |v|^2 over rows (f16)
+    unsigned *status;
+    unsigned *maxima;            // f16: bits of max |do|^2, then of max |v|^2, over the finite rows
+                                 // of each sequence and key/value head ([2][batch][hkv])
     unsigned *next;              // work items handed out, of the two main kernels
     int items;                   // this launch's
     int chunk, chunks;           // steps of an item at most; items per tile at most
@@ -136,13 +141,17 @@ __device__ __forceinline__ float2 unpack2(uint32_t u) {
     else return __half22float2(*reinterpret_cast<__half2 *>(&u));
 }
 
-// f16: the power of two by which dS is held, from the rows' largest norms.
-__device__ __forceinline__ float ds_scale(const unsigned *maxima) {
-    const float b = 2.f * sqrtf(__uint_as_float(__ldcg(maxima))) * sqrtf(__uint_as_float(__ldcg(maxima + 1)));
-    if (!(b > 0.f) || !isfinite(b)) return 1.f;
-    int e;
-    frexpf(b, &e);  // b <= 2^e
-    return exp2f((float)min(max(15 - e, -60), 60));
+// f16: the power of two by which dS of sequence b under key/value head h is held:
+// with its largest |do|^2 = x and |v|^2 = y (of finite rows: below 2^40, and above
+// 2^-48 where they are not 0), the one that brings 2 sqrt(x y) to 2^14 .. 2^15.
+__device__ __forceinline__ float ds_scale(const AtArgs &a, int b, int h) {
+    const long long at = (long long)b * a.hkv + h;
+    const float x = __uint_as_float(__ldcg(a.maxima + at)),
+                y = __uint_as_float(__ldcg(a.maxima + (long long)a.batch * a.hkv + at));
+    const float m = 4.f * x * y;
+    if (!(m > 0.f)) return 1.f;
+    const int e = (__float_as_int(m) >> 23) - 126;  // m < 2^e
+    return __int_as_float((127 + min(max(15 - ((e + 1) >> 1), -60), 60)) << 23);
 }
 
 // ---- D, lse in base 2, and (f16) the largest row norms of do and v.  One block
@@ -150,16 +159,17 @@ __device__ __forceinline__ float ds_scale(const unsigned *maxima) {
 // thread in flight.  Bound by memory: 134 MB of o and do in 26 us, 5.1 TB/s; with
 // v for f16 66 MB in 16 us.
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_tiles, int v_blocks) {
+__global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_tiles, int k_tiles, int v_blocks) {
     constexpr int LPR = DP / 8;
     const int t = threadIdx.x, lane = t % LPR;
     ptx::griddep_launch_dependents();
-    float most = 0.f;
-    int which = 0;
+    float most = 0.f;    // |row|^2 of the block's finite rows
+    long long slot = 0;  // of its maximum
     if ((int)blockIdx.x >= v_blocks) {
         const int u = (int)blockIdx.x - v_blocks;
         const int tile = u % q_tiles, h = u / q_tiles % a.hq, b = u / q_tiles / a.hq;
         const AtSeq s = at_seq(a, b);
+        slot = (long long)b * a.hkv + h / a.group;
         if (u == 0 && t == 0) {
             if (BF16) *a.status = 0;  // f16: cleared with the maxima before
             a.next[0] = a.next[1] = 0;
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
                         d += __shfl_xor_sync(0xffffffffu, d, o);
                         if (!BF16) n += __shfl_xor_sync(0xffffffffu, n, o);
                     }
-                    most = fmaxf(most, n);
+                    if (n < INFINITY) most = fmaxf(most, n);
                     if (lane == 0) {
                         // a row whose keys are all masked has lse = -inf: P = 0 too
                         const long long at = row0 + r0 + j * RPP;
@@ -214,44 +224,35 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
             }
         }
     } else if constexpr (!BF16) {
-        // v's rows: [batch][token][head] flattened, strided over the blocks
-        which = 1;
-        const long long tokens = a.cu_k ? a.total_k : a.len_k;
-        const long long rows = (a.cu_k ? 1 : (long long)a.batch) * tokens * a.hkv;
-        const long long per = (rows + v_blocks - 1) / v_blocks;
-        const long long r1 = min(rows, (blockIdx.x + 1LL) * per);
-        long long r = blockIdx.x * per + t / LPR;
-        int h = (int)(r % a.hkv);
-        long long tok = rows ? r / a.hkv % tokens : 0, b = rows ? r / a.hkv / tokens : 0;
-        constexpr int NR = 4;  // rows of a thread in flight
-        while (r - t / LPR < r1) {  // the same for all of the block
-            uint4 x[NR];
+        // v, a block per 128 keys of one head
+        const int u = (int)blockIdx.x, tile = u % k_tiles, h = u / k_tiles % a.hkv, b = u / k_tiles / a.hkv;
+        const AtSeq s = at_seq(a, b);
+        slot = (long long)(a.batch + b) * a.hkv + h;
+        const uint16_t *v = static_cast<const uint16_t *>(a.v) + b * a.sv[0] + h * a.sv[2] + lane * 8;
+        constexpr int RPP = 256 / LPR, NR = 4;
+        if (tile * kT < s.lk)
+            for (int r0 = t / LPR; r0 < kT; r0 += NR * RPP) {
+                uint4 x[NR];
 #pragma unroll
-            for (int j = 0; j < NR; ++j) {
-                x[j] = make_uint4(0, 0, 0, 0);
-                if (r < r1 && lane * 8 < a.dim)
-                    x[j] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.v) + b * a.sv[0] +
-                                                            tok * a.sv[1] + h * a.sv[2] + lane * 8);
-                r += 256 / LPR;
-                h += 256 / LPR;
-                tok += h / a.hkv;
-                h %= a.hkv;
-                while (tok >= tokens) tok -= tokens, ++b;
-            }
-#pragma unroll
-            for (int j = 0; j < NR; ++j) {
-                float n = 0.f;
-                const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 p = unpack2<false>(xs[e]);
-                    n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
+                for (int j = 0; j < NR; ++j) {
+                    const int i = tile * kT + r0 + j * RPP;
+                    x[j] = make_uint4(0, 0, 0, 0);
+                    if (i < s.lk && lane * 8 < a.dim) x[j] = *reinterpret_cast<const uint4 *>(v + (s.k0 + i) * a.sv[1]);
                 }
 #pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-                most = fmaxf(most, n);
+                for (int j = 0; j < NR; ++j) {
+                    float n = 0.f;
+                    const uint32_t xs[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 p = unpack2<false>(xs[e]);
+                        n = fmaf(p.x, p.x, fmaf(p.y, p.y, n));
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+                    if (n < INFINITY) most = fmaxf(most, n);
+                }
             }
-        }
     }
     if constexpr (!BF16) {  // a maximum does not depend on the order
 #pragma unroll
@@ -262,8 +263,8 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         if (t == 0) {
 #pragma unroll
             for (int i = 1; i < 8; ++i) most = fmaxf(most, warps[i]);
-            // thousands of blocks on one word: most of them see that it is no less already
-            if (__float_as_uint(most) > __ldcg(a.maxima + which)) atomicMax(a.maxima + which, __float_as_uint(most));
+            // many blocks on one word: most of them see that it is no less already
+            if (__float_as_uint(most) > __ldcg(a.maxima + slot)) atomicMax(a.maxima + slot, __float_as_uint(most));
         }
     }
 }
@@ -686,6 +687,7 @@ struct KvItem {
     int b, h, k0, off, qt_begin, nq;
     int it0, n;      // steps: query tiles, over the group's heads in turn
     int tile, c, used;
+    float sds;       // dS is held times this
     bool live;       // there are keys, and steps or zeros to be stored
 };
 static_assert(sizeof(KvItem) <= 128);
@@ -782,6 +784,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (w.live) break;
                 w.tile = -1;
             }
+            w.sds = BF16 || w.tile < 0 ? 1.f : ds_scale(a, w.b, w.h);
             return w;
         };
         KvItem w = live((int)blockIdx.x);
@@ -905,8 +908,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int wg = (warp - 4) >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const float cs = a.scale * kLog2e;
-        const float sds = BF16 ? 1.f : ds_scale(a.maxima);       // dS is held times sds
-        const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);    // from the held P
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             const bool r = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
             return ok = __all_sync(0xffffffffu, r) != 0;
@@ -916,6 +917,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const KvItem *w;
         for (int k = 0; (w = take_item(a, k, slots, sb, ok)) != nullptr; ++k) {
             const int n = w->n;
+            const float sds = BF16 ? 1.f : w->sds, pds = BF16 ? 1.f : sds * exp2f(-kPShift);  // pds: from the held P
             {
                 const int begin = w->qt_begin * kT, end = begin + w->nq * kT;
                 // this thread's key is seen by the queries from here on, the tile's last one by those from `all` on
@@ -1064,6 +1066,7 @@ struct QItem {
     int b, h, q0, off;
     int it0, n;      // steps: key tiles that any of the tile's queries sees
     int tile, c, used;
+    float sds;       // dS is held times this
     bool live;       // there are queries, and steps or zeros to be stored
 };
 static_assert(sizeof(QItem) <= 128);
@@ -1156,6 +1159,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (w.live) break;
                 w.tile = -1;
             }
+            w.sds = BF16 || w.tile < 0 ? 1.f : ds_scale(a, w.b, w.h / a.group);
             return w;
         };
         QItem w = live((int)blockIdx.x);
@@ -1254,8 +1258,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const int r = quarter * 32 + lane;
         const float cs = a.scale * kLog2e;
-        const float sds = BF16 ? 1.f : ds_scale(a.maxima);
-        const float pds = BF16 ? 1.f : sds * exp2f(-kPShift);
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             const bool x = ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
             return ok = __all_sync(0xffffffffu, x) != 0;
@@ -1300,6 +1302,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
         while (ok && w) {
             const int n = w->n;
+            const float sds = BF16 ? 1.f : w->sds, pds = BF16 ? 1.f : sds * exp2f(-kPShift);
             if (n > 0) {
                 const long long row = w->s.row0 + (long long)w->h * a.head_rows + w->q0 + r;
                 const float nl = __ldcg(a.nlse + row), nd = __ldcg(a.ndsum + row) * pds;
@@ -1414,7 +1417,7 @@ struct AtPlan {
     int dp, q_tiles, k_tiles;
     long long head_rows;   // padded rows of one head
     AtCut kv, q;
-    size_t off_nlse, off_ndsum, off_arrived, off_part, total;
+    size_t off_max, max_bytes, off_nlse, off_ndsum, off_arrived, off_part, total;
 };
 
 // Whether tiles of `steps` steps at most, `tiles` of them with `all` steps
@@ -1503,7 +1506,9 @@ int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
                          (long long)p->q_tiles * (d->heads_q / d->heads_kv), all, 1.75);
         p->q = plan_cut((long long)p->q_tiles * d->heads_q * d->batch, p->k_tiles, all, p->kv.tiles ? 1.25 : 2.3);
     }
-    p->off_nlse = 256;
+    p->off_max = 256;  // behind the status word's 256 bytes, with which they are cleared
+    p->max_bytes = d->type == CBA_F16 ? (size_t)2 * d->batch * d->heads_kv * sizeof(unsigned) : 0;
+    p->off_nlse = p->off_max + (p->max_bytes + 255) / 256 * 256;
     p->off_ndsum = p->off_nlse + ((size_t)rows * 4 + 255) / 256 * 256;
     p->off_arrived = p->off_ndsum + ((size_t)rows * 4 + 255) / 256 * 256;
     p->off_part = p->off_arrived + ((size_t)(p->kv.tiles + p->q.tiles) * 4 + 255) / 256 * 256;
@@ -1528,13 +1533,12 @@ template <int DP, bool BF16>
 cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a, const CUtensorMap *tm,
                         cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (!BF16) e = cudaMemsetAsync(a.status, 0, 256, st);  // the status word and the maxima
+    if (!BF16) e = cudaMemsetAsync(a.status, 0, p.off_max + p.max_bytes, st);  // the status word and the maxima
     if (e != cudaSuccess) return e;
-    // f16: the blocks that look for v's largest row, 256 rows or more each
-    const long long vrows = (d.packed ? d.total_k : (long long)d.batch * d.len_k) * d.heads_kv;
-    const int vb = BF16 ? 0 : (int)std::max(1LL, std::min<long long>(vrows / 256, 16 * kNumSMs));
+    // f16: the blocks that look for v's largest rows
+    const int vb = BF16 ? 0 : (int)((long long)p.k_tiles * d.heads_kv * d.batch);
     const unsigned qgrid = (unsigned)((long long)p.q_tiles * d.heads_q * d.batch);
-    attn_prep_kernel<DP, BF16><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), vb);
+    attn_prep_kernel<DP, BF16><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), p.k_tiles, vb);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     e = allow_smem<attn_kv_kernel<DP, BF16>>((int)Kv<DP>::SMEM);
@@ -1612,7 +1616,7 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.cnt_q = p.q.tiles;
     a.arrived = ws_at<unsigned>(workspace, p.off_arrived);
     a.part = ws_at<float>(workspace, p.off_part);
-    a.maxima = a.status + 4;
+    a.maxima = ws_at<unsigned>(workspace, p.off_max);
     a.nlse = ws_at<float>(workspace, p.off_nlse);
     a.ndsum = ws_at<float>(workspace, p.off_ndsum);
     a.head_rows = p.head_rows;
