@@ -213,12 +213,15 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
                         d += __shfl_xor_sync(0xffffffffu, d, o);
                         if (!BF16) n += __shfl_xor_sync(0xffffffffu, n, o);
                     }
-                    if (n < INFINITY) most = fmaxf(most, n);
                     if (lane == 0) {
-                        // a row whose keys are all masked has lse = -inf: P = 0 too
+                        // a row that sees no key, by the mask or (lse = -inf) the caller's own: P = 0 and D = 0
+                        // whatever the forward left in its o and lse (a softmax over nothing is NaN)
+                        const int i = tile * kT + r0 + j * RPP;
+                        const bool none = l[j] == -INFINITY || (a.causal ? i + s.lk < s.lq : s.lk == 0);
                         const long long at = row0 + r0 + j * RPP;
-                        a.nlse[at] = l[j] == -INFINITY ? -INFINITY : (BF16 ? 0.f : kPShift) - l[j] * kLog2e;
-                        a.ndsum[at] = -d;
+                        a.nlse[at] = none ? -INFINITY : (BF16 ? 0.f : kPShift) - l[j] * kLog2e;
+                        a.ndsum[at] = none ? 0.f : -d;
+                        if (!BF16 && !none && n < INFINITY) most = fmaxf(most, n);
                     }
                 }
             }

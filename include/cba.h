@@ -393,7 +393,8 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
  * are the forward's: lse fp32 = log sum_j exp S_ij, contiguous [batch][heads_q]
  * [len_q] (packed: [heads_q][total_q]).  Row i of a sequence sees the keys
  * j <= i + len_k - len_q when causal, all of them otherwise.  A row that sees
- * none (or whose lse is -infinity) has P = 0: it gets dq = 0 and adds nothing.
+ * none (or whose lse is -infinity) has P = 0 and D = 0, whatever its o holds (a
+ * softmax over nothing is NaN): it gets dq = 0 and adds nothing.
  *
  * Dense: `batch` sequences of len_q queries and len_k keys, element (b, t, h, c)
  * of a tensor at b * batch + t * token + h * head + c.  Packed: `batch`
