@@ -17,8 +17,9 @@
 // Operands are f16, products accumulate in fp32: 11 significant bits where
 // bf16, the usual choice for this iteration, has 8.  f16's short range is met
 // with powers of two: X is held times 2^round(log2(n)/2) (its elements are of
-// order 1/sqrt(n) or 1/sqrt(m n)), S and B times 2^12 (their largest elements
-// are below 3 for singular values up to 1.2, which the iteration keeps).
+// order 1/sqrt(n) or 1/sqrt(m n)), S times 2^12 and C times a power chosen from the
+// coefficients, both with room for singular values of X up to 2 (1.2 is what
+// coefficients that converge keep).
 //
 // The product kernel: TMA-fed tcgen05 tiles of 128 rows per block; with CG = 2
 // a pair of blocks computes 256 x 256 tiles (each holds half of A's and of B's
@@ -54,7 +55,7 @@ constexpr int kNsEpiWarps = 8;                 // two per quarter of a tile's ro
 constexpr int kNsThreads = 64 + 32 * kNsEpiWarps;
 constexpr int kNsStages = 6;
 constexpr int kNsBK = 64;                      // contraction elements per stage (128 bytes)
-constexpr float kNsSym = 4096.f;               // S and C are held times 2^12
+constexpr float kNsSym = 4096.f;               // S is held times 2^12: room for singular values up to 2 (and 3.9)
 constexpr int kNormBlocks = 512;               // partial sums of |G|^2 per matrix (at most)
 
 struct NsArgs {
@@ -696,7 +697,8 @@ struct SmArgs {
     int wide, R, nb;              // nb: 64-column boxes of X
     int in_type, out_type;
     long long ld_in, batch_in, ld_out, batch_out;
-    float a, b, c, eps, scale, held;
+    float a, b, c;                // of C as held, from I, from S and S S as held
+    float eps, scale, held, c_held;
     unsigned *status;
 };
 
@@ -946,14 +948,14 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < CS; ++j) {
-                q[j] = fmaf(a.c / kNsSym, q[j], a.b * s[j]);
-                if (c_s + j == r) q[j] += a.a * kNsSym;
+                q[j] = fmaf(a.c, q[j], a.b * s[j]);
+                if (c_s + j == r) q[j] += a.a;
             }
             box_put<__half>(sc, R, r, c_s, q);
         }
         if (!publish()) break;
         const bool last = step + 1 == a.steps;
-        const float alpha = (last ? a.scale / a.held : 1.f) / kNsSym;
+        const float alpha = (last ? a.scale / a.held : 1.f) / a.c_held;
         if (warp == issuer)
             for (int ch = 0; ch < min(2, nchunks); ++ch) apply(ch);
         for (int ch = 0; ch < nchunks; ++ch) {
@@ -1010,6 +1012,18 @@ __global__ void __launch_bounds__(kSmThreads, 1) ns_small_kernel(const SmArgs a)
 }
 
 // ---- host side
+
+// The power of two by which C = a I + b S + c S^2 is held in f16: its eigenvalues
+// for singular values up to 2 stay below half of the largest f16.
+float c_power(const cba_orthogonalize_desc_t &d) {
+    auto p = [&](double t) { return std::fabs(d.a + t * ((double)d.b + t * d.c)); };
+    double most = std::max(p(0.0), p(4.0));
+    const double turn = d.c != 0.f ? -0.5 * d.b / d.c : 0.0;
+    if (turn > 0.0 && turn < 4.0) most = std::max(most, p(turn));
+    int e = 0;
+    std::frexp(most, &e);  // most < 2^e
+    return std::ldexp(1.f, std::min(12, std::max(15 - e, -64)));
+}
 
 struct NsPlan {
     int m, n;
@@ -1195,7 +1209,9 @@ cudaError_t ns_small(const cba_orthogonalize_desc_t &d, const NsPlan &p, const v
     a.batch_in = d.batch_in ? d.batch_in : a.ld_in * d.rows;
     a.ld_out = d.ld_out ? d.ld_out : d.cols;
     a.batch_out = d.batch_out ? d.batch_out : a.ld_out * d.rows;
-    a.a = d.a; a.b = d.b; a.c = d.c; a.eps = d.eps; a.scale = d.scale; a.held = held;
+    a.c_held = c_power(d);
+    a.a = d.a * a.c_held; a.b = d.b * (a.c_held / kNsSym); a.c = d.c * (a.c_held / (kNsSym * kNsSym));
+    a.eps = d.eps; a.scale = d.scale; a.held = held;
     a.status = static_cast<unsigned *>(ws);
     const size_t smem = small_smem(a.R, a.nb);
     auto kern = a.R == 64 ? ns_small_kernel<64> : ns_small_kernel<128>;
@@ -1246,14 +1262,15 @@ cudaError_t ns_run(const cba_orthogonalize_desc_t &d, const NsPlan &p, const voi
     as.status = ac.status = ax.status = status;
     as.alpha = kNsSym / (held * held);
     as.out = S;
-    ac.alpha = d.c / kNsSym;
-    ac.beta = d.b;
-    ac.diag = d.a * kNsSym;
+    const float c_held = c_power(d);
+    ac.alpha = d.c * (c_held / (kNsSym * kNsSym));
+    ac.beta = d.b * (c_held / kNsSym);
+    ac.diag = d.a * c_held;
     ac.aux = S;
     ac.out = C;
     ax.M = d.rows;
     ax.N = d.cols;
-    ax.alpha = 1.f / kNsSym;
+    ax.alpha = 1.f / c_held;
     ax.out_ld = p.x_pitch;
     ax.out_batch = p.x_batch;
     for (int i = 0; i < d.steps; ++i) {

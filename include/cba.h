@@ -439,9 +439,9 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
  *
  * The products' operands are f16 scaled by powers of two, their sums fp32: O is
  * good to about 1e-3 of its size whatever out_type is, so that type is usually
- * bf16.  The range of the scaling is that of singular values up to 2, which
- * coefficients that converge keep.  Squares of G's elements are taken in fp32:
- * elements below 1e-19 count as 0.
+ * bf16.  The range of the scaling is that of singular values up to 2 before every
+ * step, whatever the coefficients (those that converge keep them below 1.3).
+ * Squares of G's elements are taken in fp32: elements below 1e-19 count as 0.
  *
  * Element types f32, f16 or bf16.  ld_*: elements from one row to the next (0:
  * cols); batch_*: from one matrix to the next (0: rows * ld).  O may be G when
