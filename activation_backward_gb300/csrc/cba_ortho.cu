@@ -585,7 +585,7 @@ __device__ __forceinline__ double block_sum(double v, double *sm) {
 
 // Partial sums of squares: block (p, b) takes the p-th part of matrix b's 16-byte
 // vectors (VEC elements; 1 where rows are not whole vectors), summed in a fixed
-// order: 4 vectors in fp32, their sums in fp64.
+// order: 4 vectors in fp32 (in fp64 where that overflows), their sums in fp64.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
     ns_norm_kernel(const T *g, int rows, int cols, long long ld, long long batch_stride, double *part) {
@@ -613,7 +613,15 @@ __global__ void __launch_bounds__(256)
             if (e + j * 256 < e1)
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) s = fmaf(to_f32(p[j].v[k]), to_f32(p[j].v[k]), s);
-        total += s;
+        if (s < INFINITY) {
+            total += s;
+        } else {  // elements past 1e19, or an infinity or NaN
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (e + j * 256 < e1)
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) total += (double)to_f32(p[j].v[k]) * to_f32(p[j].v[k]);
+        }
     }
     total = block_sum(total, sm);
     if (threadIdx.x == 0) part[(long long)blockIdx.y * kNormBlocks + blockIdx.x] = total;
@@ -712,9 +720,9 @@ __device__ __forceinline__ uint32_t box_at(int R, int r, int c8) {
 }
 
 // The sum of squares of a thread's share of `n` packs of VEC elements, `per_row`
-// packs to a row (flat: one row), 8 loads in flight.
+// packs to a row (flat: one row), 8 loads in flight; in fp64 where fp32 overflows.
 template <typename T, int VEC>
-__device__ __forceinline__ float small_squares(const T *g, int n, int per_row, long long ld, bool flat) {
+__device__ __forceinline__ double small_squares(const T *g, int n, int per_row, long long ld, bool flat) {
     float s = 0.f;
     for (int e = threadIdx.x; e < n; e += 8 * kSmThreads) {
         Pack<T, VEC> p[8];
@@ -733,7 +741,14 @@ __device__ __forceinline__ float small_squares(const T *g, int n, int per_row, l
 #pragma unroll
             for (int k = 0; k < VEC; ++k) s = fmaf(to_f32(p[j].v[k]), to_f32(p[j].v[k]), s);
     }
-    return s;
+    if (s < INFINITY) return s;
+    double big = 0.0;  // elements past 1e19, or an infinity or NaN
+    for (int e = threadIdx.x; e < n; e += kSmThreads) {
+        const int r = flat ? 0 : e / per_row;
+        const T *x = g + r * ld + (long long)(e - r * per_row) * VEC;
+        for (int k = 0; k < VEC; ++k) big += (double)to_f32(x[k]) * to_f32(x[k]);
+    }
+    return big;
 }
 
 // Rows of a wide G, scaled, as the boxes' rows: a warp per row, W elements a time,
@@ -771,7 +786,7 @@ __device__ __forceinline__ void small_load(const SmArgs &a, const T *g, uint8_t 
     const int n = a.rows * a.cols;
     const bool flat = a.ld_in == a.cols;
     constexpr int V = 16 / sizeof(T);
-    float total = flat && n % V == 0 && aligned_to(g, 16) ? small_squares<T, V>(g, n / V, n / V, 0, true)
+    double total = flat && n % V == 0 && aligned_to(g, 16) ? small_squares<T, V>(g, n / V, n / V, 0, true)
                                                            : small_squares<T, 1>(g, n, a.cols, a.ld_in, flat);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);

@@ -442,9 +442,9 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
  * 4e-3 of its norm (so its type is usually bf16).  Singular values far below the
  * leading ones grow by a factor of `a` a step, and with them the rounding errors in
  * their directions: 2e-2 of the norm of a matrix of 24 rows whose singular values
- * span four decades, 5e-3 of one of 1000.  The range of the scaling is that of singular values up to 2 before every
- * step, whatever the coefficients (those that converge keep them below 1.3).
- * Squares of G's elements are taken in fp32: elements below 1e-19 count as 0.
+ * span four decades, 5e-3 of one of 1000.  The scaling has room for singular values
+ * up to 2 before every step, whatever the coefficients (those that converge keep
+ * them below 1.3).  Elements of G below 1e-19 count as 0 in its norm.
  *
  * Element types f32, f16 or bf16.  ld_*: elements from one row to the next (0:
  * cols); batch_*: from one matrix to the next (0: rows * ld).  O may be G when
