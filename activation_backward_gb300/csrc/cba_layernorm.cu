@@ -28,6 +28,7 @@
 #include <initializer_list>
 
 #include "cba_internal.cuh"
+#include "cba_kept.cuh"
 #include "cba_ptx.cuh"
 #include "cba_types.cuh"
 
@@ -727,13 +728,12 @@ cudaError_t fwd_ring(const LnArgs &a, cudaStream_t st) {
     constexpr int ring = EPT * (int)sizeof(T) >= 128 ? 3 : 4;
     constexpr int block = ring_block(TPR), rpb = block / TPR, smem = ring * block * EPT * (int)sizeof(T);
     auto kern = ln_fwd_ring_kernel<T, P, TPR, EPT, ring>;
-    static const int per_sm = [&] {
-        int n = 0;
-        if (allow_smem<ln_fwd_ring_kernel<T, P, TPR, EPT, ring>>(smem) != cudaSuccess) return 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, block, smem) == cudaSuccess ? n : 0;
-    }();
-    if (per_sm == 0) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = allow_smem<ln_fwd_ring_kernel<T, P, TPR, EPT, ring>>(smem);
+    static std::atomic<int> kept{0};
+    int per_sm = 0;
+    cudaError_t e = allow_smem<ln_fwd_ring_kernel<T, P, TPR, EPT, ring>>(smem);
+    if (e == cudaSuccess)
+        e = kept_value(kept, &per_sm,
+                       [&](int *n) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, block, smem); });
     if (e != cudaSuccess) return e;
     const long long blocks = std::min<long long>((a.rows + rpb - 1) / rpb, (long long)kNumSMs * per_sm);
     kern<<<(unsigned)blocks, block, smem, st>>>(a);
