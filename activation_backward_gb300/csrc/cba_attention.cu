@@ -288,7 +288,9 @@ struct AtBars {
     uint64_t fix, drain, acc, stat_empty[2];
     uint64_t i_full[2], i_empty[2];    // work items handed out
     uint64_t join;                     // the compute warps, around an arrival
-    uint64_t staged;                   // the results have passed through q's ring (kv kernel, dim 128)
+    // The results of the items in turn have passed through q's ring (kv kernel, dim 128).  Two, as
+    // the load warp may wait for an item's when the next item's are through as well.
+    uint64_t staged[2];
     int last;
     uint32_t tmem_base;
     int abort_flag;
@@ -648,7 +650,7 @@ __device__ __forceinline__ void init_common(Bars &sb) {
     at_init_bars(sb.dp_full, 2, 1);
     at_init_bars(sb.ds_ready, 2, kAtWarps);
     at_init_bars(&sb.fix, 3, 1);  // fix, drain, acc
-    at_init_bars(&sb.join, 2, kAtWarps);  // join, staged
+    at_init_bars(&sb.join, 3, kAtWarps);  // join, staged
     at_init_bars(sb.i_full, 2, 1);
     at_init_bars(sb.i_empty, 2, kItemReaders);
     sb.abort_flag = 0;
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 // dim 128: the stage after an item's first q holds the results of the item before
                 // until they are stored (gt: items whose K and V have been asked for)
                 if (Kv<DP>::STAGE == 0 && it < 2 && staged < gt - 1) {
-                    if (!wait(&sb.staged, (uint32_t)staged)) break;
+                    if (!wait(&sb.staged[staged & 1], (uint32_t)(staged >> 1))) break;
                     ++staged;
                 }
                 if (nq_begun >= kQStages && !wait(&sb.a_empty[st], (uint32_t)(nq_begun / kQStages - 1))) break;
@@ -1004,7 +1006,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 if (Kv<DP>::STAGE == 0 && n > 0) {
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.staged));
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.staged[(gt - 1) & 1]));  // of item gt - 1
                 }
                 if (w->used > 1) {
                     const bool last = arrive_last(a, w->tile, w->used, sb, joined, ok);

@@ -33,3 +33,14 @@ def test_query_tiles_without_keys_between_others(cuda_lib, dim, dtype, causal):
     lens_q = [int(x) for x in rng.integers(1, 300, size=90)]
     lens_k = [0 if rng.random() < 0.4 else int(rng.integers(1, 260)) for _ in lens_q]
     check_packed(rng, lens_q, lens_k, 6, 2, dim, dtype, 0.1, causal, repeat=4)
+
+
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, BF), (128, F16)], ids=str)
+def test_items_of_one_step_far_apart(cuda_lib, dim, dtype, causal):
+    """Sequences of a tile each beside a long one: an item of one step is over long before its block has walked past the
+    tiles that do not exist to the next."""
+    rng = np.random.default_rng(dim)
+    lens = [int(x) for x in rng.integers(1, 129, size=260)]
+    lens[100] = 1500
+    check_packed(rng, lens, lens, 4, 4, dim, dtype, 0.1, causal, repeat=3)
