@@ -86,6 +86,7 @@ struct AtArgs {
                                  // of each sequence and key/value head ([2][batch][hkv])
     unsigned *next;              // work items handed out, of the two main kernels
     int items;                   // this launch's
+    int q_slots, k_slots;        // packed with loose bounds: see find_tile; 0: tiles are counted up to the bounds
     int chunk, chunks;           // steps of an item at most; items per tile at most
     int cnt_kv, cnt_q;           // tiles that have an arrival counter
     unsigned *arrived;           // this launch's counters (kv's lie before q's)
@@ -122,6 +123,33 @@ __device__ __forceinline__ AtSeq at_seq(const AtArgs &a, int b) {
     s.lk = (int)min(kb - ka, (long long)a.len_k);
     s.row0 = (qa + kT - 1) / kT * kT + (long long)b * kT;
     return s;
+}
+
+// Tiles of packed sequences whose lengths are much below their bounds are numbered
+// by the tokens instead: tile t of sequence b has the slot cu[b] / 128 + b + t.  The
+// next sequence's first slot lies past its last, so there are total / 128 + batch of
+// them at most, of which one per sequence may stand for no tile.
+__device__ __forceinline__ long long slot_of(const int *cu, long long total, int b) {
+    return min(max((long long)cu[b], 0LL), total) / kT + b;
+}
+// The sequence and tile of a slot, searched by a converged warp, 32 sequences at a
+// time.  (A slot without a tile, or before the first sequence, gives one out of
+// range; values of cu that fall give some in-range sequence.)
+__device__ __forceinline__ void find_tile(const int *cu, long long total, int batch, int slot, int &b, int &tile) {
+    int lo = 0, n = batch;  // the sequence is one of lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 31) / 32, m = lo + ((int)(threadIdx.x & 31) + 1) * step;
+        const bool past = m < lo + n && slot_of(cu, total, m) <= slot;
+        const int k = __popc(__ballot_sync(0xffffffffu, past)) * step;
+        n = min(step, n - k);
+        lo += k;
+    }
+    b = lo;
+    tile = slot - (int)slot_of(cu, total, lo);
+}
+// Slots up to the last sequence's end.
+__device__ __forceinline__ int used_slots(const int *cu, long long total, int batch) {
+    return (int)slot_of(cu, total, batch);
 }
 
 template <bool BF16>
@@ -167,7 +195,13 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
     long long slot = 0;  // of its maximum
     if ((int)blockIdx.x >= v_blocks) {
         const int u = (int)blockIdx.x - v_blocks;
-        const int tile = u % q_tiles, h = u / q_tiles % a.hq, b = u / q_tiles / a.hq;
+        int tile, h, b;
+        if (a.q_slots) {
+            h = u % a.hq;
+            find_tile(a.cu_q, a.total_q, a.batch, u / a.hq, b, tile);
+        } else {
+            tile = u % q_tiles, h = u / q_tiles % a.hq, b = u / q_tiles / a.hq;
+        }
         const AtSeq s = at_seq(a, b);
         slot = (long long)b * a.hkv + h / a.group;
         if (u == 0 && t == 0) {
@@ -176,7 +210,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         }
         if (u == 0)
             for (int i = t; i < a.cnt_kv + a.cnt_q; i += 256) a.arrived[i] = 0;
-        if (tile * kT < s.lq) {
+        if (tile >= 0 && (long long)tile * kT < s.lq) {
             const long long row0 = s.row0 + (long long)h * a.head_rows + tile * kT;
             constexpr int RPP = 256 / LPR, NR = 4;  // rows per pass; rows of a thread in flight
             for (int r0 = t / LPR; r0 < kT; r0 += NR * RPP) {
@@ -228,12 +262,19 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         }
     } else if constexpr (!BF16) {
         // v, a block per 128 keys of one head
-        const int u = (int)blockIdx.x, tile = u % k_tiles, h = u / k_tiles % a.hkv, b = u / k_tiles / a.hkv;
+        const int u = (int)blockIdx.x;
+        int tile, h, b;
+        if (a.k_slots) {
+            h = u % a.hkv;
+            find_tile(a.cu_k, a.total_k, a.batch, u / a.hkv, b, tile);
+        } else {
+            tile = u % k_tiles, h = u / k_tiles % a.hkv, b = u / k_tiles / a.hkv;
+        }
         const AtSeq s = at_seq(a, b);
         slot = (long long)(a.batch + b) * a.hkv + h;
         const uint16_t *v = static_cast<const uint16_t *>(a.v) + b * a.sv[0] + h * a.sv[2] + lane * 8;
         constexpr int RPP = 256 / LPR, NR = 4;
-        if (tile * kT < s.lk)
+        if (tile >= 0 && (long long)tile * kT < s.lk)
             for (int r0 = t / LPR; r0 < kT; r0 += NR * RPP) {
                 uint4 x[NR];
 #pragma unroll
@@ -703,7 +744,10 @@ __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
     if (a.chunks > 1) w.c = u % a.chunks, u /= a.chunks;
     w.tile = u;
     int tile;
-    if (a.tile_slow) {
+    if (a.k_slots) {
+        w.h = u % a.hkv;
+        find_tile(a.cu_k, a.total_k, a.batch, u / a.hkv, w.b, tile);
+    } else if (a.tile_slow) {
         w.b = u % a.batch, u /= a.batch;
         w.h = u % a.hkv, tile = u / a.hkv;
     } else {
@@ -711,12 +755,13 @@ __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
         w.h = u % a.hkv, w.b = u / a.hkv;
     }
     w.s = at_seq(a, w.b);
-    w.k0 = tile * kT;
+    const bool in = tile >= 0 && (long long)tile * kT < w.s.lk;
+    w.k0 = in ? tile * kT : 0;
     w.off = w.s.lk - w.s.lq;  // causal: key j is seen by the queries i >= j - off
     const int qt_end = (w.s.lq + kT - 1) / kT;
     w.qt_begin = a.causal ? min(max(w.k0 - w.off, 0) / kT, qt_end) : 0;
     w.nq = qt_end - w.qt_begin;
-    w.live = w.k0 < w.s.lk;
+    w.live = in;
     w.n = w.live ? w.nq * a.group : 0;
     cut(a, w.c, w.it0, w.n, w.used);
     w.live = w.live && w.c < w.used;
@@ -781,10 +826,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return ok;
         };
         // the next item from `item` on with anything to do
+        const int items = !a.k_slots ? a.items
+                                     : min(a.items, used_slots(a.cu_k, a.total_k, a.batch) * a.hkv * a.chunks);
         auto live = [&](int item) {
             KvItem w{};
             w.tile = -1;
-            for (; item < a.items; item = next_item(a.next)) {
+            for (; item < items; item = next_item(a.next)) {
                 w = kv_item(a, item);
                 if (w.live) break;
                 w.tile = -1;
@@ -1082,7 +1129,10 @@ __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
     if (a.chunks > 1) w.c = u % a.chunks, u /= a.chunks;
     w.tile = u;
     int tile;
-    if (a.tile_slow) {  // causal: the tiles with the most keys first
+    if (a.q_slots) {  // causal: a sequence's tiles with the most keys first
+        w.h = u % a.hq, u /= a.hq;
+        find_tile(a.cu_q, a.total_q, a.batch, a.causal ? used_slots(a.cu_q, a.total_q, a.batch) - 1 - u : u, w.b, tile);
+    } else if (a.tile_slow) {  // causal: the tiles with the most keys first
         w.b = u % a.batch, u /= a.batch;
         w.h = u % a.hq, tile = a.tiles - 1 - u / a.hq;
     } else {
@@ -1090,9 +1140,9 @@ __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
         w.h = u % a.hq, w.b = u / a.hq;
     }
     w.s = at_seq(a, w.b);
-    w.q0 = tile * kT;
+    w.live = tile >= 0 && (long long)tile * kT < w.s.lq;
+    w.q0 = w.live ? tile * kT : 0;
     w.off = w.s.lk - w.s.lq;
-    w.live = w.q0 < w.s.lq;
     w.n = w.live ? (w.s.lk + kT - 1) / kT : 0;
     if (a.causal && w.live) {
         const int last = min(w.q0 + kT, w.s.lq) - 1 + w.off;  // the last key any of its queries sees
@@ -1156,10 +1206,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ok = __all_sync(0xffffffffu, ok) != 0;
             return ok;
         };
+        const int items = !a.q_slots ? a.items
+                                     : min(a.items, used_slots(a.cu_q, a.total_q, a.batch) * a.hq * a.chunks);
         auto live = [&](int item) {
             QItem w{};
             w.tile = -1;
-            for (; item < a.items; item = next_item(a.next + 1)) {
+            for (; item < items; item = next_item(a.next + 1)) {
                 w = q_item(a, item);
                 if (w.live) break;
                 w.tile = -1;
@@ -1415,11 +1467,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
 // ---- host side
 
+// Packed: tiles are counted by the tokens where counting up to the bounds would look
+// at more than this many times as many.  A block passes a tile that does not exist in
+// about a microsecond.  (us, by the tokens / up to the bounds: 64 documents of 700 to
+// 1024 tokens, 32 heads of 128, tight bounds, 1.2 times as many 1906 / 2097, with all
+// tokens as the bound 1907 / 11193; 4 long and 100 short ones, 3 times as many 251 /
+// 367; 200 of up to 128 tokens, where every sequence is one tile and a third of the
+// slots are none, 231 / 204.)
+constexpr long long kLoose = 2;
+
 struct AtCut {
     int chunk, chunks, tiles;  // steps per item, items per tile, tiles with a counter (0: not cut)
 };
 struct AtPlan {
-    int dp, q_tiles, k_tiles;
+    int dp, q_tiles, k_tiles;  // tiles of the longest sequence
+    int q_slots, k_slots;      // tiles counted by the tokens (find_tile), 0: as below
+    long long q_units, k_units;  // tiles of one head that are looked at: of every sequence, as many as
+                                 // the longest has, or slots
     long long head_rows;   // padded rows of one head
     AtCut kv, q;
     size_t off_max, max_bytes, off_nlse, off_ndsum, off_arrived, off_part, total;
@@ -1485,8 +1549,16 @@ int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
         }
     }
     p->dp = d->dim <= 64 ? 64 : 128;
-    p->q_tiles = (d->len_q + kT - 1) / kT;
-    p->k_tiles = (d->len_k + kT - 1) / kT;
+    auto count = [&](long long len, long long total, int *tiles, int *slots, long long *units) {
+        if (d->packed) len = std::min(len, total);
+        *tiles = (int)((len + kT - 1) / kT);
+        *units = (long long)*tiles * d->batch;
+        const long long by_tokens = total / kT + d->batch;
+        *slots = d->packed && *units > kLoose * by_tokens ? (int)by_tokens : 0;
+        if (*slots) *units = by_tokens;
+    };
+    count(d->len_q, d->total_q, &p->q_tiles, &p->q_slots, &p->q_units);
+    count(d->len_k, d->total_k, &p->k_tiles, &p->k_slots, &p->k_units);
     long long rows;
     if (d->packed) {
         p->head_rows = (d->total_q + kT - 1) / kT * kT + (long long)kT * (d->batch + 1);
@@ -1495,21 +1567,24 @@ int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
         p->head_rows = (long long)p->q_tiles * kT;
         rows = p->head_rows * d->heads_q * d->batch;
     }
-    const long long grid = std::max((long long)p->k_tiles * d->heads_kv, (long long)p->q_tiles * d->heads_q);
-    if (grid * d->batch >= (1LL << 30) || rows >= (1LL << 40)) return CBA_ERR_UNSUPPORTED;
+    if (std::max(p->k_units * d->heads_kv, p->q_units * d->heads_q) >= (1LL << 30) || rows >= (1LL << 40))
+        return CBA_ERR_UNSUPPORTED;
     {
         // steps of all tiles together; packed: as if all sequences were the longest
+        auto by_length = [](long long total, long long len) {
+            return (double)total / std::max(1LL, std::min(len, total));
+        };
         const double seqs = !d->packed ? d->batch
-                                       : std::min((double)d->batch, std::max((double)d->total_q / std::max(1, d->len_q),
-                                                                             (double)d->total_k / std::max(1, d->len_k)));
+                                       : std::min((double)d->batch, std::max(by_length(d->total_q, d->len_q),
+                                                                             by_length(d->total_k, d->len_k)));
         const double all = seqs * d->heads_q * p->q_tiles * p->k_tiles * (d->causal ? 0.5 : 1.0);
         // SMs that are done with dk and dv go on to dq, so a tile of dk and dv may take the time
         // of both shares, and where those are whole a tile of dq that of what is left beside them
         // (packed 8192 h16/4: 176 us with its longest tile at 1.2 times the share whole, 184 us cut;
         // dq cut beside whole dk and dv, 4096 tokens, 4 heads: 75 us, whole 59)
-        p->kv = plan_cut((long long)p->k_tiles * d->heads_kv * d->batch,
+        p->kv = plan_cut(p->k_units * d->heads_kv,
                          (long long)p->q_tiles * (d->heads_q / d->heads_kv), all, 1.75);
-        p->q = plan_cut((long long)p->q_tiles * d->heads_q * d->batch, p->k_tiles, all, p->kv.tiles ? 1.25 : 2.3);
+        p->q = plan_cut(p->q_units * d->heads_q, p->k_tiles, all, p->kv.tiles ? 1.25 : 2.3);
     }
     p->off_max = 256;  // behind the status word's 256 bytes, with which they are cleared
     p->max_bytes = d->type == CBA_F16 ? (size_t)2 * d->batch * d->heads_kv * sizeof(unsigned) : 0;
@@ -1541,8 +1616,8 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     if (!BF16) e = cudaMemsetAsync(a.status, 0, p.off_max + p.max_bytes, st);  // the status word and the maxima
     if (e != cudaSuccess) return e;
     // f16: the blocks that look for v's largest rows
-    const int vb = BF16 ? 0 : (int)((long long)p.k_tiles * d.heads_kv * d.batch);
-    const unsigned qgrid = (unsigned)((long long)p.q_tiles * d.heads_q * d.batch);
+    const int vb = BF16 ? 0 : (int)(p.k_units * d.heads_kv);
+    const unsigned qgrid = (unsigned)(p.q_units * d.heads_q);
     attn_prep_kernel<DP, BF16><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), p.k_tiles, vb);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -1553,7 +1628,7 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
         a.tiles = p.k_tiles;
         a.chunk = p.kv.chunk;
         a.chunks = p.kv.chunks;
-        a.items = (int)((long long)p.k_tiles * d.heads_kv * d.batch) * a.chunks;
+        a.items = (int)(p.k_units * d.heads_kv) * a.chunks;
         e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)std::min(a.items, kNumSMs)),
                        dim3(kAtThreads), Kv<DP>::SMEM, st, tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
@@ -1613,6 +1688,7 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.batch = d->batch; a.hq = d->heads_q; a.hkv = d->heads_kv; a.group = d->heads_q / d->heads_kv;
     a.dim = d->dim; a.len_q = d->len_q; a.len_k = d->len_k;
     a.total_q = d->total_q; a.total_k = d->total_k;
+    a.q_slots = p.q_slots; a.k_slots = p.k_slots;
     a.causal = d->causal; a.tile_slow = d->causal; a.scale = d->scale;
     a.lse = lse;
     a.status = static_cast<unsigned *>(workspace);
