@@ -35,6 +35,12 @@ def _workspace(nbytes, what, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _check_status(ws, what):
+    code = B.cba_get_status(ws)
+    if code != B.CBA_OK:
+        raise B.CbaError(code, what)
+
+
 def _norm_desc(x, gamma, beta, eps, **strides):
     for p in (gamma, beta):
         if p is not None and (p.shape != x.shape[-1:] or not p.is_contiguous()):
@@ -92,13 +98,14 @@ def layer_norm_backward(x, dy, gamma, mean, rstd, residual=None, dgamma=None, db
 
 
 def attention_backward(q, k, v, o, lse, dout, causal=False, scale=None, cu_q=None, cu_k=None,
-                       max_q=None, max_k=None):
+                       max_q=None, max_k=None, check=False):
     """(dq, dk, dv) of softmax(scale q k^T) v.
 
     Dense: [batch, len, heads, dim] tensors of any strides, lse fp32 [batch,
     heads, len].  Packed: [tokens, heads, dim] with cu_q and cu_k (int32 starts
     of the sequences, one more than there are; cu_k defaults to cu_q) and lse
-    [heads, tokens]."""
+    [heads, tokens].  check: wait for the call and raise if one of its device waits
+    ran out."""
     outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
     _on_device_of(q, lse=lse, cu_q=cu_q, cu_k=cu_k)
     sequences = None
@@ -115,13 +122,16 @@ def attention_backward(q, k, v, o, lse, dout, causal=False, scale=None, cu_q=Non
                               sequences=sequences, max_q=max_q, max_k=max_k)
     ws = _workspace(B.cba_attention_workspace_bytes(d), "cba_attention_workspace_bytes", q.device)
     B.cba_attention_backward(d, q, k, v, o, lse, dout, cu_q, cu_k, *outs, ws)
+    if check:
+        _check_status(ws, "cba_attention_backward")
     return tuple(outs)
 
 
 def orthogonalize(G, steps=5, coefficients=B.NEWTON_SCHULZ, eps=1e-7, scale=1.0,
-                  out_dtype=torch.bfloat16):
+                  out_dtype=torch.bfloat16, check=False):
     """The Newton-Schulz iterate of each matrix of G [..., rows, cols] (a
-    convolution's dW [K, C, R, S] as dW.view(K, -1))."""
+    convolution's dW [K, C, R, S] as dW.view(K, -1)).  check: wait for the call and
+    raise if one of its device waits ran out."""
     g = G.reshape(-1, *G.shape[-2:]).contiguous()
     out = torch.empty(G.shape, dtype=out_dtype, device=G.device)
     d = B.make_orthogonalize_desc(*g.shape, in_type=B.dtype_code(G.dtype),
@@ -130,4 +140,6 @@ def orthogonalize(G, steps=5, coefficients=B.NEWTON_SCHULZ, eps=1e-7, scale=1.0,
     ws = _workspace(B.cba_orthogonalize_workspace_bytes(d), "cba_orthogonalize_workspace_bytes",
                     G.device)
     B.cba_orthogonalize(d, g, out, ws)
+    if check:
+        _check_status(ws, "cba_orthogonalize")
     return out

@@ -20,3 +20,20 @@ def test_host_tensors_are_refused(cuda_lib):
     torch.cuda.synchronize()
     y, mean, _ = tr.layer_norm(x.cuda())  # a refused call leaves nothing behind
     assert torch.allclose(mean.cpu(), x.mean(1), atol=1e-5) and torch.isfinite(y).all()
+
+
+def test_check_reports_a_device_timeout(cuda_lib, monkeypatch):
+    """The status word as a bounded wait that ran out leaves it (the library's self-test makes one, of a millisecond)."""
+    q, lse = torch.randn(1, 8, 2, 64, device="cuda").bfloat16(), torch.zeros(1, 2, 8, device="cuda")
+    G = torch.randn(40, 60, device="cuda")
+    calls = (lambda **kw: tr.attention_backward(q, q, q, q, lse, q, **kw), lambda **kw: tr.orthogonalize(G, **kw))
+    for call in calls:
+        assert all(torch.equal(a, b) for a, b in zip(call(), call(check=True)))
+    for name in ("cba_attention_backward", "cba_orthogonalize"):
+        plain = getattr(tr.B, name)
+        monkeypatch.setattr(tr.B, name, lambda *a, _f=plain: (_f(*a), cba.cba_selftest_bounded_wait(a[-1], timeout_us=1000)))
+    for call in calls:
+        call()
+        with pytest.raises(cba.CbaError) as e:
+            call(check=True)
+        assert e.value.code == cba.CBA_ERR_DEVICE_TIMEOUT

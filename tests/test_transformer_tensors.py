@@ -180,3 +180,21 @@ def test_statistics_and_parameter_gradients_are_fp32_whatever_the_default_type(c
     dx, dgamma, dbeta = tr.layer_norm_backward(x, x, None, mean, rstd)
     assert dx.dtype == torch.bfloat16 and dgamma.dtype == dbeta.dtype == torch.float32
     assert [c[0] for c in calls] == ["cba_layernorm_forward", "cba_layernorm_backward"]
+
+
+# ---- device status
+
+@pytest.mark.parametrize("call", [lambda **kw: tr.attention_backward(**attn_args(), **kw),
+                                  lambda **kw: tr.orthogonalize(torch.randn(2, 6, 9), **kw)], ids=["attention", "orthogonalize"])
+def test_a_timeout_can_be_asked_for(calls, monkeypatch, call):
+    """The workspace with the status word is the call's own: `check` reads it before it is gone."""
+    asked, code = [], [B.CBA_ERR_DEVICE_TIMEOUT]
+    monkeypatch.setattr(B, "cba_get_status", lambda ws: asked.append(ws) or code[0])
+    call()
+    assert len(calls) == 1 and not asked  # without it the call stays asynchronous
+    with pytest.raises(B.CbaError) as e:
+        call(check=True)
+    assert e.value.code == B.CBA_ERR_DEVICE_TIMEOUT and asked[0] is calls[1][-1]
+    code[0] = B.CBA_OK
+    call(check=True)
+    assert len(asked) == 2
