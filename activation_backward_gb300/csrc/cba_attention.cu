@@ -1508,16 +1508,18 @@ AtCut plan_cut(long long tiles, long long steps, double all, double most) {
     return c;
 }
 
-void fill_strides(const cba_attn_strides_t &s, int heads, int dim, long long len, long long *out) {
+// The strides that the kernels use; packed sequences have none from one to the next.
+void fill_strides(const cba_attention_desc_t &d, const cba_attn_strides_t &s, int heads, long long len, long long *out) {
     if (s.batch == 0 && s.token == 0 && s.head == 0) {
-        out[0] = len * heads * dim;
-        out[1] = (long long)heads * dim;
-        out[2] = dim;
+        out[0] = len * heads * d.dim;
+        out[1] = (long long)heads * d.dim;
+        out[2] = d.dim;
     } else {
         out[0] = s.batch;
         out[1] = s.token;
         out[2] = s.head;
     }
+    if (d.packed) out[0] = 0;
 }
 
 int check_attn(const cba_attention_desc_t *d, AtPlan *p) {
@@ -1703,14 +1705,14 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     a.head_rows = p.head_rows;
     a.o = o; a.dout = dout; a.v = v; a.dq = dq; a.dk = dk; a.dv = dv;
     long long sq[3], sk[3];
-    fill_strides(d->q, d->heads_q, d->dim, tq, sq);
-    fill_strides(d->k, d->heads_kv, d->dim, tk, sk);
-    fill_strides(d->v, d->heads_kv, d->dim, tk, a.sv);
-    fill_strides(d->o, d->heads_q, d->dim, tq, a.so);
-    fill_strides(d->dout, d->heads_q, d->dim, tq, a.sdo);
-    fill_strides(d->dq, d->heads_q, d->dim, tq, a.sdq);
-    fill_strides(d->dk, d->heads_kv, d->dim, tk, a.sdk);
-    fill_strides(d->dv, d->heads_kv, d->dim, tk, a.sdv);
+    fill_strides(*d, d->q, d->heads_q, tq, sq);
+    fill_strides(*d, d->k, d->heads_kv, tk, sk);
+    fill_strides(*d, d->v, d->heads_kv, tk, a.sv);
+    fill_strides(*d, d->o, d->heads_q, tq, a.so);
+    fill_strides(*d, d->dout, d->heads_q, tq, a.sdo);
+    fill_strides(*d, d->dq, d->heads_q, tq, a.sdq);
+    fill_strides(*d, d->dk, d->heads_kv, tk, a.sdk);
+    fill_strides(*d, d->dv, d->heads_kv, tk, a.sdv);
     // without queries (or keys) the main kernels load nothing of them
     CUtensorMap tm[4] = {};
     if (tq > 0 && tk > 0 &&

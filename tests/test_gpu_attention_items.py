@@ -100,3 +100,32 @@ def test_the_torch_call_without_bounds(cuda_lib):
     loose = tr.attention_backward(q, k, v, o, lse, do, causal=True, scale=0.1, cu_q=cu[0])
     tight = run(q, k, v, o, lse, do, 0.1, True, cu_q=cu[0], cu_k=cu[0], sequences=1500, max_q=60, max_k=60)
     assert all(torch.equal(x, y) for x, y in zip(loose, tight))
+
+
+@pytest.mark.parametrize("batch_stride", [0, 1 << 37], ids=["contiguous", "batch strides"])
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (72, F16), (128, F16)], ids=str)
+def test_packed_batch_strides_are_not_used(cuda_lib, dim, dtype, batch_stride):
+    """Strides of 0 (contiguous) or with anything as the batch stride: a packed sequence starts where cu says."""
+    rng = np.random.default_rng(15)
+    lens_q, lens_k = (40, 0, 150, 9), (60, 30, 140, 200)
+    parts, (q, k, v, o, lse, do), cu = pack(rng, lens_q, lens_k, 4, 2, dim, dtype, 0.1, True)
+    outs = [torch.full_like(t, 9.0) for t in (q, k, v)]
+    d = cba.make_attention_desc(q, k, v, o, do, *outs, causal=True, scale=0.1, sequences=4, max_q=150, max_k=200)
+    for name in ("q", "k", "v", "o", "dout", "dq", "dk", "dv"):
+        s = getattr(d, name)
+        setattr(d, name, cba.cba_attn_strides_t(batch_stride, s.token, s.head) if batch_stride else cba.cba_attn_strides_t(0, 0, 0))
+    ws = torch.empty(cba.cba_attention_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    cba.cba_attention_backward(d, q, k, v, o, lse, do, *cu, *outs, ws)
+    assert cba.cba_get_status(ws) == cba.CBA_OK
+    at = [0, 0]
+    for p, a, b in zip(parts, lens_q, lens_k):
+        own = [outs[0][None, at[0]:at[0] + a], outs[1][None, at[1]:at[1] + b], outs[2][None, at[1]:at[1] + b]]
+        compare(p, own, 0.1, True, dtype)
+        at = [at[0] + a, at[1] + b]
+
+
+@pytest.mark.parametrize("dtype", [BF, F16], ids=str)
+def test_one_packed_query_of_one_head(cuda_lib, dtype):
+    """Every axis of q has one index, so that its descriptor has no strides; the query belongs to the third sequence."""
+    rng = np.random.default_rng(16)
+    check_packed(rng, (0, 0, 1, 0), (30, 7, 50, 0), 1, 1, 64, dtype, 0.1, False)
