@@ -438,13 +438,15 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
  * (3.4445, -4.7750, 2.0315) and 5 steps they end near 1.
  *
  * The products' operands are f16 scaled by powers of two, their sums fp32,
- * whatever the element types are: with the coefficients above O's error is 1e-3 to
- * 4e-3 of its norm (so its type is usually bf16).  Singular values far below the
- * leading ones grow by a factor of `a` a step, and with them the rounding errors in
- * their directions: 2e-2 of the norm of a matrix of 24 rows whose singular values
- * span four decades, 5e-3 of one of 1000.  The scaling has room for singular values
- * up to 2 before every step, whatever the coefficients (those that converge keep
- * them below 1.3).  Elements of G below 1e-19 count as 0 in its norm.
+ * whatever the element types are: with the coefficients above O's error is 1e-3
+ * to 4e-3 of its norm (so its type is usually bf16), and to 1e-2 in matrices of
+ * a few rows, whose singular values may all meet the polynomial where it is
+ * steep.  Singular values far below the leading ones grow by a factor of `a` a
+ * step, and with them the rounding errors in their directions: where they span
+ * four decades, 5e-2 of the norm of a matrix of 2 rows, 2e-2 of one of 24 rows,
+ * 5e-3 of one of 1000.  The scaling has room for singular values up to 2 before
+ * every step, whatever the coefficients (those that converge keep them below
+ * 1.3).  Elements of G below 1e-19 count as 0 in its norm.
  *
  * Element types f32, f16 or bf16.  ld_*: elements from one row to the next (0:
  * cols); batch_*: from one matrix to the next (0: rows * ld).  O may be G when

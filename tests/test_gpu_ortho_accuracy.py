@@ -47,3 +47,31 @@ def test_singular_values_over_four_decades(cuda_lib, shape):
     m = min(shape)
     u, _, v = np.linalg.svd(rng.normal(size=shape), full_matrices=False)
     assert relative_error((u * np.logspace(0, -4, m)) @ v) <= FLAT + np.sqrt(5 / m) * 3.4445 ** 5 * R
+
+
+def steep_bar(G):
+    """The few singular values of a matrix of few rows may all meet the polynomial where it is steep.  An error e of X becomes at
+    most D e, D the largest of |p'(s)| and p(s) / s between the smallest and the largest singular value; to it come the roundings
+    of S, |b + 2 c t| r |S| sigma at most, of C, r |C| sigma, and of the new X."""
+    a, b, c = 3.4445, -4.7750, 2.0315
+    X = G if G.shape[0] <= G.shape[1] else G.T
+    X = X / np.linalg.norm(X)
+    e = R * np.linalg.norm(X)
+    for _ in range(5):
+        s = np.linalg.svd(X, compute_uv=False)
+        grid = np.linspace(s.min(), s.max(), 200)
+        t = grid ** 2
+        D = max(np.abs(a + 3 * b * t + 5 * c * t * t).max(), np.abs(a + b * t + c * t * t).max())
+        S = X @ X.T
+        C = a * np.eye(len(S)) + b * S + c * S @ S
+        X = C @ X
+        e = D * e + R * (s.max() * (np.abs(b + 2 * c * t).max() * np.linalg.norm(S) + np.linalg.norm(C)) + np.linalg.norm(X))
+    return e / np.linalg.norm(X)
+
+
+@pytest.mark.parametrize("shape", [(2, 9), (3, 31), (3, 104), (4, 1419), (1134, 4), (105, 3)], ids=str)
+def test_few_rows(cuda_lib, shape):
+    rng = np.random.default_rng(shape[0] + shape[1])
+    for _ in range(10):
+        A = rng.normal(size=shape).astype(np.float32)
+        assert relative_error(A) <= steep_bar(A.astype(np.float64))
