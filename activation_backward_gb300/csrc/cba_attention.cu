@@ -186,7 +186,7 @@ __device__ __forceinline__ float ds_scale(const AtArgs &a, int b, int h) {
 // per 128-row tile of one head; 16 (DP = 128) or 8 lanes per row, four rows of a
 // thread in flight.  Bound by memory: 134 MB of o and do in 26 us, 5.1 TB/s; with
 // v for f16 66 MB in 16 us.
-template <int DP, bool BF16>
+template <int DP, bool BF16, bool SLOTS>
 __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_tiles, int k_tiles, int v_blocks) {
     constexpr int LPR = DP / 8;
     const int t = threadIdx.x, lane = t % LPR;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
     if ((int)blockIdx.x >= v_blocks) {
         const int u = (int)blockIdx.x - v_blocks;
         int tile, h, b;
-        if (a.q_slots) {
+        if (SLOTS && a.q_slots) {
             h = u % a.hq;
             find_tile(a.cu_q, a.total_q, a.batch, u / a.hq, b, tile);
         } else {
@@ -210,8 +210,9 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         }
         if (u == 0)
             for (int i = t; i < a.cnt_kv + a.cnt_q; i += 256) a.arrived[i] = 0;
-        if (tile >= 0 && (long long)tile * kT < s.lq) {
+        if (tile >= 0 && tile < (s.lq + kT - 1) / kT) {
             const long long row0 = s.row0 + (long long)h * a.head_rows + tile * kT;
+            const int unseen = a.causal ? s.lq - s.lk : s.lk == 0 ? s.lq : 0;  // rows before it see no key
             constexpr int RPP = 256 / LPR, NR = 4;  // rows per pass; rows of a thread in flight
             for (int r0 = t / LPR; r0 < kT; r0 += NR * RPP) {
                 uint4 x[NR], y[NR];
@@ -228,8 +229,9 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
                                                                 (s.q0 + i) * a.sdo[1] + h * a.sdo[2] + lane * 8);
                     }
                     if (i < s.lq && lane == 0)
-                        l[j] = a.lse[a.cu_q ? (long long)h * a.total_q + s.q0 + i
-                                            : ((long long)b * a.hq + h) * a.len_q + i];
+                        l[j] = i < unseen ? -INFINITY
+                                          : a.lse[a.cu_q ? (long long)h * a.total_q + s.q0 + i
+                                                         : ((long long)b * a.hq + h) * a.len_q + i];
                 }
 #pragma unroll
                 for (int j = 0; j < NR; ++j) {
@@ -250,8 +252,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
                     if (lane == 0) {
                         // a row that sees no key, by the mask or (lse = -inf) the caller's own: P = 0 and D = 0
                         // whatever the forward left in its o and lse (a softmax over nothing is NaN)
-                        const int i = tile * kT + r0 + j * RPP;
-                        const bool none = l[j] == -INFINITY || (a.causal ? i + s.lk < s.lq : s.lk == 0);
+                        const bool none = l[j] == -INFINITY;
                         const long long at = row0 + r0 + j * RPP;
                         a.nlse[at] = none ? -INFINITY : (BF16 ? 0.f : kPShift) - l[j] * kLog2e;
                         a.ndsum[at] = none ? 0.f : -d;
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         // v, a block per 128 keys of one head
         const int u = (int)blockIdx.x;
         int tile, h, b;
-        if (a.k_slots) {
+        if (SLOTS && a.k_slots) {
             h = u % a.hkv;
             find_tile(a.cu_k, a.total_k, a.batch, u / a.hkv, b, tile);
         } else {
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_ti
         slot = (long long)(a.batch + b) * a.hkv + h;
         const uint16_t *v = static_cast<const uint16_t *>(a.v) + b * a.sv[0] + h * a.sv[2] + lane * 8;
         constexpr int RPP = 256 / LPR, NR = 4;
-        if (tile >= 0 && (long long)tile * kT < s.lk)
+        if (tile >= 0 && tile < (s.lk + kT - 1) / kT)
             for (int r0 = t / LPR; r0 < kT; r0 += NR * RPP) {
                 uint4 x[NR];
 #pragma unroll
@@ -738,13 +739,14 @@ struct KvItem {
 };
 static_assert(sizeof(KvItem) <= 128);
 
+template <bool SLOTS>
 __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
     KvItem w;
     w.c = 0;
     if (a.chunks > 1) w.c = u % a.chunks, u /= a.chunks;
     w.tile = u;
     int tile;
-    if (a.k_slots) {
+    if (SLOTS && a.k_slots) {
         w.h = u % a.hkv;
         find_tile(a.cu_k, a.total_k, a.batch, u / a.hkv, w.b, tile);
     } else if (a.tile_slow) {
@@ -755,7 +757,7 @@ __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
         w.h = u % a.hkv, w.b = u / a.hkv;
     }
     w.s = at_seq(a, w.b);
-    const bool in = tile >= 0 && (long long)tile * kT < w.s.lk;
+    const bool in = tile >= 0 && tile < (w.s.lk + kT - 1) / kT;
     w.k0 = in ? tile * kT : 0;
     w.off = w.s.lk - w.s.lq;  // causal: key j is seen by the queries i >= j - off
     const int qt_end = (w.s.lq + kT - 1) / kT;
@@ -769,7 +771,7 @@ __device__ __forceinline__ KvItem kv_item(const AtArgs &a, int u) {
     return w;
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, bool SLOTS>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_kv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -826,13 +828,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             return ok;
         };
         // the next item from `item` on with anything to do
-        const int items = !a.k_slots ? a.items
+        const int items = !SLOTS || !a.k_slots ? a.items
                                      : min(a.items, used_slots(a.cu_k, a.total_k, a.batch) * a.hkv * a.chunks);
         auto live = [&](int item) {
             KvItem w{};
             w.tile = -1;
             for (; item < items; item = next_item(a.next)) {
-                w = kv_item(a, item);
+                w = kv_item<SLOTS>(a, item);
                 if (w.live) break;
                 w.tile = -1;
             }
@@ -1123,13 +1125,14 @@ struct QItem {
 };
 static_assert(sizeof(QItem) <= 128);
 
+template <bool SLOTS>
 __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
     QItem w;
     w.c = 0;
     if (a.chunks > 1) w.c = u % a.chunks, u /= a.chunks;
     w.tile = u;
     int tile;
-    if (a.q_slots) {  // causal: a sequence's tiles with the most keys first
+    if (SLOTS && a.q_slots) {  // causal: a sequence's tiles with the most keys first
         w.h = u % a.hq, u /= a.hq;
         find_tile(a.cu_q, a.total_q, a.batch, a.causal ? used_slots(a.cu_q, a.total_q, a.batch) - 1 - u : u, w.b, tile);
     } else if (a.tile_slow) {  // causal: the tiles with the most keys first
@@ -1140,7 +1143,7 @@ __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
         w.h = u % a.hq, w.b = u / a.hq;
     }
     w.s = at_seq(a, w.b);
-    w.live = tile >= 0 && (long long)tile * kT < w.s.lq;
+    w.live = tile >= 0 && tile < (w.s.lq + kT - 1) / kT;
     w.q0 = w.live ? tile * kT : 0;
     w.off = w.s.lk - w.s.lq;
     w.n = w.live ? (w.s.lk + kT - 1) / kT : 0;
@@ -1154,7 +1157,7 @@ __device__ __forceinline__ QItem q_item(const AtArgs &a, int u) {
     return w;
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, bool SLOTS>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_q_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -1206,13 +1209,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             ok = __all_sync(0xffffffffu, ok) != 0;
             return ok;
         };
-        const int items = !a.q_slots ? a.items
+        const int items = !SLOTS || !a.q_slots ? a.items
                                      : min(a.items, used_slots(a.cu_q, a.total_q, a.batch) * a.hq * a.chunks);
         auto live = [&](int item) {
             QItem w{};
             w.tile = -1;
             for (; item < items; item = next_item(a.next + 1)) {
-                w = q_item(a, item);
+                w = q_item<SLOTS>(a, item);
                 if (w.live) break;
                 w.tile = -1;
             }
@@ -1611,7 +1614,10 @@ bool attn_map(CUtensorMap *m, const void *base, const cba_attention_desc_t &d, i
     return tma_encode_16(m, base, d.type == CBA_BF16, 4, dims, strides, box);
 }
 
-template <int DP, bool BF16>
+// The search for slots is in kernels of its own: with it the preparation of f16 takes 69
+// registers for 60, a block less on each SM (32x676 20.4 us, 16.4), and the main kernels
+// of a small call 0.3 to 0.4 us more each (2x169: 14.3 us, 12.3).
+template <int DP, bool BF16, bool SLOTS>
 cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a, const CUtensorMap *tm,
                         cudaStream_t st) {
     cudaError_t e = cudaSuccess;
@@ -1620,18 +1626,18 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
     // f16: the blocks that look for v's largest rows
     const int vb = BF16 ? 0 : (int)(p.k_units * d.heads_kv);
     const unsigned qgrid = (unsigned)(p.q_units * d.heads_q);
-    attn_prep_kernel<DP, BF16><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), p.k_tiles, vb);
+    attn_prep_kernel<DP, BF16, SLOTS><<<std::max(1u, qgrid) + vb, 256, 0, st>>>(a, std::max(1, p.q_tiles), p.k_tiles, vb);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = allow_smem<attn_kv_kernel<DP, BF16>>((int)Kv<DP>::SMEM);
-    if (e == cudaSuccess) e = allow_smem<attn_q_kernel<DP, BF16>>((int)Qk<DP>::SMEM);
+    e = allow_smem<attn_kv_kernel<DP, BF16, SLOTS>>((int)Kv<DP>::SMEM);
+    if (e == cudaSuccess) e = allow_smem<attn_q_kernel<DP, BF16, SLOTS>>((int)Qk<DP>::SMEM);
     if (e != cudaSuccess) return e;
     if (p.k_tiles > 0) {
         a.tiles = p.k_tiles;
         a.chunk = p.kv.chunk;
         a.chunks = p.kv.chunks;
         a.items = (int)(p.k_units * d.heads_kv) * a.chunks;
-        e = launch_pdl(attn_kv_kernel<DP, BF16>, dim3((unsigned)std::min(a.items, kNumSMs)),
+        e = launch_pdl(attn_kv_kernel<DP, BF16, SLOTS>, dim3((unsigned)std::min(a.items, kNumSMs)),
                        dim3(kAtThreads), Kv<DP>::SMEM, st, tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
     }
@@ -1645,10 +1651,10 @@ cudaError_t attn_launch(const cba_attention_desc_t &d, const AtPlan &p, AtArgs a
         const unsigned blocks = (unsigned)std::min(a.items, kNumSMs);
         // without keys there is no launch between this one and the preparation
         if (p.k_tiles > 0)
-            e = launch_pdl(attn_q_kernel<DP, BF16>, dim3(blocks), dim3(kAtThreads), Qk<DP>::SMEM, st, tm[0],
+            e = launch_pdl(attn_q_kernel<DP, BF16, SLOTS>, dim3(blocks), dim3(kAtThreads), Qk<DP>::SMEM, st, tm[0],
                            tm[1], tm[2], tm[3], a);
         else
-            attn_q_kernel<DP, BF16><<<blocks, kAtThreads, Qk<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], tm[3], a);
+            attn_q_kernel<DP, BF16, SLOTS><<<blocks, kAtThreads, Qk<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], tm[3], a);
         if (e != cudaSuccess) return e;
     }
     return cudaGetLastError();
@@ -1723,9 +1729,11 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = select_device_of(workspace);
     if (e == cudaSuccess) {
-        const bool bf = d->type == CBA_BF16;
-        if (p.dp == 64) e = bf ? attn_launch<64, true>(*d, p, a, tm, st) : attn_launch<64, false>(*d, p, a, tm, st);
-        else e = bf ? attn_launch<128, true>(*d, p, a, tm, st) : attn_launch<128, false>(*d, p, a, tm, st);
+        const bool bf = d->type == CBA_BF16, slots = p.q_slots || p.k_slots;
+        auto launch = [&](auto dp, auto b, auto sl) { return attn_launch<dp(), b(), sl()>(*d, p, a, tm, st); };
+        auto typed = [&](auto dp, auto b) { return slots ? launch(dp, b, std::true_type{}) : launch(dp, b, std::false_type{}); };
+        auto sized = [&](auto dp) { return bf ? typed(dp, std::true_type{}) : typed(dp, std::false_type{}); };
+        e = p.dp == 64 ? sized(std::integral_constant<int, 64>{}) : sized(std::integral_constant<int, 128>{});
     }
     return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
 }
