@@ -30,14 +30,15 @@
 //
 // Measured (us; launches overlap, so a call takes less than their sum; rates count
 // the formulas' 5 products):
-//   8192 tokens, 32/8 heads of 128, causal, bf16   27 + 655 + 504, call 1125 (1221 where calls
-//       follow each other without a pause): 1.22 PFLOP/s, 1.7 with the 7 products that run.
-//       The tensor cores bound it, at the clock that the power limit leaves them
-//   9 documents of 8192 tokens, 16/4 heads of 128  15 + 103 + 92, call 166: the longest tile
-//   32 x 676 tokens, 8 heads of 64, f16            16 + 95 + 83, call 186: the compute warps,
+//   8192 tokens, 32/8 heads of 128, causal, bf16   27 + 654 + 504, call 1125 after a pause and
+//       1216 to 1242 where calls follow each other: 1.1 PFLOP/s, 1.56 with the 7 products that
+//       run (1.7 after a pause).  The tensor cores bound it, at the clock that the power limit
+//       leaves them
+//   9 documents of 8192 tokens, 16/4 heads of 128  16 + 104 + 92, call 169: the longest tile
+//   32 x 676 tokens, 8 heads of 64, f16            17 + 95 + 85, call 189: the compute warps,
 //       whose two halves of a step (P, then dS) take 850 and 1000 cycles of latency; the tensor
 //       cores are active for 38% of the cycles, the issue slots taken for 47%
-//   2 x 169 tokens, 8 heads of 64, bf16            call 12.3: three launches, a tile or two each
+//   2 x 169 tokens, 8 heads of 64, bf16            call 12.3 to 13.2: three launches, a tile or two each
 // The preparation reads o and do at 5.1 TB/s in the first case.
 //
 // Roles of a block: warp 0 issues the TMA loads (and zeroes the rows of a
@@ -71,7 +72,7 @@ constexpr uint32_t kBoxBytes = kT * 128u;     // 128 rows x 64 16-bit elements
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 12.f;               // f16: P is held as 2^12 P
 
-// A query- or key-side tensor on the host: bytes between batches, tokens, heads.
+// What the kernels of a call get; strides in elements.
 struct AtArgs {
     const int *cu_q, *cu_k;      // packed: sequence starts; dense: NULL
     int batch, hq, hkv, group, dim, len_q, len_k;  // packed: the lengths are upper bounds
@@ -93,7 +94,7 @@ struct AtArgs {
     float *part;                 // fp32 tiles of the items of a tile
     const void *o, *dout, *v;
     void *dq, *dk, *dv;
-    long long so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head (elements)
+    long long so[3], sdo[3], sv[3], sdq[3], sdk[3], sdv[3];  // batch, token, head
 };
 
 // The sequence b: its first query and key token, its lengths, and the first
@@ -185,7 +186,7 @@ __device__ __forceinline__ float ds_scale(const AtArgs &a, int b, int h) {
 // ---- D, lse in base 2, and (f16) the largest row norms of do and v.  One block
 // per 128-row tile of one head; 16 (DP = 128) or 8 lanes per row, four rows of a
 // thread in flight.  Bound by memory: 134 MB of o and do in 26 us, 5.1 TB/s; with
-// v for f16 66 MB in 16 us.
+// v for f16 66 MB in 17 us.
 template <int DP, bool BF16, bool SLOTS>
 __global__ void __launch_bounds__(256) attn_prep_kernel(const AtArgs a, int q_tiles, int k_tiles, int v_blocks) {
     constexpr int LPR = DP / 8;
@@ -684,7 +685,7 @@ __device__ __forceinline__ void store_sums(const float4 *at, int used, long long
     }
 }
 
-// Bars of one pipeline stage's ring: initialised by one thread.
+// The barriers that both main kernels have, by one thread.
 template <typename Bars>
 __device__ __forceinline__ void init_common(Bars &sb) {
     at_init_bars(sb.s_full, 2, 1);

@@ -17,12 +17,12 @@
 // (no atomics: the result does not depend on scheduling).
 //
 // Measured (us, and of the measured copy rate where memory bounds it):
-//   forward 65536 x 2048 bf16                    98: 5.4 TB/s, 0.81
-//   backward 32768 x 4096 bf16 with a residual   190: 5.6 TB/s, 0.84 (187 + 3.5 of column sums)
-//   backward 43264 x 255 fp32                    29: 4.6 TB/s, 0.68 (26 + 3.5; rows that are not
+//   forward 65536 x 2048 bf16                    103: 5.2 TB/s, 0.77 (96 after a pause)
+//   backward 32768 x 4096 bf16 with a residual   193: 5.6 TB/s, 0.83 (187 + 3.5 of column sums)
+//   backward 43264 x 255 fp32                    31: 4.3 TB/s, 0.63 (26 + 3.5; rows that are not
 //       whole vectors move 4 bytes a thread)
-//   169 x 512 fp32                               3 and 5.4 on the device; a call from Python takes
-//       5.1 and 8.0, the time in which the host issues it
+//   169 x 512 fp32                               3 and 5.5 on the device; a call from Python takes
+//       5.2 and 8.1, the time in which the host issues it
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>

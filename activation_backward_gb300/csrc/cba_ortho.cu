@@ -32,11 +32,11 @@
 // waits (bounded) for copies and MMAs in flight, frees its TMEM and returns.
 //
 // Measured, 5 steps (us):
-//   2 of 8192 x 2048  844 (893 where calls follow each other without a pause); per step S 56,
-//       C 24, X' 82: X' at 1.67 PFLOP/s, 0.98 of what cuBLAS sustains under the power limit;
+//   2 of 8192 x 2048  858 after a pause, 900 to 935 where calls follow each other; per step S 58,
+//       C 23, X' 82: X' at 1.67 PFLOP/s, 0.98 of what cuBLAS sustains under the power limit;
 //       S and C are one round of tiles over the SMs, whose beginning and end nothing covers
-//   512 x 2304        107: 15 dependent launches of 5 to 9, latency
-//   50 x 500          24, one launch: 2 in reading G, 4 to 5 a step, 2 in writing O
+//   512 x 2304        106: 15 dependent launches of 5 to 9, latency
+//   50 x 500          25 (a call 27), one launch: 2 in reading G, 4 to 5 a step, 2 in writing O
 #include <cuda.h>
 
 #include <algorithm>

@@ -58,7 +58,7 @@ def _ld(t):
 
 def layer_norm(x, gamma=None, beta=None, eps=1e-5):
     """(y, mean, rstd) over the last axis of x; mean and rstd (fp32, one per
-    row) are what the backward pass takes."""
+    row) are what the backward pass takes.  x: any row stride, but no expanded rows."""
     rows = _rows(x)
     _on_device_of(x, gamma=gamma, beta=beta)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -104,8 +104,10 @@ def attention_backward(q, k, v, o, lse, dout, causal=False, scale=None, cu_q=Non
     Dense: [batch, len, heads, dim] tensors of any strides, lse fp32 [batch,
     heads, len].  Packed: [tokens, heads, dim] with cu_q and cu_k (int32 starts
     of the sequences, one more than there are; cu_k defaults to cu_q) and lse
-    [heads, tokens].  check: wait for the call and raise if one of its device waits
-    ran out."""
+    [heads, tokens]; the starts run from 0 to the number of tokens (rows of tokens
+    outside are not written).  max_q and max_k: upper bounds of the sequences' lengths
+    (default: all tokens).  check: wait for the call and raise if one of its device
+    waits ran out.  Expanded tensors, and tensors of another device, are refused."""
     outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
     _on_device_of(q, lse=lse, cu_q=cu_q, cu_k=cu_k)
     sequences = None

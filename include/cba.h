@@ -368,7 +368,8 @@ typedef struct {
     long long ld_x, ld_y, ld_dy, ld_dx, ld_residual;
 } cba_layernorm_desc_t;
 
-/* gamma, beta: NULL for 1 and 0.  mean, rstd: NULL when not wanted.  y may be x. */
+/* gamma, beta: NULL for 1 and 0.  mean, rstd: NULL when not wanted.  y may be x
+ * (of the same ld). */
 int cba_layernorm_forward(const cba_layernorm_desc_t *d, const void *x, const void *gamma,
                           const void *beta, void *y, float *mean, float *rstd, void *stream);
 
@@ -376,8 +377,8 @@ int cba_layernorm_forward(const cba_layernorm_desc_t *d, const void *x, const vo
 size_t cba_layernorm_workspace_bytes(const cba_layernorm_desc_t *d);
 
 /* residual (nullable): the shortcut's delta, added to dx.  gamma NULL: 1.
- * dgamma, dbeta: NULL when not wanted.  dx may be x, dy or residual.  With
- * rows = 0, dgamma and dbeta become 0 (accumulate = 0) or stay. */
+ * dgamma, dbeta: NULL when not wanted.  dx may be x, dy or residual (of the same
+ * ld).  With rows = 0, dgamma and dbeta become 0 (accumulate = 0) or stay. */
 int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const void *dy,
                            const void *gamma, const float *mean, const float *rstd,
                            const void *residual, void *dx, float *dgamma, float *dbeta,
@@ -399,15 +400,19 @@ int cba_layernorm_backward(const cba_layernorm_desc_t *d, const void *x, const v
  * Dense: `batch` sequences of len_q queries and len_k keys, element (b, t, h, c)
  * of a tensor at b * batch + t * token + h * head + c.  Packed: `batch`
  * sequences one after another, cu_q and cu_k DEVICE int32 [batch + 1] with their
- * first tokens (non-decreasing, from 0 to total_q / total_k); len_q and len_k are
- * upper bounds of the sequences' lengths (tokens past them are not computed) and
- * the batch strides are not used.  A sequence may be empty.  Strides all 0 mean
- * contiguous [batch][token][head][dim].  Strides must be multiples of 8 elements
- * and bases 16-byte aligned (CBA_ERR_ALIGN).  Outputs must not overlap inputs.
+ * first tokens (non-decreasing, within 0 and total_q / total_k; tokens outside
+ * all sequences are neither used nor written); len_q and len_k are upper bounds
+ * of the sequences' lengths (tokens past them are not computed; total_q and
+ * total_k will do) and the batch strides are not used.  A sequence may be
+ * empty.  Strides all 0 mean contiguous [batch][token][head][dim].  Strides must
+ * be multiples of 8 elements and bases 16-byte aligned (CBA_ERR_ALIGN).  Outputs
+ * must not overlap inputs.
  *
- * P and dS are rounded to the elements' type for their products, the sums are
- * fp32.  In a sequence's own rows, infinities and NaN spread as in the formulas
- * (a masked pair still multiplies its row by 0); another sequence's never do. */
+ * P and dS are rounded to the elements' type for their products (f16: times
+ * powers of two, dS's from the largest finite rows of dout and v of its own
+ * sequence and key/value head), the sums are fp32.  In a sequence's own rows,
+ * infinities and NaN spread as in the formulas (a masked pair still multiplies
+ * its row by 0); another sequence's never do. */
 typedef struct { long long batch, token, head; } cba_attn_strides_t;
 typedef struct {
     int batch, heads_q, heads_kv, dim;
