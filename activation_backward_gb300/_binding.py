@@ -54,6 +54,9 @@ EXPORTS = ("cba_workspace_bytes", "cba_workspace_bytes_ex", "cba_workspace_bytes
            "cba_version", "cba_plan_info",
            "cba_layernorm_forward", "cba_layernorm_workspace_bytes", "cba_layernorm_backward",
            "cba_attention_workspace_bytes", "cba_attention_backward",
+           "cba_attention_forward_workspace_bytes", "cba_attention_forward",
+           "cba_qk_norm_rope_forward", "cba_qk_norm_rope_workspace_bytes",
+           "cba_qk_norm_rope_backward", "cba_dropout",
            "cba_orthogonalize_workspace_bytes", "cba_orthogonalize")
 CBA_ROUTE_MAX_INPUTS = 8
 CBA_WS_RECOMPUTE_Z = 1
@@ -103,6 +106,21 @@ class cba_attention_desc_t(ctypes.Structure):
                 [("total_q", ctypes.c_longlong), ("total_k", ctypes.c_longlong),
                  ("causal", ctypes.c_int), ("scale", ctypes.c_float)] +
                 [(n, cba_attn_strides_t) for n in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")])
+
+
+class cba_qk_norm_rope_desc_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("batch", "len", "heads_q", "heads_k", "dim", "type",
+                                              "param_type", "norm", "rot_dim", "interleaved",
+                                              "positions", "accumulate")] +
+                [("eps", ctypes.c_float)] +
+                [(n, cba_attn_strides_t) for n in ("q", "k", "yq", "yk", "dyq", "dyk", "dq", "dk")])
+
+
+class cba_dropout_desc_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("cols", ctypes.c_longlong), ("type", ctypes.c_int),
+                ("p", ctypes.c_float), ("seed", ctypes.c_ulonglong),
+                ("offset", ctypes.c_ulonglong), ("ld_x", ctypes.c_longlong),
+                ("ld_residual", ctypes.c_longlong), ("ld_y", ctypes.c_longlong)]
 
 
 class cba_orthogonalize_desc_t(ctypes.Structure):
@@ -185,6 +203,19 @@ def load(path=LIB_PATH):
     L.cba_attention_workspace_bytes.argtypes = [at]
     L.cba_attention_backward.restype = ctypes.c_int
     L.cba_attention_backward.argtypes = [at] + [vp] * 12 + [sz, vp]
+    L.cba_attention_forward_workspace_bytes.restype = sz
+    L.cba_attention_forward_workspace_bytes.argtypes = [at]
+    L.cba_attention_forward.restype = ctypes.c_int
+    L.cba_attention_forward.argtypes = [at] + [vp] * 8 + [sz, vp]
+    qk = ctypes.POINTER(cba_qk_norm_rope_desc_t)
+    L.cba_qk_norm_rope_forward.restype = ctypes.c_int
+    L.cba_qk_norm_rope_forward.argtypes = [qk] + [vp] * 9
+    L.cba_qk_norm_rope_workspace_bytes.restype = sz
+    L.cba_qk_norm_rope_workspace_bytes.argtypes = [qk]
+    L.cba_qk_norm_rope_backward.restype = ctypes.c_int
+    L.cba_qk_norm_rope_backward.argtypes = [qk] + [vp] * 13 + [sz, vp]
+    L.cba_dropout.restype = ctypes.c_int
+    L.cba_dropout.argtypes = [ctypes.POINTER(cba_dropout_desc_t)] + [vp] * 5
     ns = ctypes.POINTER(cba_orthogonalize_desc_t)
     L.cba_orthogonalize_workspace_bytes.restype = sz
     L.cba_orthogonalize_workspace_bytes.argtypes = [ns]
@@ -445,15 +476,33 @@ def cba_layernorm_backward(desc, x, dy, gamma, mean, rstd, residual, dx, dgamma,
     return _checked(rc, "cba_layernorm_backward", check)
 
 
-def make_attention_desc(q, k, v, o, dout, dq, dk, dv, causal=False, scale=None, sequences=None,
-                        max_q=None, max_k=None):
-    """The descriptor of a call on these tensors (their shapes, strides and type).
+def _check_strides(name, t):
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the innermost axis is not contiguous")
+    # (strides of 0 on every axis would read as the descriptor's "contiguous")
+    if t.numel() and any(n > 1 and s < t.shape[-1] for n, s in zip(t.shape[:-1], t.stride())):
+        raise ValueError(f"{name}: indices of an axis lie on one another (it is expanded): make it contiguous")
+
+
+def _attn_strides(t, no_batch):
+    """The descriptor's strides of [(batch,) len, heads, dim], None for contiguous."""
+    # an axis of one index has no stride that matters
+    st = [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    if t.numel() and any(st):
+        return cba_attn_strides_t(0 if no_batch else st[0], st[-2], st[-1])
+    return None
+
+
+def make_attention_desc(q, k, v, o, dout=None, dq=None, dk=None, dv=None, causal=False, scale=None,
+                        sequences=None, max_q=None, max_k=None):
+    """The descriptor of a call on these tensors (their shapes, strides and type); the
+    forward pass takes no dout, dq, dk and dv.
 
     Dense: [batch, len, heads, dim].  Packed: [tokens, heads, dim], with the
     number of ``sequences`` and upper bounds of their lengths (default: all
     tokens).  Any strides whose innermost one is 1.  ``scale`` defaults to
     dim ** -0.5."""
-    tensors = dict(q=q, k=k, v=v, o=o, dout=dout, dq=dq, dk=dk, dv=dv)
+    tensors = {n: t for n, t in dict(q=q, k=k, v=v, o=o, dout=dout, dq=dq, dk=dk, dv=dv).items() if t is not None}
     packed = q.dim() == 3
     if packed and sequences is None:
         raise ValueError("packed tensors need the number of sequences")
@@ -465,11 +514,7 @@ def make_attention_desc(q, k, v, o, dout, dq, dk, dv, causal=False, scale=None, 
         want = k if name in ("k", "v", "dk", "dv") else q
         if t.shape != want.shape or t.dtype != q.dtype or t.device != q.device:
             raise ValueError(f"{name}: shape, type or device differs from {'k' if want is k else 'q'}'s")
-        if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name}: the innermost axis is not contiguous")
-        # (strides of 0 on every axis would read as the descriptor's "contiguous")
-        if t.numel() and any(n > 1 and s < t.shape[-1] for n, s in zip(t.shape[:-1], t.stride())):
-            raise ValueError(f"{name}: indices of an axis lie on one another (it is expanded): make it contiguous")
+        _check_strides(name, t)
     d = cba_attention_desc_t()
     d.heads_q, d.heads_kv, d.dim = q.shape[-2], k.shape[-2], q.shape[-1]
     d.type, d.causal, d.packed = dtype_code(q.dtype), int(causal), int(packed)
@@ -481,10 +526,9 @@ def make_attention_desc(q, k, v, o, dout, dq, dk, dv, causal=False, scale=None, 
     else:
         d.batch, d.len_q, d.len_k = q.shape[0], q.shape[1], k.shape[1]
     for name, t in tensors.items():
-        # an axis of one index has no stride that matters
-        st = [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
-        if t.numel() and any(st):
-            setattr(d, name, cba_attn_strides_t(0 if packed else st[0], st[-2], st[-1]))
+        st = _attn_strides(t, packed)
+        if st is not None:
+            setattr(d, name, st)
     return d
 
 
@@ -503,6 +547,95 @@ def cba_attention_backward(desc, q, k, v, o, lse, dout, cu_q, cu_k, dq, dk, dv, 
         _ptr(cu_q), _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), wsb,
         _stream(stream))
     return _checked(rc, "cba_attention_backward", check)
+
+
+def cba_attention_forward_workspace_bytes(desc):
+    return load().cba_attention_forward_workspace_bytes(ctypes.byref(desc))
+
+
+def cba_attention_forward(desc, q, k, v, cu_q, cu_k, o, lse, workspace, workspace_bytes=None,
+                          stream=None, check=True):
+    """o = softmax(scale q k^T) v and, when given, lse (fp32 [batch, heads, len],
+    packed [heads, tokens]), the rows' log-sum-exp; cu_q and cu_k as in the backward."""
+    wsb = _bytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    rc = load().cba_attention_forward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(o), _ptr(lse),
+        _ptr(workspace), wsb, _stream(stream))
+    return _checked(rc, "cba_attention_forward", check)
+
+
+def make_qk_norm_rope_desc(q, k, yq=None, yk=None, dyq=None, dyk=None, dq=None, dk=None,
+                           rot_dim=None, interleaved=False, positions=0, norm=True, eps=1e-6,
+                           param_type=CBA_F32, accumulate=0):
+    """The descriptor of a call on these tensors: [batch, len, heads, dim], or one
+    sequence [len, heads, dim], of any strides whose innermost one is 1; k (and what
+    belongs to it) may be None.  The forward takes yq and yk, the backward dyq, dyk, dq
+    and dk.  ``rot_dim`` defaults to dim, ``positions`` are the table's rows."""
+    tensors = {n: t for n, t in dict(q=q, k=k, yq=yq, yk=yk, dyq=dyq, dyk=dyk, dq=dq, dk=dk).items() if t is not None}
+    if q.dim() not in (3, 4):
+        raise ValueError("q is [batch, len, heads, dim] or [len, heads, dim]")
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]):
+        raise ValueError("q and k differ in more than their heads")
+    for name, t in tensors.items():
+        want = k if name.endswith("k") else q
+        if want is None or t.shape != want.shape or t.dtype != q.dtype or t.device != q.device:
+            raise ValueError(f"{name}: shape, type or device differs from {'k' if name.endswith('k') else 'q'}'s")
+        _check_strides(name, t)
+    d = cba_qk_norm_rope_desc_t()
+    single = q.dim() == 3
+    d.batch, d.len = (1, q.shape[0]) if single else (q.shape[0], q.shape[1])
+    d.heads_q, d.heads_k, d.dim = q.shape[-2], 0 if k is None else k.shape[-2], q.shape[-1]
+    d.type, d.param_type, d.norm = dtype_code(q.dtype), param_type, int(norm)
+    d.rot_dim = d.dim if rot_dim is None else rot_dim
+    d.interleaved, d.positions, d.accumulate, d.eps = int(interleaved), positions, int(accumulate), eps
+    for name, t in tensors.items():
+        st = _attn_strides(t, single)
+        if st is not None:
+            setattr(d, name, st)
+    return d
+
+
+def cba_qk_norm_rope_forward(desc, q, k, gamma_q, gamma_k, table, pos, yq, yk, stream=None,
+                             check=True):
+    """yq and yk: each head of q and k over its root mean square, times gamma, turned by
+    the table's row (fp32 [positions, rot_dim / 2, 2], cos and sin) of its token's pos
+    (int32 [batch, len]; None: the index in the sequence)."""
+    rc = load().cba_qk_norm_rope_forward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(table), _ptr(pos),
+        _ptr(yq), _ptr(yk), _stream(stream))
+    return _checked(rc, "cba_qk_norm_rope_forward", check)
+
+
+def cba_qk_norm_rope_workspace_bytes(desc):
+    return load().cba_qk_norm_rope_workspace_bytes(ctypes.byref(desc))
+
+
+def cba_qk_norm_rope_backward(desc, q, k, gamma_q, gamma_k, table, pos, dyq, dyk, dq, dk, dgamma_q,
+                              dgamma_k, workspace, workspace_bytes=None, stream=None, check=True):
+    """dq and dk from dyq and dyk and the forward's inputs; dgamma_q and dgamma_k (fp32
+    [dim]) written or accumulated when given."""
+    wsb = _bytes(workspace) if workspace_bytes is None else int(workspace_bytes)
+    rc = load().cba_qk_norm_rope_backward(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(gamma_q), _ptr(gamma_k), _ptr(table), _ptr(pos),
+        _ptr(dyq), _ptr(dyk), _ptr(dq), _ptr(dk), _ptr(dgamma_q), _ptr(dgamma_k), _ptr(workspace),
+        wsb, _stream(stream))
+    return _checked(rc, "cba_qk_norm_rope_backward", check)
+
+
+def make_dropout_desc(rows, cols, type=CBA_F32, p=0.1, seed=0, offset=0, ld_x=0, ld_residual=0,
+                      ld_y=0):
+    for name, v in (("seed", seed), ("offset", offset)):
+        if not 0 <= v < 1 << 64:
+            raise ValueError(f"{name} is a whole number from 0 to 2^64 - 1")
+    return cba_dropout_desc_t(rows, cols, type, p, seed, offset, ld_x, ld_residual, ld_y)
+
+
+def cba_dropout(desc, x, residual, step, y, stream=None, check=True):
+    """y = x / (1 - p) where the element's random word keeps it, 0 elsewhere, plus the
+    residual; step: None, or a device tensor of 8 bytes added to the offset."""
+    rc = load().cba_dropout(ctypes.byref(desc), _ptr(x), _ptr(residual), _ptr(step), _ptr(y),
+                            _stream(stream))
+    return _checked(rc, "cba_dropout", check)
 
 
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)

@@ -335,8 +335,8 @@ int cba_pooled_size(int in, int kernel, int stride, int pad);
 int cba_maxpool_backward(const cba_pool_desc_t *d, const float *top_diff, const int *mask,
                          float *bottom_diff, void *stream);
 
-/* ---- Operators of transformer layers: layer norm, attention, orthogonalised
- * updates ----
+/* ---- Operators of transformer layers: layer norm, attention, query and key norms
+ * with rotation, dropout, orthogonalised updates ----
  * Conventions as above: device pointers owned by the caller, stream-ordered,
  * asynchronous, no allocation, capturable; scratch from the caller's 256-byte
  * aligned workspace (two calls that share one must not overlap in time); on an
@@ -432,6 +432,99 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
                            const void *v, const void *o, const float *lse, const void *dout,
                            const int *cu_q, const int *cu_k, void *dq, void *dk, void *dv,
                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Attention's forward pass, whose o and lse the backward pass above takes: with S as
+ * there, over the allowed pairs,
+ *   lse = log sum_j exp S_ij,  o = sum_j exp(S_ij - lse) v_j
+ * The descriptor is the backward's (dout, dq, dk and dv and their strides do not count):
+ * the same types, layouts, head sharing, masks, packing and limits.  lse: NULL when not
+ * wanted.  A row that sees no key gets o = 0 and lse = -infinity.  o must not overlap
+ * the inputs; tokens outside all packed sequences, or past the bounds of the lengths,
+ * are not written.
+ *
+ * P is rounded to the elements' type for its product with v, as a share of the row's
+ * largest (f16: times a power of two); its sums, the maxima and o's are fp32.  Few rows
+ * with many keys are cut along the keys and joined in a fixed order.  In a sequence's
+ * own rows, infinities and NaN spread as in the formulas (a masked pair may still
+ * multiply its row of v by 0); another sequence's never do. */
+size_t cba_attention_forward_workspace_bytes(const cba_attention_desc_t *d);
+int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const void *k,
+                          const void *v, const int *cu_q, const int *cu_k, void *o, float *lse,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Norms of queries and keys for each head, with the rotation by position in the same
+ * pass.  For every head's elements x of q [batch][len][heads_q][dim] and of k
+ * [batch][len][heads_k][dim]:
+ *   forward   r = 1 / sqrt(mean_c x^2 + eps), n = x r, h = n gamma (norm = 0: h = x),
+ *             y = h with the pairs j < rot_dim / 2 turned: (a, b) becomes
+ *             (a cos - b sin, a sin + b cos), cos and sin = table[position][j];
+ *             a and b are the elements j and j + rot_dim / 2 (interleaved = 1: 2j and
+ *             2j + 1), those from rot_dim on stay
+ *   backward  g = dy turned back, w = g gamma, dx = r (w - n mean_c(w n)) (norm = 0:
+ *             dx = g), dgamma (= or +=) sum g n over the tokens and heads
+ * q, k and the outputs have elements of `type`; gamma_q and gamma_k [dim] of `param_type`
+ * (fp32, or the same as type: CBA_ERR_UNSUPPORTED otherwise); dgamma_q and dgamma_k [dim]
+ * are fp32.  table: fp32 [positions][rot_dim / 2][2], cos and sin.  pos: int32
+ * [batch][len], contiguous, the tokens' rows of the table; NULL: a token's index in its
+ * sequence (len <= positions, or CBA_ERR_ARG).  Values outside 0 .. positions - 1 are
+ * taken as the nearest of these.  dim: a multiple of 8 up to 256, rot_dim even.  heads_k may be 0
+ * (then k and what belongs to it are not used).
+ *
+ * Strides as of attention, in multiples of 16 bytes, bases (gamma and table too) 16-byte
+ * aligned (CBA_ERR_ALIGN); all 0: contiguous.  An output may be the input of the same
+ * strides (yq q; dq dyq or q), and must not overlap inputs otherwise. */
+typedef struct {
+    int batch, len, heads_q, heads_k, dim;
+    int type, param_type; /* cba_dtype_t */
+    int norm;             /* 1: norm and rotation, 0: rotation alone (gamma, dgamma NULL) */
+    int rot_dim, interleaved;
+    int positions;        /* rows of the table */
+    int accumulate;       /* dgamma: 0 writes, 1 adds onto its contents */
+    float eps;
+    cba_attn_strides_t q, k, yq, yk, dyq, dyk, dq, dk;
+} cba_qk_norm_rope_desc_t;
+
+/* gamma_q, gamma_k: NULL for 1.  table: may be NULL with rot_dim = 0. */
+int cba_qk_norm_rope_forward(const cba_qk_norm_rope_desc_t *d, const void *q, const void *k,
+                             const void *gamma_q, const void *gamma_k, const float *table,
+                             const int *pos, void *yq, void *yk, void *stream);
+
+/* Bytes of scratch of one backward call (0 on an invalid descriptor). */
+size_t cba_qk_norm_rope_workspace_bytes(const cba_qk_norm_rope_desc_t *d);
+
+/* q, k: the forward's inputs (norm = 0: not used).  dgamma_q, dgamma_k: NULL when not
+ * wanted.  With len = 0, dgamma becomes 0 (accumulate = 0) or stays. */
+int cba_qk_norm_rope_backward(const cba_qk_norm_rope_desc_t *d, const void *q, const void *k,
+                              const void *gamma_q, const void *gamma_k, const float *table,
+                              const int *pos, const void *dyq, const void *dyk, void *dq, void *dk,
+                              float *dgamma_q, float *dgamma_k, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Dropout whose mask is never stored, with the shortcut added.  With i = row * cols + col:
+ *   y = (word_i >= p 2^32 ? x / (1 - p) : 0) + residual
+ * word_i: word i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, 2011) with the
+ * key `seed` (low word first) and the counter offset + *step + i / 4 in its low 64 bits,
+ * modulo 2^64; p 2^32 is rounded to a whole number, and p = 1 drops all.  Dropped elements count as 0
+ * whatever they hold.  The gradient is the same call on dy without the residual.
+ * A call uses the counters from offset + *step on, (rows * cols + 3) / 4 of them: the
+ * next one starts behind them.
+ *
+ * step: NULL for 0, or DEVICE memory (8-byte aligned) read when the call runs, so that
+ * a captured call that is replayed draws anew once the program has moved it on.
+ * residual: NULL for none.  ld_*: elements from one row to the next (0: cols).  y may be x or
+ * residual (of the same ld).  Tensors without gaps between rows, or with rows and
+ * strides of 16-byte multiples, on 16-byte aligned bases move as vectors; any other
+ * element-aligned layout is correct and slower. */
+typedef struct {
+    long long rows, cols; /* rows may be 0; rows * cols up to 2^40 */
+    int type;             /* cba_dtype_t */
+    float p;              /* 0 to 1 */
+    unsigned long long seed, offset;
+    long long ld_x, ld_residual, ld_y;
+} cba_dropout_desc_t;
+
+int cba_dropout(const cba_dropout_desc_t *d, const void *x, const void *residual,
+                const unsigned long long *step, void *y, void *stream);
 
 /* Orthogonalising a matrix by Newton-Schulz products (the update of a Muon
  * optimiser, e.g. of a momentum of dW [K][C*R*S]).  For each of `batch` matrices

@@ -1,5 +1,6 @@
 """64-bit reference of the transformer-layer operators (plain numpy): layer
-norm, attention's backward pass and Newton-Schulz orthogonalisation.  Test
+norm, attention, query and key norms with rotation, dropout and Newton-Schulz
+orthogonalisation.  Test
 infrastructure only; written from the formulas, sharing nothing with the CUDA
 library, and pinned to central differences and closed forms."""
 import numpy as np
@@ -91,3 +92,68 @@ def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
             S = X.T @ X
             X = a * X + X @ (b * S + c * S @ S)
     return scale * X
+
+
+def rotate(x, table, pos, interleaved, back=False):
+    """x [tokens, heads, dim] with the pairs of its first 2 * table.shape[1] elements turned
+    by the angles of table [positions, pairs, 2] at the tokens' pos (taken into its range)."""
+    x, table = np.array(x, f8), np.asarray(table, f8)
+    n = table.shape[1]
+    row = table[np.clip(np.asarray(pos), 0, table.shape[0] - 1)][:, None]
+    cos, sin = row[..., 0], -row[..., 1] if back else row[..., 1]
+    i = np.arange(n)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+    y = x.copy()
+    y[..., a] = x[..., a] * cos - x[..., b] * sin
+    y[..., b] = x[..., a] * sin + x[..., b] * cos
+    return y
+
+
+def norm_rope_forward(x, gamma, table, pos, eps, norm=True, interleaved=False):
+    """Each head of x [tokens, heads, dim] normed, scaled and turned (table None: not)."""
+    x = np.asarray(x, f8)
+    if norm:
+        x = x / np.sqrt((x * x).sum(-1, keepdims=True) / x.shape[-1] + eps)
+        if gamma is not None:
+            x = x * np.asarray(gamma, f8)
+    return x if table is None else rotate(x, table, pos, interleaved)
+
+
+def norm_rope_backward(x, dy, gamma, table, pos, eps, norm=True, interleaved=False):
+    """(dx, dgamma); dgamma is None without the norm."""
+    x, dy = np.asarray(x, f8), np.asarray(dy, f8)
+    g = dy if table is None else rotate(dy, table, pos, interleaved, back=True)
+    if not norm:
+        return g, None
+    rms = np.sqrt((x * x).sum(-1, keepdims=True) / x.shape[-1] + eps)
+    n = x / rms
+    w = g if gamma is None else g * np.asarray(gamma, f8)
+    return (w - n * ((w * n).sum(-1, keepdims=True) / x.shape[-1])) / rms, (g * n).sum((0, 1))
+
+
+def philox(seed, counters):
+    """The four 32-bit words (uint64 [n, 4]) of Philox4x32-10 at 64-bit counters."""
+    low, u = np.uint64(0xFFFFFFFF), np.uint64
+    c = np.asarray(counters, np.uint64)
+    x = [c & low, c >> u(32), np.zeros_like(c), np.zeros_like(c)]
+    k = [seed & 0xFFFFFFFF, seed >> 32]
+    for _ in range(10):
+        p, q = x[0] * u(0xD2511F53), x[2] * u(0xCD9E8D57)
+        x = [(q >> u(32)) ^ x[1] ^ u(k[0]), q & low, (p >> u(32)) ^ x[3] ^ u(k[1]), p & low]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return np.stack(x, 1)
+
+
+def dropout_keep(shape, p, seed, offset):
+    """Which elements are kept; p as the fp32 number that it is given as."""
+    n = int(np.prod(shape))
+    counters = np.uint64(offset) + np.arange((n + 3) // 4, dtype=np.uint64)
+    words = philox(seed, counters).reshape(-1)[:n]
+    return (words >= np.uint64(np.rint(f8(np.float32(p)) * 2.0 ** 32))).reshape(shape)
+
+
+def dropout(x, p, seed, offset=0, residual=None):
+    x = np.asarray(x, f8)
+    keep = dropout_keep(x.shape, p, seed, offset)
+    scaled = np.where(keep, x, 0.0) / (1.0 - f8(np.float32(p)) if keep.any() else 1.0)
+    return scaled if residual is None else scaled + np.asarray(residual, f8)
