@@ -3,12 +3,34 @@
 //   S = scale q k^T,  m = max_j S_ij over the allowed pairs
 //   l = sum_j exp(S_ij - m),  o = sum_j exp(S_ij - m) v_j / l,  lse = m + log l
 //
-// One pass over the keys with a running maximum and sum: when the maximum grows,
-// the sums so far are scaled down.  A warp per query row, the row's elements over
-// its lanes.
+// One pass over the keys.  A block takes two tiles of 128 query rows and walks
+// their keys, 128 at a time: S of a tile by the tensor cores into TMEM, P = exp(S -
+// m) by a warpgroup, a thread per row, back into TMEM in 16 bits, o += P v by the tensor
+// cores.  While one tile's warpgroup computes P, the tensor cores have the other's
+// products.  The running maximum m lags: it is raised, and o and l scaled down, only
+// when a row's new one is past it by 2^8, so that most steps leave o alone.  (P is
+// then 2^8 at most, in f16 2^15 with its power of two: nothing overflows.)
+//
+// The rows of a tile are the query heads that share a key/value head (or as many of
+// them as fill 128 rows) by as many tokens as fit: a single token of eight such
+// heads reads its keys once.
+//
+// Blocks come from the grid in order, heaviest first where the mask makes work fall;
+// a block that is done takes over the next that has not started (cluster launch
+// control), so that its loads and first products run under the last ones of the
+// item before.  Where there are fewer pairs of tiles than SMs the keys are cut, each
+// item leaves fp32 sums, and a second kernel joins them in the order of the keys.
+//
+// Roles: warp 0 loads (TMA) and takes items, warp 1 issues the products, warps 4-7
+// and 8-11 are the two tiles' warpgroups.  Every wait is bounded (2 s); on a timeout the
+// block sets the workspace's status bit, stops, waits (bounded) for its copies in
+// flight, frees its TMEM and returns.
+#include <cuda.h>
+
 #include <algorithm>
 #include <cmath>
 
+#include "cba_attn.cuh"
 #include "cba_internal.cuh"
 #include "cba_ptx.cuh"
 #include "cba_types.cuh"
@@ -17,93 +39,604 @@ namespace cba {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kAfThreads = 384;
+constexpr int kAfWarps = 8;                    // that compute P
+// Registers per thread: 168 at launch, then moved to the two computing warpgroups, which
+// hold a row of S.
+constexpr int kAfCtlRegs = 72, kAfCompRegs = 216;
+static_assert(128 * kAfCtlRegs + 256 * kAfCompRegs <= kAfThreads * 168);
+constexpr float kLag = 8.f;                    // log2 by which m may lag behind
+constexpr float kLargeLog = 1024.f;            // |m| in log2 from which S - m is formed first
+constexpr float kHalfShift = 7.f;              // f16: P is held as 2^7 P
 
 struct AfArgs {
     const int *cu_q, *cu_k;
     int batch, hq, hkv, group, dim, len_q, len_k;
     long long total_q, total_k;
     int causal;
-    float scale;
-    const void *q, *k, *v;
+    float cs;          // |scale| / ln 2
+    int negative;      // scale < 0
+    int hp;            // heads side by side in a tile
+    int hparts;        // heads_q / hp
+    int tt;            // tokens of a tile
+    int pairs;         // of the longest sequence; with slots, all
+    int slots;         // packed with loose bounds: pairs are numbered by the tokens
+    int heads_at_once; // causal: heads (of all sequences) whose heaviest pairs come first together
+    int chunk, chunks; // steps of an item at most; items per pair at most
+    int units, items;
     void *o;
     float *lse;
-    long long sq[3], sk[3], sv[3], so[3];
+    long long so[3];
     unsigned *status;
+    float *part;       // fp32 sums of cut items: [unit][chunk][tile][DP / 4][128 rows] float4
+    float2 *ml;        // their m (in S's unit) and l: [unit][chunk][tile][128 rows]
 };
 
-template <typename T>
-__global__ void __launch_bounds__(128) attn_fwd_rows_kernel(const AfArgs a) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    const int lane = threadIdx.x & 31;
-    const long long tokens = a.cu_q ? a.total_q : (long long)a.batch * a.len_q;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= tokens * a.hq) return;
-    const int h = (int)(row / tokens);
-    const long long t = row - (long long)h * tokens;
-    // the row's sequence and index in it
-    int b, i, lq, lk;
-    long long q0 = 0, k0 = 0;
-    if (a.cu_q) {
-        int lo = 0, hi = a.batch;  // the last sequence that starts at t or before
+// One item: the keys it0 * 128 .. of a pair of tiles.
+struct AfItem {
+    long long q0, k0;    // first tokens of the sequence
+    int b, h0, hk;       // head of the tiles' first row, key/value head
+    int t0, lq, lk;      // first token of the pair, lengths
+    int it0, n, cnt[2];  // steps from it0 on, of the pair and of each tile
+    int unit, c, used;   // item c of `used`
+    int live;
+};
+static_assert(sizeof(AfItem) <= 128);
+
+// Sequence b's range of tokens; values of cu are clamped into the tensors, so that
+// wrong ones give wrong results but no access out of bounds.
+__device__ __forceinline__ void af_seq(const AfArgs &a, AfItem &w) {
+    if (a.cu_q == nullptr) {
+        w.q0 = w.k0 = 0;
+        w.lq = a.len_q, w.lk = a.len_k;
+        return;
+    }
+    const long long qa = min(max((long long)a.cu_q[w.b], 0LL), a.total_q);
+    const long long qb = min(max((long long)a.cu_q[w.b + 1], qa), a.total_q);
+    const long long ka = min(max((long long)a.cu_k[w.b], 0LL), a.total_k);
+    const long long kb = min(max((long long)a.cu_k[w.b + 1], ka), a.total_k);
+    w.q0 = qa, w.k0 = ka;
+    w.lq = (int)min(qb - qa, (long long)a.len_q);
+    w.lk = (int)min(kb - ka, (long long)a.len_k);
+}
+
+// Numbering by the tokens: pair t of sequence b has the slot cu[b] / (2 tt) + b + t.
+// The next sequence's first slot lies past its last, so there are total / (2 tt) +
+// batch at most, of which one per sequence may stand for no pair.
+__device__ __forceinline__ int af_slot(const AfArgs &a, int b) {
+    return (int)(min(max((long long)a.cu_q[b], 0LL), a.total_q) / (2 * a.tt)) + b;
+}
+
+// Item `i` of the grid.  Called by any threads, each for itself.
+__device__ __forceinline__ AfItem af_item(const AfArgs &a, int i) {
+    AfItem w;
+    w.c = i % a.chunks;
+    const int u = w.unit = i / a.chunks;
+    const int heads = a.slots ? a.hparts : a.hparts * a.batch;
+    int head, pair;
+    if (a.causal) {  // the pairs with the most keys first, a few heads at a time
+        const int block = u / (a.heads_at_once * a.pairs), first = block * a.heads_at_once;
+        const int n = min(a.heads_at_once, heads - first), r = u - first * a.pairs;
+        head = first + r % n;
+        pair = a.pairs - 1 - r / n;
+    } else {
+        pair = u % a.pairs;
+        head = u / a.pairs;
+    }
+    if (a.slots) {
+        int lo = 0, hi = a.batch;  // the last sequence whose slots begin at `pair` or before
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (a.cu_q[mid] <= t) lo = mid;
+            if (af_slot(a, mid) <= pair) lo = mid;
             else hi = mid;
         }
-        b = 0;
-        q0 = min(max((long long)a.cu_q[lo], 0LL), a.total_q);
-        const long long q1 = min(max((long long)a.cu_q[lo + 1], q0), a.total_q);
-        k0 = min(max((long long)a.cu_k[lo], 0LL), a.total_k);
-        const long long k1 = min(max((long long)a.cu_k[lo + 1], k0), a.total_k);
-        if (t < q0 || t >= q1 || t - q0 >= a.len_q) return;
-        lq = (int)min(q1 - q0, (long long)a.len_q);
-        lk = (int)min(k1 - k0, (long long)a.len_k);
-        i = (int)(t - q0);
+        w.b = lo;
+        pair -= af_slot(a, lo);
     } else {
-        b = (int)(t / a.len_q);
-        i = (int)(t - (long long)b * a.len_q);
-        lq = a.len_q, lk = a.len_k;
+        w.b = head / a.hparts;
+        head -= w.b * a.hparts;
     }
-    const int hk = h / a.group;
-    const T *q = static_cast<const T *>(a.q) + b * a.sq[0] + (q0 + i) * a.sq[1] + h * a.sq[2];
-    const T *k = static_cast<const T *>(a.k) + b * a.sk[0] + k0 * a.sk[1] + hk * a.sk[2];
-    const T *v = static_cast<const T *>(a.v) + b * a.sv[0] + k0 * a.sv[1] + hk * a.sv[2];
-    float qs[4], acc[4];
+    w.h0 = head * a.hp;
+    w.hk = w.h0 / a.group;
+    af_seq(a, w);
+    // (a slot before the first sequence's, or past a sequence's last)
+    const bool in = pair >= 0 && (long long)pair * 2 * a.tt < w.lq;
+    w.t0 = in ? pair * 2 * a.tt : 0;
+    int n[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        qs[e] = lane * 4 + e < a.dim ? to_f32(q[lane * 4 + e]) : 0.f;
-        acc[e] = 0.f;
+    for (int x = 0; x < 2; ++x) {
+        const int last = min(w.t0 + (x + 1) * a.tt, w.lq) - 1;  // the tile's last token
+        int keys = in && w.t0 + x * a.tt < w.lq ? w.lk : 0;
+        if (a.causal) keys = min(keys, max(last + w.lk - w.lq + 1, 0));
+        n[x] = (keys + kT - 1) / kT;
     }
-    const int n = a.causal ? min(lk, i + lk - lq + 1) : lk;
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < n; ++j) {
-        float s = 0.f, vs[4];
+    const int all = max(n[0], n[1]);
+    w.used = 1, w.it0 = 0, w.n = all;
+    if (a.chunks > 1) {
+        w.used = max(1, (all + a.chunk - 1) / a.chunk);
+        const int each = (all + w.used - 1) / w.used;
+        w.it0 = w.c * each;
+        w.n = min(each, all - w.it0);
+    }
+    w.live = in && w.c < w.used;
+    if (!w.live) w.n = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = lane * 4 + e < a.dim;
-            s = fmaf(qs[e], in ? to_f32(k[j * a.sk[1] + lane * 4 + e]) : 0.f, s);
-            vs[e] = in ? to_f32(v[j * a.sv[1] + lane * 4 + e]) : 0.f;
+    for (int x = 0; x < 2; ++x) w.cnt[x] = min(max(n[x] - w.it0, 0), w.n);
+    return w;
+}
+
+template <int DP>
+struct Af {
+    static constexpr int ST = DP == 64 ? 8 : 4;  // tiles of the ring of keys and values
+    static constexpr uint32_t TILE = DP / 64 * kBoxBytes;
+    static constexpr uint32_t STAGE = kAfWarps * 2048;
+    static constexpr uint32_t RING = 2 * TILE, OUT = RING + ST * TILE, BARS = OUT + STAGE;
+    struct Bars {
+        uint64_t q_full[2], q_empty[2];
+        uint64_t kv_full[ST], kv_empty[ST];
+        uint64_t s_full[2], p_ready[2], acc[2];
+        uint64_t i_full[2], i_empty[2];
+        uint64_t fix, drain, clc;
+        uint32_t tmem_base;
+        int abort_flag;
+    };
+    // and the items, and the answer of the launch control
+    static constexpr uint32_t ITEMS = (BARS + sizeof(Bars) + 15) / 16 * 16, CLC = ITEMS + 2 * 128, SMEM = CLC + 16;
+};
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kAfThreads, 1)
+    attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                    const __grid_constant__ CUtensorMap tv, const AfArgs a) {
+    using A = Af<DP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    constexpr uint32_t TILE = A::TILE;
+    constexpr int ST = A::ST;
+    const uint32_t sbase = ptx::smem_u32(smem), sQ = sbase, sKV = sbase + A::RING;
+    auto &sb = *reinterpret_cast<typename A::Bars *>(smem + A::BARS);
+    AfItem *slots = reinterpret_cast<AfItem *>(smem + A::ITEMS);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && tid == 0) *a.status = 0;  // (a timeout takes two seconds more)
+    if (sbase & 1023) {  // the swizzled tiles need it
+        if (tid == 0) atomicOr(a.status, kStatusTimeout);
+        return;
+    }
+    if (tid == 0) {
+        at_init_bars(sb.q_full, 4, 1);
+        at_init_bars(sb.kv_full, 2 * ST, 1);
+        at_init_bars(sb.s_full, 2, 1);
+        at_init_bars(sb.p_ready, 2, kAfWarps / 2);
+        at_init_bars(sb.acc, 2, 1);
+        at_init_bars(sb.i_full, 2, 1);
+        at_init_bars(sb.i_empty, 2, 1 + kAfWarps);
+        at_init_bars(&sb.fix, 3, 1);
+        sb.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::griddep_launch_dependents();
+    const uint32_t tmem = sb.tmem_base;
+    // S of the two tiles (P over its first half), then o of the two
+    const uint32_t tS = tmem, tO = tmem + 256;
+    volatile int *ab = &sb.abort_flag;
+    const bool packed = a.cu_q != nullptr;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
+        return ok = __all_sync(0xffffffffu, ok) != 0;
+    };
+    // the k-th item handed out, NULL past the last (or on a timeout)
+    auto take = [&](int k) -> const AfItem * {
+        return wait(&sb.i_full[k & 1], (uint32_t)(k / 2)) && slots[k & 1].live ? slots + (k & 1) : nullptr;
+    };
+    auto done = [&](int k) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.i_empty[k & 1]));
+    };
+
+    if (warp < 4) {
+        ptx::regs_dec<kAfCtlRegs>();
+        if (warp == 0) {
+            uint32_t fphase = 0;
+            const uint32_t bfix = ptx::smem_u32(&sb.fix), bclc = ptx::smem_u32(&sb.clc), answer = sbase + A::CLC;
+            int kv = 0, nq[2] = {0, 0}, asked = 0, k = 0;
+            auto hand_out = [&](const AfItem &w) {
+                if (k >= 2 && !wait(&sb.i_empty[k & 1], (uint32_t)(k / 2 - 1))) return;
+                if (lane == 0) {
+                    slots[k & 1] = w;
+                    ptx::mbar_arrive(ptx::smem_u32(&sb.i_full[k & 1]));
+                }
+                __syncwarp();
+                ++k;
+            };
+            auto load_kv = [&](const CUtensorMap *tm, const AfItem &w, int key, bool fix) {
+                const int st = kv % ST;
+                if (kv >= ST && !wait(&sb.kv_empty[st], (uint32_t)(kv / ST - 1))) return;
+                ++kv;
+                ok = load_tile<DP>(sKV + st * TILE, tm, w.k0 + key, w.hk, packed ? 0 : w.b, fix ? w.lk - key : kT, packed,
+                                   ptx::smem_u32(&sb.kv_full[st]), bfix, fphase, ab, a.status);
+            };
+            for (int i = (int)blockIdx.x; ok && i >= 0;) {
+                const AfItem w = af_item(a, i);
+                if (w.live) {
+                    hand_out(w);
+                    for (int x = 0; ok && x < 2; ++x) {
+                        if (w.cnt[x] == 0) continue;
+                        if (nq[x] > 0 && !wait(&sb.q_empty[x], (uint32_t)(nq[x] - 1))) break;
+                        ++nq[x];
+                        if (lane == 0) {
+                            const uint32_t bar = ptx::smem_u32(&sb.q_full[x]);
+                            ptx::mbar_arrive_expect_tx(bar, DP / 64 * a.hp * a.tt * 128);
+#pragma unroll
+                            for (int j = 0; j < DP / 64; ++j)
+                                ptx::tma_load_4d(sQ + x * TILE + j * kBoxBytes, &tq, j * 64, w.h0, (int)(w.q0 + w.t0 + x * a.tt),
+                                                 packed ? 0 : w.b, bar);
+                        }
+                        __syncwarp();
+                        // the second tile is not needed before the first's keys
+                        if (x == 0) load_kv(&tk, w, w.it0 * kT, false);
+                    }
+                    if (w.cnt[0] == 0 && w.n > 0) load_kv(&tk, w, w.it0 * kT, false);
+                    for (int it = 0; ok && it < w.n; ++it) {
+                        const int key = (w.it0 + it) * kT;
+                        if (it > 0) load_kv(&tk, w, key, false);
+                        // (rows past the sequence: of k masked, of v multiplied by P = 0)
+                        if (ok) load_kv(&tv, w, key, true);
+                    }
+                }
+                if (!ok) break;
+                // the next item, once this one's loads have begun: earlier, and the items
+                // would be dealt out before it is known who is done first
+                if (lane == 0) {
+                    ptx::fence_proxy_async_smem();
+                    ptx::mbar_arrive_expect_tx(bclc, 16);
+                    ptx::try_cancel_block(answer, bclc);
+                }
+                __syncwarp();
+                if (!wait(&sb.clc, (uint32_t)asked++)) break;
+                i = ptx::cancelled_block(answer);
+                __syncwarp();
+            }
+            if (ok) {
+                AfItem end{};
+                hand_out(end);
+            }
+            if (!ok) {
+                drain_ring(sb.q_full, 1, nq[0], a.status);
+                drain_ring(sb.q_full + 1, 1, nq[1], a.status);
+                drain_ring(sb.kv_full, ST, kv, a.status);
+                drain_ring(&sb.clc, 1, asked, a.status);
+            }
+        } else if (warp == 1) {
+            // The whole warp walks the loop and one elected lane issues.
+            constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
+            const int steps = (a.dim + 15) / 16;
+            const uint32_t id_o = ptx::idesc_f16(128, steps * 16, BF16, true);
+            Ring rk, rv;       // the ring's stage of the next keys, of the next values
+            rv.step(ST);
+            int gq[2] = {0, 0}, gp[2] = {0, 0};  // queries, P so far
+            auto two = [&](Ring &r) { r.step(ST), r.step(ST); };
+            auto full = [&](Ring r) { return AtWait{&sb.kv_full[r.s], r.ph}; };
+            auto both = [&](AtWait x, AtWait y) { return ok = ok && wait_both(x, y, ab, a.status); };
+            // S of tile x with the keys at rk; `free`: their last use; `last`: the queries' too
+            auto mma_s = [&](int x, bool free, bool last) {
+                const ptx::Desc dq = ptx::desc_of(sQ + x * TILE, 16, 1024, 2), dk = ptx::desc_of(sKV + rk.s * TILE, 16, 1024, 2);
+                if (ptx::elect_one()) {
+                    auto step = [&](int ks) {
+                        const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
+                        ptx::mma_f16(tS + x * 128, dq, off, dk, off, id_s, ks > 0);
+                    };
+                    if (steps == DP / 16) {  // a condition in each step doubles its issue time
+#pragma unroll
+                        for (int ks = 0; ks < DP / 16; ++ks) step(ks);
+                    } else {
+                        for (int ks = 0; ks < steps; ++ks) step(ks);
+                    }
+                    ptx::mma_commit(ptx::smem_u32(&sb.s_full[x]));
+                    if (free) ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[rk.s]));
+                    if (last) ptx::mma_commit(ptx::smem_u32(&sb.q_empty[x]));
+                }
+                __syncwarp();
+            };
+            auto mma_o = [&](int x, bool first, bool free, bool last) {
+                const ptx::Desc dv = ptx::desc_of(sKV + rv.s * TILE, kBoxBytes, 1024, 2);
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < kT / 16; ++ks)
+                        ptx::mma_f16_ts(tO + x * DP, tS + x * 128 + ks * 8, dv, ks * (2048 >> 4), id_o, !first || ks > 0);
+                    if (free) ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[rv.s]));
+                    if (last) ptx::mma_commit(ptx::smem_u32(&sb.acc[x]));
+                }
+                __syncwarp();
+            };
+            const AfItem *w;
+            for (int k = 0; (w = take(k)) != nullptr; ++k) {
+                const int n = w->n, cnt[2] = {w->cnt[0], w->cnt[1]};
+                done(k);
+                if (n == 0) continue;
+                // a step's last user of its keys and values is the second tile, if it has the step
+                auto frees = [&](int x, int it) { return x == 1 || it >= cnt[1]; };
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (cnt[x] > 0) {
+                        if (!both({&sb.q_full[x], (uint32_t)gq[x]}, full(rk))) break;
+                        ++gq[x];
+                        mma_s(x, frees(x, 0), cnt[x] == 1);
+                    }
+                if (!ok) break;
+                two(rk);
+                for (int it = 0; ok && it < n; ++it) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (it >= cnt[x]) continue;
+                        const bool more = it + 1 < cnt[x];
+                        if (!both({&sb.p_ready[x], (uint32_t)gp[x]}, full(rv))) break;
+                        ++gp[x];
+                        mma_o(x, it == 0, frees(x, it), !more);
+                        if (more) {
+                            // S overwrites P: this warp's products run in the order of issue
+                            if (!both(full(rk), full(rk))) break;
+                            mma_s(x, frees(x, it + 1), it + 2 == cnt[x]);
+                        }
+                    }
+                    two(rv);
+                    if (it + 1 < n) two(rk);
+                }
+                if (!ok) break;
+            }
+            // every product issued has finished before TMEM is released
+            if (ptx::elect_one()) {
+                if (!ok) *const_cast<volatile int *>(&sb.abort_flag) = 1;
+                ptx::mma_commit(ptx::smem_u32(&sb.drain));
+            }
+            __syncwarp();
+            int no = 0;
+            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kAtLimitNs);
+            __syncwarp();
         }
+    } else {
+        ptx::regs_inc<kAfCompRegs>();
+        const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tS + x * 128 + lanes, to = tO + x * DP + lanes;
+        constexpr float shift = BF16 ? 0.f : kHalfShift;
+        const float cs = a.cs;
+        const float2 cs2 = make_float2(cs, cs);
+        // this thread's row: token and head in its tile
+        const int tok = r / a.hp, hd = r - tok * a.hp;
+        uint8_t *stage = smem + A::OUT + (warp - 4) * 2048;
+        int gs = 0, ga = 0;
+        const AfItem *wp;
+        for (int k = 0; (wp = take(k)) != nullptr; ++k) {
+            const volatile AfItem &w = *wp;  // read where it is used: the registers hold a row of S
+            const int cnt = w.cnt[x];
+            // counted from the item's first step: the row sees the keys before `sees`; steps
+            // that end by `all` need no mask
+            int sees, all;
+            {
+                const int it0 = w.it0 * kT, first = w.t0 + x * a.tt, diag = w.lk - w.lq + 1 - it0;
+                sees = all = w.lk - it0;
+                if (a.causal) sees = min(sees, first + tok + diag), all = min(all, first + diag);
+            }
+            float m = -INFINITY;  // in S's unit
+            float2 l0 = make_float2(0.f, 0.f), l1 = l0;
+            for (int it = 0; it < cnt; ++it) {
+                if (!wait(&sb.s_full[x], (uint32_t)gs)) break;
+                ++gs;
+                ptx::tc_fence_after();
+                float s[4][32];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.scale;
-        const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top;
-        const float was = expf(m - ref), p = expf(s - ref);
-        l = l * was + p;
+                for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + c * 32, s[c]);
+                ptx::tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = acc[e] * was + p * vs[e];
-        m = top;
+                for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c >> 5][c & 31]));  // used behind the wait
+                if (a.negative) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c >> 5][c & 31] = -s[c >> 5][c & 31];
+                }
+                if (it * kT + kT > all) {
+                    const int lim = sees - it * kT;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= lim) s[c >> 5][c & 31] = -INFINITY;
+                }
+                float top[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    top[c] = s[c][0];
+#pragma unroll
+                    for (int e = 1; e < 31; e += 2) top[c] = fmaxf(fmaxf(top[c], s[c][e]), s[c][e + 1]);
+                    top[c] = fmaxf(top[c], s[c][31]);
+                }
+                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // (-inf - -inf and inf - inf are NaN, which raises nothing)
+                if (__any_sync(0xffffffffu, (now - m) * cs > kLag)) {
+                    const float up = fmaxf(m, now);
+                    const float f = up == -INFINITY ? 1.f : ptx::ex2((m - up) * cs);
+                    m = up;
+                    l0 = ptx::mul2(l0, make_float2(f, f));
+                    l1 = ptx::mul2(l1, make_float2(f, f));
+                    if (it > 0) {  // (the product before S has finished with it)
+#pragma unroll
+                        for (int c = 0; c < DP; c += 32) {
+                            float v[32];
+                            ptx::tmem_ld32(to + c, v);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                asm volatile("" : "+f"(v[e]));
+                                v[e] *= f;
+                            }
+                            ptx::tmem_st32(to + c, v);
+                        }
+                        ptx::tmem_st_wait();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+                float nm = shift - ref * cs;
+                // S cs - m cs in one rounding, off by 2^-24 of m cs: of large ones the difference first
+                if (__any_sync(0xffffffffu, fabsf(nm) > kLargeLog)) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c >> 5][c & 31] -= ref;
+                    nm = shift;
+                }
+                const float2 nm2 = make_float2(nm, nm);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 v = ptx::fma2(make_float2(s[c][2 * e], s[c][2 * e + 1]), cs2, nm2);
+                        v = make_float2(ptx::ex2(v.x), ptx::ex2(v.y));
+                        if (e & 1) l1 = ptx::add2(l1, v);
+                        else l0 = ptx::add2(l0, v);
+                        p[e] = pack2<BF16>(v.x, v.y);
+                    }
+                    ptx::tmem_st16(ts + c * 16, p);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[x]));
+            }
+            if (!ok || (cnt > 0 && !wait(&sb.acc[x], (uint32_t)ga))) break;
+            if (cnt > 0) ++ga;
+            ptx::tc_fence_after();
+            const int t = w.t0 + x * a.tt + tok;
+            const bool row = tok < a.tt && t < w.lq;
+            const float l = (l0.x + l0.y) + (l1.x + l1.y);
+            const bool none = l == 0.f;  // no key, or all of them at -infinity
+            if (w.used > 1) {
+                const long long slot = ((long long)w.unit * a.chunks + w.c) * 2 + x;
+                a.ml[slot * kT + r] = make_float2(m, l);
+                if (cnt > 0) {
+                    float4 *at = reinterpret_cast<float4 *>(a.part) + slot * (DP / 4) * kT + r;
+#pragma unroll
+                    for (int c = 0; c < DP; c += 32) {
+                        float v[32];
+                        ptx::tmem_ld32(to + c, v);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) asm volatile("" : "+f"(v[e]));
+                        if (row)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                __stcg(at + (c + e) / 4 * kT, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                        __syncwarp();
+                    }
+                }
+                ptx::tc_fence_before();
+                done(k);
+                continue;
+            }
+            if (row && a.lse)
+                a.lse[packed ? (long long)(w.h0 + hd) * a.total_q + w.q0 + t
+                             : ((long long)w.b * a.hq + w.h0 + hd) * a.len_q + t] =
+                    none ? -INFINITY : fmaf(m, cs, __log2f(l) - shift) * kLn2;
+            // 32 columns at a time through 2 KB of the warp's own (row = lane, its 16-byte chunk j
+            // at j ^ ((row >> 1) & 3)); then four lanes store a row's 64 bytes
+            const float inv = none ? 0.f : 1.f / l;
+            uint16_t *out = static_cast<uint16_t *>(a.o) + w.b * a.so[0];
+            long long at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = quarter * 32 + i * 8 + (lane >> 2), tk2 = rr / a.hp, tt = w.t0 + x * a.tt + tk2;
+                at[i] = tk2 < a.tt && tt < w.lq ? (w.q0 + tt) * a.so[1] + (w.h0 + rr - tk2 * a.hp) * a.so[2] : -1;
+            }
+#pragma unroll
+            for (int c = 0; c < DP; c += 32) {
+                float v[32];
+                if (cnt > 0) {
+                    ptx::tmem_ld32(to + c, v);
+                    ptx::tmem_ld_wait();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    asm volatile("" : "+f"(v[e]));
+                    v[e] = none ? 0.f : v[e] * inv;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint4 u;
+                    u.x = pack2<BF16>(v[8 * j], v[8 * j + 1]);
+                    u.y = pack2<BF16>(v[8 * j + 2], v[8 * j + 3]);
+                    u.z = pack2<BF16>(v[8 * j + 4], v[8 * j + 5]);
+                    u.w = pack2<BF16>(v[8 * j + 6], v[8 * j + 7]);
+                    *reinterpret_cast<uint4 *>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = u;
+                }
+                __syncwarp();
+                const int j = lane & 3;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = i * 8 + (lane >> 2);
+                    if (at[i] >= 0 && c + j * 8 < a.dim)
+                        *reinterpret_cast<uint4 *>(out + at[i] + c + j * 8) =
+                            *reinterpret_cast<const uint4 *>(stage + rr * 64 + ((j ^ ((rr >> 1) & 3)) << 4));
+                }
+                __syncwarp();
+            }
+            ptx::tc_fence_before();
+            done(k);
+        }
     }
-    T *o = static_cast<T *>(a.o) + b * a.so[0] + (q0 + i) * a.so[1] + h * a.so[2];
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the items of a tile that was cut: weights exp(m_i - max m), in the items' order.
+// A block per tile, a thread per row and 8 columns.
+template <bool BF16>
+__global__ void __launch_bounds__(256) attn_fwd_join_kernel(const AfArgs a, int dp) {
+    const int unit = blockIdx.x >> 1, x = blockIdx.x & 1;
+    AfItem w = af_item(a, unit * a.chunks);
+    ptx::griddep_wait();
+    if (!w.live || w.used == 1) return;
+    constexpr float shift = BF16 ? 0.f : kHalfShift;
+    const int first = w.t0 + x * a.tt, rows = max(0, min(a.tt, w.lq - first)) * a.hp, cols = a.dim / 8;
+    for (int i = threadIdx.x; i < rows * cols; i += 256) {
+        const int r = i % rows, c = i / rows;
+        float m = -INFINITY;
+        const long long slot0 = (long long)unit * a.chunks * 2 + x;
+        for (int j = 0; j < w.used; ++j) m = fmaxf(m, __ldcg(a.ml + (slot0 + 2 * j) * kT + r).x);
+        float l = 0.f, v[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (lane * 4 + e < a.dim) o[lane * 4 + e] = from_f32<T>(l == 0.f ? 0.f : acc[e] * inv);
-    if (lane == 0 && a.lse)
-        a.lse[a.cu_q ? (long long)h * a.total_q + t : ((long long)b * a.hq + h) * a.len_q + i] =
-            l == 0.f ? -INFINITY : m + logf(l);
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        for (int j = 0; j < w.used; ++j) {
+            const long long slot = slot0 + 2 * j;
+            const float2 ml = __ldcg(a.ml + slot * kT + r);
+            if (ml.y == 0.f) continue;  // none of its keys: its sums may not have been written
+            const float f = ptx::ex2((ml.x - m) * a.cs);
+            l = fmaf(f, ml.y, l);
+            const float4 *at = reinterpret_cast<const float4 *>(a.part) + (slot * (dp / 4) + 2 * c) * kT + r;
+            const float4 y = __ldcg(at), z = __ldcg(at + kT);
+            v[0] = fmaf(f, y.x, v[0]), v[1] = fmaf(f, y.y, v[1]), v[2] = fmaf(f, y.z, v[2]), v[3] = fmaf(f, y.w, v[3]);
+            v[4] = fmaf(f, z.x, v[4]), v[5] = fmaf(f, z.y, v[5]), v[6] = fmaf(f, z.z, v[6]), v[7] = fmaf(f, z.w, v[7]);
+        }
+        const bool none = l == 0.f;
+        const float inv = none ? 0.f : 1.f / l;
+        const int tok = r / a.hp, h = w.h0 + r - tok * a.hp;
+        const long long t = first + tok;
+        uint4 u;
+        u.x = pack2<BF16>(v[0] * inv, v[1] * inv);
+        u.y = pack2<BF16>(v[2] * inv, v[3] * inv);
+        u.z = pack2<BF16>(v[4] * inv, v[5] * inv);
+        u.w = pack2<BF16>(v[6] * inv, v[7] * inv);
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + w.b * a.so[0] + (w.q0 + t) * a.so[1] + h * a.so[2] + c * 8) = u;
+        if (c == 0 && a.lse)
+            a.lse[a.cu_q ? (long long)h * a.total_q + w.q0 + t : ((long long)w.b * a.hq + h) * a.len_q + t] =
+                none ? -INFINITY : fmaf(m, a.cs, __log2f(l) - shift) * kLn2;
+    }
 }
 
 // ---- host side
@@ -139,12 +672,103 @@ int check_desc(const cba_attention_desc_t *d) {
     return CBA_OK;
 }
 
-// The strides that the kernels use; packed sequences have none from one to the next.
-void fill_strides(const cba_attention_desc_t &d, const cba_attn_strides_t &s, int heads, long long len, long long *out) {
-    const bool none = !s.batch && !s.token && !s.head;
-    out[0] = d.packed ? 0 : none ? len * heads * d.dim : s.batch;
-    out[1] = none ? (long long)heads * d.dim : s.token;
-    out[2] = none ? d.dim : s.head;
+// Packed: pairs are counted by the tokens where counting up to the bounds would look at
+// more than this many times as many.
+constexpr long long kLoose = 2;
+
+struct AfPlan {
+    int dp, hp, hparts, tt, pairs, slots, heads_at_once, chunk, chunks, units;
+    size_t off_ml, off_part, total;
+};
+
+// The heads side by side in a tile: the most of a group that leave no more than 8 of its
+// 128 rows empty.
+int heads_in_tile(int group) {
+    for (int d = std::min(group, kT); d > 1; --d)
+        if (group % d == 0 && kT / d * d >= kT - 8) return d;
+    return 1;
+}
+
+// Steps of an item at most, for `units` pairs of `n` steps, `all` of them together, that are
+// equally long (even) or of any lengths up to that.  A step, a begun item and a joined one are
+// taken to cost 1, 1.5 and a quarter, and the second kernel 3.
+int plan_chunk(double units, int n, double all, bool even) {
+    int best = n;
+    double least = 0;
+    for (int k = 1; k <= std::min(64, (n + 3) / 4); ++k) {
+        const int c = (n + k - 1) / k;
+        const double rounds = std::ceil(units * k / kNumSMs);
+        const double t = (even ? rounds * (c + 1.5) : std::max(all / kNumSMs + 0.7 * c, (double)c) + 1.5 * rounds) +
+                         (k > 1 ? 3 + 0.25 * k : 0);
+        if (k == 1 || t < least) best = c, least = t;
+    }
+    return best;
+}
+
+int check_attn(const cba_attention_desc_t *d, AfPlan *p) {
+    const int rc = check_desc(d);
+    if (rc != CBA_OK) return rc;
+    p->dp = d->dim <= 64 ? 64 : 128;
+    p->hp = heads_in_tile(d->heads_q / d->heads_kv);
+    p->hparts = d->heads_q / p->hp;
+    p->tt = kT / p->hp;
+    const long long len_q = d->packed ? std::min((long long)d->len_q, d->total_q) : d->len_q;
+    const long long len_k = d->packed ? std::min((long long)d->len_k, d->total_k) : d->len_k;
+    const long long two = 2 * p->tt;
+    long long pairs = (len_q + two - 1) / two, units = pairs * d->batch * p->hparts;
+    p->slots = 0;
+    if (d->packed) {
+        const long long by_tokens = d->total_q / two + d->batch;
+        if (pairs * d->batch > kLoose * by_tokens) p->slots = 1, pairs = by_tokens, units = pairs * p->hparts;
+    }
+    if (units >= (1LL << 24)) return CBA_ERR_UNSUPPORTED;
+    p->pairs = (int)pairs;
+    p->units = (int)units;
+    // keys and values of the heads that are worked on together stay in the L2
+    const double bytes = 4.0 * std::max(1LL, len_k) * d->dim;
+    p->heads_at_once = (int)std::min((double)p->hparts * d->batch, std::max(16.0, 48e6 / bytes));
+    p->chunk = std::max(1, (int)((len_k + kT - 1) / kT));
+    p->chunks = 1;
+    if (units > 0 && units < 2 * kNumSMs && p->chunk > 4) {
+        const int n = p->chunk;
+        const bool even = !d->packed && (!d->causal || len_q <= two);
+        p->chunk = plan_chunk((double)units, n, (double)units * n * (d->causal && !even ? 0.5 : 1.0), even);
+        p->chunks = (n + p->chunk - 1) / p->chunk;
+    }
+    const size_t tiles = p->chunks > 1 ? (size_t)p->units * p->chunks * 2 : 0;
+    p->off_ml = 256;
+    p->off_part = p->off_ml + tiles * kT * sizeof(float2);
+    p->total = p->off_part + tiles * kT * p->dp * sizeof(float);
+    return CBA_OK;
+}
+
+// The map of k or v: (dim, token, head, batch), boxes of 128 tokens x 64; of q: (dim, head,
+// token, batch), boxes of a tile's tokens x heads x 64.
+bool af_map(CUtensorMap *m, const void *base, const cba_attention_desc_t &d, int heads, long long tokens, const long long *st,
+            const AfPlan *q) {
+    uint64_t dims[4] = {(uint64_t)d.dim, (uint64_t)tokens, (uint64_t)heads, (uint64_t)(d.packed ? 1 : d.batch)};
+    uint64_t strides[3] = {(uint64_t)st[1] * 2, (uint64_t)st[2] * 2, (uint64_t)st[0] * 2};
+    uint32_t box[4] = {64, kT, 1, 1};
+    if (q) {
+        std::swap(dims[1], dims[2]);
+        std::swap(strides[0], strides[1]);
+        box[1] = (uint32_t)q->hp;
+        box[2] = (uint32_t)q->tt;
+    }
+    for (int i = 0; i < 3; ++i)  // an axis of one index has no stride of its own
+        if (dims[i + 1] == 1) strides[i] = 16;
+    return tma_encode_16(m, base, d.type == CBA_BF16, 4, dims, strides, box);
+}
+
+template <int DP, bool BF16>
+cudaError_t af_launch(const AfPlan &p, const AfArgs &a, const CUtensorMap *tm, cudaStream_t st) {
+    cudaError_t e = allow_smem<attn_fwd_kernel<DP, BF16>>((int)Af<DP>::SMEM);
+    if (e != cudaSuccess) return e;
+    attn_fwd_kernel<DP, BF16><<<(unsigned)std::max(1, a.items), kAfThreads, Af<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && p.chunks > 1)
+        e = launch_pdl(attn_fwd_join_kernel<BF16>, dim3((unsigned)p.units * 2), dim3(256), 0, st, a, DP);
+    return e;
 }
 
 }  // namespace
@@ -156,13 +780,15 @@ using namespace cba;
 extern "C" {
 
 size_t cba_attention_forward_workspace_bytes(const cba_attention_desc_t *d) {
-    return check_desc(d) == CBA_OK ? 256 : 0;
+    AfPlan p;
+    return check_attn(d, &p) == CBA_OK ? p.total : 0;
 }
 
 int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const void *k, const void *v,
                           const int *cu_q, const int *cu_k, void *o, float *lse, void *workspace,
                           size_t workspace_bytes, void *stream) {
-    const int rc = check_desc(d);
+    AfPlan p;
+    const int rc = check_attn(d, &p);
     if (rc != CBA_OK) return rc;
     const long long tq = d->packed ? d->total_q : d->len_q, tk = d->packed ? d->total_k : d->len_k;
     if (tq > 0 && (!q || !o)) return CBA_ERR_ARG;
@@ -172,29 +798,44 @@ int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const vo
     for (const void *x : ptrs)
         if (!aligned_to(x, 16)) return CBA_ERR_ALIGN;
     if (!aligned_to(lse, 4) || !aligned_to(cu_q, 4) || !aligned_to(cu_k, 4)) return CBA_ERR_ALIGN;
-    if (!workspace || workspace_bytes < cba_attention_forward_workspace_bytes(d)) return CBA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < p.total) return CBA_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return CBA_ERR_ALIGN;
+
     AfArgs a{};
     a.cu_q = cu_q; a.cu_k = cu_k;
     a.batch = d->batch; a.hq = d->heads_q; a.hkv = d->heads_kv; a.group = d->heads_q / d->heads_kv;
     a.dim = d->dim; a.len_q = d->len_q; a.len_k = d->len_k;
     a.total_q = d->total_q; a.total_k = d->total_k;
-    a.causal = d->causal; a.scale = d->scale;
-    a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
+    a.causal = d->causal;
+    // S is negated for a negative scale, so that its largest is the exponent's; a scale of 0 becomes one whose
+    // products with fp32 logits of size vanish, and with the masked -infinity do not become NaN
+    a.cs = d->scale == 0.f ? 1e-37f : std::fabs(d->scale) * kLog2e;
+    a.negative = d->scale < 0.f;
+    a.hp = p.hp; a.hparts = p.hparts; a.tt = p.tt; a.pairs = p.pairs; a.slots = p.slots;
+    a.heads_at_once = p.heads_at_once; a.chunk = p.chunk; a.chunks = p.chunks;
+    a.units = p.units; a.items = p.units * p.chunks;
+    a.o = o; a.lse = lse;
     a.status = static_cast<unsigned *>(workspace);
-    fill_strides(*d, d->q, d->heads_q, tq, a.sq);
-    fill_strides(*d, d->k, d->heads_kv, tk, a.sk);
-    fill_strides(*d, d->v, d->heads_kv, tk, a.sv);
+    a.ml = ws_at<float2>(workspace, p.off_ml);
+    a.part = ws_at<float>(workspace, p.off_part);
+    long long sq[3], sk[3], sv[3];
+    fill_strides(*d, d->q, d->heads_q, tq, sq);
+    fill_strides(*d, d->k, d->heads_kv, tk, sk);
+    fill_strides(*d, d->v, d->heads_kv, tk, sv);
     fill_strides(*d, d->o, d->heads_q, tq, a.so);
+    // without queries (or keys) the kernel loads nothing of them
+    CUtensorMap tm[3] = {};
+    if (tq > 0 && tk > 0 &&
+        (!af_map(&tm[0], q, *d, d->heads_q, tq, sq, &p) || !af_map(&tm[1], k, *d, d->heads_kv, tk, sk, nullptr) ||
+         !af_map(&tm[2], v, *d, d->heads_kv, tk, sv, nullptr)))
+        return CBA_ERR_UNSUPPORTED;
     cudaGetLastError();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = select_device_of(workspace);
     if (e == cudaSuccess) {
-        const long long rows = (d->packed ? tq : tq * d->batch) * d->heads_q;
-        const unsigned grid = (unsigned)std::max(1LL, (rows + 3) / 4);
-        if (d->type == CBA_BF16) attn_fwd_rows_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
-        else attn_fwd_rows_kernel<__half><<<grid, 128, 0, st>>>(a);
-        e = cudaGetLastError();
+        const bool bf = d->type == CBA_BF16;
+        if (p.dp == 64) e = bf ? af_launch<64, true>(p, a, tm, st) : af_launch<64, false>(p, a, tm, st);
+        else e = bf ? af_launch<128, true>(p, a, tm, st) : af_launch<128, false>(p, a, tm, st);
     }
     return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
 }

@@ -516,6 +516,32 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *tmap,
         : "memory");
 }
 
+// ---- cluster launch control: a running block takes over one that has not started
+
+// Asks for the next block of the grid that has not been launched; the 16-byte answer
+// arrives at `dst` (shared memory) and is counted on `bar`.  Not to be asked again
+// once an answer was "none".
+__device__ __forceinline__ void try_cancel_block(uint32_t dst, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+        "r"(bar)
+        : "memory");
+}
+// The x index of the block that an answer hands over, or -1 for none.
+__device__ __forceinline__ int cancelled_block(uint32_t src) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return got ? (int)x : -1;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
