@@ -175,7 +175,7 @@ struct Af {
     struct Bars {
         uint64_t q_full[2], q_empty[2];
         uint64_t kv_full[ST], kv_empty[ST];
-        uint64_t s_full[2], p_ready[2], acc[2];
+        uint64_t s_full[2], p_ready[4], acc[2];  // (P in halves)
         uint64_t i_full[2], i_empty[2];
         uint64_t fix, drain, clc;
         uint32_t tmem_base;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         at_init_bars(sb.q_full, 4, 1);
         at_init_bars(sb.kv_full, 2 * ST, 1);
         at_init_bars(sb.s_full, 2, 1);
-        at_init_bars(sb.p_ready, 2, kAfWarps / 2);
+        at_init_bars(sb.p_ready, 4, kAfWarps / 2);
         at_init_bars(sb.acc, 2, 1);
         at_init_bars(sb.i_full, 2, 1);
         at_init_bars(sb.i_empty, 2, 1 + kAfWarps);
@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             }
         } else if (warp == 1) {
             // The whole warp walks the loop and one elected lane issues.
-            constexpr uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false);
+            // (a negative scale negates q in the product, so that S's largest is the exponent's)
+            const uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false) | (a.negative ? ptx::kNegateA : 0u);
             const int steps = (a.dim + 15) / 16;
             const uint32_t id_o = ptx::idesc_f16(128, steps * 16, BF16, true);
             Ring rk, rv;       // the ring's stage of the next keys, of the next values
@@ -345,12 +346,12 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 }
                 __syncwarp();
             };
-            auto mma_o = [&](int x, bool first, bool free, bool last) {
-                const ptx::Desc dv = ptx::desc_of(sKV + rv.s * TILE, kBoxBytes, 1024, 2);
+            auto mma_o = [&](int x, int half, bool first, bool free, bool last) {
+                const ptx::Desc dv = ptx::desc_of(sKV + rv.s * TILE + half * (kT / 2 * 128), kBoxBytes, 1024, 2);
                 if (ptx::elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < kT / 16; ++ks)
-                        ptx::mma_f16_ts(tO + x * DP, tS + x * 128 + ks * 8, dv, ks * (2048 >> 4), id_o, !first || ks > 0);
+                    for (int ks = 0; ks < kT / 32; ++ks)
+                        ptx::mma_f16_ts(tO + x * DP, tS + x * 128 + half * 32 + ks * 8, dv, ks * (2048 >> 4), id_o, !first || ks > 0);
                     if (free) ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[rv.s]));
                     if (last) ptx::mma_commit(ptx::smem_u32(&sb.acc[x]));
                 }
@@ -377,14 +378,14 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     for (int x = 0; x < 2; ++x) {
                         if (it >= cnt[x]) continue;
                         const bool more = it + 1 < cnt[x];
-                        if (!both({&sb.p_ready[x], (uint32_t)gp[x]}, full(rv))) break;
+                        if (!both({&sb.p_ready[2 * x], (uint32_t)gp[x]}, full(rv))) break;
+                        mma_o(x, 0, it == 0, false, false);
+                        const AtWait second{&sb.p_ready[2 * x + 1], (uint32_t)gp[x]};
+                        if (!both(second, more ? full(rk) : second)) break;
                         ++gp[x];
-                        mma_o(x, it == 0, frees(x, it), !more);
-                        if (more) {
-                            // S overwrites P: this warp's products run in the order of issue
-                            if (!both(full(rk), full(rk))) break;
-                            mma_s(x, frees(x, it + 1), it + 2 == cnt[x]);
-                        }
+                        mma_o(x, 1, false, frees(x, it), !more);
+                        // S overwrites P: this warp's products run in the order of issue
+                        if (more) mma_s(x, frees(x, it + 1), it + 2 == cnt[x]);
                     }
                     two(rv);
                     if (it + 1 < n) two(rk);
@@ -437,10 +438,6 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 ptx::tmem_ld_wait();
 #pragma unroll
                 for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c >> 5][c & 31]));  // used behind the wait
-                if (a.negative) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c >> 5][c & 31] = -s[c >> 5][c & 31];
-                }
                 if (it * kT + kT > all) {
                     const int lim = sees - it * kT;
 #pragma unroll
@@ -465,16 +462,17 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     l1 = ptx::mul2(l1, make_float2(f, f));
                     if (it > 0) {  // (the product before S has finished with it)
 #pragma unroll
-                        for (int c = 0; c < DP; c += 32) {
-                            float v[32];
-                            ptx::tmem_ld32(to + c, v);
+                        for (int c = 0; c < DP; c += 16) {
+                            float v[16];
+                            uint32_t u[16];
+                            ptx::tmem_ld16(to + c, v);
                             ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
+                            for (int e = 0; e < 16; ++e) {
                                 asm volatile("" : "+f"(v[e]));
-                                v[e] *= f;
+                                u[e] = __float_as_uint(v[e] * f);
                             }
-                            ptx::tmem_st32(to + c, v);
+                            ptx::tmem_st16(to + c, u);
                         }
                         ptx::tmem_st_wait();
                     }
@@ -500,11 +498,13 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                         p[e] = pack2<BF16>(v.x, v.y);
                     }
                     ptx::tmem_st16(ts + c * 16, p);
+                    if (c & 1) {  // half of P: its product begins
+                        ptx::tmem_st_wait();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[2 * x + (c >> 1)]));
+                    }
                 }
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[x]));
             }
             if (!ok || (cnt > 0 && !wait(&sb.acc[x], (uint32_t)ga))) break;
             if (cnt > 0) ++ga;

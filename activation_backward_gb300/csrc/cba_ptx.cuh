@@ -392,6 +392,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16, bool b
            ((a_mmajor ? 1u : 0u) << 15) | ((b_nmajor ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// The instruction descriptor's bit that negates A.
+constexpr uint32_t kNegateA = 1u << 13;
+
 // A shared-memory matrix descriptor as two words: the low one holds the address
 // in 16-byte units (steps are additions to it) and the leading offset, the high
 // one the stride offset and the modes.
