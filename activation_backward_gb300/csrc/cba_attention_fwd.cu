@@ -21,8 +21,8 @@
 // item before.  Where there are fewer pairs of tiles than SMs the keys are cut, each
 // item leaves fp32 sums, and a second kernel joins them in the order of the keys.
 //
-// Roles: warp 0 loads (TMA) and takes items, warp 1 issues the products, warps 4-7
-// and 8-11 are the two tiles' warpgroups.  Every wait is bounded (2 s); on a timeout the
+// Roles: warp 0 loads (TMA) and takes items, warp 1 (past dim 64 warps 1 and 2) issues
+// the products, warps 4-7 and 8-11 are the two tiles' warpgroups.  Every wait is bounded (2 s); on a timeout the
 // block sets the workspace's status bit, stops, waits (bounded) for its copies in
 // flight, frees its TMEM and returns.
 #include <cuda.h>
@@ -73,7 +73,7 @@ struct AfArgs {
     float2 *ml;        // their m (in S's unit) and l: [unit][chunk][tile][128 rows]
 };
 
-// One item: the keys it0 * 128 .. of a pair of tiles.
+// One item: the keys from step it0 on of a pair of tiles.
 struct AfItem {
     long long q0, k0;    // first tokens of the sequence
     int b, h0, hk;       // head of the tiles' first row, key/value head
@@ -106,6 +106,29 @@ __device__ __forceinline__ void af_seq(const AfArgs &a, AfItem &w) {
 // batch at most, of which one per sequence may stand for no pair.
 __device__ __forceinline__ int af_slot(const AfArgs &a, int b) {
     return (int)(min(max((long long)a.cu_q[b], 0LL), a.total_q) / (2 * a.tt)) + b;
+}
+
+// A whole warp's wait for barriers, each lane's its own: one vote where the phases are
+// over.  (Lanes that leave a loop one by one, and a vote after it, cost a product's
+// issuer 200 cycles and more; this 15.)
+__device__ __forceinline__ bool warp_wait(AtWait w, volatile int *abort, unsigned *status) {
+    const uint32_t bar = ptx::smem_u32(w.bar);
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, w.parity & 1u))) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, w.parity & 1u))) return true;
+        if ((it & 63u) == 0) {
+            const bool late = ptx::globaltimer_ns() - t0 > kAtLimitNs;
+            if (__any_sync(0xffffffffu, late || *abort != 0)) {
+                if (late) {
+                    *abort = 1;
+                    atomicOr(status, kStatusTimeout);
+                }
+                __syncwarp();
+                return false;
+            }
+        }
+    }
 }
 
 // Item `i` of the grid.  Called by any threads, each for itself.
@@ -168,7 +191,9 @@ __device__ __forceinline__ AfItem af_item(const AfArgs &a, int i) {
 
 template <int DP>
 struct Af {
-    static constexpr int ST = DP == 64 ? 8 : 4;  // tiles of the ring of keys and values
+    static constexpr int ST = DP == 64 ? 8 : 4;   // tiles of the ring of keys and values
+    // two warps issue the products in turns; up to dim 64, where a step's are few, one warp both tiles'
+    static constexpr bool TURNS = DP == 128;
     static constexpr uint32_t TILE = DP / 64 * kBoxBytes;
     static constexpr uint32_t STAGE = kAfWarps * 2048;
     static constexpr uint32_t RING = 2 * TILE, OUT = RING + ST * TILE, BARS = OUT + STAGE;
@@ -177,7 +202,7 @@ struct Af {
         uint64_t kv_full[ST], kv_empty[ST];
         uint64_t s_full[2], p_ready[4], acc[2];  // (P in halves)
         uint64_t i_full[2], i_empty[2];
-        uint64_t fix, drain, clc;
+        uint64_t fix, clc, drain[2], turn[2];
         uint32_t tmem_base;
         int abort_flag;
     };
@@ -204,13 +229,14 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     }
     if (tid == 0) {
         at_init_bars(sb.q_full, 4, 1);
-        at_init_bars(sb.kv_full, 2 * ST, 1);
+        at_init_bars(sb.kv_full, ST, 1);
+        at_init_bars(sb.kv_empty, ST, A::TURNS ? 2 : 1);
         at_init_bars(sb.s_full, 2, 1);
         at_init_bars(sb.p_ready, 4, kAfWarps / 2);
         at_init_bars(sb.acc, 2, 1);
         at_init_bars(sb.i_full, 2, 1);
-        at_init_bars(sb.i_empty, 2, 1 + kAfWarps);
-        at_init_bars(&sb.fix, 3, 1);
+        at_init_bars(sb.i_empty, 2, (A::TURNS ? 2 : 1) + kAfWarps);
+        at_init_bars(&sb.fix, 6, 1);
         sb.abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -229,8 +255,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     const bool packed = a.cu_q != nullptr;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        ok = ok && ptx::mbar_wait_bounded(ptx::smem_u32(bar), parity & 1u, ab, a.status, kAtLimitNs);
-        return ok = __all_sync(0xffffffffu, ok) != 0;
+        return ok = ok && warp_wait(AtWait{bar, parity}, ab, a.status);
     };
     // the k-th item handed out, NULL past the last (or on a timeout)
     auto take = [&](int k) -> const AfItem * {
@@ -239,6 +264,46 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     auto done = [&](int k) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.i_empty[k & 1]));
+    };
+
+    // Products: a whole warp walks its loop and one elected lane issues.  Loops and conditions go by
+    // votes, and which tile it is by a constant: descriptors and counters known to be uniform take
+    // half the time to issue a product.
+    // (a negative scale negates q in the product, so that S's largest is the exponent's)
+    const uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false) | (a.negative ? ptx::kNegateA : 0u);
+    const int steps = (a.dim + 15) / 16;
+    const uint32_t id_o = ptx::idesc_f16(128, steps * 16, BF16, true);
+    auto some = [&](bool p) { return __any_sync(0xffffffffu, p) != 0; };
+    // (of an elected lane) S of tile x with the keys in stage st; o += a half of P times the values
+    auto issue_s = [&](int x, int st) {
+        const ptx::Desc dq = ptx::desc_of(sQ + x * TILE, 16, 1024, 2), dk = ptx::desc_of(sKV + st * TILE, 16, 1024, 2);
+        auto step = [&](int ks) {
+            const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
+            ptx::mma_f16(tS + x * kT, dq, off, dk, off, id_s, ks > 0);
+        };
+        if (steps == DP / 16) {  // a condition in each step doubles its issue time
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) step(ks);
+        } else {
+            for (int ks = 0; ks < steps; ++ks) step(ks);
+        }
+    };
+    auto issue_o = [&](int x, int st, int half, bool first) {
+        const ptx::Desc dv = ptx::desc_of(sKV + st * TILE + half * (64 * 128), kBoxBytes, 1024, 2);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+            ptx::mma_f16_ts(tO + x * DP, tS + x * kT + half * 32 + ks * 8, dv, ks * (2048 >> 4), id_o, !first || ks > 0);
+    };
+    // the end: every product issued has finished before TMEM is released
+    auto finish = [&](int x) {
+        if (ptx::elect_one()) {
+            if (!ok) *const_cast<volatile int *>(&sb.abort_flag) = 1;
+            ptx::mma_commit(ptx::smem_u32(&sb.drain[x]));
+        }
+        __syncwarp();
+        int no = 0;
+        ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain[x]), 0, &no, a.status, kAtLimitNs);
+        __syncwarp();
     };
 
     if (warp < 4) {
@@ -314,32 +379,19 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 drain_ring(sb.kv_full, ST, kv, a.status);
                 drain_ring(&sb.clc, 1, asked, a.status);
             }
-        } else if (warp == 1) {
-            // The whole warp walks the loop and one elected lane issues.
-            // (a negative scale negates q in the product, so that S's largest is the exponent's)
-            const uint32_t id_s = ptx::idesc_f16(128, 128, BF16, false) | (a.negative ? ptx::kNegateA : 0u);
-            const int steps = (a.dim + 15) / 16;
-            const uint32_t id_o = ptx::idesc_f16(128, steps * 16, BF16, true);
-            Ring rk, rv;       // the ring's stage of the next keys, of the next values
+        } else if (!A::TURNS && warp == 1) {
+            // The products of both tiles, in the order of their steps.  (32 x 676 tokens, 8 heads of 64: 64 us, in
+            // turns 70.)
+            Ring rk, rv;             // the ring's stage of the next keys, of the next values
             rv.step(ST);
             int gq[2] = {0, 0}, gp[2] = {0, 0};  // queries, P so far
             auto two = [&](Ring &r) { r.step(ST), r.step(ST); };
             auto full = [&](Ring r) { return AtWait{&sb.kv_full[r.s], r.ph}; };
-            auto both = [&](AtWait x, AtWait y) { return ok = ok && wait_both(x, y, ab, a.status); };
+            auto both = [&](AtWait u, AtWait v) { return ok = ok && warp_wait(lane & 1 ? v : u, ab, a.status); };
             // S of tile x with the keys at rk; `free`: their last use; `last`: the queries' too
             auto mma_s = [&](int x, bool free, bool last) {
-                const ptx::Desc dq = ptx::desc_of(sQ + x * TILE, 16, 1024, 2), dk = ptx::desc_of(sKV + rk.s * TILE, 16, 1024, 2);
                 if (ptx::elect_one()) {
-                    auto step = [&](int ks) {
-                        const uint32_t off = ((ks >> 2) * kBoxBytes + (ks & 3) * 32) >> 4;
-                        ptx::mma_f16(tS + x * 128, dq, off, dk, off, id_s, ks > 0);
-                    };
-                    if (steps == DP / 16) {  // a condition in each step doubles its issue time
-#pragma unroll
-                        for (int ks = 0; ks < DP / 16; ++ks) step(ks);
-                    } else {
-                        for (int ks = 0; ks < steps; ++ks) step(ks);
-                    }
+                    issue_s(x, rk.s);
                     ptx::mma_commit(ptx::smem_u32(&sb.s_full[x]));
                     if (free) ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[rk.s]));
                     if (last) ptx::mma_commit(ptx::smem_u32(&sb.q_empty[x]));
@@ -347,11 +399,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 __syncwarp();
             };
             auto mma_o = [&](int x, int half, bool first, bool free, bool last) {
-                const ptx::Desc dv = ptx::desc_of(sKV + rv.s * TILE + half * (kT / 2 * 128), kBoxBytes, 1024, 2);
                 if (ptx::elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < kT / 32; ++ks)
-                        ptx::mma_f16_ts(tO + x * DP, tS + x * 128 + half * 32 + ks * 8, dv, ks * (2048 >> 4), id_o, !first || ks > 0);
+                    issue_o(x, rv.s, half, first);
                     if (free) ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[rv.s]));
                     if (last) ptx::mma_commit(ptx::smem_u32(&sb.acc[x]));
                 }
@@ -361,52 +410,138 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             for (int k = 0; (w = take(k)) != nullptr; ++k) {
                 const int n = w->n, cnt[2] = {w->cnt[0], w->cnt[1]};
                 done(k);
-                if (n == 0) continue;
                 // a step's last user of its keys and values is the second tile, if it has the step
-                auto frees = [&](int x, int it) { return x == 1 || it >= cnt[1]; };
+                auto frees = [&](int x, int it) { return x == 1 || some(it >= cnt[1]); };
+                if (!some(n > 0)) continue;
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    if (cnt[x] > 0) {
-                        if (!both({&sb.q_full[x], (uint32_t)gq[x]}, full(rk))) break;
-                        ++gq[x];
-                        mma_s(x, frees(x, 0), cnt[x] == 1);
+                    if (some(cnt[x] > 0)) {
+                        if (!both({&sb.q_full[x], (uint32_t)gq[x]++}, full(rk))) break;
+                        ptx::tc_fence_after();
+                        mma_s(x, frees(x, 0), some(cnt[x] == 1));
                     }
-                if (!ok) break;
                 two(rk);
-                for (int it = 0; ok && it < n; ++it) {
+                for (int it = 0; ok && some(it < n); ++it) {
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (it >= cnt[x]) continue;
-                        const bool more = it + 1 < cnt[x];
-                        if (!both({&sb.p_ready[2 * x], (uint32_t)gp[x]}, full(rv))) break;
+                        if (!some(it < cnt[x])) continue;
+                        const bool more = some(it + 1 < cnt[x]);
+                        // P's first half, the values, and the keys of the next S
+                        if (!both({&sb.p_ready[2 * x], (uint32_t)gp[x]}, lane & 2 && more ? full(rk) : full(rv))) break;
+                        ptx::tc_fence_after();
                         mma_o(x, 0, it == 0, false, false);
-                        const AtWait second{&sb.p_ready[2 * x + 1], (uint32_t)gp[x]};
-                        if (!both(second, more ? full(rk) : second)) break;
-                        ++gp[x];
+                        const AtWait second{&sb.p_ready[2 * x + 1], (uint32_t)gp[x]++};
+                        if (!both(second, second)) break;
+                        ptx::tc_fence_after();
                         mma_o(x, 1, false, frees(x, it), !more);
                         // S overwrites P: this warp's products run in the order of issue
-                        if (more) mma_s(x, frees(x, it + 1), it + 2 == cnt[x]);
+                        if (more) mma_s(x, frees(x, it + 1), some(it + 2 == cnt[x]));
                     }
                     two(rv);
-                    if (it + 1 < n) two(rk);
+                    if (some(it + 1 < n)) two(rk);
                 }
                 if (!ok) break;
             }
-            // every product issued has finished before TMEM is released
-            if (ptx::elect_one()) {
-                if (!ok) *const_cast<volatile int *>(&sb.abort_flag) = 1;
-                ptx::mma_commit(ptx::smem_u32(&sb.drain));
+            finish(0);
+        } else if (A::TURNS && warp > 0 && warp < 3) {
+            // The products of tile x, by a warp for each.  They take turns, of a step's products: products
+            // that alternate between accumulators run at half the rate, and the waits of one hide
+            // behind the other's turn.  (8192 tokens, 32/8 heads of 128: 353 us, with one warp for both
+            // tiles 370.)
+            auto products = [&](auto tile) {
+            constexpr int x = decltype(tile)::value;
+            Ring r;                  // the next tile of keys or values
+            int gq = 0, gp = 0, turns = 0;  // queries, P, turns so far
+            auto both = [&](AtWait u, AtWait v) { return ok = ok && warp_wait(lane & 1 ? v : u, ab, a.status); };
+            auto full = [&]() { return AtWait{&sb.kv_full[r.s], r.ph}; };
+            bool shared = false;  // both tiles have steps in this item
+            auto my_turn = [&]() {
+                if (!shared) return ok;
+                const int j = turns++ - (1 - x);  // the other's pass that this one waits for
+                return j < 0 || wait(&sb.turn[x], (uint32_t)j);
+            };
+            const uint32_t pass = ptx::smem_u32(&sb.turn[1 - x]);
+            auto pass_on = [&]() {
+                if (shared && lane == 0) ptx::mbar_arrive(pass);
+                __syncwarp();
+            };
+            // S, the end of a turn
+            auto mma_s = [&](bool last) {
+                if (ptx::elect_one()) {
+                    issue_s(x, r.s);
+                    // (any earlier, and the other's products come between: S is late)
+                    if (shared) ptx::mbar_arrive(pass);
+                    ptx::mma_commit(ptx::smem_u32(&sb.s_full[x]));
+                    ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[r.s]));
+                    if (last) ptx::mma_commit(ptx::smem_u32(&sb.q_empty[x]));
+                }
+                __syncwarp();
+                r.step(ST);
+            };
+            auto mma_o = [&](int half, bool first) {
+                if (ptx::elect_one()) {
+                    issue_o(x, r.s, half, first);
+                }
+                __syncwarp();
+            };
+            const AfItem *w;
+            for (int k = 0; (w = take(k)) != nullptr; ++k) {
+                const int n = w->n, cnt = w->cnt[x], others = w->cnt[1 - x];
+                done(k);
+                if (!some(n > 0)) continue;
+                const bool any = some(cnt > 0);
+                shared = any && some(others > 0);
+                if (any && !both({&sb.q_full[x], (uint32_t)gq++}, full())) break;
+                if (!my_turn()) break;
+                ptx::tc_fence_after();
+                if (any) mma_s(some(cnt == 1));
+                else pass_on();
+                for (int it = 0; ok && some(it < cnt); ++it) {
+                    // S overwrites P: this warp's products run in the order of issue
+                    const bool more = some(it + 1 < cnt);
+                    Ring next = r;
+                    next.step(ST);
+                    const AtWait p0{&sb.p_ready[2 * x], (uint32_t)gp}, p1{&sb.p_ready[2 * x + 1], (uint32_t)gp};
+                    ++gp;
+                    if (!both(p0, lane & 2 && more ? AtWait{&sb.kv_full[next.s], next.ph} : full())) break;
+                    if (!my_turn()) break;
+                    ptx::tc_fence_after();
+                    mma_o(0, it == 0);
+                    if (!both(p1, p1)) break;
+                    ptx::tc_fence_after();
+                    mma_o(1, false);
+                    if (ptx::elect_one()) {
+                        ptx::mma_commit(ptx::smem_u32(&sb.kv_empty[r.s]));
+                        if (!more) ptx::mma_commit(ptx::smem_u32(&sb.acc[x]));
+                    }
+                    __syncwarp();
+                    r.step(ST);
+                    if (more) mma_s(some(it + 2 == cnt));
+                    else pass_on();
+                }
+                // the other tile's steps alone: turns, keys and values that this one lets pass
+                for (int it = cnt; ok && some(it < n); ++it) {
+                    if (!my_turn()) break;
+                    pass_on();
+                    for (int j = 0; j < 2; ++j) {
+                        if (!both(full(), full())) break;
+                        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.kv_empty[r.s]));
+                        __syncwarp();
+                        r.step(ST);
+                    }
+                }
+                if (!ok) break;
             }
-            __syncwarp();
-            int no = 0;
-            ptx::mbar_wait_bounded(ptx::smem_u32(&sb.drain), 0, &no, a.status, kAtLimitNs);
-            __syncwarp();
+            finish(x);
+            };
+            if (warp == 1) products(std::integral_constant<int, 0>{});
+            else products(std::integral_constant<int, 1>{});
         }
     } else {
         ptx::regs_inc<kAfCompRegs>();
         const int x = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tS + x * 128 + lanes, to = tO + x * DP + lanes;
+        const uint32_t ts = tS + x * kT + lanes, to = tO + x * DP + lanes;
         constexpr float shift = BF16 ? 0.f : kHalfShift;
         const float cs = a.cs;
         const float2 cs2 = make_float2(cs, cs);
@@ -432,37 +567,61 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 if (!wait(&sb.s_full[x], (uint32_t)gs)) break;
                 ++gs;
                 ptx::tc_fence_after();
+                if (__builtin_expect(it * kT + kT > all, 0)) {  // -infinity over the masked columns of S
+                    const int lim = sees - it * kT;
+#pragma unroll 1
+                    for (int c = max(all - it * kT, 0) & ~15; c < kT; c += 16) {
+                        float v[16];
+                        uint32_t u[16];
+                        ptx::tmem_ld16(ts + c, v);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            asm volatile("" : "+f"(v[e]));
+                            u[e] = __float_as_uint(c + e >= lim ? -INFINITY : v[e]);
+                        }
+                        ptx::tmem_st16(ts + c, u);
+                    }
+                    ptx::tmem_st_wait();
+                }
                 float s[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + c * 32, s[c]);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c >> 5][c & 31]));  // used behind the wait
-                if (it * kT + kT > all) {
-                    const int lim = sees - it * kT;
+                for (int c = 0; c < kT; ++c) asm volatile("" : "+f"(s[c >> 5][c & 31]));  // used behind the wait
+                float now = -INFINITY;
+                {
+                    float top[4];
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= lim) s[c >> 5][c & 31] = -INFINITY;
+                    for (int c = 0; c < 4; ++c) {
+                        constexpr int Q = kT / 4;
+                        auto at = [&](int e) { return s[(c * Q + e) >> 5][(c * Q + e) & 31]; };
+                        top[c] = fmaxf(at(0), at(Q - 1));
+#pragma unroll
+                        for (int e = 1; e < Q - 1; e += 2) top[c] = ptx::max3(top[c], at(e), at(e + 1));
+                    }
+                    now = fmaxf(ptx::max3(top[0], top[1], top[2]), top[3]);
                 }
-                float top[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    top[c] = s[c][0];
-#pragma unroll
-                    for (int e = 1; e < 31; e += 2) top[c] = fmaxf(fmaxf(top[c], s[c][e]), s[c][e + 1]);
-                    top[c] = fmaxf(top[c], s[c][31]);
-                }
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                // (-inf - -inf and inf - inf are NaN, which raises nothing)
-                if (__any_sync(0xffffffffu, (now - m) * cs > kLag)) {
-                    const float up = fmaxf(m, now);
-                    const float f = up == -INFINITY ? 1.f : ptx::ex2((m - up) * cs);
-                    m = up;
-                    l0 = ptx::mul2(l0, make_float2(f, f));
-                    l1 = ptx::mul2(l1, make_float2(f, f));
-                    if (it > 0) {  // (the product before S has finished with it)
-#pragma unroll
-                        for (int c = 0; c < DP; c += 16) {
+                auto hand_over = [&](int h) {
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[2 * x + h]));
+                };
+                if (tok >= a.tt) now = -INFINITY;  // no row: whatever lies there raises nothing
+                // One vote for what is rare.  (-inf - -inf and inf - inf are NaN, which raises nothing.)
+                const bool grown = (now - m) * cs > kLag, large = fabsf(fmaxf(m, now)) * cs > kLargeLog && now > -INFINITY;
+                if (__builtin_expect(__any_sync(0xffffffffu, grown || large), 0)) {
+                    if (__any_sync(0xffffffffu, grown)) {
+                        const float up = fmaxf(m, now);
+                        const float f = up == -INFINITY ? 1.f : ptx::ex2((m - up) * cs);
+                        m = up;
+                        l0 = ptx::mul2(l0, make_float2(f, f));
+                        l1 = ptx::mul2(l1, make_float2(f, f));
+                        // (the product before S has finished with o; the first one overwrites it)
+#pragma unroll 1
+                        for (int c = it > 0 ? 0 : DP; c < DP; c += 16) {
                             float v[16];
                             uint32_t u[16];
                             ptx::tmem_ld16(to + c, v);
@@ -474,17 +633,31 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                             }
                             ptx::tmem_st16(to + c, u);
                         }
-                        ptx::tmem_st_wait();
+                    }
+                    // S cs - m cs in one rounding is off by 2^-24 of m cs: where that is large, S - m comes first
+                    if (__any_sync(0xffffffffu, fabsf(m) * cs > kLargeLog && m > -INFINITY)) {
+                        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+                        for (int c = 0; c < kT; c += 16) {
+                            float v[16];
+                            uint32_t p[8];
+                            ptx::tmem_ld16(ts + c, v);
+                            ptx::tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                asm volatile("" : "+f"(v[2 * e]), "+f"(v[2 * e + 1]));
+                                const float2 u = make_float2(ptx::ex2(fmaf(v[2 * e] - ref, cs, shift)),
+                                                             ptx::ex2(fmaf(v[2 * e + 1] - ref, cs, shift)));
+                                l0 = ptx::add2(l0, u);
+                                p[e] = pack2<BF16>(u.x, u.y);
+                            }
+                            ptx::tmem_st8(ts + c / 2, p);  // (over columns that have been read)
+                        }
+                        hand_over(0), hand_over(1);
+                        continue;
                     }
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
-                float nm = shift - ref * cs;
-                // S cs - m cs in one rounding, off by 2^-24 of m cs: of large ones the difference first
-                if (__any_sync(0xffffffffu, fabsf(nm) > kLargeLog)) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c >> 5][c & 31] -= ref;
-                    nm = shift;
-                }
+                const float nm = shift - (m == -INFINITY ? 0.f : m) * cs;
                 const float2 nm2 = make_float2(nm, nm);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -497,14 +670,10 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                         else l0 = ptx::add2(l0, v);
                         p[e] = pack2<BF16>(v.x, v.y);
                     }
+                    if (c == 2) hand_over(0);  // the first half's stores have had the time of 32 columns
                     ptx::tmem_st16(ts + c * 16, p);
-                    if (c & 1) {  // half of P: its product begins
-                        ptx::tmem_st_wait();
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[2 * x + (c >> 1)]));
-                    }
                 }
+                hand_over(1);
             }
             if (!ok || (cnt > 0 && !wait(&sb.acc[x], (uint32_t)ga))) break;
             if (cnt > 0) ++ga;
@@ -518,7 +687,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 a.ml[slot * kT + r] = make_float2(m, l);
                 if (cnt > 0) {
                     float4 *at = reinterpret_cast<float4 *>(a.part) + slot * (DP / 4) * kT + r;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < DP; c += 32) {
                         float v[32];
                         ptx::tmem_ld32(to + c, v);
@@ -550,7 +719,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 const int rr = quarter * 32 + i * 8 + (lane >> 2), tk2 = rr / a.hp, tt = w.t0 + x * a.tt + tk2;
                 at[i] = tk2 < a.tt && tt < w.lq ? (w.q0 + tt) * a.so[1] + (w.h0 + rr - tk2 * a.hp) * a.so[2] : -1;
             }
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 float v[32];
                 if (cnt > 0) {
@@ -742,18 +911,18 @@ int check_attn(const cba_attention_desc_t *d, AfPlan *p) {
     return CBA_OK;
 }
 
-// The map of k or v: (dim, token, head, batch), boxes of 128 tokens x 64; of q: (dim, head,
+// The map of k or v: (dim, token, head, batch), boxes of a step's keys x 64; of q: (dim, head,
 // token, batch), boxes of a tile's tokens x heads x 64.
 bool af_map(CUtensorMap *m, const void *base, const cba_attention_desc_t &d, int heads, long long tokens, const long long *st,
-            const AfPlan *q) {
+            const AfPlan &p, bool is_q) {
     uint64_t dims[4] = {(uint64_t)d.dim, (uint64_t)tokens, (uint64_t)heads, (uint64_t)(d.packed ? 1 : d.batch)};
     uint64_t strides[3] = {(uint64_t)st[1] * 2, (uint64_t)st[2] * 2, (uint64_t)st[0] * 2};
-    uint32_t box[4] = {64, kT, 1, 1};
-    if (q) {
+    uint32_t box[4] = {64, (uint32_t)kT, 1, 1};
+    if (is_q) {
         std::swap(dims[1], dims[2]);
         std::swap(strides[0], strides[1]);
-        box[1] = (uint32_t)q->hp;
-        box[2] = (uint32_t)q->tt;
+        box[1] = (uint32_t)p.hp;
+        box[2] = (uint32_t)p.tt;
     }
     for (int i = 0; i < 3; ++i)  // an axis of one index has no stride of its own
         if (dims[i + 1] == 1) strides[i] = 16;
@@ -826,8 +995,8 @@ int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const vo
     // without queries (or keys) the kernel loads nothing of them
     CUtensorMap tm[3] = {};
     if (tq > 0 && tk > 0 &&
-        (!af_map(&tm[0], q, *d, d->heads_q, tq, sq, &p) || !af_map(&tm[1], k, *d, d->heads_kv, tk, sk, nullptr) ||
-         !af_map(&tm[2], v, *d, d->heads_kv, tk, sv, nullptr)))
+        (!af_map(&tm[0], q, *d, d->heads_q, tq, sq, p, true) || !af_map(&tm[1], k, *d, d->heads_kv, tk, sk, p, false) ||
+         !af_map(&tm[2], v, *d, d->heads_kv, tk, sv, p, false)))
         return CBA_ERR_UNSUPPORTED;
     cudaGetLastError();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
