@@ -8,8 +8,10 @@
 //
 // Each element is read once and each result written once: the bound is memory.  A
 // head's elements lie in the registers of 1 to 32 lanes, 8 (PAIRS_SPLIT: 8 of each
-// half) to a lane, and its sums are shuffles.  A warp takes a token's heads in
-// turn, kSteps x 32 / lanes of them, with all their loads ahead of the first use.
+// half) to a lane, and its sums are shuffles.  A warp walks tokens and, within one, its
+// heads, 32 / lanes of them a step; lanes copy their own elements asynchronously to
+// shared memory a few steps ahead, and the warp its tokens' rows of the table.  Blocks
+// are the queries' or the keys', in the proportion of their steps.
 #include <algorithm>
 #include <cmath>
 
@@ -23,8 +25,9 @@ namespace {
 
 constexpr int kQkMaxDim = 256;
 constexpr int kWarps = 8;                     // of a block
-constexpr int kSteps = 4, kBwdSteps = 2;      // heads of a lane in flight
-constexpr int kBwdBlocks = 2 * kNumSMs;       // at most; one partial row of dgamma each
+// Steps in flight; blocks per SM.
+__host__ __device__ constexpr int qk_ahead(bool bwd) { return bwd ? 2 : 4; }
+constexpr int kQkPerSm = 2;
 
 // Where the two elements of a pair lie.
 enum Pairs {
@@ -38,14 +41,15 @@ struct QkArgs {
     const void *x[2], *dy[2], *gamma[2];
     void *out[2];
     long long sx[2][3], sdy[2][3], so[2][3];  // batch, token, head
-    int heads[2], parts[2];                   // parts: a warp's tasks per token
+    int heads[2], steps[2];                   // steps: of a token
     const float2 *table;
     const int *pos;
     int tokens, len, dim, rot, positions, norm;
     float sign, eps, inv_dim;                 // sign: -1 turns back
     int lanes_log;                            // lanes of a head
-    int q_blocks;                             // backward: blocks of the queries
-    float *partial;
+    int q_blocks;                             // blocks of the queries
+    int warp_bytes, row_bytes;                // shared memory of a warp, of a row of the table
+    float *partial;                           // backward: a row of dgamma per block
 };
 
 template <typename T>
@@ -59,6 +63,38 @@ __device__ __forceinline__ Vec<T> load8(const void *p, long long at) {
     for (int i = 0; i < (int)sizeof(Vec<T>) / 16; ++i) reinterpret_cast<uint4 *>(&v)[i] = s[i];
     return v;
 }
+// Elements 2 j and 2 j + 1 of a vector, a word at a time (halves put together one by one
+// cost as many instructions again), and the other way.
+template <typename T>
+__device__ __forceinline__ float2 two_of(const Vec<T> &v, int j) {
+    if constexpr (sizeof(T) == 4) return make_float2(v.v[2 * j], v.v[2 * j + 1]);
+    const uint32_t u = reinterpret_cast<const uint32_t *>(&v)[j];
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ void set_two(Vec<T> &v, int j, float2 x) {
+    if constexpr (sizeof(T) == 4) {
+        v.v[2 * j] = x.x, v.v[2 * j + 1] = x.y;
+    } else if constexpr (std::is_same<T, __half>::value) {
+        reinterpret_cast<__half2 *>(&v)[j] = __float22half2_rn(x);
+    } else {
+        reinterpret_cast<__nv_bfloat162 *>(&v)[j] = __float22bfloat162_rn(x);
+    }
+}
+
+// Asynchronous copies of this thread, global to shared.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void *from) {
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ void store8(void *p, long long at, const Vec<T> &v) {
     uint4 *s = reinterpret_cast<uint4 *>(static_cast<T *>(p) + at);
@@ -66,260 +102,325 @@ __device__ __forceinline__ void store8(void *p, long long at, const Vec<T> &v) {
     for (int i = 0; i < (int)sizeof(Vec<T>) / 16; ++i) s[i] = reinterpret_cast<const uint4 *>(&v)[i];
 }
 
-// A lane's place in its head and the angles of its elements at one position.
+// A lane's place in its head, and what turns its elements at one position.
 template <int PAIRS>
 struct Lane {
     static constexpr int NV = PAIRS == PAIRS_SPLIT ? 2 : 1;  // vectors of 8 elements
-    static constexpr int NE = 8 * NV;
+    static constexpr int NE = 8 * NV, N2 = NE / 2;
     static constexpr int NC = PAIRS == PAIRS_LOCAL ? 4 : 8;  // angles
-    int slot, l, at[NV];
+    int slot, l, at[NV], lanes;
     bool on;
     float cs[NC], sn[NC];
 
     __device__ __forceinline__ Lane(const QkArgs &a) {
         const int lane = threadIdx.x & 31;
+        lanes = 1 << a.lanes_log;
         slot = lane >> a.lanes_log;
-        l = lane & ((1 << a.lanes_log) - 1);
+        l = lane & (lanes - 1);
         at[0] = l * 8;
         if constexpr (NV == 2) at[1] = a.dim / 2 + l * 8;
         on = l * 8 < a.dim / NV;
     }
-    // (an element past rot_dim turns by the angle 0)
-    __device__ __forceinline__ void angles(const QkArgs &a, int token) {
-        if (a.rot == 0) {
+    // The angles of a token, from its row of the table.  (An element past rot_dim turns by the angle 0.)
+    __device__ __forceinline__ void angles(const QkArgs &a, const float2 *row) {
+        if constexpr (PAIRS == PAIRS_SPLIT) {  // (a lane past the head's elements holds zeros, whatever it reads)
+            const float4 *r4 = reinterpret_cast<const float4 *>(row + (on ? l * 8 : 0));
+            const float2 s2 = make_float2(a.sign, a.sign);
 #pragma unroll
-            for (int i = 0; i < NC; ++i) cs[i] = 1.f, sn[i] = 0.f;
-            return;
-        }
-        const int p = min(max(a.pos ? a.pos[token] : token % a.len, 0), a.positions - 1);
-        const float2 *row = a.table + (long long)p * (a.rot / 2);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            int j;
-            bool in;
-            if constexpr (PAIRS == PAIRS_LOCAL) {
-                j = l * 4 + i, in = on && j < a.rot / 2;
-            } else if constexpr (PAIRS == PAIRS_SPLIT) {
-                j = l * 8 + i, in = on;
-            } else {
-                const int e = l * 8 + i;
-                j = e < a.rot / 2 ? e : e - a.rot / 2, in = on && e < a.rot;
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = r4[i];
+                const float2 s = ptx::mul2(make_float2(v.y, v.w), s2);
+                cs[2 * i] = v.x, cs[2 * i + 1] = v.z;
+                sn[2 * i] = s.x, sn[2 * i + 1] = s.y;
             }
-            const float2 v = in ? __ldg(row + j) : make_float2(1.f, 0.f);
-            cs[i] = v.x;
-            sn[i] = a.sign * v.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int e = l * 8 + i;
+                const int j = PAIRS == PAIRS_LOCAL ? l * NC + i : e < a.rot / 2 ? e : e - a.rot / 2;
+                const bool in = on && (PAIRS == PAIRS_ANY ? e < a.rot : j < a.rot / 2);
+                const float2 v = in ? row[j] : make_float2(1.f, 0.f);
+                cs[i] = v.x;
+                sn[i] = a.sign * v.y;
+            }
         }
     }
     // The sum over the lanes of a head.
-    __device__ __forceinline__ float head_sum(const QkArgs &a, float v) const {
-        for (int o = (1 << a.lanes_log) >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __device__ __forceinline__ float head_sum(float v) const {
+        for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    // Turns h in place; `inverse`: by the opposite angles.  buf: the warp's 256 floats.
-    __device__ __forceinline__ void turn(const QkArgs &a, float (&h)[NE], float *buf) const {
+    // Turns h in place by the angles.  buf: the warp's 256 floats.
+    __device__ __forceinline__ void turn(const QkArgs &a, float2 (&h)[N2], float *buf) const {
         if constexpr (PAIRS == PAIRS_LOCAL) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = h[2 * i], y = h[2 * i + 1];
-                h[2 * i] = x * cs[i] - y * sn[i];
-                h[2 * i + 1] = x * sn[i] + y * cs[i];
+                const float2 x = h[i];
+                h[i] = make_float2(x.x * cs[i] - x.y * sn[i], x.x * sn[i] + x.y * cs[i]);
             }
         } else if constexpr (PAIRS == PAIRS_SPLIT) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x = h[i], y = h[8 + i];
-                h[i] = x * cs[i] - y * sn[i];
-                h[8 + i] = x * sn[i] + y * cs[i];
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = h[i], y = h[4 + i];
+                const float2 c = make_float2(cs[2 * i], cs[2 * i + 1]), s = make_float2(sn[2 * i], sn[2 * i + 1]);
+                h[i] = ptx::fma2(x, c, ptx::mul2(y, make_float2(-s.x, -s.y)));
+                h[4 + i] = ptx::fma2(x, s, ptx::mul2(y, c));
             }
         } else {
-            float *mine = buf + (slot << a.lanes_log) * 8;
+            float *mine = buf + slot * lanes * 8;
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mine[l * 8 + i] = h[i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(mine + l * 8 + 2 * i) = h[i];
             __syncwarp();
             const int half = a.rot / 2;
+            float *v = reinterpret_cast<float *>(h);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int e = l * 8 + i;
-                if (e < half) h[i] = h[i] * cs[i] - mine[e + half] * sn[i];
-                else if (e < a.rot) h[i] = h[i] * cs[i] + mine[e - half] * sn[i];
+                if (e < half) v[i] = v[i] * cs[i] - mine[e + half] * sn[i];
+                else if (e < a.rot) v[i] = v[i] * cs[i] + mine[e - half] * sn[i];
             }
         }
     }
     // 1 / sqrt(mean x^2 + eps) of a head.  Squares that overflow are summed again at
     // 2^-66 times the elements: the mean is then so large that eps does not count.
-    __device__ __forceinline__ float rnorm(const QkArgs &a, const float (&x)[NE]) const {
-        float s = 0.f;
+    __device__ __forceinline__ float rnorm(const QkArgs &a, const float2 (&x)[N2]) const {
+        float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) s = fmaf(x[i], x[i], s);
-        s = head_sum(a, s);
-        float r = 1.f / sqrtf(fmaf(s, a.inv_dim, a.eps));
+        for (int i = 0; i < N2; ++i) q = ptx::fma2(x[i], x[i], q);
+        const float s = head_sum(q.x + q.y);
+        float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));  // (2 ulp: below the sum's own error)
         if (__any_sync(0xffffffffu, !(s < INFINITY))) {
             float t = 0.f;
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const float y = x[i] * 0x1p-66f;
-                t = fmaf(y, y, t);
+            for (int i = 0; i < N2; ++i) {
+                const float y = x[i].x * 0x1p-66f, z = x[i].y * 0x1p-66f;
+                t = fmaf(y, y, fmaf(z, z, t));
             }
-            t = head_sum(a, t);
-            if (!(s < INFINITY)) r = 0x1p-66f / sqrtf(t * a.inv_dim);
+            t = head_sum(t);
+            if (!(s < INFINITY)) r = 0x1p-66f * rsqrtf(t * a.inv_dim);
         }
         return r;
     }
 };
 
-template <typename P, int NE, int NV>
-__device__ __forceinline__ void load_gamma(const void *gamma, const int (&at)[NV], bool on, float (&g)[NE]) {
+template <typename P, int N2, int NV>
+__device__ __forceinline__ void load_gamma(const void *gamma, const int (&at)[NV], bool on, float2 (&g)[N2]) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         Vec<P> p;
         if (gamma && on) p = load8<P>(gamma, at[v]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[v * 8 + i] = gamma && on ? to_f32(p.v[i]) : 1.f;
+        for (int i = 0; i < 4; ++i) g[v * 4 + i] = gamma && on ? two_of<P>(p, i) : make_float2(1.f, 1.f);
     }
 }
 
-template <typename T, int NE, int NV>
-__device__ __forceinline__ void unpack(const Vec<T> (&v)[NV], bool on, float (&x)[NE]) {
+template <typename T, int N2, int NV>
+__device__ __forceinline__ void unpack(const Vec<T> (&v)[NV], float2 (&x)[N2]) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[k * 8 + i] = on ? to_f32(v[k].v[i]) : 0.f;
+        for (int i = 0; i < 4; ++i) x[k * 4 + i] = two_of<T>(v[k], i);
 }
-
-template <typename T, typename P, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const QkArgs a) {
-    using L = Lane<PAIRS>;
-    constexpr int NV = L::NV, NE = L::NE;
-    __shared__ float bufs[PAIRS == PAIRS_ANY ? kWarps * 256 : 1];
-    const int warp = threadIdx.x >> 5, parts = a.parts[0] + a.parts[1];
-    const unsigned task = blockIdx.x * kWarps + warp;
-    const int token = (int)(task / parts);
-    if (token >= a.tokens) return;
-    int part = (int)(task - (unsigned)token * parts);
-    const int w = part >= a.parts[0];
-    if (w) part -= a.parts[0];
-    L lane(a);
-    const int per = 32 >> a.lanes_log;
-    const long long b = token / a.len, t = token - b * a.len;
-    const long long x0 = b * a.sx[w][0] + t * a.sx[w][1], o0 = b * a.so[w][0] + t * a.so[w][1];
-    Vec<T> px[kSteps][NV];
+template <typename T, int N2, int NV>
+__device__ __forceinline__ void pack_store(T *out, const int (&at)[NV], const float2 (&x)[N2]) {
 #pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-        const int h = (part * kSteps + u) * per + lane.slot;
-        if (lane.on && h < a.heads[w])
+    for (int v = 0; v < NV; ++v) {
+        Vec<T> y;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) px[u][v] = load8<T>(a.x[w], x0 + h * a.sx[w][2] + lane.at[v]);
-    }
-    lane.angles(a, token);
-    float gamma[NE];
-    load_gamma<P>(a.gamma[w], lane.at, lane.on, gamma);
-#pragma unroll
-    for (int u = 0; u < kSteps; ++u) {
-        const int first = (part * kSteps + u) * per, h = first + lane.slot;
-        if (first >= a.heads[w]) break;  // the whole warp
-        const bool on = lane.on && h < a.heads[w];
-        float x[NE];
-        unpack<T>(px[u], on, x);
-        if (a.norm) {
-            const float r = lane.rnorm(a, x);
-#pragma unroll
-            for (int i = 0; i < NE; ++i) x[i] = x[i] * r * gamma[i];
-        }
-        lane.turn(a, x, bufs + warp * (PAIRS == PAIRS_ANY ? 256 : 0));
-        if (on) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                Vec<T> y;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y.v[i] = from_f32<T>(x[v * 8 + i]);
-                store8<T>(a.out[w], o0 + h * a.so[w][2] + lane.at[v], y);
-            }
-        }
+        for (int i = 0; i < 4; ++i) set_two<T>(y, i, x[v * 4 + i]);
+        store8<T>(out, at[v], y);
     }
 }
 
-// Blocks below q_blocks walk the queries' tasks, the others the keys'; a warp adds
-// up its lanes' parts of dgamma, a block its warps', in a fixed order.
-template <typename T, typename P, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 2) qk_bwd_kernel(const QkArgs a) {
+// Blocks below q_blocks walk the queries' heads, the others the keys'.  Backward: a warp
+// adds up its lanes' parts of dgamma, a block its warps', in a fixed order.
+template <typename T, typename P, int PAIRS, bool BWD>
+__global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs a) {
     using L = Lane<PAIRS>;
-    constexpr int NV = L::NV, NE = L::NE;
-    __shared__ float bufs[kWarps * 256];
+    constexpr int NV = L::NV, NE = L::NE, N2 = L::N2, AHEAD = qk_ahead(BWD), NT = BWD ? 2 : 1, Q = sizeof(T) / 2;
+    constexpr uint32_t STEP = NT * NV * Q * 512;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane_id = threadIdx.x & 31;
-    ptx::griddep_launch_dependents();
+    if (BWD) ptx::griddep_launch_dependents();
     const int w = (int)blockIdx.x >= a.q_blocks;
-    const unsigned blk = w ? blockIdx.x - a.q_blocks : blockIdx.x, blks = w ? gridDim.x - a.q_blocks : a.q_blocks;
-    const unsigned tasks = (unsigned)a.tokens * a.parts[w];
+    const int blk = w ? (int)blockIdx.x - a.q_blocks : (int)blockIdx.x;
+    const int stride = (w ? (int)gridDim.x - a.q_blocks : a.q_blocks) * kWarps;  // from one token of a warp to its next
     L lane(a);
-    const int per = 32 >> a.lanes_log;
-    float gamma[NE], dg[NE];
-    load_gamma<P>(a.gamma[w], lane.at, lane.on, gamma);
+    const int per = 32 >> a.lanes_log, heads = a.heads[w];
+    uint8_t *ring = smem + warp * a.warp_bytes, *rows = ring + AHEAD * STEP;
+    float *buf = reinterpret_cast<float *>(rows + (AHEAD + 1) * a.row_bytes);  // PAIRS_ANY: 256 floats
+    const uint32_t to = ptx::smem_u32(ring) + lane_id * 16, to_rows = ptx::smem_u32(rows);
+
+    // A token's sequence and index in it, moved on by `stride` tokens.  (Divisions cost as much as a step.)
+    struct Place {
+        int token, b, t;
+    };
+    const int sb = stride / a.len, sr = stride - sb * a.len;
+    auto begin = [&]() {
+        const int token = blk * kWarps + warp, b = token / a.len;
+        return Place{token, b, token - b * a.len};
+    };
+    auto move_on = [&](Place &p) {
+        p.token += stride, p.b += sb, p.t += sr;
+        if (p.t >= a.len) p.t -= a.len, ++p.b;
+    };
+    // the copies' place: token, head in it, stage of the ring and of the rows, the next token's position;
+    // pointers to the lane's head move on by `per` heads
+    const T *fx = nullptr, *fdy = nullptr;
+    const long long xs = per * a.sx[w][2], ds = per * a.sdy[w][2], os = per * a.so[w][2];
+    Place f = begin();
+    int fh = lane.slot, fs = 0, fr = 0;
+    auto position = [&](const Place &p) {
+        if (p.token >= a.tokens || a.rot == 0) return 0;
+        return min(max(a.pos ? __ldg(a.pos + p.token) : p.t, 0), a.positions - 1);
+    };
+    auto place = [&]() {
+        fx = static_cast<const T *>(a.x[w]) + f.b * a.sx[w][0] + f.t * a.sx[w][1] + lane.slot * a.sx[w][2];
+        if (BWD) fdy = static_cast<const T *>(a.dy[w]) + f.b * a.sdy[w][0] + f.t * a.sdy[w][1] + lane.slot * a.sdy[w][2];
+    };
+    place();
+    auto after = [&](Place p) {
+        move_on(p);
+        return position(p);
+    };
+    int at_pos = position(f), next_pos = after(f);
+    auto fetch = [&]() {
+        if (f.token < a.tokens) {
+            if (fh == lane.slot)
+                for (int j = lane_id; j < a.rot / 2; j += 32)
+                    copy_async<8>(to_rows + fr * a.row_bytes + j * 8, a.table + (long long)at_pos * (a.rot / 2) + j);
+            if (lane.on && fh < heads) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) dg[i] = 0.f;
-    for (unsigned task = blk * kWarps + warp; task < tasks; task += blks * kWarps) {
-        const int token = (int)(task / a.parts[w]), part = (int)(task - (unsigned)token * a.parts[w]);
-        const long long b = token / a.len, t = token - b * a.len;
-        const long long x0 = b * a.sx[w][0] + t * a.sx[w][1], o0 = b * a.so[w][0] + t * a.so[w][1],
-                        d0 = b * a.sdy[w][0] + t * a.sdy[w][1];
-        Vec<T> px[kBwdSteps][NV], pd[kBwdSteps][NV];
+                for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int u = 0; u < kBwdSteps; ++u) {
-            const int h = (part * kBwdSteps + u) * per + lane.slot;
-            if (lane.on && h < a.heads[w])
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    px[u][v] = load8<T>(a.x[w], x0 + h * a.sx[w][2] + lane.at[v]);
-                    pd[u][v] = load8<T>(a.dy[w], d0 + h * a.sdy[w][2] + lane.at[v]);
-                }
-        }
-        lane.angles(a, token);
-#pragma unroll
-        for (int u = 0; u < kBwdSteps; ++u) {
-            const int first = (part * kBwdSteps + u) * per, h = first + lane.slot;
-            if (first >= a.heads[w]) break;
-            const bool on = lane.on && h < a.heads[w];
-            float x[NE], g[NE];
-            unpack<T>(px[u], on, x);
-            unpack<T>(pd[u], on, g);
-            lane.turn(a, g, bufs + warp * 256);
-            const float r = lane.rnorm(a, x);
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                x[i] = on ? x[i] * r : 0.f;  // n (of a lane without a head r may be infinite)
-                dg[i] = fmaf(g[i], x[i], dg[i]);
-                g[i] *= gamma[i];
-                s = fmaf(g[i], x[i], s);
+                    for (int q = 0; q < Q; ++q) {
+                        const uint32_t at = to + fs * STEP + (v * Q + q) * 512;
+                        copy_async<16>(at, fx + lane.at[v] + q * 4);
+                        if (BWD) copy_async<16>(at + NV * Q * 512, fdy + lane.at[v] + q * 4);
+                    }
             }
-            s = lane.head_sum(a, s) * a.inv_dim;
-            if (on) {
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    Vec<T> y;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y.v[i] = from_f32<T>(r * (g[v * 8 + i] - x[v * 8 + i] * s));
-                    store8<T>(a.out[w], o0 + h * a.so[w][2] + lane.at[v], y);
-                }
-            }
         }
-    }
-    // the heads of a warp side by side, then the block's warps
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-        for (int o = 16; o >= 1 << a.lanes_log; o >>= 1) dg[i] += __shfl_xor_sync(0xffffffffu, dg[i], o);
-    __syncwarp();
-    if (lane_id < 1 << a.lanes_log && lane.on)
+        copies_commit();
+        fs = fs + 1 == AHEAD ? 0 : fs + 1;
+        fx += xs, fh += per;
+        if (BWD) fdy += ds;
+        if (fh - lane.slot >= heads) {  // (the same for all lanes)
+            fh = lane.slot;
+            move_on(f);
+            fr = fr == AHEAD ? 0 : fr + 1;
+            at_pos = next_pos;
+            next_pos = after(f);
+            place();
+        }
+    };
+    auto have = [&](int st, int which, bool on, float2 (&x)[N2]) {
+        Vec<T> p[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) bufs[warp * 256 + lane.at[v] + i] = dg[v * 8 + i];
+            for (int q = 0; q < Q; ++q) {
+                uint4 u = *reinterpret_cast<const uint4 *>(ring + st * STEP + (which * NV * Q + v * Q + q) * 512 + lane_id * 16);
+                if (!on) u = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4 *>(&p[v])[q] = u;
+            }
+        unpack<T>(p, x);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch();
+    float2 gamma[N2], dg[BWD ? N2 : 1];
+    load_gamma<P>(a.gamma[w], lane.at, lane.on, gamma);
+    if constexpr (BWD)
+#pragma unroll
+        for (int i = 0; i < N2; ++i) dg[i] = make_float2(0.f, 0.f);
+    int st = 0, row = 0;
+    for (Place c = begin(); c.token < a.tokens; move_on(c)) {
+        T *out = static_cast<T *>(a.out[w]) + c.b * a.so[w][0] + c.t * a.so[w][1] + lane.slot * a.so[w][2];
+        // forward, PAIRS_SPLIT: (a, b) becomes r (ca a + cb b, da a + db b)
+        float2 ca[4], cb[4], da[4], db[4];
+        for (int h = lane.slot; h - lane.slot < heads; h += per, out += os) {
+            copies_wait<AHEAD - 1>();
+            if (h == lane.slot) {
+                __syncwarp();  // the row was copied by all lanes
+                lane.angles(a, reinterpret_cast<const float2 *>(rows + row * a.row_bytes));
+                __syncwarp();  // read by all before it is copied over
+                row = row == AHEAD ? 0 : row + 1;
+                if constexpr (!BWD && PAIRS == PAIRS_SPLIT) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 c = make_float2(lane.cs[2 * j], lane.cs[2 * j + 1]), s = make_float2(lane.sn[2 * j], lane.sn[2 * j + 1]);
+                        ca[j] = ptx::mul2(gamma[j], c);
+                        cb[j] = ptx::mul2(gamma[4 + j], make_float2(-s.x, -s.y));
+                        da[j] = ptx::mul2(gamma[j], s);
+                        db[j] = ptx::mul2(gamma[4 + j], c);
+                    }
+                }
+            }
+            const bool on = lane.on && h < heads;
+            float2 x[N2];
+            have(st, 0, on, x);
+            if constexpr (BWD) {
+                float2 g[N2];
+                have(st, 1, on, g);
+                fetch();
+                lane.turn(a, g, buf);
+                const float r = lane.rnorm(a, x);
+                const float2 r2 = make_float2(r, r);
+                float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < N2; ++e) {
+                    if (on) x[e] = ptx::mul2(x[e], r2);  // n (of a lane without a head 0: r may be infinite)
+                    dg[e] = ptx::fma2(g[e], x[e], dg[e]);
+                    g[e] = ptx::mul2(g[e], gamma[e]);
+                    q = ptx::fma2(g[e], x[e], q);
+                }
+                const float s = lane.head_sum(q.x + q.y) * -a.inv_dim;
+#pragma unroll
+                for (int e = 0; e < N2; ++e) x[e] = ptx::mul2(ptx::fma2(x[e], make_float2(s, s), g[e]), r2);
+            } else {
+                fetch();
+                const float r = a.norm ? lane.rnorm(a, x) : 1.f;
+                const float2 r2 = make_float2(r, r);
+                if constexpr (PAIRS == PAIRS_SPLIT) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 u = ptx::mul2(x[j], r2), v = ptx::mul2(x[4 + j], r2);
+                        x[j] = ptx::fma2(u, ca[j], ptx::mul2(v, cb[j]));
+                        x[4 + j] = ptx::fma2(u, da[j], ptx::mul2(v, db[j]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < N2; ++j) x[j] = ptx::mul2(ptx::mul2(x[j], r2), gamma[j]);
+                    lane.turn(a, x, buf);
+                }
+            }
+            if (on) pack_store<T>(out, lane.at, x);
+            st = st + 1 == AHEAD ? 0 : st + 1;
+        }
+    }
+    if constexpr (BWD) {
+    copies_wait<0>();
+    __syncthreads();
+    float *bufs = reinterpret_cast<float *>(smem);
+    // the heads of a warp side by side, then the block's warps
+    float sums[NE];
+#pragma unroll
+    for (int i = 0; i < N2; ++i) sums[2 * i] = dg[i].x, sums[2 * i + 1] = dg[i].y;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        for (int o = 16; o >= lane.lanes; o >>= 1) sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], o);
+    if (lane_id < lane.lanes && lane.on)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bufs[warp * 256 + lane.at[v] + i] = sums[v * 8 + i];
     __syncthreads();
     for (int c = threadIdx.x; c < a.dim; c += kWarps * 32) {
         float s = bufs[c];
 #pragma unroll
         for (int k = 1; k < kWarps; ++k) s += bufs[k * 256 + c];
         a.partial[(long long)blockIdx.x * a.dim + c] = s;
+    }
     }
 }
 
@@ -360,8 +461,8 @@ int check_desc(const cba_qk_norm_rope_desc_t *d) {
     if (!(std::isfinite(d->eps) && d->eps >= 0.f)) return CBA_ERR_ARG;
     if (d->param_type != CBA_F32 && d->param_type != d->type) return CBA_ERR_UNSUPPORTED;
     if (d->dim % 8 != 0 || d->dim > kQkMaxDim) return CBA_ERR_UNSUPPORTED;
-    // tasks are counted in 32 bits: one per token and head at most
-    if ((double)d->batch * d->len * ((double)d->heads_q + d->heads_k + 2) >= 2147483648.0) return CBA_ERR_UNSUPPORTED;
+    // tokens are counted in 32 bits, beside a grid's stride of them
+    if ((double)d->batch * d->len > 2147483648.0 - 65536.0) return CBA_ERR_UNSUPPORTED;
     const int vec = 16 / (int)dtype_bytes(d->type);
     const cba_attn_strides_t *ss[] = {&d->q, &d->k, &d->yq, &d->yk, &d->dyq, &d->dyk, &d->dq, &d->dk};
     for (int i = 0; i < 8; ++i) {
@@ -389,8 +490,8 @@ Pairs pairs_of(const cba_qk_norm_rope_desc_t &d) {
     return d.rot_dim == d.dim && d.dim % 16 == 0 ? PAIRS_SPLIT : PAIRS_ANY;
 }
 
-// What both directions share; `steps`: a warp's heads per lane.
-QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int *pos, int steps) {
+// What both directions share.
+QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int *pos) {
     QkArgs a{};
     a.table = reinterpret_cast<const float2 *>(table);
     a.pos = pos;
@@ -405,23 +506,24 @@ QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int
     a.inv_dim = 1.f / (float)d.dim;
     const int lanes = pairs_of(d) == PAIRS_SPLIT ? d.dim / 16 : d.dim / 8;
     while ((1 << a.lanes_log) < lanes) ++a.lanes_log;
-    const int per = (32 >> a.lanes_log) * steps;
+    const int per = 32 >> a.lanes_log;
     a.heads[0] = d.heads_q;
     a.heads[1] = d.heads_k;
-    for (int w = 0; w < 2; ++w) a.parts[w] = (a.heads[w] + per - 1) / per;
+    for (int w = 0; w < 2; ++w) a.steps[w] = (a.heads[w] + per - 1) / per;
+    a.row_bytes = (d.rot_dim * 4 + 15) / 16 * 16;
     return a;
 }
 
-// Blocks of the backward pass, and the queries' among them: as many as have a task
-// for each warp, shared by the heads.
-void plan_blocks(const cba_qk_norm_rope_desc_t &d, int *blocks, int *q_blocks) {
-    const QkArgs a = base_args(d, nullptr, nullptr, kBwdSteps);
-    long long need[2];
-    for (int w = 0; w < 2; ++w) need[w] = ((long long)a.tokens * a.parts[w] + kWarps - 1) / kWarps;
-    if (need[0] + need[1] > kBwdBlocks) {
-        const long long all = need[0] + need[1];
-        need[1] = d.heads_k ? std::max(1LL, kBwdBlocks * need[1] / all) : 0;
-        need[0] = kBwdBlocks - need[1];
+// Blocks, and the queries' among them: as many as have a token for each warp, or that the
+// SMs hold, shared by the steps.
+void plan_blocks(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, bool bwd, int *blocks, int *q_blocks) {
+    const int most = kQkPerSm * kNumSMs;
+    const long long each = ((long long)a.tokens + kWarps - 1) / kWarps;
+    long long need[2] = {each, d.heads_k ? each : 0};
+    if (need[0] + need[1] > most) {
+        const long long all = a.steps[0] + a.steps[1];
+        need[1] = d.heads_k ? std::min(each, std::max(1LL, (most * (long long)a.steps[1] + all / 2) / all)) : 0;
+        need[0] = std::min(each, most - need[1]);
     }
     *q_blocks = (int)need[0];
     *blocks = (int)(need[0] + need[1]);
@@ -440,10 +542,22 @@ cudaError_t dispatch(const cba_qk_norm_rope_desc_t &d, F f) {
     return d.type == CBA_F32 ? param(0.f) : d.type == CBA_F16 ? param(__half{}) : param(__nv_bfloat16{});
 }
 
-cudaError_t launch_fwd(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, cudaStream_t st) {
-    const long long tasks = (long long)a.tokens * (a.parts[0] + a.parts[1]);
+template <bool BWD>
+cudaError_t launch(const cba_qk_norm_rope_desc_t &d, QkArgs a, int *blocks, cudaStream_t st) {
+    plan_blocks(d, a, BWD, blocks, &a.q_blocks);
     return dispatch(d, [&](auto t, auto p, auto pairs) {
-        qk_fwd_kernel<decltype(t), decltype(p), pairs()><<<(unsigned)((tasks + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a);
+        using T = decltype(t);
+        using P = decltype(p);
+        constexpr int PAIRS = decltype(pairs)::value, AHEAD = qk_ahead(BWD);
+        constexpr auto kern = qk_kernel<T, P, PAIRS, BWD>;
+        const int step = (BWD ? 2 : 1) * Lane<PAIRS>::NV * (int)sizeof(T) * 256;
+        a.warp_bytes = AHEAD * step + (AHEAD + 1) * a.row_bytes + (PAIRS == PAIRS_ANY ? 1024 : 0);
+        // (backward: the block's sums at the end)
+        const int bytes = std::max(kWarps * a.warp_bytes, BWD ? kWarps * 1024 : 0);
+        const int most = kWarps * (AHEAD * step + (AHEAD + 1) * kQkMaxDim * 4 + 1024);
+        cudaError_t e = allow_smem<kern>(most);
+        if (e != cudaSuccess) return e;
+        kern<<<(unsigned)*blocks, kWarps * 32, bytes, st>>>(a);
         return cudaGetLastError();
     });
 }
@@ -481,7 +595,7 @@ int cba_qk_norm_rope_forward(const cba_qk_norm_rope_desc_t *d, const void *q, co
     rc = check_shared(*d, need, 4, gamma_q, gamma_k, table, pos);
     if (rc != CBA_OK) return rc;
     if (d->len == 0) return CBA_OK;
-    QkArgs a = base_args(*d, table, pos, kSteps);
+    QkArgs a = base_args(*d, table, pos);
     a.x[0] = q; a.x[1] = k;
     a.gamma[0] = gamma_q; a.gamma[1] = gamma_k;
     a.out[0] = yq; a.out[1] = yk;
@@ -491,14 +605,15 @@ int cba_qk_norm_rope_forward(const cba_qk_norm_rope_desc_t *d, const void *q, co
     strides_of(*d, d->yk, d->heads_k, a.so[1]);
     cudaGetLastError();
     cudaError_t e = select_device_of(yq);
-    if (e == cudaSuccess) e = launch_fwd(*d, a, static_cast<cudaStream_t>(stream));
+    int blocks;
+    if (e == cudaSuccess) e = launch<false>(*d, a, &blocks, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
 }
 
 size_t cba_qk_norm_rope_workspace_bytes(const cba_qk_norm_rope_desc_t *d) {
     if (check_desc(d) != CBA_OK) return 0;
     int blocks, q_blocks;
-    plan_blocks(*d, &blocks, &q_blocks);
+    plan_blocks(*d, base_args(*d, nullptr, nullptr), true, &blocks, &q_blocks);
     return std::max((size_t)256, ((size_t)blocks * d->dim * sizeof(float) + 255) / 256 * 256);
 }
 
@@ -517,7 +632,7 @@ int cba_qk_norm_rope_backward(const cba_qk_norm_rope_desc_t *d, const void *q, c
     if (!aligned_to(dgamma_q, 4) || !aligned_to(dgamma_k, 4)) return CBA_ERR_ALIGN;
     if (!workspace || workspace_bytes < cba_qk_norm_rope_workspace_bytes(d)) return CBA_ERR_WORKSPACE;
     if (!aligned_to(workspace, 256)) return CBA_ERR_ALIGN;
-    QkArgs a = base_args(*d, table, pos, d->norm ? kBwdSteps : kSteps);
+    QkArgs a = base_args(*d, table, pos);
     a.sign = -1.f;
     a.x[0] = d->norm ? q : dyq; a.x[1] = d->norm ? k : dyk;
     a.dy[0] = dyq; a.dy[1] = dyk;
@@ -532,22 +647,19 @@ int cba_qk_norm_rope_backward(const cba_qk_norm_rope_desc_t *d, const void *q, c
     cudaGetLastError();
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = select_device_of(workspace);
+    int blocks = 0;
     if (e == cudaSuccess && !d->norm) {
-        if (d->len > 0) e = launch_fwd(*d, a, st);
+        if (d->len > 0) e = launch<false>(*d, a, &blocks, st);
         return e == cudaSuccess ? CBA_OK : report_cuda_error(e);
     }
-    int blocks;
-    plan_blocks(*d, &blocks, &a.q_blocks);
     a.partial = static_cast<float *>(workspace);
-    if (e == cudaSuccess && blocks > 0)
-        e = dispatch(*d, [&](auto t, auto p, auto pairs) {
-            qk_bwd_kernel<decltype(t), decltype(p), pairs()><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
-            return cudaGetLastError();
-        });
+    if (e == cudaSuccess && d->len > 0) e = launch<true>(*d, a, &blocks, st);
     if (e == cudaSuccess && (dgamma_q || dgamma_k)) {
         const dim3 grid((unsigned)(d->dim + 31) / 32, 2);
-        if (blocks > 0)
-            e = launch_pdl(qk_dgamma_kernel, grid, dim3(1024), 0, st, (const float *)a.partial, d->dim, a.q_blocks, blocks,
+        int q_blocks;
+        plan_blocks(*d, a, true, &blocks, &q_blocks);
+        if (d->len > 0)
+            e = launch_pdl(qk_dgamma_kernel, grid, dim3(1024), 0, st, (const float *)a.partial, d->dim, q_blocks, blocks,
                            dgamma_q, dgamma_k, d->accumulate);
         else
             qk_dgamma_kernel<<<grid, 1024, 0, st>>>(a.partial, d->dim, 0, 0, dgamma_q, dgamma_k, d->accumulate);

@@ -120,7 +120,7 @@ def test_qk_rejects_a_bad_descriptor(lib, bad):
 
 
 def test_qk_limits(lib):
-    for kw in (dict(dim=60, rot_dim=0), dict(dim=264, rot_dim=0), dict(param_type=cba.CBA_F16), dict(batch=1 << 20, len=1 << 10),
+    for kw in (dict(dim=60, rot_dim=0), dict(dim=264, rot_dim=0), dict(param_type=cba.CBA_F16), dict(batch=1 << 21, len=1 << 10),
                dict(q=ST(1 << 40, 256, 64))):
         d = qk(**kw)
         assert qk_fwd(lib, d) == cba.CBA_ERR_UNSUPPORTED and qk_bwd(lib, d) == cba.CBA_ERR_UNSUPPORTED, kw
