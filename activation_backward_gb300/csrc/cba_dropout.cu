@@ -55,12 +55,22 @@ __device__ __forceinline__ float drop(const DrArgs &a, float x, unsigned word) {
     return word >= a.bound && !a.all ? x * a.scale : 0.f;
 }
 
+// i / d and the remainder; in 32 bits where they do (a 64-bit division takes five times as long).
+__device__ __forceinline__ void divide(long long i, long long d, bool small, long long &q, long long &r) {
+    if (small) {
+        const unsigned n = (unsigned)i / (unsigned)d;
+        q = n, r = (unsigned)i - n * (unsigned)d;
+    } else {
+        q = i / d, r = i - q * d;
+    }
+}
+
 // Vectors of 16 bytes: rows without gaps (FLAT: the tensors are one run of n elements),
 // or rows of whole vectors.  Two vectors of a thread in flight.
 template <typename T, bool RES, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(const DrArgs a) {
     constexpr int V = 16 / sizeof(T), U = 2;
-    const long long vecs = FLAT ? a.n / V : a.n / V;
+    const long long vecs = a.n / V;
     const long long v0 = (long long)blockIdx.x * (256 * U) + threadIdx.x;
     Pack<T, V> x[U], r[U];
     long long oy[U];
@@ -72,7 +82,9 @@ __global__ void __launch_bounds__(256) dropout_vec_kernel(const DrArgs a) {
         if (FLAT) {
             ox = orr = oy[u] = v * V;
         } else {
-            const long long per = a.cols / V, row = v / per, c = (v - row * per) * V;
+            long long row, c;
+            divide(v, a.cols / V, a.n < (1LL << 32), row, c);
+            c *= V;
             ox = row * a.ld_x + c, orr = row * a.ld_res + c, oy[u] = row * a.ld_y + c;
         }
         x[u] = *reinterpret_cast<const Pack<T, V> *>(static_cast<const T *>(a.x) + ox);
@@ -117,12 +129,22 @@ __global__ void __launch_bounds__(256) dropout_any_kernel(const DrArgs a) {
     if (i0 >= a.n) return;
     float x[4], r[4];
     long long oy[4];
+    long long row, c;
+    divide(i0 + lane, a.cols, a.n < (1LL << 32), row, c);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const long long i = i0 + j * 32 + lane;
+        if (j > 0) {
+            c += 32;
+            if (a.cols >= 32) {
+                if (c >= a.cols) c -= a.cols, ++row;
+            } else {
+                const unsigned n = (unsigned)c / (unsigned)a.cols;
+                row += n, c -= n * a.cols;
+            }
+        }
         oy[j] = -1;
         if (i >= a.n) continue;
-        const long long row = i / a.cols, c = i - row * a.cols;
         x[j] = to_f32(static_cast<const T *>(a.x)[row * a.ld_x + c]);
         if (RES) r[j] = to_f32(static_cast<const T *>(a.res)[row * a.ld_res + c]);
         oy[j] = row * a.ld_y + c;
