@@ -240,15 +240,26 @@ __global__ void __launch_bounds__(kAfThreads, 1)
         sb.abort_flag = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == 1) {
-        ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 512);
-        ptx::tmem_relinquish();
+    if (warp == 0) {
+        // the loads begin while TMEM is allocated
+        if (lane == 0) {
+            ptx::prefetch_map(&tq);
+            ptx::prefetch_map(&tk);
+            ptx::prefetch_map(&tv);
+        }
+        __syncwarp();
+        ptx::named_bar_arrive(1, kAfThreads);
+    } else {
+        if (warp == 1) {
+            ptx::tmem_alloc(ptx::smem_u32(&sb.tmem_base), 512);
+            ptx::tmem_relinquish();
+        }
+        ptx::tc_fence_before();
+        ptx::named_bar_sync(1, kAfThreads);
+        ptx::tc_fence_after();
     }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
     ptx::griddep_launch_dependents();
-    const uint32_t tmem = sb.tmem_base;
+    const uint32_t tmem = warp == 0 ? 0 : *const_cast<volatile uint32_t *>(&sb.tmem_base);
     // S of the two tiles (P over its first half), then o of the two
     const uint32_t tS = tmem, tO = tmem + 256;
     volatile int *ab = &sb.abort_flag;

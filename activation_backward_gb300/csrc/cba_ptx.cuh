@@ -356,6 +356,16 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool pred) {
     return r != 0;
 }
 
+// Arrives on a named barrier without waiting for it.
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// Asks for a tensor map (of the kernel's arguments) ahead of its first copy.
+__device__ __forceinline__ void prefetch_map(const void *tmap) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // Named barrier over `count` threads.
 __device__ __forceinline__ void named_bar_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
