@@ -65,6 +65,7 @@ struct AfArgs {
     int heads_at_once; // causal: heads (of all sequences) whose heaviest pairs come first together
     int chunk, chunks; // steps of an item at most; items per pair at most
     int units, items;
+    int maps;          // there are queries and keys, and so tensor maps
     void *o;
     float *lse;
     long long so[3];
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
     }
     if (warp == 0) {
         // the loads begin while TMEM is allocated
-        if (lane == 0) {
+        if (lane == 0 && a.maps) {
             ptx::prefetch_map(&tq);
             ptx::prefetch_map(&tk);
             ptx::prefetch_map(&tv);
@@ -847,8 +848,6 @@ int check_desc(const cba_attention_desc_t *d) {
             if (v[j] >= (1LL << 38)) return CBA_ERR_UNSUPPORTED;
         }
     }
-    const double rows = d->packed ? (double)d->total_q : (double)d->batch * d->len_q;
-    if (rows * d->heads_q >= 4294967296.0) return CBA_ERR_UNSUPPORTED;
     return CBA_OK;
 }
 
@@ -895,18 +894,20 @@ int check_attn(const cba_attention_desc_t *d, AfPlan *p) {
     const long long len_q = d->packed ? std::min((long long)d->len_q, d->total_q) : d->len_q;
     const long long len_k = d->packed ? std::min((long long)d->len_k, d->total_k) : d->len_k;
     const long long two = 2 * p->tt;
-    long long pairs = (len_q + two - 1) / two, units = pairs * d->batch * p->hparts;
+    long long pairs = (len_q + two - 1) / two;
     p->slots = 0;
     if (d->packed) {
         const long long by_tokens = d->total_q / two + d->batch;
-        if (pairs * d->batch > kLoose * by_tokens) p->slots = 1, pairs = by_tokens, units = pairs * p->hparts;
+        if (pairs * d->batch > kLoose * by_tokens) p->slots = 1, pairs = by_tokens;
     }
-    if (units >= (1LL << 24)) return CBA_ERR_UNSUPPORTED;
+    const double all_units = (double)pairs * (p->slots ? 1 : d->batch) * p->hparts;
+    if (all_units >= (double)(1LL << 30)) return CBA_ERR_UNSUPPORTED;
+    const long long units = (long long)all_units;
     p->pairs = (int)pairs;
     p->units = (int)units;
     // keys and values of the heads that are worked on together stay in the L2
     const double bytes = 4.0 * std::max(1LL, len_k) * d->dim;
-    p->heads_at_once = (int)std::min((double)p->hparts * d->batch, std::max(16.0, 48e6 / bytes));
+    p->heads_at_once = (int)std::min((double)p->hparts * (p->slots ? 1 : d->batch), std::max(16.0, 48e6 / bytes));
     p->chunk = std::max(1, (int)((len_k + kT - 1) / kT));
     p->chunks = 1;
     if (units > 0 && units < 2 * kNumSMs && p->chunk > 4) {
@@ -942,9 +943,11 @@ bool af_map(CUtensorMap *m, const void *base, const cba_attention_desc_t &d, int
 
 template <int DP, bool BF16>
 cudaError_t af_launch(const AfPlan &p, const AfArgs &a, const CUtensorMap *tm, cudaStream_t st) {
+    // without queries there is nothing but the status to be written
+    if (a.items == 0) return cudaMemsetAsync(a.status, 0, sizeof(unsigned), st);
     cudaError_t e = allow_smem<attn_fwd_kernel<DP, BF16>>((int)Af<DP>::SMEM);
     if (e != cudaSuccess) return e;
-    attn_fwd_kernel<DP, BF16><<<(unsigned)std::max(1, a.items), kAfThreads, Af<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], a);
+    attn_fwd_kernel<DP, BF16><<<(unsigned)a.items, kAfThreads, Af<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], a);
     e = cudaGetLastError();
     if (e == cudaSuccess && p.chunks > 1)
         e = launch_pdl(attn_fwd_join_kernel<BF16>, dim3((unsigned)p.units * 2), dim3(256), 0, st, a, DP);
@@ -989,7 +992,7 @@ int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const vo
     a.causal = d->causal;
     // S is negated for a negative scale, so that its largest is the exponent's; a scale of 0 becomes one whose
     // products with fp32 logits of size vanish, and with the masked -infinity do not become NaN
-    a.cs = d->scale == 0.f ? 1e-37f : std::fabs(d->scale) * kLog2e;
+    a.cs = d->scale == 0.f ? 1e-37f : std::min(std::fabs(d->scale) * kLog2e, 3e38f);
     a.negative = d->scale < 0.f;
     a.hp = p.hp; a.hparts = p.hparts; a.tt = p.tt; a.pairs = p.pairs; a.slots = p.slots;
     a.heads_at_once = p.heads_at_once; a.chunk = p.chunk; a.chunks = p.chunks;
@@ -1005,7 +1008,8 @@ int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const vo
     fill_strides(*d, d->o, d->heads_q, tq, a.so);
     // without queries (or keys) the kernel loads nothing of them
     CUtensorMap tm[3] = {};
-    if (tq > 0 && tk > 0 &&
+    a.maps = tq > 0 && tk > 0;
+    if (a.maps &&
         (!af_map(&tm[0], q, *d, d->heads_q, tq, sq, p, true) || !af_map(&tm[1], k, *d, d->heads_kv, tk, sk, p, false) ||
          !af_map(&tm[2], v, *d, d->heads_kv, tk, sv, p, false)))
         return CBA_ERR_UNSUPPORTED;

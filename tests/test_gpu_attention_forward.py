@@ -397,3 +397,78 @@ def test_two_streams_at_once(cuda_lib):
     for w, gs in zip(want, got):
         for g in gs:
             assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
+
+
+# ---- ends of the ranges
+
+def test_no_tokens_at_all(cuda_lib):
+    """Packed calls without queries, or with bounds of 0, write nothing and leave a status that says so."""
+    k = torch.randn(20, 1, 64, device="cuda").to(BF)
+    cu = torch.tensor([0, 0, 0], dtype=torch.int32, device="cuda")
+    ck = torch.tensor([0, 9, 20], dtype=torch.int32, device="cuda")
+    run(k[:0], k, k, 0.125, True, cu_q=cu, cu_k=ck, sequences=2)
+    o, lse = run(k, k, k, 0.125, True, cu_q=ck, cu_k=ck, sequences=2, max_q=0, max_k=0)
+    assert (o == 9).all() and (lse == 9).all()
+    o, lse = run(k, k[:0], k[:0], 0.125, False, cu_q=ck, cu_k=cu, sequences=2)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_starts_that_are_wrong_stay_in_the_tensors(cuda_lib):
+    """Values of cu past the tensors, negative or falling give some result, and rows of one good sequence its own."""
+    q = torch.randn(300, 2, 64, device="cuda").to(BF)
+    for starts in ([0, 1 << 30, 300], [-5, 200, 100, 1 << 31 - 1], [300, 0, 300]):
+        cu = torch.tensor(starts, dtype=torch.int64).clamp(max=2 ** 31 - 1).int().cuda()
+        for bound in ({}, dict(max_q=40, max_k=40)):
+            run(q, q, q, 0.125, True, cu_q=cu, cu_k=cu, sequences=len(starts) - 1, **bound)
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38, 1e-42])
+def test_scales_at_the_ends_of_fp32(cuda_lib, scale):
+    """Logits that overflow are infinite, equal or none: a row of zeros keeps equal shares."""
+    q, k = torch.zeros(1, 3, 1, 64, device="cuda", dtype=BF), torch.zeros(1, 200, 1, 64, device="cuda", dtype=BF)
+    v = torch.randn(1, 200, 1, 64, device="cuda").to(BF)
+    o, lse = run(q, k, v, scale, False)
+    assert torch.allclose(o[0, :, 0].double(), v[0, :, 0].double().mean(0).expand(3, 64), atol=2.0 ** -8)
+    assert torch.allclose(lse.double(), torch.full_like(lse.double(), math.log(200)), atol=1e-5)
+
+
+def test_many_sequences_of_one_token(cuda_lib):
+    """4000 packed sequences of a token each, and one long one: slots and search past a warp's width."""
+    lens = [1] * 4000 + [700] + [0] * 30 + [1] * 70
+    rng = np.random.default_rng(1)
+    cu = np.cumsum([0] + lens)
+    q, k, v = (place(rng.normal(size=(1, int(cu[-1]), 1, 64)), "bshd", BF)[0] for _ in range(3))
+    c = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    for bound in ({}, dict(max_q=700, max_k=700)):
+        o, lse = run(q, k, v, 0.125, True, cu_q=c, cu_k=c, sequences=len(lens), **bound)
+        ones = [i for i in range(4000)] + list(range(4700, 4770))
+        assert torch.equal(o[ones], v[ones])
+        wo, wl, bo, bl = bars(f8(q[4000:4700]), f8(k[4000:4700]), f8(v[4000:4700]), 0.125, True, BF)
+        check(o[4000:4700], wo, bo, "o")
+        check(lse[:, 4000:4700], wl, bl, "lse")
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """Keys and values of a cache whose tokens lie 2^16 elements apart: offsets past 2^31 elements."""
+    n, gap = 40000, 1 << 16
+    big = torch.empty(n * gap, dtype=BF, device="cuda")
+    k = big.as_strided((1, n, 1, 64), (n * gap, gap, 64, 1))
+    v = big.as_strided((1, n, 1, 64), (n * gap, gap, 64, 1), 4096)
+    k.copy_(torch.randn(1, n, 1, 64, device="cuda").to(BF))
+    v.copy_(torch.randn(1, n, 1, 64, device="cuda").to(BF))
+    q = torch.randn(1, 5, 1, 64, device="cuda").to(BF)
+    a, la = run(q, k, v, 0.125, True)
+    b, lb = run(q, k.contiguous(), v.contiguous(), 0.125, True)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    del k, v, big
+    # o and q the same way
+    big = torch.empty(n * gap, dtype=BF, device="cuda")
+    q = big.as_strided((1, n, 1, 64), (n * gap, gap, 64, 1))
+    o = big.as_strided((1, n, 1, 64), (n * gap, gap, 64, 1), 4096)
+    q.copy_(torch.randn(1, n, 1, 64, device="cuda").to(BF))
+    kv = torch.randn(1, 50, 1, 64, device="cuda").to(BF)
+    d = cba.make_attention_desc(q, kv, kv, o, scale=0.125)
+    ws = torch.empty(cba.cba_attention_forward_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    cba.cba_attention_forward(d, q, kv, kv, None, None, o, None, ws)
+    want, _ = run(q.contiguous(), kv, kv, 0.125, False)
+    assert cba.cba_get_status(ws) == cba.CBA_OK and torch.equal(o, want)

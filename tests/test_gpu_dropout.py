@@ -141,3 +141,18 @@ def test_a_replayed_graph_draws_anew(cuda_lib):
 
 def test_empty(cuda_lib):
     assert tr.dropout(torch.empty(0, 16, device="cuda"), 0.5, 1).shape == (0, 16)
+
+
+def test_more_than_2_to_the_31_elements(cuda_lib):
+    """Past 2^32 elements, with and without gaps between rows: the ends against the oracle."""
+    cols = 4099
+    rows_n = (1 << 32) // cols + 3
+    x = torch.ones(rows_n, cols + 1, dtype=F16, device="cuda")
+    for t in (x[:, :cols], x.view(-1)[: rows_n * cols].view(rows_n, cols)):
+        y = tr.dropout(t, 0.5, 21, 7)
+        for r in (0, rows_n // 2, rows_n - 1):
+            first = r * cols // 4 * 4
+            words = T.philox(21, np.uint64(7) + np.arange(first // 4, (r * cols + cols + 3) // 4, dtype=np.uint64)).reshape(-1)
+            keep = words[r * cols - first:][:cols] >= np.uint64(1 << 31)
+            assert np.array_equal(f8(y[r]), np.where(keep, 2.0, 0.0))
+        del y

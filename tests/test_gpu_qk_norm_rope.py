@@ -273,3 +273,20 @@ def test_same_bits_graphs_and_streams(cuda_lib):
     got = [t.clone() for t in (dq, dk, gq, gk)]
     want = tr.qk_norm_rope_backward(q, k, dyq, dyk, table=table)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """Tokens that lie 2^16 elements apart: offsets past 2^31 elements, loads and stores."""
+    n, gap = 40000, 1 << 16
+    big = torch.empty(n * gap, dtype=BF, device="cuda")
+    q = big.as_strided((n, 2, 64), (gap, 64, 1))
+    y = big.as_strided((n, 2, 64), (gap, 64, 1), 4096)
+    q.copy_(torch.randn(n, 2, 64, device="cuda").to(BF))
+    table, gamma = make_table(n, 64), torch.rand(64, device="cuda") + 0.5
+    want, _ = tr.qk_norm_rope(q.contiguous(), None, gamma_q=gamma, table=table)
+    d = cba.make_qk_norm_rope_desc(q, None, yq=y, positions=n)
+    cba.cba_qk_norm_rope_forward(d, q, None, gamma, None, table, None, y, None)
+    assert torch.equal(y, want)
+    got = tr.qk_norm_rope_backward(q, None, y, None, gamma_q=gamma, table=table)
+    want = tr.qk_norm_rope_backward(q.contiguous(), None, y.contiguous(), None, gamma_q=gamma, table=table)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])

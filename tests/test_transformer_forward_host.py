@@ -48,7 +48,8 @@ def test_attention_rejects_a_bad_descriptor(lib, bad):
 
 
 def test_attention_limits(lib):
-    for kw in (dict(type=cba.CBA_F32), dict(dim=136), dict(dim=60), dict(len_q=1 << 31 - 1), dict(batch=1 << 24, len_q=1 << 14)):
+    for kw in (dict(type=cba.CBA_F32), dict(dim=136), dict(dim=60), dict(len_q=1 << 31 - 1), dict(batch=1 << 24, len_q=1 << 14),
+               dict(batch=(1 << 31) - 1, len_q=1 << 30, heads_q=(1 << 31) - 1, heads_kv=(1 << 31) - 1)):
         assert at_fwd(lib, at(**kw)) == cba.CBA_ERR_UNSUPPORTED, kw
     d = at(o=ST(1 << 20, 260, 64))
     assert at_fwd(lib, d) == cba.CBA_ERR_ALIGN and lib.cba_attention_forward_workspace_bytes(ctypes.byref(d)) == 0
