@@ -65,11 +65,14 @@ __device__ __forceinline__ void divide(long long i, long long d, bool small, lon
     }
 }
 
+constexpr int kVectors = 4;
+
 // Vectors of 16 bytes: rows without gaps (FLAT: the tensors are one run of n elements),
-// or rows of whole vectors.  Two vectors of a thread in flight.
+// or rows of whole vectors.  (65536 x 2048 bf16 with a residual: 4 vectors of a thread in
+// flight 134 us, 2 138, 1 165.)
 template <typename T, bool RES, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(const DrArgs a) {
-    constexpr int V = 16 / sizeof(T), U = 2;
+    constexpr int V = 16 / sizeof(T), U = kVectors;
     const long long vecs = a.n / V;
     const long long v0 = (long long)blockIdx.x * (256 * U) + threadIdx.x;
     Pack<T, V> x[U], r[U];
@@ -170,7 +173,7 @@ cudaError_t dropout_launch(const DrArgs &a, cudaStream_t st) {
     const bool flat = a.ld_x == a.cols && a.ld_y == a.cols && (!RES || a.ld_res == a.cols);
     const bool bases = aligned_to(a.x, 16) && aligned_to(a.y, 16) && (!RES || aligned_to(a.res, 16));
     const bool rows = a.cols % V == 0 && vec(a.x, a.ld_x) && vec(a.y, a.ld_y) && (!RES || vec(a.res, a.ld_res));
-    const long long blocks = (a.n + 512 * V - 1) / (512 * V);
+    const long long blocks = (a.n + 256 * kVectors * V - 1) / (256 * kVectors * V);
     if (flat && bases) dropout_vec_kernel<T, RES, true><<<(unsigned)blocks, 256, 0, st>>>(a);
     else if (rows) dropout_vec_kernel<T, RES, false><<<(unsigned)blocks, 256, 0, st>>>(a);
     else dropout_any_kernel<T, RES><<<(unsigned)((a.n + 1023) / 1024), 256, 0, st>>>(a);
