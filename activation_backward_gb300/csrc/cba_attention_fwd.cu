@@ -21,10 +21,24 @@
 // item before.  Where there are fewer pairs of tiles than SMs the keys are cut, each
 // item leaves fp32 sums, and a second kernel joins them in the order of the keys.
 //
+// Measured (us; rates count the products of the pairs that the mask allows):
+//   8192 tokens, 32/8 heads of 128, causal, bf16   346 after a pause, 368 in turn with other
+//       calls: 1.59 and 1.49 PFLOP/s.  The chain S -> P -> o of the two tiles bounds it: 3300
+//       cycles a step of the pair, of which the tensor cores have products for 2048
+//   9 documents of 8192 tokens, 16/4 heads of 128  58: the items of the longest one
+//   32 x 676 tokens, 8 heads of 64, f16            64: the same chain with half the products;
+//       the exponentials' unit is active for 29% of the cycles, issue slots are taken for 41%
+//   8 x 1 tokens over 8192 keys, 32/8 heads of 128 53: the keys and values at 5.1 TB/s, the
+//       second kernel included
+//   2 x 169 tokens, 8 heads of 64, bf16            10.2: one launch, two steps
+// Tried: four warpgroups with half a row each (420 in the first case: they exchange maxima), both
+// warpgroups on each tile (370), S two steps ahead in steps of 64 keys (430: products of 64 columns
+// take more than half the time of 128), waits that spin in place of try_wait's own (367).
+//
 // Roles: warp 0 loads (TMA) and takes items, warp 1 (past dim 64 warps 1 and 2) issues
-// the products, warps 4-7 and 8-11 are the two tiles' warpgroups.  Every wait is bounded (2 s); on a timeout the
-// block sets the workspace's status bit, stops, waits (bounded) for its copies in
-// flight, frees its TMEM and returns.
+// the products, warps 4-7 and 8-11 are the two tiles' warpgroups.  Every wait is
+// bounded (2 s); on a timeout the block sets the workspace's status bit, stops, waits
+// (bounded) for its copies in flight, frees its TMEM and returns.
 #include <cuda.h>
 
 #include <algorithm>
@@ -852,7 +866,9 @@ int check_desc(const cba_attention_desc_t *d) {
 }
 
 // Packed: pairs are counted by the tokens where counting up to the bounds would look at
-// more than this many times as many.
+// more than this many times as many.  (64 documents of 700 to 1024 tokens, 32 heads of 128,
+// causal: with bounds of all tokens 650 us by the tokens and 3170 up to the bounds; with tight
+// ones 650 and 600, since then a head's longest pairs come first.)
 constexpr long long kLoose = 2;
 
 struct AfPlan {
@@ -861,7 +877,8 @@ struct AfPlan {
 };
 
 // The heads side by side in a tile: the most of a group that leave no more than 8 of its
-// 128 rows empty.
+// 128 rows empty.  (32/8 heads of 128, single tokens over 8 x 8192 keys: 56 us, with one head
+// a tile 163; 2 x 4096 tokens, 28/4 heads, causal, where the keys are read often anyway: 191, 198.)
 int heads_in_tile(int group) {
     for (int d = std::min(group, kT); d > 1; --d)
         if (group % d == 0 && kT / d * d >= kT - 8) return d;
@@ -870,7 +887,9 @@ int heads_in_tile(int group) {
 
 // Steps of an item at most, for `units` pairs of `n` steps, `all` of them together, that are
 // equally long (even) or of any lengths up to that.  A step, a begun item and a joined one are
-// taken to cost 1, 1.5 and a quarter, and the second kernel 3.
+// taken to cost 1, 1.5 and a quarter, and the second kernel 3.  (32/8 heads of 128: single
+// tokens over 8 x 8192 keys 56 us, not cut 91, over 65536 keys 68 and 638; 256 tokens over 8192,
+// 16 heads 70 and 109.)
 int plan_chunk(double units, int n, double all, bool even) {
     int best = n;
     double least = 0;
@@ -905,7 +924,9 @@ int check_attn(const cba_attention_desc_t *d, AfPlan *p) {
     const long long units = (long long)all_units;
     p->pairs = (int)pairs;
     p->units = (int)units;
-    // keys and values of the heads that are worked on together stay in the L2
+    // Keys and values of the heads that are worked on together stay in the L2.  (Causal: 8 x 8192 tokens,
+    // 32/8 heads of 128: 2770 us, all heads together 2920; 64 documents of 700 to 1024 tokens, 32 heads: 600,
+    // all 677, with 4 together, whose light ends leave SMs idle, 750.)
     const double bytes = 4.0 * std::max(1LL, len_k) * d->dim;
     p->heads_at_once = (int)std::min((double)p->hparts * (p->slots ? 1 : d->batch), std::max(16.0, 48e6 / bytes));
     p->chunk = std::max(1, (int)((len_k + kT - 1) / kT));

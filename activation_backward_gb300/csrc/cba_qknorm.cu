@@ -12,6 +12,10 @@
 // heads, 32 / lanes of them a step; lanes copy their own elements asynchronously to
 // shared memory a few steps ahead, and the warp its tokens' rows of the table.  Blocks
 // are the queries' or the keys', in the proportion of their steps.
+//
+// Measured (us), 4 x 8192 tokens, 32/8 heads of 128, bf16: forward 134 (0.74 of the copy rate; issue
+// slots 51% taken), backward 185, of which 6 for the sum of dgamma's rows (0.81; 58%).  2 x 169
+// tokens, 8 heads of 64: 5.8 and 9.7, one and two launches.
 #include <algorithm>
 #include <cmath>
 
@@ -25,7 +29,8 @@ namespace {
 
 constexpr int kQkMaxDim = 256;
 constexpr int kWarps = 8;                     // of a block
-// Steps in flight; blocks per SM.
+// Steps in flight; blocks per SM.  (Above: forward 4 steps 134 us, 6 136; backward 2 steps 185, 4
+// 192; 3 blocks, whose registers spill, 195 and 340; without shared memory 190 and 294.)
 __host__ __device__ constexpr int qk_ahead(bool bwd) { return bwd ? 2 : 4; }
 constexpr int kQkPerSm = 2;
 
