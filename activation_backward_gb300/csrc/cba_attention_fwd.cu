@@ -28,7 +28,7 @@
 //   9 documents of 8192 tokens, 16/4 heads of 128  58: the items of the longest one
 //   32 x 676 tokens, 8 heads of 64, f16            64: the same chain with half the products;
 //       the exponentials' unit is active for 29% of the cycles, issue slots are taken for 41%
-//   8 x 1 tokens over 8192 keys, 32/8 heads of 128 53: the keys and values at 5.1 TB/s, the
+//   8 x 1 tokens over 8192 keys, 32/8 heads of 128 51: the keys and values at 5.2 TB/s, the
 //       second kernel included
 //   2 x 169 tokens, 8 heads of 64, bf16            10.2: one launch, two steps
 // Tried: four warpgroups with half a row each (420 in the first case: they exchange maxima), both
@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kAfThreads, 1)
 }
 
 // Joins the items of a tile that was cut: weights exp(m_i - max m), in the items' order.
-// A block per tile, a thread per row and 8 columns.
+// Blocks (., y) per tile, a thread per row and 8 columns.
 template <bool BF16>
 __global__ void __launch_bounds__(256) attn_fwd_join_kernel(const AfArgs a, int dp) {
     const int unit = blockIdx.x >> 1, x = blockIdx.x & 1;
@@ -799,24 +799,37 @@ __global__ void __launch_bounds__(256) attn_fwd_join_kernel(const AfArgs a, int 
     if (!w.live || w.used == 1) return;
     constexpr float shift = BF16 ? 0.f : kHalfShift;
     const int first = w.t0 + x * a.tt, rows = max(0, min(a.tt, w.lq - first)) * a.hp, cols = a.dim / 8;
-    for (int i = threadIdx.x; i < rows * cols; i += 256) {
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * cols; i += gridDim.y * 256) {
         const int r = i % rows, c = i / rows;
         float m = -INFINITY;
         const long long slot0 = (long long)unit * a.chunks * 2 + x;
-        for (int j = 0; j < w.used; ++j) m = fmaxf(m, __ldcg(a.ml + (slot0 + 2 * j) * kT + r).x);
+        // (four items at a time, the last one again for those that are not there: loads in flight together)
+        auto at = [&](int j) { return slot0 + 2 * min(j, w.used - 1); };
+        for (int j0 = 0; j0 < w.used; j0 += 4)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) m = fmaxf(m, __ldcg(a.ml + at(j0 + u) * kT + r).x);
         float l = 0.f, v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        for (int j = 0; j < w.used; ++j) {
-            const long long slot = slot0 + 2 * j;
-            const float2 ml = __ldcg(a.ml + slot * kT + r);
-            if (ml.y == 0.f) continue;  // none of its keys: its sums may not have been written
-            const float f = ptx::ex2((ml.x - m) * a.cs);
-            l = fmaf(f, ml.y, l);
-            const float4 *at = reinterpret_cast<const float4 *>(a.part) + (slot * (dp / 4) + 2 * c) * kT + r;
-            const float4 y = __ldcg(at), z = __ldcg(at + kT);
-            v[0] = fmaf(f, y.x, v[0]), v[1] = fmaf(f, y.y, v[1]), v[2] = fmaf(f, y.z, v[2]), v[3] = fmaf(f, y.w, v[3]);
-            v[4] = fmaf(f, z.x, v[4]), v[5] = fmaf(f, z.y, v[5]), v[6] = fmaf(f, z.z, v[6]), v[7] = fmaf(f, z.w, v[7]);
+        for (int j0 = 0; j0 < w.used; j0 += 4) {
+            float2 ml[4];
+            float4 y[4], z[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 *from = reinterpret_cast<const float4 *>(a.part) + (at(j0 + u) * (dp / 4) + 2 * c) * kT + r;
+                ml[u] = __ldcg(a.ml + at(j0 + u) * kT + r);
+                y[u] = __ldcg(from), z[u] = __ldcg(from + kT);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                // (without keys l is 0, and the sums may not have been written)
+                if (j0 + u >= w.used || ml[u].y == 0.f) continue;
+                const float f = ptx::ex2((ml[u].x - m) * a.cs);
+                l = fmaf(f, ml[u].y, l);
+                v[0] = fmaf(f, y[u].x, v[0]), v[1] = fmaf(f, y[u].y, v[1]), v[2] = fmaf(f, y[u].z, v[2]);
+                v[3] = fmaf(f, y[u].w, v[3]), v[4] = fmaf(f, z[u].x, v[4]), v[5] = fmaf(f, z[u].y, v[5]);
+                v[6] = fmaf(f, z[u].z, v[6]), v[7] = fmaf(f, z[u].w, v[7]);
+            }
         }
         const bool none = l == 0.f;
         const float inv = none ? 0.f : 1.f / l;
@@ -886,18 +899,22 @@ int heads_in_tile(int group) {
 }
 
 // Steps of an item at most, for `units` pairs of `n` steps, `all` of them together, that are
-// equally long (even) or of any lengths up to that.  A step, a begun item and a joined one are
-// taken to cost 1, 1.5 and a quarter, and the second kernel 3.  (32/8 heads of 128: single
-// tokens over 8 x 8192 keys 56 us, not cut 91, over 65536 keys 68 and 638; 256 tokens over 8192,
-// 16 heads 70 and 109.)
-int plan_chunk(double units, int n, double all, bool even) {
+// equally long (even) or of any lengths up to that.  In steps of 1.7 us: a begun item is taken to
+// cost 1.5, its fp32 sums 1.7 times `part` (1: 256 rows of 128 elements) to be written and 0.0155 times
+// `part` to be read by all SMs, the second kernel 3; items of any lengths keep the SMs even but for half an
+// item, uncut ones, of which the heaviest come first, but for nothing.  (32/8 heads of 128: single tokens over
+// 8 x 8192 keys 51 us, not cut 86, over 65536 keys 52 and 634; causal, 2 x 1634 tokens, 2/1 heads 17
+// and 25; 1 x 4096, 16/4 heads, not cut 54, cut by 8 94.)
+int plan_chunk(double units, int n, double all, bool even, double part) {
     int best = n;
     double least = 0;
-    for (int k = 1; k <= std::min(64, (n + 3) / 4); ++k) {
+    for (int k = 1; k <= std::min(64, (n + 2) / 3); ++k) {
         const int c = (n + k - 1) / k;
-        const double rounds = std::ceil(units * k / kNumSMs);
-        const double t = (even ? rounds * (c + 1.5) : std::max(all / kNumSMs + 0.7 * c, (double)c) + 1.5 * rounds) +
-                         (k > 1 ? 3 + 0.25 * k : 0);
+        const double items = even || k == 1 ? units * k : std::min(units * k, all / c + 0.5 * units);
+        const double rounds = std::ceil(items / kNumSMs);
+        double t = even ? rounds * c : std::max(all / kNumSMs + (k > 1 ? 0.5 * c : 0), (double)c);
+        t += 1.5 * rounds;
+        if (k > 1) t += 1.7 * part * rounds + 3 + 0.1 * k + 0.0155 * part * items;
         if (k == 1 || t < least) best = c, least = t;
     }
     return best;
@@ -934,7 +951,10 @@ int check_attn(const cba_attention_desc_t *d, AfPlan *p) {
     if (units > 0 && units < 2 * kNumSMs && p->chunk > 4) {
         const int n = p->chunk;
         const bool even = !d->packed && (!d->causal || len_q <= two);
-        p->chunk = plan_chunk((double)units, n, (double)units * n * (d->causal && !even ? 0.5 : 1.0), even);
+        // the share of the pairs that a causal mask leaves
+        const double seen = !d->causal || even ? 1 : len_q <= len_k ? 1 - 0.5 * len_q / len_k : 0.5 * len_k / len_q;
+        const double part = (double)std::min(len_q, two) / two * p->dp / 128;
+        p->chunk = plan_chunk((double)units, n, seen * units * n, even, part);
         p->chunks = (n + p->chunk - 1) / p->chunk;
     }
     const size_t tiles = p->chunks > 1 ? (size_t)p->units * p->chunks * 2 : 0;
@@ -971,7 +991,8 @@ cudaError_t af_launch(const AfPlan &p, const AfArgs &a, const CUtensorMap *tm, c
     attn_fwd_kernel<DP, BF16><<<(unsigned)a.items, kAfThreads, Af<DP>::SMEM, st>>>(tm[0], tm[1], tm[2], a);
     e = cudaGetLastError();
     if (e == cudaSuccess && p.chunks > 1)
-        e = launch_pdl(attn_fwd_join_kernel<BF16>, dim3((unsigned)p.units * 2), dim3(256), 0, st, a, DP);
+        e = launch_pdl(attn_fwd_join_kernel<BF16>, dim3((unsigned)p.units * 2, (unsigned)(a.dim + 15) / 16), dim3(256), 0, st,
+                       a, DP);
     return e;
 }
 
