@@ -7,7 +7,7 @@
 //   table's row of the token's position, elements past rot_dim stay
 //
 // Each element is read once and each result written once: the bound is memory.  A
-// head's elements lie in the registers of 1 to 32 lanes, 8 (PAIRS_SPLIT: 8 of each
+// head's elements lie in the registers of 1 to 32 lanes, 8 (or 8 of each
 // half) to a lane, and its sums are shuffles.  A warp walks tokens and, within one, its
 // heads, 32 / lanes of them a step; lanes copy their own elements asynchronously to
 // shared memory a few steps ahead, and the warp its tokens' rows of the table.  Blocks
@@ -34,11 +34,18 @@ constexpr int kWarps = 8;                     // of a block
 __host__ __device__ constexpr int qk_ahead(bool bwd) { return bwd ? 2 : 4; }
 constexpr int kQkPerSm = 2;
 
-// Where the two elements of a pair lie.
+// Where the two elements of a pair lie.  A lane has 8 elements of a head, or, where dim is a multiple of
+// 16, 8 of either half: a step's sums and addresses cost what they cost for 8.  (2 x 8192 tokens, 16/4
+// heads of 128, half of each turned, forward and backward: 47.5 and 67 us, with 8 elements 60 and 77; pairs
+// (2j, 2j + 1): 48 and 68, with 8 elements 55 and 73.  2 x 16384, heads of 40: shuffles do not reach,
+// through shared memory 86 and 101.)
 enum Pairs {
-    PAIRS_LOCAL,  // (2j, 2j + 1), or no rotation: in one lane's 8 elements
-    PAIRS_SPLIT,  // (j, j + dim / 2) with dim / 2 a multiple of 8: a lane holds 8 of either half
-    PAIRS_ANY     // (j, j + rot / 2): exchanged through shared memory
+    PAIRS_LOCAL,   // (2j, 2j + 1), or no rotation: in one lane's 8 elements
+    PAIRS_LOCAL2,  // the same of either half
+    PAIRS_SPLIT,   // (j, j + dim / 2): in the two halves
+    PAIRS_LANES,   // (j, j + rot / 2) with rot / 2 a multiple of 8: in two lanes, exchanged by shuffles
+    PAIRS_LANES2,  // the same in the first half, with the second beside it
+    PAIRS_ANY      // (j, j + rot / 2): exchanged through shared memory
 };
 
 struct QkArgs {
@@ -110,10 +117,13 @@ __device__ __forceinline__ void store8(void *p, long long at, const Vec<T> &v) {
 // A lane's place in its head, and what turns its elements at one position.
 template <int PAIRS>
 struct Lane {
-    static constexpr int NV = PAIRS == PAIRS_SPLIT ? 2 : 1;  // vectors of 8 elements
+    [[maybe_unused]] static constexpr bool kLocal = PAIRS == PAIRS_LOCAL || PAIRS == PAIRS_LOCAL2;
+    [[maybe_unused]] static constexpr bool kLanes = PAIRS == PAIRS_LANES || PAIRS == PAIRS_LANES2;
+    static constexpr int NV = PAIRS == PAIRS_LOCAL || PAIRS == PAIRS_LANES || PAIRS == PAIRS_ANY ? 1 : 2;  // vectors of 8 elements
     static constexpr int NE = 8 * NV, N2 = NE / 2;
-    static constexpr int NC = PAIRS == PAIRS_LOCAL ? 4 : 8;  // angles
-    int slot, l, at[NV], lanes;
+    static constexpr int NC = PAIRS == PAIRS_LOCAL ? 4 : 8;   // angles
+    int slot, l, at[NV], lanes, other;  // other: kLanes: the lane with the pairs' other elements
+    int place[PAIRS == PAIRS_ANY ? 8 : 1];  // of the pairs' other elements in shared memory
     bool on;
     float cs[NC], sn[NC];
 
@@ -125,8 +135,20 @@ struct Lane {
         at[0] = l * 8;
         if constexpr (NV == 2) at[1] = a.dim / 2 + l * 8;
         on = l * 8 < a.dim / NV;
+        const int apart = a.rot / 16;
+        other = lane + (l < apart ? apart : l < 2 * apart ? -apart : 0);
+        if constexpr (PAIRS == PAIRS_ANY)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int e = l * 8 + i, half = a.rot / 2;
+                place[i] = e < a.rot ? spread(lane * 8 + i + (e < half ? half : -half)) : kZero;
+            }
     }
-    // The angles of a token, from its row of the table.  (An element past rot_dim turns by the angle 0.)
+    // PAIRS_ANY: where element i of a warp's 256 lies, so that lanes that read 8 elements apart use
+    // different banks; behind them a -0 for elements past rot_dim.
+    static constexpr int kZero = 256 + 7, kPlaces = 256 + 8;
+    static __device__ __forceinline__ int spread(int i) { return i + (i >> 5); }
+    // The angles of a token, from its row of the table.  (Elements past rot_dim: 1 and 0.)
     __device__ __forceinline__ void angles(const QkArgs &a, const float2 *row) {
         if constexpr (PAIRS == PAIRS_SPLIT) {  // (a lane past the head's elements holds zeros, whatever it reads)
             const float4 *r4 = reinterpret_cast<const float4 *>(row + (on ? l * 8 : 0));
@@ -138,15 +160,26 @@ struct Lane {
                 cs[2 * i] = v.x, cs[2 * i + 1] = v.z;
                 sn[2 * i] = s.x, sn[2 * i + 1] = s.y;
             }
+        } else if constexpr (kLanes) {
+            const bool second = l >= a.rot / 16, in = l < a.rot / 8;
+            const float4 *r4 = reinterpret_cast<const float4 *>(row + (in ? l * 8 - (second ? a.rot / 2 : 0) : 0));
+            const float sign = second ? a.sign : -a.sign;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = r4[i];
+                cs[2 * i] = in ? v.x : 1.f, cs[2 * i + 1] = in ? v.z : 1.f;
+                sn[2 * i] = in ? sign * v.y : 0.f, sn[2 * i + 1] = in ? sign * v.w : 0.f;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int e = l * 8 + i;
-                const int j = PAIRS == PAIRS_LOCAL ? l * NC + i : e < a.rot / 2 ? e : e - a.rot / 2;
-                const bool in = on && (PAIRS == PAIRS_ANY ? e < a.rot : j < a.rot / 2);
+                const bool second = !kLocal && e >= a.rot / 2;
+                const int j = kLocal ? at[i / 4] / 2 + i % 4 : second ? e - a.rot / 2 : e;
+                const bool in = on && j < a.rot / 2;
                 const float2 v = in ? row[j] : make_float2(1.f, 0.f);
                 cs[i] = v.x;
-                sn[i] = a.sign * v.y;
+                sn[i] = in ? (kLocal || second ? a.sign : -a.sign) * v.y : 0.f;
             }
         }
     }
@@ -155,13 +188,14 @@ struct Lane {
         for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    // Turns h in place by the angles.  buf: the warp's 256 floats.
+    // Turns h in place by the angles.  buf: the warp's kPlaces floats.
     __device__ __forceinline__ void turn(const QkArgs &a, float2 (&h)[N2], float *buf) const {
-        if constexpr (PAIRS == PAIRS_LOCAL) {
+        if constexpr (kLocal) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NC; ++i) {
                 const float2 x = h[i];
-                h[i] = make_float2(x.x * cs[i] - x.y * sn[i], x.x * sn[i] + x.y * cs[i]);
+                // (past rot_dim an infinity times the angle's 0 would be NaN)
+                if (at[i / 4] / 2 + i % 4 < a.rot / 2) h[i] = make_float2(x.x * cs[i] - x.y * sn[i], x.x * sn[i] + x.y * cs[i]);
             }
         } else if constexpr (PAIRS == PAIRS_SPLIT) {
 #pragma unroll
@@ -171,20 +205,24 @@ struct Lane {
                 h[i] = ptx::fma2(x, c, ptx::mul2(y, make_float2(-s.x, -s.y)));
                 h[4 + i] = ptx::fma2(x, s, ptx::mul2(y, c));
             }
-        } else {
-            float *mine = buf + slot * lanes * 8;
-            __syncwarp();
+        } else if constexpr (kLanes) {
+            const bool in = l < a.rot / 8;  // (past rot_dim, where an infinity times 0 would be NaN, -0 is added)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<float2 *>(mine + l * 8 + 2 * i) = h[i];
-            __syncwarp();
-            const int half = a.rot / 2;
-            float *v = reinterpret_cast<float *>(h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int e = l * 8 + i;
-                if (e < half) v[i] = v[i] * cs[i] - mine[e + half] * sn[i];
-                else if (e < a.rot) v[i] = v[i] * cs[i] + mine[e - half] * sn[i];
+            for (int i = 0; i < 4; ++i) {
+                float2 y = make_float2(__shfl_sync(0xffffffffu, h[i].x, other), __shfl_sync(0xffffffffu, h[i].y, other));
+                if (!in) y = make_float2(-0.f, -0.f);
+                const float2 c = make_float2(cs[2 * i], cs[2 * i + 1]), s = make_float2(sn[2 * i], sn[2 * i + 1]);
+                h[i] = ptx::fma2(h[i], c, ptx::mul2(y, s));
             }
+        } else {
+            float *v = reinterpret_cast<float *>(h);
+            const int mine = spread((threadIdx.x & 31) * 8);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) buf[mine + i] = v[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], cs[i], buf[place[i]] * sn[i]);
         }
     }
     // 1 / sqrt(mean x^2 + eps) of a head.  Squares that overflow are summed again at
@@ -254,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     L lane(a);
     const int per = 32 >> a.lanes_log, heads = a.heads[w];
     uint8_t *ring = smem + warp * a.warp_bytes, *rows = ring + AHEAD * STEP;
-    float *buf = reinterpret_cast<float *>(rows + (AHEAD + 1) * a.row_bytes);  // PAIRS_ANY: 256 floats
+    float *buf = reinterpret_cast<float *>(rows + (AHEAD + 1) * a.row_bytes);  // PAIRS_ANY
     const uint32_t to = ptx::smem_u32(ring) + lane_id * 16, to_rows = ptx::smem_u32(rows);
 
     // A token's sequence and index in it, moved on by `stride` tokens.  (Divisions cost as much as a step.)
@@ -333,6 +371,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch();
+    if (PAIRS == PAIRS_ANY && lane_id == 0) buf[L::kZero] = -0.f;
     float2 gamma[N2], dg[BWD ? N2 : 1];
     load_gamma<P>(a.gamma[w], lane.at, lane.on, gamma);
     if constexpr (BWD)
@@ -491,8 +530,11 @@ void strides_of(const cba_qk_norm_rope_desc_t &d, const cba_attn_strides_t &s, i
 }
 
 Pairs pairs_of(const cba_qk_norm_rope_desc_t &d) {
-    if (d.interleaved || d.rot_dim == 0) return PAIRS_LOCAL;
-    return d.rot_dim == d.dim && d.dim % 16 == 0 ? PAIRS_SPLIT : PAIRS_ANY;
+    const bool halves = d.dim % 16 == 0;
+    if (d.interleaved || d.rot_dim == 0) return halves ? PAIRS_LOCAL2 : PAIRS_LOCAL;
+    if (d.rot_dim % 16 != 0) return PAIRS_ANY;
+    if (d.rot_dim == d.dim) return PAIRS_SPLIT;
+    return halves && d.rot_dim <= d.dim / 2 ? PAIRS_LANES2 : PAIRS_LANES;
 }
 
 // What both directions share.
@@ -509,7 +551,8 @@ QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int
     a.sign = 1.f;
     a.eps = d.eps;
     a.inv_dim = 1.f / (float)d.dim;
-    const int lanes = pairs_of(d) == PAIRS_SPLIT ? d.dim / 16 : d.dim / 8;
+    const Pairs pairs = pairs_of(d);
+    const int lanes = pairs == PAIRS_LOCAL || pairs == PAIRS_LANES || pairs == PAIRS_ANY ? d.dim / 8 : d.dim / 16;
     while ((1 << a.lanes_log) < lanes) ++a.lanes_log;
     const int per = 32 >> a.lanes_log;
     a.heads[0] = d.heads_q;
@@ -538,8 +581,11 @@ template <typename F>
 cudaError_t dispatch(const cba_qk_norm_rope_desc_t &d, F f) {
     auto pairs = [&](auto t, auto p) {
         switch (pairs_of(d)) {
+            case PAIRS_LOCAL2: return f(t, p, std::integral_constant<int, PAIRS_LOCAL2>{});
+            case PAIRS_LANES2: return f(t, p, std::integral_constant<int, PAIRS_LANES2>{});
             case PAIRS_LOCAL: return f(t, p, std::integral_constant<int, PAIRS_LOCAL>{});
             case PAIRS_SPLIT: return f(t, p, std::integral_constant<int, PAIRS_SPLIT>{});
+            case PAIRS_LANES: return f(t, p, std::integral_constant<int, PAIRS_LANES>{});
             default: return f(t, p, std::integral_constant<int, PAIRS_ANY>{});
         }
     };
@@ -556,10 +602,10 @@ cudaError_t launch(const cba_qk_norm_rope_desc_t &d, QkArgs a, int *blocks, cuda
         constexpr int PAIRS = decltype(pairs)::value, AHEAD = qk_ahead(BWD);
         constexpr auto kern = qk_kernel<T, P, PAIRS, BWD>;
         const int step = (BWD ? 2 : 1) * Lane<PAIRS>::NV * (int)sizeof(T) * 256;
-        a.warp_bytes = AHEAD * step + (AHEAD + 1) * a.row_bytes + (PAIRS == PAIRS_ANY ? 1024 : 0);
+        a.warp_bytes = AHEAD * step + (AHEAD + 1) * a.row_bytes + (PAIRS == PAIRS_ANY ? Lane<PAIRS>::kPlaces * 4 : 0);
         // (backward: the block's sums at the end)
         const int bytes = std::max(kWarps * a.warp_bytes, BWD ? kWarps * 1024 : 0);
-        const int most = kWarps * (AHEAD * step + (AHEAD + 1) * kQkMaxDim * 4 + 1024);
+        const int most = kWarps * (AHEAD * step + (AHEAD + 1) * kQkMaxDim * 4 + Lane<PAIRS>::kPlaces * 4);
         cudaError_t e = allow_smem<kern>(most);
         if (e != cudaSuccess) return e;
         kern<<<(unsigned)*blocks, kWarps * 32, bytes, st>>>(a);

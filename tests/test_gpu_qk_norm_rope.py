@@ -147,6 +147,29 @@ def test_norm_or_rotation_alone(cuda_lib, norm, rot, interleaved):
     both(2, 30, 4, 2, 64, rot, F32, F32, interleaved, norm, gammas=False)
 
 
+@pytest.mark.parametrize("dim,rot", [(24, 16), (40, 16), (96, 48), (256, 144), (72, 46), (256, 250)])
+def test_part_of_a_head_turned(cuda_lib, dim, rot):
+    for dtype, param in ((F32, F32), (BF, F32), (F16, F16)):
+        both(2, 150, 5, 2, dim, rot, dtype, param)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [32, 30, 0])
+def test_elements_past_the_turned_ones_stay(cuda_lib, rot, interleaved):
+    """Bit by bit, infinities and the sign of a zero among them, and NaN as some NaN (IEEE 754 leaves open which one an
+    operation gives); the turned ones stay finite."""
+    q = torch.randn(7, 4, 64, device="cuda", dtype=BF)
+    q[:, 1, rot], q[:, 2, 40], q[:, 3, 63], q[:, 0, 50] = math.inf, math.nan, -math.inf, -0.0
+    for sign in (1, -1):
+        kw = dict(table=make_table(7, rot) if rot else None, norm=False, interleaved=interleaved)
+        y = tr.qk_norm_rope(q, None, **kw)[0] if sign > 0 else tr.qk_norm_rope_backward(q, None, q, None, **kw)[0]
+        got, want = (t[..., rot:].contiguous() for t in (y, q))
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        number = ~torch.isnan(want)
+        assert torch.equal(got.view(torch.int16)[number], want.view(torch.int16)[number])
+        assert torch.isfinite(y[..., :rot]).all()
+
+
 def test_queries_alone(cuda_lib):
     q, dy = torch.randn(2, 10, 3, 64, device="cuda"), torch.randn(2, 10, 3, 64, device="cuda")
     table = make_table(10, 64)
