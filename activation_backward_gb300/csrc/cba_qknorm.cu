@@ -13,9 +13,9 @@
 // shared memory a few steps ahead, and the warp its tokens' rows of the table.  Blocks
 // are the queries' or the keys', in the proportion of their steps.
 //
-// Measured (us), 4 x 8192 tokens, 32/8 heads of 128, bf16: forward 134 (0.74 of the copy rate; issue
-// slots 51% taken), backward 185, of which 6 for the sum of dgamma's rows (0.81; 58%).  2 x 169
-// tokens, 8 heads of 64: 5.8 and 9.7, one and two launches.
+// Measured (us), 4 x 8192 tokens, 32/8 heads of 128, bf16: forward 135 (0.73 of the copy rate; issue
+// slots 51% taken), backward 186, of which 6 for the sum of dgamma's rows (0.81; 58%).  2 x 169
+// tokens, 8 heads of 64: 5.8 and 9.7, one and two launches (3.5 and 6.4 on the device).
 #include <algorithm>
 #include <cmath>
 
@@ -48,12 +48,16 @@ enum Pairs {
     PAIRS_ANY      // (j, j + rot / 2): exchanged through shared memory
 };
 
+__host__ __device__ constexpr bool is_local(int p) { return p == PAIRS_LOCAL || p == PAIRS_LOCAL2; }
+__host__ __device__ constexpr bool is_lanes(int p) { return p == PAIRS_LANES || p == PAIRS_LANES2; }
+
 struct QkArgs {
     // queries and keys
     const void *x[2], *dy[2], *gamma[2];
     void *out[2];
     long long sx[2][3], sdy[2][3], so[2][3];  // batch, token, head
     int heads[2], steps[2];                   // steps: of a token
+    int parts[2];                             // warps that share a token's heads: 1, 2, 4 or 8
     const float2 *table;
     const int *pos;
     int tokens, len, dim, rot, positions, norm;
@@ -117,12 +121,10 @@ __device__ __forceinline__ void store8(void *p, long long at, const Vec<T> &v) {
 // A lane's place in its head, and what turns its elements at one position.
 template <int PAIRS>
 struct Lane {
-    [[maybe_unused]] static constexpr bool kLocal = PAIRS == PAIRS_LOCAL || PAIRS == PAIRS_LOCAL2;
-    [[maybe_unused]] static constexpr bool kLanes = PAIRS == PAIRS_LANES || PAIRS == PAIRS_LANES2;
     static constexpr int NV = PAIRS == PAIRS_LOCAL || PAIRS == PAIRS_LANES || PAIRS == PAIRS_ANY ? 1 : 2;  // vectors of 8 elements
     static constexpr int NE = 8 * NV, N2 = NE / 2;
     static constexpr int NC = PAIRS == PAIRS_LOCAL ? 4 : 8;   // angles
-    int slot, l, at[NV], lanes, other;  // other: kLanes: the lane with the pairs' other elements
+    int slot, l, at[NV], lanes, other;  // other: PAIRS_LANES: the lane with the pairs' other elements
     int place[PAIRS == PAIRS_ANY ? 8 : 1];  // of the pairs' other elements in shared memory
     bool on;
     float cs[NC], sn[NC];
@@ -160,7 +162,7 @@ struct Lane {
                 cs[2 * i] = v.x, cs[2 * i + 1] = v.z;
                 sn[2 * i] = s.x, sn[2 * i + 1] = s.y;
             }
-        } else if constexpr (kLanes) {
+        } else if constexpr (is_lanes(PAIRS)) {
             const bool second = l >= a.rot / 16, in = l < a.rot / 8;
             const float4 *r4 = reinterpret_cast<const float4 *>(row + (in ? l * 8 - (second ? a.rot / 2 : 0) : 0));
             const float sign = second ? a.sign : -a.sign;
@@ -174,12 +176,12 @@ struct Lane {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const int e = l * 8 + i;
-                const bool second = !kLocal && e >= a.rot / 2;
-                const int j = kLocal ? at[i / 4] / 2 + i % 4 : second ? e - a.rot / 2 : e;
+                const bool second = !is_local(PAIRS) && e >= a.rot / 2;
+                const int j = is_local(PAIRS) ? at[i / 4] / 2 + i % 4 : second ? e - a.rot / 2 : e;
                 const bool in = on && j < a.rot / 2;
                 const float2 v = in ? row[j] : make_float2(1.f, 0.f);
                 cs[i] = v.x;
-                sn[i] = in ? (kLocal || second ? a.sign : -a.sign) * v.y : 0.f;
+                sn[i] = in ? (is_local(PAIRS) || second ? a.sign : -a.sign) * v.y : 0.f;
             }
         }
     }
@@ -190,7 +192,7 @@ struct Lane {
     }
     // Turns h in place by the angles.  buf: the warp's kPlaces floats.
     __device__ __forceinline__ void turn(const QkArgs &a, float2 (&h)[N2], float *buf) const {
-        if constexpr (kLocal) {
+        if constexpr (is_local(PAIRS)) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const float2 x = h[i];
@@ -205,7 +207,7 @@ struct Lane {
                 h[i] = ptx::fma2(x, c, ptx::mul2(y, make_float2(-s.x, -s.y)));
                 h[4 + i] = ptx::fma2(x, s, ptx::mul2(y, c));
             }
-        } else if constexpr (kLanes) {
+        } else if constexpr (is_lanes(PAIRS)) {
             const bool in = l < a.rot / 8;  // (past rot_dim, where an infinity times 0 would be NaN, -0 is added)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -288,9 +290,13 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     if (BWD) ptx::griddep_launch_dependents();
     const int w = (int)blockIdx.x >= a.q_blocks;
     const int blk = w ? (int)blockIdx.x - a.q_blocks : (int)blockIdx.x;
-    const int stride = (w ? (int)gridDim.x - a.q_blocks : a.q_blocks) * kWarps;  // from one token of a warp to its next
+    const int parts = a.parts[w], own = blk * kWarps + warp;
+    // from one token of a warp to its next
+    const int stride = (w ? (int)gridDim.x - a.q_blocks : a.q_blocks) * kWarps / parts;
     L lane(a);
-    const int per = 32 >> a.lanes_log, heads = a.heads[w];
+    const int per = 32 >> a.lanes_log, share = (a.steps[w] + parts - 1) / parts * per, from = own % parts * share;
+    // the lane's first head, and the end of the warp's
+    const int first = from + lane.slot, heads = min(a.heads[w], from + share);
     uint8_t *ring = smem + warp * a.warp_bytes, *rows = ring + AHEAD * STEP;
     float *buf = reinterpret_cast<float *>(rows + (AHEAD + 1) * a.row_bytes);  // PAIRS_ANY
     const uint32_t to = ptx::smem_u32(ring) + lane_id * 16, to_rows = ptx::smem_u32(rows);
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     };
     const int sb = stride / a.len, sr = stride - sb * a.len;
     auto begin = [&]() {
-        const int token = blk * kWarps + warp, b = token / a.len;
+        const int token = from < heads ? own / parts : a.tokens, b = token / a.len;
         return Place{token, b, token - b * a.len};
     };
     auto move_on = [&](Place &p) {
@@ -313,14 +319,14 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     const T *fx = nullptr, *fdy = nullptr;
     const long long xs = per * a.sx[w][2], ds = per * a.sdy[w][2], os = per * a.so[w][2];
     Place f = begin();
-    int fh = lane.slot, fs = 0, fr = 0;
+    int fh = first, fs = 0, fr = 0;
     auto position = [&](const Place &p) {
         if (p.token >= a.tokens || a.rot == 0) return 0;
         return min(max(a.pos ? __ldg(a.pos + p.token) : p.t, 0), a.positions - 1);
     };
     auto place = [&]() {
-        fx = static_cast<const T *>(a.x[w]) + f.b * a.sx[w][0] + f.t * a.sx[w][1] + lane.slot * a.sx[w][2];
-        if (BWD) fdy = static_cast<const T *>(a.dy[w]) + f.b * a.sdy[w][0] + f.t * a.sdy[w][1] + lane.slot * a.sdy[w][2];
+        fx = static_cast<const T *>(a.x[w]) + f.b * a.sx[w][0] + f.t * a.sx[w][1] + first * a.sx[w][2];
+        if (BWD) fdy = static_cast<const T *>(a.dy[w]) + f.b * a.sdy[w][0] + f.t * a.sdy[w][1] + first * a.sdy[w][2];
     };
     place();
     auto after = [&](Place p) {
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     int at_pos = position(f), next_pos = after(f);
     auto fetch = [&]() {
         if (f.token < a.tokens) {
-            if (fh == lane.slot)
+            if (fh == first)
                 for (int j = lane_id; j < a.rot / 2; j += 32)
                     copy_async<8>(to_rows + fr * a.row_bytes + j * 8, a.table + (long long)at_pos * (a.rot / 2) + j);
             if (lane.on && fh < heads) {
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
         fx += xs, fh += per;
         if (BWD) fdy += ds;
         if (fh - lane.slot >= heads) {  // (the same for all lanes)
-            fh = lane.slot;
+            fh = first;
             move_on(f);
             fr = fr == AHEAD ? 0 : fr + 1;
             at_pos = next_pos;
@@ -379,12 +385,12 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
         for (int i = 0; i < N2; ++i) dg[i] = make_float2(0.f, 0.f);
     int st = 0, row = 0;
     for (Place c = begin(); c.token < a.tokens; move_on(c)) {
-        T *out = static_cast<T *>(a.out[w]) + c.b * a.so[w][0] + c.t * a.so[w][1] + lane.slot * a.so[w][2];
+        T *out = static_cast<T *>(a.out[w]) + c.b * a.so[w][0] + c.t * a.so[w][1] + first * a.so[w][2];
         // forward, PAIRS_SPLIT: (a, b) becomes r (ca a + cb b, da a + db b)
         float2 ca[4], cb[4], da[4], db[4];
-        for (int h = lane.slot; h - lane.slot < heads; h += per, out += os) {
+        for (int h = first; h - lane.slot < heads; h += per, out += os) {
             copies_wait<AHEAD - 1>();
-            if (h == lane.slot) {
+            if (h == first) {
                 __syncwarp();  // the row was copied by all lanes
                 lane.angles(a, reinterpret_cast<const float2 *>(rows + row * a.row_bytes));
                 __syncwarp();  // read by all before it is copied over
@@ -557,7 +563,15 @@ QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int
     const int per = 32 >> a.lanes_log;
     a.heads[0] = d.heads_q;
     a.heads[1] = d.heads_k;
-    for (int w = 0; w < 2; ++w) a.steps[w] = (a.heads[w] + per - 1) / per;
+    // Few tokens share their heads among warps, up to a block for each SM.  (32/8 heads, forward and backward:
+    // 8 x 1 tokens, heads of 128 3.3 and 5.8 us, a warp for a token's heads 5.8 and 9.7; 4 x 8, heads of 256
+    // 3.9 and 6.5, 9.7 and 16.9.)
+    for (int w = 0; w < 2; ++w) {
+        a.steps[w] = (a.heads[w] + per - 1) / per;
+        a.parts[w] = 1;
+        while (a.parts[w] < kWarps && 2 * a.parts[w] <= a.steps[w] && 4LL * a.parts[w] * a.tokens <= kNumSMs * kWarps)
+            a.parts[w] *= 2;
+    }
     a.row_bytes = (d.rot_dim * 4 + 15) / 16 * 16;
     return a;
 }
@@ -567,7 +581,8 @@ QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int
 void plan_blocks(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, bool bwd, int *blocks, int *q_blocks) {
     const int most = kQkPerSm * kNumSMs;
     const long long each = ((long long)a.tokens + kWarps - 1) / kWarps;
-    long long need[2] = {each, d.heads_k ? each : 0};
+    auto warps = [&](int w) { return ((long long)a.tokens * a.parts[w] + kWarps - 1) / kWarps; };
+    long long need[2] = {warps(0), d.heads_k ? warps(1) : 0};
     if (need[0] + need[1] > most) {
         const long long all = a.steps[0] + a.steps[1];
         need[1] = d.heads_k ? std::min(each, std::max(1LL, (most * (long long)a.steps[1] + all / 2) / all)) : 0;
