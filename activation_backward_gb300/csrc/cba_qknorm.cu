@@ -576,9 +576,9 @@ QkArgs base_args(const cba_qk_norm_rope_desc_t &d, const float *table, const int
     return a;
 }
 
-// Blocks, and the queries' among them: as many as have a token for each warp, or that the
+// Blocks, and the queries' among them: as many as have a token (or a part of its heads) for each warp, or that the
 // SMs hold, shared by the steps.
-void plan_blocks(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, bool bwd, int *blocks, int *q_blocks) {
+void plan_blocks(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, int *blocks, int *q_blocks) {
     const int most = kQkPerSm * kNumSMs;
     const long long each = ((long long)a.tokens + kWarps - 1) / kWarps;
     auto warps = [&](int w) { return ((long long)a.tokens * a.parts[w] + kWarps - 1) / kWarps; };
@@ -610,7 +610,7 @@ cudaError_t dispatch(const cba_qk_norm_rope_desc_t &d, F f) {
 
 template <bool BWD>
 cudaError_t launch(const cba_qk_norm_rope_desc_t &d, QkArgs a, int *blocks, cudaStream_t st) {
-    plan_blocks(d, a, BWD, blocks, &a.q_blocks);
+    plan_blocks(d, a, blocks, &a.q_blocks);
     return dispatch(d, [&](auto t, auto p, auto pairs) {
         using T = decltype(t);
         using P = decltype(p);
@@ -679,7 +679,7 @@ int cba_qk_norm_rope_forward(const cba_qk_norm_rope_desc_t *d, const void *q, co
 size_t cba_qk_norm_rope_workspace_bytes(const cba_qk_norm_rope_desc_t *d) {
     if (check_desc(d) != CBA_OK) return 0;
     int blocks, q_blocks;
-    plan_blocks(*d, base_args(*d, nullptr, nullptr), true, &blocks, &q_blocks);
+    plan_blocks(*d, base_args(*d, nullptr, nullptr), &blocks, &q_blocks);
     return std::max((size_t)256, ((size_t)blocks * d->dim * sizeof(float) + 255) / 256 * 256);
 }
 
@@ -723,7 +723,7 @@ int cba_qk_norm_rope_backward(const cba_qk_norm_rope_desc_t *d, const void *q, c
     if (e == cudaSuccess && (dgamma_q || dgamma_k)) {
         const dim3 grid((unsigned)(d->dim + 31) / 32, 2);
         int q_blocks;
-        plan_blocks(*d, a, true, &blocks, &q_blocks);
+        plan_blocks(*d, a, &blocks, &q_blocks);
         if (d->len > 0)
             e = launch_pdl(qk_dgamma_kernel, grid, dim3(1024), 0, st, (const float *)a.partial, d->dim, q_blocks, blocks,
                            dgamma_q, dgamma_k, d->accumulate);
