@@ -146,6 +146,13 @@ def test_few_rows_over_many_keys(cuda_lib, batch, len_q, len_k, hq, hk, causal, 
     one(len_q + len_k, batch, len_q, len_k, hq, hk, dim, dtype, "bshd", causal)
 
 
+@pytest.mark.parametrize("len_k", [640, 900, 1300, 1700, 2900, 20000, 33000])
+@pytest.mark.parametrize("len_q,hq,hk,causal", [(1, 8, 1, False), (3, 2, 2, True), (300, 2, 1, True)])
+def test_numbers_of_items_joined(cuda_lib, len_k, len_q, hq, hk, causal):
+    """From two items of a pair of tiles to more than fifty, some of them without keys under the mask."""
+    one(len_k, 1, len_q, len_k, hq, hk, 72, BF, "bshd", causal)
+
+
 @pytest.mark.parametrize("scale", [1.0, -0.3, 0.0, 1e-3, 20.0])
 @pytest.mark.parametrize("dtype", [BF, F16])
 def test_scales(cuda_lib, scale, dtype):

@@ -170,6 +170,25 @@ def test_elements_past_the_turned_ones_stay(cuda_lib, rot, interleaved):
         assert torch.isfinite(y[..., :rot]).all()
 
 
+@pytest.mark.parametrize("batch,n", [(1, 1), (8, 1), (2, 9), (1, 75), (1, 77), (1, 152), (1, 305), (2, 304)])
+@pytest.mark.parametrize("hq,hk", [(32, 8), (20, 0), (71, 5)])
+def test_few_tokens_of_many_heads(cuda_lib, batch, n, hq, hk):
+    """A token's heads shared by one to eight warps, some of them without any."""
+    for dim, rot, interleaved in ((128, 128, False), (64, 32, False), (256, 256, True), (40, 40, False)):
+        if hk:
+            both(batch, n, hq, hk, dim, rot, BF, F32, interleaved)
+        else:
+            rng = np.random.default_rng(n)
+            q, dy = (torch.from_numpy(rng.normal(size=(batch, n, hq, dim))).to("cuda", BF) for _ in range(2))
+            gamma, table = torch.rand(dim, device="cuda") + 0.5, make_table(n, rot)
+            kw = dict(gamma_q=gamma, table=table, interleaved=interleaved, eps=EPS)
+            at = np.tile(np.arange(n), batch)
+            y, _ = tr.qk_norm_rope(q, None, **kw)
+            check_forward(q, y, gamma, table, at, True, interleaved, "q")
+            dq, _, dg, _ = tr.qk_norm_rope_backward(q, None, dy, None, **kw)
+            check_backward(q, dy, dq, dg, gamma, table, at, True, interleaved, "dq")
+
+
 def test_queries_alone(cuda_lib):
     q, dy = torch.randn(2, 10, 3, 64, device="cuda"), torch.randn(2, 10, 3, 64, device="cuda")
     table = make_table(10, 64)
