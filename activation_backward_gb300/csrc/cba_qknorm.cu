@@ -13,8 +13,8 @@
 // shared memory a few steps ahead, and the warp its tokens' rows of the table.  Blocks
 // are the queries' or the keys', in the proportion of their steps.
 //
-// Measured (us), 4 x 8192 tokens, 32/8 heads of 128, bf16: forward 135 (0.73 of the copy rate; issue
-// slots 51% taken), backward 186, of which 6 for the sum of dgamma's rows (0.81; 58%).  2 x 169
+// Measured (us), 4 x 8192 tokens, 32/8 heads of 128, bf16: forward 134 (0.74 of the copy rate; issue
+// slots 51% taken), backward 187, of which 6 for the sum of dgamma's rows (0.81; 58%).  2 x 169
 // tokens, 8 heads of 64: 5.8 and 9.7, one and two launches (3.5 and 6.4 on the device).
 #include <algorithm>
 #include <cmath>
@@ -280,7 +280,7 @@ __device__ __forceinline__ void pack_store(T *out, const int (&at)[NV], const fl
 
 // Blocks below q_blocks walk the queries' heads, the others the keys'.  Backward: a warp
 // adds up its lanes' parts of dgamma, a block its warps', in a fixed order.
-template <typename T, typename P, int PAIRS, bool BWD>
+template <typename T, typename P, int PAIRS, bool BWD, bool SHARED>
 __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs a) {
     using L = Lane<PAIRS>;
     constexpr int NV = L::NV, NE = L::NE, N2 = L::N2, AHEAD = qk_ahead(BWD), NT = BWD ? 2 : 1, Q = sizeof(T) / 2;
@@ -290,13 +290,13 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     if (BWD) ptx::griddep_launch_dependents();
     const int w = (int)blockIdx.x >= a.q_blocks;
     const int blk = w ? (int)blockIdx.x - a.q_blocks : (int)blockIdx.x;
-    const int parts = a.parts[w], own = blk * kWarps + warp;
+    // (SHARED: warps share a token's heads; in one kernel for both long calls take 2% longer)
+    const int parts = SHARED ? a.parts[w] : 1, own = blk * kWarps + warp;
     // from one token of a warp to its next
     const int stride = (w ? (int)gridDim.x - a.q_blocks : a.q_blocks) * kWarps / parts;
     L lane(a);
-    const int per = 32 >> a.lanes_log, share = (a.steps[w] + parts - 1) / parts * per, from = own % parts * share;
-    // the lane's first head, and the end of the warp's
-    const int first = from + lane.slot, heads = min(a.heads[w], from + share);
+    const int per = 32 >> a.lanes_log, share = (a.steps[w] + parts - 1) / parts * per, from = SHARED ? own % parts * share : 0;
+    const int heads = SHARED ? min(a.heads[w], from + share) : a.heads[w];  // the end of the warp's
     uint8_t *ring = smem + warp * a.warp_bytes, *rows = ring + AHEAD * STEP;
     float *buf = reinterpret_cast<float *>(rows + (AHEAD + 1) * a.row_bytes);  // PAIRS_ANY
     const uint32_t to = ptx::smem_u32(ring) + lane_id * 16, to_rows = ptx::smem_u32(rows);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     };
     const int sb = stride / a.len, sr = stride - sb * a.len;
     auto begin = [&]() {
-        const int token = from < heads ? own / parts : a.tokens, b = token / a.len;
+        const int token = !SHARED ? own : from < heads ? own / parts : a.tokens, b = token / a.len;
         return Place{token, b, token - b * a.len};
     };
     auto move_on = [&](Place &p) {
@@ -319,14 +319,14 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     const T *fx = nullptr, *fdy = nullptr;
     const long long xs = per * a.sx[w][2], ds = per * a.sdy[w][2], os = per * a.so[w][2];
     Place f = begin();
-    int fh = first, fs = 0, fr = 0;
+    int fh = from, fs = 0, fr = 0;
     auto position = [&](const Place &p) {
         if (p.token >= a.tokens || a.rot == 0) return 0;
         return min(max(a.pos ? __ldg(a.pos + p.token) : p.t, 0), a.positions - 1);
     };
     auto place = [&]() {
-        fx = static_cast<const T *>(a.x[w]) + f.b * a.sx[w][0] + f.t * a.sx[w][1] + first * a.sx[w][2];
-        if (BWD) fdy = static_cast<const T *>(a.dy[w]) + f.b * a.sdy[w][0] + f.t * a.sdy[w][1] + first * a.sdy[w][2];
+        fx = static_cast<const T *>(a.x[w]) + f.b * a.sx[w][0] + f.t * a.sx[w][1] + (from + lane.slot) * a.sx[w][2];
+        if (BWD) fdy = static_cast<const T *>(a.dy[w]) + f.b * a.sdy[w][0] + f.t * a.sdy[w][1] + (from + lane.slot) * a.sdy[w][2];
     };
     place();
     auto after = [&](Place p) {
@@ -336,10 +336,10 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
     int at_pos = position(f), next_pos = after(f);
     auto fetch = [&]() {
         if (f.token < a.tokens) {
-            if (fh == first)
+            if (fh == from)
                 for (int j = lane_id; j < a.rot / 2; j += 32)
                     copy_async<8>(to_rows + fr * a.row_bytes + j * 8, a.table + (long long)at_pos * (a.rot / 2) + j);
-            if (lane.on && fh < heads) {
+            if (lane.on && fh + lane.slot < heads) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
         fs = fs + 1 == AHEAD ? 0 : fs + 1;
         fx += xs, fh += per;
         if (BWD) fdy += ds;
-        if (fh - lane.slot >= heads) {  // (the same for all lanes)
-            fh = first;
+        if (fh >= heads) {
+            fh = from;
             move_on(f);
             fr = fr == AHEAD ? 0 : fr + 1;
             at_pos = next_pos;
@@ -385,12 +385,12 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
         for (int i = 0; i < N2; ++i) dg[i] = make_float2(0.f, 0.f);
     int st = 0, row = 0;
     for (Place c = begin(); c.token < a.tokens; move_on(c)) {
-        T *out = static_cast<T *>(a.out[w]) + c.b * a.so[w][0] + c.t * a.so[w][1] + first * a.so[w][2];
+        T *out = static_cast<T *>(a.out[w]) + c.b * a.so[w][0] + c.t * a.so[w][1] + (from + lane.slot) * a.so[w][2];
         // forward, PAIRS_SPLIT: (a, b) becomes r (ca a + cb b, da a + db b)
         float2 ca[4], cb[4], da[4], db[4];
-        for (int h = first; h - lane.slot < heads; h += per, out += os) {
+        for (int h = from; h < heads; h += per, out += os) {
             copies_wait<AHEAD - 1>();
-            if (h == first) {
+            if (h == from) {
                 __syncwarp();  // the row was copied by all lanes
                 lane.angles(a, reinterpret_cast<const float2 *>(rows + row * a.row_bytes));
                 __syncwarp();  // read by all before it is copied over
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
                     }
                 }
             }
-            const bool on = lane.on && h < heads;
+            const bool on = lane.on && h + lane.slot < heads;
             float2 x[N2];
             have(st, 0, on, x);
             if constexpr (BWD) {
@@ -615,15 +615,16 @@ cudaError_t launch(const cba_qk_norm_rope_desc_t &d, QkArgs a, int *blocks, cuda
         using T = decltype(t);
         using P = decltype(p);
         constexpr int PAIRS = decltype(pairs)::value, AHEAD = qk_ahead(BWD);
-        constexpr auto kern = qk_kernel<T, P, PAIRS, BWD>;
+        constexpr auto alone = qk_kernel<T, P, PAIRS, BWD, false>, shared = qk_kernel<T, P, PAIRS, BWD, true>;
+        const bool share = a.parts[0] > 1 || a.parts[1] > 1;
         const int step = (BWD ? 2 : 1) * Lane<PAIRS>::NV * (int)sizeof(T) * 256;
         a.warp_bytes = AHEAD * step + (AHEAD + 1) * a.row_bytes + (PAIRS == PAIRS_ANY ? Lane<PAIRS>::kPlaces * 4 : 0);
         // (backward: the block's sums at the end)
         const int bytes = std::max(kWarps * a.warp_bytes, BWD ? kWarps * 1024 : 0);
         const int most = kWarps * (AHEAD * step + (AHEAD + 1) * kQkMaxDim * 4 + Lane<PAIRS>::kPlaces * 4);
-        cudaError_t e = allow_smem<kern>(most);
+        cudaError_t e = share ? allow_smem<shared>(most) : allow_smem<alone>(most);
         if (e != cudaSuccess) return e;
-        kern<<<(unsigned)*blocks, kWarps * 32, bytes, st>>>(a);
+        (share ? shared : alone)<<<(unsigned)*blocks, kWarps * 32, bytes, st>>>(a);
         return cudaGetLastError();
     });
 }
