@@ -585,7 +585,8 @@ void plan_blocks(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, int *blocks,
     long long need[2] = {warps(0), d.heads_k ? warps(1) : 0};
     if (need[0] + need[1] > most) {
         const long long all = a.steps[0] + a.steps[1];
-        need[1] = d.heads_k ? std::min(each, std::max(1LL, (most * (long long)a.steps[1] + all / 2) / all)) : 0;
+        // (either side has a block at least, however few its heads beside the other's)
+        need[1] = d.heads_k ? std::min({each, most - 1LL, std::max(1LL, (most * (long long)a.steps[1] + all / 2) / all)}) : 0;
         need[0] = std::min(each, most - need[1]);
     }
     *q_blocks = (int)need[0];

@@ -332,3 +332,27 @@ def test_offsets_past_32_bits(cuda_lib):
     got = tr.qk_norm_rope_backward(q, None, y, None, gamma_q=gamma, table=table)
     want = tr.qk_norm_rope_backward(q.contiguous(), None, y.contiguous(), None, gamma_q=gamma, table=table)
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("heads_q,heads_k", [(1, 606), (1, 607), (1, 700), (700, 1), (2, 1300)])
+def test_one_side_with_nearly_all_heads(cuda_lib, heads_q, heads_k):
+    """More tokens than warps and so many heads on one side that the other's share of the blocks is less than one."""
+    n, dim, rot = 2500, 136, 30
+    table, gamma = make_table(n, rot), torch.rand(dim, device="cuda") + 0.5
+    q, k, dyq, dyk = (torch.randn(n, h, dim, device="cuda").to(BF) for h in (heads_q, heads_k) * 2)
+    kw = dict(gamma_q=gamma, table=table, eps=EPS)
+    yq, yk = tr.qk_norm_rope(q, k, gamma_k=gamma, **kw)
+    dq, dk, gq, gk = tr.qk_norm_rope_backward(q, k, dyq, dyk, gamma_k=gamma, **kw)
+    few, many = ((q, dyq, yq, dq, gq), (k, dyk, yk, dk, gk))[:: 1 if heads_q < heads_k else -1]
+    x, dy, y, dx, dg = few
+    check_forward(x, y, gamma, table, np.arange(n), True, False, "the few heads")
+    check_backward(x, dy, dx, dg, gamma, table, np.arange(n), True, False, "the few heads' gradient")
+    x, dy, y, dx, dg = many  # the same bits as by themselves
+    assert torch.equal(y, tr.qk_norm_rope(x, None, **kw)[0])
+    want = tr.qk_norm_rope_backward(x, None, dy, None, **kw)
+    assert torch.equal(dx, want[0])
+    # sums of the same terms by other blocks: each off by (terms + 4) u of the sum of absolute terms
+    n2 = tr.qk_norm_rope(x, None, eps=EPS)[0]
+    g2 = tr.qk_norm_rope_backward(x, None, dy, None, table=table, norm=False)[0]
+    terms = (n2.double() * g2.double()).abs().sum((0, 1)) * 1.02  # (n2 and g2 are rounded to bf16)
+    assert ((dg.double() - want[2].double()).abs() <= 2 * (n * x.shape[1] + 4) * U * terms).all() and (dg != 0).any()
