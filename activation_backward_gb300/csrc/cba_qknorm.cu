@@ -228,7 +228,8 @@ struct Lane {
         }
     }
     // 1 / sqrt(mean x^2 + eps) of a head.  Squares that overflow are summed again at
-    // 2^-66 times the elements: the mean is then so large that eps does not count.
+    // 2^-70 times the elements, where 256 of the largest have 2^124: the mean is then so
+    // large (an element is 2^60 or more) that eps does not count.
     __device__ __forceinline__ float rnorm(const QkArgs &a, const float2 (&x)[N2]) const {
         float2 q = make_float2(0.f, 0.f);
 #pragma unroll
@@ -239,11 +240,11 @@ struct Lane {
             float t = 0.f;
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                const float y = x[i].x * 0x1p-66f, z = x[i].y * 0x1p-66f;
+                const float y = x[i].x * 0x1p-70f, z = x[i].y * 0x1p-70f;
                 t = fmaf(y, y, fmaf(z, z, t));
             }
             t = head_sum(t);
-            if (!(s < INFINITY)) r = 0x1p-66f * rsqrtf(t * a.inv_dim);
+            if (!(s < INFINITY)) r = 0x1p-70f * rsqrtf(t * a.inv_dim);
         }
         return r;
     }
