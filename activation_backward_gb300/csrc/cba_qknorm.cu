@@ -190,6 +190,9 @@ struct Lane {
         for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
+    // What a square below 2^-149 loses is 2^-50 of this mean.  Raised, elements are below 2^54, and the
+    // smallest number's square is 2^-98.
+    static constexpr float kSmallMean = 0x1p-100f, kRaise = 0x1p100f;
     // Turns h in place by the angles.  buf: the warp's kPlaces floats.
     __device__ __forceinline__ void turn(const QkArgs &a, float2 (&h)[N2], float *buf) const {
         if constexpr (is_local(PAIRS)) {
@@ -227,24 +230,32 @@ struct Lane {
             for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], cs[i], buf[place[i]] * sn[i]);
         }
     }
-    // 1 / sqrt(mean x^2 + eps) of a head.  Squares that overflow are summed again at
-    // 2^-70 times the elements, where 256 of the largest have 2^124: the mean is then so
-    // large (an element is 2^60 or more) that eps does not count.
-    __device__ __forceinline__ float rnorm(const QkArgs &a, const float2 (&x)[N2]) const {
+    // 1 / sqrt(mean x^2 + eps) of a head, r, as r / raise by which x, raised, becomes n.  Squares that
+    // overflow are summed again at 2^-70 times the elements, where 256 of the largest have 2^124.
+    // Where mean and eps together are below kSmallMean, squares may have lost bits or vanished: x
+    // becomes kRaise x, whose squares are summed.  (A branch behind dx for an r past the largest
+    // number, a mean below 2^-256, takes 2% of the backward call: 4 x 8192 tokens, 32/8 heads of 128 187 us,
+    // 190.)
+    __device__ __forceinline__ float rnorm(const QkArgs &a, float2 (&x)[N2], float &raise) const {
         float2 q = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < N2; ++i) q = ptx::fma2(x[i], x[i], q);
-        const float s = head_sum(q.x + q.y);
-        float r = rsqrtf(fmaf(s, a.inv_dim, a.eps));  // (2 ulp: below the sum's own error)
-        if (__any_sync(0xffffffffu, !(s < INFINITY))) {
+        const float s = fmaf(head_sum(q.x + q.y), a.inv_dim, a.eps);
+        float r = rsqrtf(s);  // (2 ulp: below the sum's own error)
+        const bool large = !(s < INFINITY), small = s < kSmallMean;
+        raise = 1.f;
+        if (__any_sync(0xffffffffu, large || small)) {
+            const float f = large ? 0x1p-70f : small ? kRaise : 1.f;
             float t = 0.f;
 #pragma unroll
             for (int i = 0; i < N2; ++i) {
-                const float y = x[i].x * 0x1p-70f, z = x[i].y * 0x1p-70f;
-                t = fmaf(y, y, fmaf(z, z, t));
+                const float2 y = make_float2(x[i].x * f, x[i].y * f);
+                t = fmaf(y.x, y.x, fmaf(y.y, y.y, t));
+                if (small) x[i] = y;
             }
-            t = head_sum(t);
-            if (!(s < INFINITY)) r = 0x1p-70f * rsqrtf(t * a.inv_dim);
+            t = rsqrtf(fmaf(head_sum(t), a.inv_dim, a.eps * f * f));
+            if (large) r = f * t;
+            if (small) r = t, raise = kRaise;
         }
         return r;
     }
@@ -415,7 +426,8 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
                 have(st, 1, on, g);
                 fetch();
                 lane.turn(a, g, buf);
-                const float r = lane.rnorm(a, x);
+                float raise;
+                const float r = lane.rnorm(a, x, raise);
                 const float2 r2 = make_float2(r, r);
                 float2 q = make_float2(0.f, 0.f);
 #pragma unroll
@@ -425,12 +437,13 @@ __global__ void __launch_bounds__(kWarps * 32, kQkPerSm) qk_kernel(const QkArgs 
                     g[e] = ptx::mul2(g[e], gamma[e]);
                     q = ptx::fma2(g[e], x[e], q);
                 }
-                const float s = lane.head_sum(q.x + q.y) * -a.inv_dim;
+                const float s = lane.head_sum(q.x + q.y) * -a.inv_dim, rx = r * raise;
 #pragma unroll
-                for (int e = 0; e < N2; ++e) x[e] = ptx::mul2(ptx::fma2(x[e], make_float2(s, s), g[e]), r2);
+                for (int e = 0; e < N2; ++e) x[e] = ptx::mul2(ptx::fma2(x[e], make_float2(s, s), g[e]), make_float2(rx, rx));
             } else {
                 fetch();
-                const float r = a.norm ? lane.rnorm(a, x) : 1.f;
+                float raise;
+                const float r = a.norm ? lane.rnorm(a, x, raise) : 1.f;
                 const float2 r2 = make_float2(r, r);
                 if constexpr (PAIRS == PAIRS_SPLIT) {
 #pragma unroll

@@ -47,6 +47,7 @@ def turned(x, table, interleaved):
 
 def check(q, dy, rot, interleaved, eps):
     """Both directions of q [tokens, heads, dim]."""
+    eps = float(np.float32(eps))
     n, _, dim = q.shape
     angle = np.random.default_rng(dim).uniform(-math.pi, math.pi, (n, rot // 2))
     table = torch.from_numpy(np.stack([np.cos(angle), np.sin(angle)], -1)).float().cuda() if rot else None
@@ -67,8 +68,10 @@ def check(q, dy, rot, interleaved, eps):
     r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
     norm, g = np.abs(x * r), turned(np.abs(f8(dy)), t, interleaved)
     terms = r * (g * gm + norm * (g * gm * norm).mean(-1, keepdims=True))
-    assert np.abs(want).max() < 1e38  # no infinities asked for
-    within(f8(dx), want, bar(terms, want, 2 * dim + 32), "dx")
+    assert np.abs(want).max() < 1e38  # no infinities asked for, but where r itself is past fp32's numbers
+    got, past = f8(dx), np.broadcast_to(r > 3.4e38, want.shape)
+    assert not np.isfinite(got[past]).any()
+    within(np.where(past, want, got), want, bar(terms, want, 2 * dim + 32), "dx")
     within(f8(dgamma), wg, (x.shape[0] * x.shape[1] + 2 * dim + 32) * U * (g * norm).sum((0, 1)) + 1e-30, "dgamma")
 
 
@@ -85,3 +88,29 @@ def test_heads_near_the_largest_number(cuda_lib, dim, rot, interleaved, dtype, b
     assert torch.isfinite(q).all()
     dy = (torch.randn(q.shape, generator=g, device="cuda") * 1e6).to(dtype)
     check(q, dy, rot, interleaved, 1e-6)
+
+
+@pytest.mark.parametrize("dtype,size,eps", [(F32, 1e-18, 0.0), (F32, 1e-25, 0.0), (F32, 1e-38, 0.0), (F32, 1e-42, 0.0), (F32, 3e-45, 0.0),
+                                            (F32, 1e-20, 1e-40), (F32, 1e-25, 1e-45), (F32, 1e-17, 1e-31), (F32, 1e-40, 1e-30),
+                                            (BF, 1e-25, 0.0), (BF, 1e-37, 0.0), (BF, 1e-39, 0.0), (BF, 1e-20, 1e-38)])
+@pytest.mark.parametrize("dim,rot,interleaved", KINDS)
+def test_heads_of_small_numbers(cuda_lib, dim, rot, interleaved, dtype, size, eps):
+    """Squares that vanish in fp32, with no eps or one as small; heads of order 1 in the same warps.  The gradients are small
+    enough for dx, 1 / size times as large, to stay below 1e38; where 1 / size does not, dx has no finite value."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    q, dy = (torch.randn((9, 3, dim), generator=g, device="cuda") for _ in range(2))
+    q[..., 0] = 2.0  # (no head of zeros alone)
+    q[:, 1:], dy[:, 1:] = q[:, 1:] * size, dy[:, 1:] * min(1.0, size * 1e36)
+    check(q.to(dtype), dy.to(dtype), rot, interleaved, eps)
+
+
+def test_heads_of_zeros_without_eps_are_0_over_0(cuda_lib):
+    """NaN, as by the formula, in their own rows alone."""
+    q, dy = (torch.randn((5, 4, 64), device="cuda") for _ in range(2))
+    y, dx = tr.qk_norm_rope(q, None, eps=0.0)[0], tr.qk_norm_rope_backward(q, None, dy, None, eps=0.0)[0]
+    p = q.clone()
+    p[2, 1] = 0
+    y2, dx2 = tr.qk_norm_rope(p, None, eps=0.0)[0], tr.qk_norm_rope_backward(p, None, dy, None, eps=0.0)[0]
+    keep = torch.ones(5, 4, dtype=torch.bool, device="cuda")
+    keep[2, 1] = False
+    assert torch.isnan(y2[2, 1]).all() and torch.equal(y2[keep], y[keep]) and torch.equal(dx2[keep], dx[keep])
