@@ -587,6 +587,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                 sees = all = w.lk - it0;
                 if (a.causal) sees = min(sees, first + tok + diag), all = min(all, first + diag);
             }
+            const int t = w.t0 + x * a.tt + tok;
+            const bool row = tok < a.tt && t < w.lq;
             float m = -INFINITY;  // in S's unit
             float2 l0 = make_float2(0.f, 0.f), l1 = l0;
             for (int it = 0; it < cnt; ++it) {
@@ -635,7 +637,8 @@ __global__ void __launch_bounds__(kAfThreads, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sb.p_ready[2 * x + h]));
                 };
-                if (tok >= a.tt) now = -INFINITY;  // no row: whatever lies there raises nothing
+                // no row: whatever lies there (the next sequence's queries) raises nothing and has no vote
+                if (!row) now = -INFINITY;
                 // One vote for what is rare.  (-inf - -inf and inf - inf are NaN, which raises nothing.)
                 const bool grown = (now - m) * cs > kLag, large = fabsf(fmaxf(m, now)) * cs > kLargeLog && now > -INFINITY;
                 if (__builtin_expect(__any_sync(0xffffffffu, grown || large), 0)) {
@@ -704,8 +707,6 @@ __global__ void __launch_bounds__(kAfThreads, 1)
             if (!ok || (cnt > 0 && !wait(&sb.acc[x], (uint32_t)ga))) break;
             if (cnt > 0) ++ga;
             ptx::tc_fence_after();
-            const int t = w.t0 + x * a.tt + tok;
-            const bool row = tok < a.tt && t < w.lq;
             const float l = (l0.x + l0.y) + (l1.x + l1.y);
             const bool none = l == 0.f;  // no key, or all of them at -infinity
             if (w.used > 1) {

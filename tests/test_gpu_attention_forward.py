@@ -479,3 +479,32 @@ def test_offsets_past_32_bits(cuda_lib):
     cba.cba_attention_forward(d, q, kv, kv, None, None, o, None, ws)
     want, _ = run(q.contiguous(), kv, kv, 0.125, False)
     assert cba.cba_get_status(ws) == cba.CBA_OK and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("dim,dtype", [(64, BF), (128, BF), (64, F16)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_packed_results_do_not_depend_on_the_neighbours_queries(cuda_lib, dim, dtype, causal):
+    """A tile's rows behind a sequence hold the next one's queries: whatever their logits, the sequence keeps its bits, over
+    several steps of keys."""
+    rng = np.random.default_rng(dim)
+    lens = [500, 60, 700, 33]
+    cu = torch.tensor(np.cumsum([0] + lens), dtype=torch.int32, device="cuda")
+    n = sum(lens)
+    for hq, hk in ((2, 2), (6, 2)):
+        q = place(rng.normal(size=(1, n, hq, dim)), "bshd", dtype)[0]
+        k, v = (place(rng.normal(size=(1, n, hk, dim)), "bshd", dtype)[0] for _ in range(2))
+        for bound in ({}, dict(max_q=700, max_k=700)):
+            kw = dict(cu_q=cu, cu_k=cu, sequences=4, **bound)
+            o, lse = run(q, k, v, 0.25, causal, **kw)
+            for other in (slice(500, 560), slice(1260, 1293)):
+                keep = [i for i in range(n) if not other.start <= i < other.stop]
+                for change in ("large", "growing", "infinite"):
+                    q2 = q.clone()
+                    if change == "large":
+                        q2[other] *= 1000
+                    elif change == "growing":
+                        q2[other] *= 4
+                    else:
+                        q2[other, :, 3] = math.inf
+                    o2, lse2 = run(q2, k, v, 0.25, causal, **kw)
+                    assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[:, keep], lse[:, keep]), change
