@@ -90,6 +90,23 @@ def test_attention_descriptor_without_gradients():
     assert (d.k.token, d.dq.token, d.dout.token) == (256, 0, 0)
 
 
+@pytest.mark.parametrize("kw", [dict(len_q=(1 << 30) + 1), dict(len_k=(1 << 30) + 1), dict(len_q=(1 << 31) - 1),
+                                dict(packed=1, total_q=(1 << 30) + 1), dict(packed=1, total_k=1 << 40),
+                                dict(q=ST(1 << 38, 256, 64)), dict(type=cba.CBA_F32), dict(dim=136), dict(dim=60),
+                                dict(batch=1 << 24, len_q=1 << 14)], ids=str)
+def test_attention_past_its_limits_has_no_workspace(lib, kw):
+    """Refused by the checks themselves: the workspace query, which needs no driver, refuses the descriptor too."""
+    d = at(**kw)
+    assert lib.cba_attention_forward_workspace_bytes(ctypes.byref(d)) == 0
+    cu = dict(cu_q=FAKE, cu_k=FAKE) if d.packed else {}
+    assert at_fwd(lib, d, **cu) == cba.CBA_ERR_UNSUPPORTED
+
+
+def test_attention_takes_lengths_up_to_its_limit(lib):
+    for kw in (dict(len_q=1 << 30), dict(len_k=1 << 30), dict(packed=1, total_q=1 << 30, total_k=1 << 30)):
+        assert lib.cba_attention_forward_workspace_bytes(ctypes.byref(at(**kw))) >= 256, kw
+
+
 # ---- query and key norms with rotation
 
 def qk(**kw):
