@@ -70,6 +70,29 @@ def test_philox_words_of_the_published_vectors():
     assert [int(v) for v in T.philox(0, [0])[0]] == [0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8]
 
 
+def philox_of_four(key, counter):
+    """Philox4x32-10 in whole numbers, with all four words of the counter."""
+    k, x = list(key), list(counter)
+    for _ in range(10):
+        a, b = x[0] * 0xD2511F53, x[2] * 0xCD9E8D57
+        x = [b >> 32 ^ x[1] ^ k[0], b & 0xFFFFFFFF, a >> 32 ^ x[3] ^ k[1], a & 0xFFFFFFFF]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return x
+
+
+def test_philox_has_the_order_of_the_published_words():
+    """The known answers with a key and a counter in all words pin the order of both; the reference, whose counter has zeros
+    in its upper words, agrees with the same steps on other seeds and counters, their low words first."""
+    ones, pi = [0xFFFFFFFF] * 4, [0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344]
+    assert philox_of_four(ones[:2], ones) == [0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD]
+    assert philox_of_four([0xA4093822, 0x299F31D0], pi) == [0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1]
+    rng = np.random.default_rng(7)
+    for _ in range(50):
+        key, low = ([int(v) for v in rng.integers(0, 1 << 32, 2)] for _ in range(2))
+        words = T.philox(key[0] | key[1] << 32, [low[0] | low[1] << 32])[0]
+        assert [int(v) for v in words] == philox_of_four(key, low + [0, 0])
+
+
 def test_philox_uses_all_words_of_seed_and_counter():
     base = T.philox(5, [7])[0]
     for seed, c in ((5 | 1 << 40, 7), (5, 7 | 1 << 40), (6, 7), (5, 8)):
