@@ -508,3 +508,47 @@ def test_packed_results_do_not_depend_on_the_neighbours_queries(cuda_lib, dim, d
                         q2[other, :, 3] = math.inf
                     o2, lse2 = run(q2, k, v, 0.25, causal, **kw)
                     assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[:, keep], lse[:, keep]), change
+
+
+def guarded(t, value):
+    """t [tokens, ...] inside a larger buffer whose other elements are `value`; the view and the buffer."""
+    big = torch.full((t.shape[0] + 600, *t.shape[1:]), value, device="cuda", dtype=t.dtype)
+    big[300:-300] = t
+    return big[300:-300], big
+
+
+@pytest.mark.parametrize("hq,hk,dim,dtype", [(2, 2, 64, BF), (8, 2, 128, F16)])
+@pytest.mark.parametrize("bound", [{}, dict(max_q=300, max_k=300), dict(max_q=40, max_k=70)], ids=str)
+@pytest.mark.parametrize("starts,good", [
+    ([-5, 120, 1 << 30], [(0, 120), (120, 300)]),                     # taken as 0, 120, 300
+    ([0, 120, 300, 90, 90, 2 ** 31 - 1], []),                         # falling, then up past the end, over the others
+    ([0, 120, 300, 90, 90], [(0, 120), (120, 300)]),
+    ([-2 ** 31, -7, 0, 200, 300, 2 ** 31 - 1], [(0, 200), (200, 300)]),
+    ([300, 2 ** 31 - 1, 0], [])])
+def test_wrong_starts_leave_the_good_sequences_and_all_else(cuda_lib, starts, good, bound, hq, hk, dim, dtype):
+    """Good sequences among wrong starts get their own values; nothing outside the tensors is read (NaN) or written."""
+    rng = np.random.default_rng(len(starts))
+    (q, _), (k, _), (v, _) = (guarded(place(rng.normal(size=(1, 300, h, dim)), "bshd", dtype)[0], math.nan) for h in (hq, hk, hk))
+    o, big_o = guarded(torch.full((300, hq, dim), 9.0, device="cuda", dtype=dtype), 7.0)
+    lse_ends = torch.full((hq * 300 + 600,), 7.0, device="cuda")
+    lse = lse_ends[300:-300].view(hq, 300).fill_(9.0)
+    cu = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    d = cba.make_attention_desc(q, k, v, o, causal=True, scale=dim ** -0.5, sequences=len(starts) - 1, **bound)
+    ws = torch.full((cba.cba_attention_forward_workspace_bytes(d),), 255, dtype=torch.uint8, device="cuda")
+    cba.cba_attention_forward(d, q, k, v, cu, cu, o, lse, ws)
+    assert cba.cba_get_status(ws) == cba.CBA_OK
+    ends = [min(max(s, 0), 300) for s in starts]
+    reached = [max(b, a) for a, b in zip(ends, ends[1:])]
+    for s, e in good:
+        assert sum(a < b and a < e and b > s for a, b in zip(ends, reached)) == 1  # no other sequence writes its rows
+        m, n = min(e - s, bound.get("max_q", 300)), min(e - s, bound.get("max_k", 300))
+        wo, wl, bo, bl = bars(f8(q[s:s + m]), f8(k[s:s + n]), f8(v[s:s + n]), dim ** -0.5, True, dtype)
+        check(o[s:s + m], wo, bo, f"o of {s}")
+        check(lse[:, s:s + m], wl, bl, f"lse of {s}")
+        assert (o[s + m:e] == 9).all() and (lse[:, s + m:e] == 9).all()
+    touched = torch.zeros(300, dtype=torch.bool, device="cuda")
+    for a, b in zip(ends, reached):
+        touched[a:b] = True
+    assert (o[~touched] == 9).all() and (lse[:, ~touched] == 9).all() and torch.isfinite(o.float()).all()
+    for ends_of in (big_o[:300], big_o[-300:], lse_ends[:300], lse_ends[-300:]):
+        assert (ends_of == 7).all()
