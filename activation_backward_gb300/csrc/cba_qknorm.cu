@@ -525,8 +525,9 @@ int check_desc(const cba_qk_norm_rope_desc_t *d) {
     if (!(std::isfinite(d->eps) && d->eps >= 0.f)) return CBA_ERR_ARG;
     if (d->param_type != CBA_F32 && d->param_type != d->type) return CBA_ERR_UNSUPPORTED;
     if (d->dim % 8 != 0 || d->dim > kQkMaxDim) return CBA_ERR_UNSUPPORTED;
-    // tokens are counted in 32 bits, beside a grid's stride of them
+    // tokens and heads are counted in 32 bits, beside a grid's stride of tokens and a warp's of heads
     if ((double)d->batch * d->len > 2147483648.0 - 65536.0) return CBA_ERR_UNSUPPORTED;
+    if (d->heads_q > (1 << 30) || d->heads_k > (1 << 30)) return CBA_ERR_UNSUPPORTED;
     const int vec = 16 / (int)dtype_bytes(d->type);
     const cba_attn_strides_t *ss[] = {&d->q, &d->k, &d->yq, &d->yk, &d->dyq, &d->dyk, &d->dq, &d->dk};
     for (int i = 0; i < 8; ++i) {
@@ -598,7 +599,7 @@ void plan_blocks(const cba_qk_norm_rope_desc_t &d, const QkArgs &a, int *blocks,
     auto warps = [&](int w) { return ((long long)a.tokens * a.parts[w] + kWarps - 1) / kWarps; };
     long long need[2] = {warps(0), d.heads_k ? warps(1) : 0};
     if (need[0] + need[1] > most) {
-        const long long all = a.steps[0] + a.steps[1];
+        const long long all = (long long)a.steps[0] + a.steps[1];
         // (either side has a block at least, however few its heads beside the other's)
         need[1] = d.heads_k ? std::min({each, most - 1LL, std::max(1LL, (most * (long long)a.steps[1] + all / 2) / all)}) : 0;
         need[0] = std::min(each, most - need[1]);

@@ -467,10 +467,11 @@ int cba_attention_forward(const cba_attention_desc_t *d, const void *q, const vo
  * are fp32.  table: fp32 [positions][rot_dim / 2][2], cos and sin.  pos: int32
  * [batch][len], contiguous, the tokens' rows of the table; NULL: a token's index in its
  * sequence (len <= positions, or CBA_ERR_ARG).  Values outside 0 .. positions - 1 are
- * taken as the nearest of these.  dim: a multiple of 8 up to 256, rot_dim even.  heads_k may be 0
- * (then k and what belongs to it are not used).
- * Heads of any finite elements give the formula's values, with eps = 0 too; but dx of a head with
- * r past the largest fp32 number (a root mean square below 2^-128) is infinite or NaN.
+ * taken as the nearest of these.  dim: a multiple of 8 up to 256, rot_dim even, heads up
+ * to 2^30.  heads_k may be 0 (then k and what belongs to it are not used).
+ *
+ * Heads of any finite elements give the formula's values, with eps = 0 too; but dx of a head
+ * with r past the largest fp32 number (a root mean square below 2^-128) is infinite or NaN.
  *
  * Strides as of attention, in multiples of 16 bytes, bases (gamma and table too) 16-byte
  * aligned (CBA_ERR_ALIGN); all 0: contiguous.  An output may be the input of the same

@@ -147,6 +147,16 @@ def test_qk_limits(lib):
     assert qk_fwd(lib, qk(type=cba.CBA_F32, q=ST(2640, 260, 64)), q=None) == cba.CBA_ERR_ARG  # 1040 bytes: a multiple of 16
 
 
+@pytest.mark.parametrize("kw", [dict(heads_q=(1 << 31) - 1), dict(heads_k=(1 << 31) - 31), dict(heads_q=(1 << 30) + 1)], ids=str)
+def test_qk_heads_past_32_bit_steps(lib, kw):
+    """A warp's next head, or the sum of a side's steps, would pass 2^31."""
+    d = qk(dim=8, rot_dim=8, **kw)
+    assert lib.cba_qk_norm_rope_workspace_bytes(ctypes.byref(d)) == 0
+    assert qk_fwd(lib, d) == cba.CBA_ERR_UNSUPPORTED and qk_bwd(lib, d) == cba.CBA_ERR_UNSUPPORTED
+    most = qk(dim=256, rot_dim=30, len=3000, heads_q=1 << 30, heads_k=1 << 30)
+    assert 0 < lib.cba_qk_norm_rope_workspace_bytes(ctypes.byref(most)) <= 1 << 20
+
+
 def test_qk_pointers_alignment_workspace(lib):
     d = qk()
     for name in ("q", "k", "yq", "yk", "table"):
