@@ -10,8 +10,9 @@
 // computes the words again.
 //
 // Memory bounds large calls, with the words' products close behind.  Measured: 65536 x 2048 bf16
-// with a residual 134 us (0.88 of the copy rate; issue slots 66% taken), 43264 x 255 fp32 as one run
-// 14.9 us (0.87), 338 x 512 fp32 5.1.
+// with a residual 133 us (0.89 of the copy rate; issue slots 66% taken), 43264 x 255 fp32 as one run
+// 14.9 us (0.87; 18.4 from a cold start), 338 x 512 fp32 5.1.  Rows with gaps that are no whole vectors:
+// 20000 x 1001 fp32, gaps of 3, 57 us, with a residual 64 (0.41, 0.56).
 #include <algorithm>
 #include <cmath>
 
@@ -73,7 +74,7 @@ constexpr int kVectors = 4;
 
 // Vectors of 16 bytes: rows without gaps (FLAT: the tensors are one run of n elements),
 // or rows of whole vectors.  (65536 x 2048 bf16 with a residual: 4 vectors of a thread in
-// flight 134 us, 2 138, 1 165.)
+// flight 133 us, 2 138, 1 165.)
 template <typename T, bool RES, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_vec_kernel(const DrArgs a) {
     constexpr int V = 16 / sizeof(T), U = kVectors;

@@ -14,7 +14,7 @@
 // are the queries' or the keys', in the proportion of their steps.
 //
 // Measured (us), 4 x 8192 tokens, 32/8 heads of 128, bf16: forward 134 (0.74 of the copy rate; issue
-// slots 51% taken), backward 187, of which 6 for the sum of dgamma's rows (0.81; 58%).  2 x 169
+// slots 51% taken), backward 187, of which 6 for the sum of dgamma's rows (0.80; 57%).  2 x 169
 // tokens, 8 heads of 64: 5.8 and 9.7, one and two launches (3.5 and 6.4 on the device).
 #include <algorithm>
 #include <cmath>

@@ -443,7 +443,9 @@ int cba_attention_backward(const cba_attention_desc_t *d, const void *q, const v
  * are not written.
  *
  * P is rounded to the elements' type for its product with v, as a share of the row's
- * largest (f16: times a power of two); its sums, the maxima and o's are fp32.  Few rows
+ * largest (f16: times a power of two); its sums, the maxima and o's are fp32.  Shares are of
+ * a running largest, so up to 2^8 before the division: in bf16, o is finite as long as
+ * 2^8 sum |v| over a row's keys is within fp32's range.  Few rows
  * with many keys are cut along the keys and joined in a fixed order.  In a sequence's
  * own rows, infinities and NaN spread as in the formulas (a masked pair may still
  * multiply its row of v by 0); another sequence's never do. */

@@ -552,3 +552,17 @@ def test_wrong_starts_leave_the_good_sequences_and_all_else(cuda_lib, starts, go
     assert (o[~touched] == 9).all() and (lse[:, ~touched] == 9).all() and torch.isfinite(o.float()).all()
     for ends_of in (big_o[:300], big_o[-300:], lse_ends[:300], lse_ends[-300:]):
         assert (ends_of == 7).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 200])
+def test_values_near_the_largest_number(cuda_lib, dim, rows):
+    """bf16 values whose sum times 2^8 is just within fp32's range: 1000 of up to 2^109 (2^8 x 1000 x 2^109 < 2^127), under
+    logits that come within 2^8 of a new largest one."""
+    rng = np.random.default_rng(dim)
+    q, k = np.zeros((1, rows, 1, dim)), np.zeros((1, 1000, 1, dim))
+    q[..., 0], k[0, 500:, 0, 0] = 1.0, 5.5
+    v = 2.0 ** 109 * rng.uniform(0.5, 1, (1, 1000, 1, dim)) * (1 if rows == 1 else rng.choice([-1, 1], (1, 1000, 1, dim)))
+    q, k, v = (place(t, "bshd", BF) for t in (q, k, v))
+    o, lse = run(q, k, v, 1.0, False)
+    compare(q, k, v, o, lse, 1.0, False)
